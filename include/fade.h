@@ -433,6 +433,99 @@ fade_status_t fade_decode_attention_noalloc(const fade_config_t* cfg, const fade
 fade_status_t fade_h2o_accumulate(const fade_config_t* cfg, fade_layer_t* layer,
                                   const float* logits_ws, const float* ml_ws, void* stream);
 
+/* ---- Drafted tokens: a tree of up to FADE_TREE_MAX_NODES tokens per row, verified against the
+ * cache in one pass. A step drafts after its maintenance (fade_cache_demote, fade_evict_rerope):
+ * fade_tree_layout once, then per layer fade_qk_norm_rope, fade_tree_attention and, once the
+ * accepted path is known, fade_tree_commit. (The pages decode one token at a time; FADE-zh
+ * §核心机制 fixes the tiers that these calls read and append to.)
+ *
+ * Per-head vectors of several tokens, fp16, the d channels of a head contiguous: element strides
+ * from one row, token and head to the next, so a slice of a fused projection's output
+ * ([rows][tokens][heads][d]) or a head-major prompt ([rows][heads][tokens][d]) is passed as it
+ * lies. x 16-byte aligned, strides multiples of 8 elements. */
+typedef struct {
+  uint16_t* x;
+  int64_t row_stride, token_stride, head_stride;
+} fade_heads_t;
+
+#define FADE_TREE_MAX_NODES 64
+
+/* Masks and positions of every row's tree, from its parents. parents: DEVICE i32 [B][T], the
+ * parent of node i (a lower index), -1 for a child of the last cached token; a value outside
+ * [0, i) reads as -1. n_nodes: DEVICE i32 [B] (clamped to [0, T]), NULL = T in every row.
+ * base_pos: DEVICE i32 [B], the position of a root (fade_next_position). Writes mask: u64 [B][T],
+ * bit j of node i set if j is i or an ancestor of it, 0 past the row's nodes; and pos: i32
+ * [B][T], base_pos + the node's depth (base_pos past the row's nodes). 1 <= T <=
+ * FADE_TREE_MAX_NODES; B = cfg->batch. */
+fade_status_t fade_tree_layout(const fade_config_t* cfg, int32_t T, const int32_t* parents,
+                               const int32_t* n_nodes, const int32_t* base_pos, uint64_t* mask,
+                               int32_t* pos, void* stream);
+
+/* Per-head RMS norm and RoPE in one pass: q (Hq heads) and k (H heads) of n_rows x n_tokens
+ * tokens. Each vector x of d channels: y = x / sqrt(mean(x^2) + eps) * w in fp32 (w: fp16 [d],
+ * q_weight or k_weight, 16-byte aligned; NULL: no norm, y = x), then rotated to its token's
+ * position as fade_rope_apply does (the same table; nothing for FADE_ROPE_NONE), rounded once to
+ * fp16. pos: DEVICE i32 [n_rows][n_tokens], or NULL: token t of every row is at position t
+ * (n_tokens <= max_pos then). Positions outside [0, max_pos) are clamped. A NULL q_in or k_in
+ * leaves that side out. An output may be its input (the same pointer and strides); otherwise they
+ * must not overlap, and the vectors of an output must not overlap each other. eps > 0 and finite
+ * where a weight is given. */
+fade_status_t fade_qk_norm_rope(const fade_config_t* cfg, const float* table, int32_t max_pos,
+                                const fade_heads_t* q_in, const fade_heads_t* q_out,
+                                const uint16_t* q_weight, const fade_heads_t* k_in,
+                                const fade_heads_t* k_out, const uint16_t* k_weight, float eps,
+                                const int32_t* pos, int64_t n_rows, int32_t n_tokens,
+                                void* stream);
+
+/* Workspace bytes of fade_tree_attention and fade_tree_commit for trees of up to T nodes; 0 on an
+ * invalid configuration or T (fade_last_error says why). */
+size_t fade_tree_ws_bytes(const fade_config_t* cfg, int32_t T);
+
+/* Attention of a tree of drafted tokens. q_rot: fp16 [B][T][Hq][d], tree_k and tree_v: the
+ * nodes' rotated keys and their values (H heads), all at the nodes' positions. Every query head
+ * of node i attends, with scale 1/sqrt(d), to every token its KV head holds (sinks, middle,
+ * recent) and to the nodes j of mask[b][i] (u64 [B][T]; bits at or past the row's node count are
+ * ignored). n_nodes: DEVICE i32 [B] (clamped to [0, T]) or NULL: T. out: fp16 [B][T][Hq][d]; lse:
+ * f32 [B][T][Hq], the log of the sum of exp(s) over what the node attends to. A node that attends
+ * to nothing (an empty cache and an empty mask) gets zeros and -inf; a node past the row's count
+ * is left as it was, in out and lse, and what its q, k, v and mask hold does not matter. What a
+ * node does not attend to does not reach its output, whatever it holds (infinities and NaN
+ * included). The cache may be empty.
+ * The middle tier's codes are multiplied by their scales and rounded to fp16 (half a step, 2^-11
+ * relative, of the kind an FP16 cache makes), products accumulate in fp32, the softmax is fp32
+ * and its probabilities are rounded to fp16 before they meet V.
+ * Every count is read on the device and the launch does not depend on the counts: a captured call
+ * stays valid while the cache grows or is evicted from. ws: DEVICE, 16-byte aligned,
+ * fade_tree_ws_bytes(cfg, T) bytes at least; calls that may overlap (two streams, two graphs)
+ * need workspaces of their own. */
+fade_status_t fade_tree_attention(const fade_config_t* cfg, const fade_layer_t* layer, int32_t T,
+                                  const uint16_t* q_rot, const fade_heads_t* tree_k,
+                                  const fade_heads_t* tree_v, const uint64_t* mask,
+                                  const int32_t* n_nodes, uint16_t* out, float* lse, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* Commit an accepted path: row b's nodes path[b][0 .. h_n_path[b] - 1] (DEVICE i32 [B][T], each
+ * the parent of the next and the first a root; h_n_path: HOST i32 [B], each in [0, T]) become the
+ * row's newest tokens, as that many decode steps without eviction would make them: each is
+ * appended (a sink while fewer than n_sink are held, else the newest recent token) after the
+ * oldest token of a full recent window is demoted as fade_cache_demote does. Scores (H2O, EMA):
+ * the path nodes' probabilities of the preceding fade_tree_attention, p = exp(s - lse) summed over
+ * the query heads of the KV head, with keys as that call saw them, are accumulated node by node as
+ * fade_h2o_accumulate does, a node joining with score 0 before its own probabilities are added.
+ * A row with h_n_path 0 is left unchanged. Pending evictions are made by the next
+ * fade_evict_rerope: mid_capacity has to hold them (budget + T is always enough when every step
+ * starts with its maintenance); FADE_ERR_CAPACITY, nothing enqueued, if a row's middle tier would
+ * overflow. Rows sharing their tier decisions need equal path lengths. A path node outside [0, T)
+ * is recorded in the layer's status and read as node 0.
+ * q_rot, lse: as in fade_tree_attention, and ws (16-byte aligned, fade_tree_ws_bytes(cfg, T)):
+ * needed by H2O and EMA, otherwise ignored (may be NULL). h_n_path is read at the call: a
+ * captured commit replays the same lengths. */
+fade_status_t fade_tree_commit(const fade_config_t* cfg, fade_layer_t* layer, int32_t T,
+                               const uint16_t* q_rot, const float* lse,
+                               const fade_heads_t* tree_k, const fade_heads_t* tree_v,
+                               const int32_t* path, const int32_t* h_n_path, void* ws,
+                               size_t ws_bytes, void* stream);
+
 /* Host: cache position of row `row`'s next token = held tokens after the next step's
  * demotion and eviction (KVLong §1.2.2: positions inside the cache). -1 on bad arguments. */
 int32_t fade_next_position(const fade_config_t* cfg, const fade_layer_t* layer, int32_t row);

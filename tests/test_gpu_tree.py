@@ -1,0 +1,638 @@
+"""Drafted-token operators on the GPU against plain 64-bit implementations.
+
+Tolerances count roundings. u = 2^-11 is half a step of fp16 relative to the value, 2^-24 of fp32.
+Attention: a dequantised middle key rounds to fp16 once, which moves a logit by at most
+delta = u * scale * sum_c |q_c k_c|; the softmax then moves every probability by a factor within
+e^(+-2 delta); probabilities and dequantised values round to fp16 once each (u each), the output
+once (u |out|); fp32 sums over d channels and N tokens add (N + d) 2^-24, the fast exponential and
+logarithm 2^-20.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import pq, quant
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -11
+
+
+@pytest.fixture(scope="module")
+def F():
+    from tiered_mixed_precision_gb300 import build
+
+    build.build()
+    from tiered_mixed_precision_gb300 import fade as F
+
+    return F
+
+
+def dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).cuda()
+
+
+def random_parents(rng, B, T, kind="tree"):
+    if kind == "chain":
+        return np.tile(np.arange(T, dtype=np.int32) - 1, (B, 1))
+    if kind == "flat":
+        return np.full((B, T), -1, np.int32)
+    p = np.full((B, T), -1, np.int32)
+    for i in range(1, T):
+        p[:, i] = rng.integers(-1, i, B)
+    return p
+
+
+def plain_layout(parents, n):
+    """Ancestor sets as a bool [T][T] and depths, by walking up the parents."""
+    T = len(parents)
+    see, depth = np.zeros((T, T), bool), np.zeros(T, int)
+    for i in range(n):
+        j = i
+        while True:
+            see[i, j] = True
+            p = parents[j]
+            if not 0 <= p < j:
+                break
+            depth[i] += 1
+            j = p
+    return see, depth
+
+
+def mask_words(see):
+    """bool [B][T][T] -> i64 [B][T]"""
+    w = (see.astype(np.uint64) << np.arange(see.shape[-1], dtype=np.uint64)).sum(-1, dtype=np.uint64)
+    return w.view(np.int64)
+
+
+# --------------------------------------------------------------------------- layout
+@pytest.mark.parametrize("B,T,kind", [(1, 1, "tree"), (3, 2, "chain"), (2, 64, "chain"),
+                                      (5, 64, "tree"), (256, 33, "tree"), (2, 17, "flat")])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_layout(F, B, T, kind, ragged):
+    rng = np.random.default_rng(B * 100 + T)
+    par = random_parents(rng, B, T, kind)
+    if T > 4:   # what is no lower index is a root
+        par[0, 2], par[0, 3], par[B - 1, 4] = 2, 60000, -7
+    n = rng.integers(0, T + 1, B).astype(np.int32) if ragged else None
+    if ragged:
+        n[0] = T + 5    # clamped
+    base = rng.integers(0, 1 << 20, B).astype(np.int32)
+    cfg = F.Config(batch=B, num_q_heads=4, num_kv_heads=1, head_dim=64, mid_capacity=16)
+    mask = torch.full((B, T), -1, dtype=torch.int64, device="cuda")
+    pos = torch.full((B, T), -1, dtype=torch.int32, device="cuda")
+    F.fade_tree_layout(cfg, dev(par), None if n is None else dev(n), dev(base), mask, pos)
+    for b in range(B):
+        nb = T if n is None else min(int(n[b]), T)
+        see, depth = plain_layout(par[b], nb)
+        assert np.array_equal(mask[b].cpu().numpy(), mask_words(see)), b
+        assert np.array_equal(pos[b].cpu().numpy(), base[b] + depth), b
+
+
+# --------------------------------------------------------------------------- norm + rotation
+def norm_reference(x, w, eps, table, pos, r):
+    """x [n][t][heads][d] fp16, table [max_pos][d/4][4] -> (fp64 result, error bound)."""
+    x = x.astype(np.float64)
+    d = x.shape[-1]
+    y = x if w is None else (x / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+                             * w.astype(np.float64))
+    a, b = y[..., :r // 2], y[..., r // 2:r]
+    rows = table[pos][..., :r // 4, :].astype(np.float64)
+    c = rows[..., 0:2].reshape(*pos.shape, 1, r // 2)
+    s = rows[..., 2:4].reshape(*pos.shape, 1, r // 2)
+    out = np.concatenate([a * c - b * s, b * c + a * s, y[..., r:]], -1)
+    mag = np.abs(y)
+    pair = np.abs(a) + np.abs(b)
+    mag = np.concatenate([pair, pair, mag[..., r:]], -1)
+    # one rounding to fp16 (half a subnormal step at least) after at most d/8 + 16 fp32 roundings
+    return out, U * np.abs(out) + 2.0 ** -25 + (d / 8 + 16) * 2.0 ** -24 * mag * (1 + U)
+
+
+@pytest.mark.parametrize("d,heads,rows,tokens,rotary,weights,layout", [
+    (128, (16, 2), 1, 1, 0, "both", "fused"),
+    (64, (8, 8), 2, 3, 0, "both", "tokens"),
+    (128, (32, 8), 3, 37, 0, "both", "heads"),
+    (128, (8, 1), 2, 513, 96, "both", "fused"),
+    (64, (4, 2), 5, 7, 4, "q", "tokens"),
+    (64, (1, 1), 1, 5000, 44, "k", "heads"),
+    (128, (4, 4), 2, 2, 124, "none", "tokens"),
+    (128, (32, 8), 64, 16, 0, "both", "in place"),
+])
+def test_norm(F, d, heads, rows, tokens, rotary, weights, layout):
+    rng = np.random.default_rng(d + tokens)
+    hq, h = heads
+    maxpos = 5003
+    cfg = F.Config(batch=1, num_q_heads=hq, num_kv_heads=h, head_dim=d, mid_capacity=16,
+                   rope_rotary_dim=rotary)
+    table = torch.zeros(maxpos * d, device="cuda")
+    F.fade_rope_table_init(cfg, table, maxpos)
+    x = rng.standard_normal((rows, tokens, hq + 2 * h, d)).astype(np.float16)
+    x[0, 0, 0] = 0                           # a vector of zeros
+    x[-1, -1, hq] = 6e4                      # squares past fp16
+    x[0, -1, hq - 1] *= np.float16(2e-6)     # subnormal channels
+    gx = dev(x)
+    if layout == "heads":
+        q = gx[:, :, :hq].transpose(1, 2).contiguous().transpose(1, 2)
+        k = gx[:, :, hq:hq + h].transpose(1, 2).contiguous().transpose(1, 2)
+    elif layout == "tokens":
+        q, k = gx[:, :, :hq].contiguous(), gx[:, :, hq:hq + h].contiguous()
+    else:
+        q, k = gx[:, :, :hq], gx[:, :, hq:hq + h]
+    w = [(1 + 0.3 * rng.standard_normal(d)).astype(np.float16) for _ in range(2)]
+    qw = w[0] if weights in ("both", "q") else None
+    kw = w[1] if weights in ("both", "k") else None
+    pos = rng.integers(0, maxpos, (rows, tokens)).astype(np.int32)
+    pos[0, 0], pos[-1, -1] = -3, maxpos + 9   # clamped
+    if layout == "in place":
+        qo, ko = q, k
+    else:
+        qo = torch.empty((rows, tokens, hq, d), dtype=torch.float16, device="cuda")
+        ko = torch.empty((rows, h, tokens, d), dtype=torch.float16, device="cuda").transpose(1, 2)
+    opt = lambda a: None if a is None else dev(a)
+    F.fade_qk_norm_rope(cfg, table, maxpos, q, k, opt(qw), opt(kw), 1e-6, dev(pos), qo, ko)
+    tab = table.cpu().numpy().reshape(maxpos, d // 4, 4)
+    cl = np.clip(pos, 0, maxpos - 1)
+    for got, src, ww in ((qo, x[:, :, :hq], qw), (ko, x[:, :, hq:hq + h], kw)):
+        ref, tol = norm_reference(src, ww, 1e-6, tab, cl, rotary or d)
+        err = np.abs(got.double().cpu().numpy() - ref)
+        fits = np.abs(ref) + tol < 65504
+        assert (err[fits] <= tol[fits]).all(), float((err - tol)[fits].max())
+    if layout in ("fused", "in place"):   # the projection's v is not touched
+        assert torch.equal(gx[:, :, hq + h:].cpu(), torch.from_numpy(x[:, :, hq + h:]))
+
+
+def test_norm_without_weights_is_rope_apply(F):
+    """No weights: bit for bit the rotation fade_rope_apply makes, and a copy without RoPE."""
+    for kind in ("llama3", "none"):
+        cfg = F.Config(batch=3, num_q_heads=8, num_kv_heads=2, head_dim=128, mid_capacity=16,
+                       rope_kind=kind, rope_factor=8.0)
+        table = torch.zeros(400 * 128, device="cuda")
+        if kind != "none":
+            F.fade_rope_table_init(cfg, table, 400)
+        q = torch.randn((3, 1, 8, 128), device="cuda").half()
+        pos = torch.tensor([[0], [399], [77]], dtype=torch.int32, device="cuda")
+        got, want = torch.empty_like(q), torch.empty_like(q)
+        F.fade_qk_norm_rope(cfg, table, 400, q, None, None, None, 1.0, pos, got, None)
+        F.fade_rope_apply(cfg, table, 400, q, want, 3, 8, pos, 0)
+        assert torch.equal(got, want)
+
+
+# --------------------------------------------------------------------------- attention
+class Cache:
+    """One layer with random contents in cache order, and its tiers on the host."""
+
+    def __init__(self, F, rng, B, hq, h, d, lens, S=4, W=64, rec=None, kb=4, vb=2, codec="int",
+                 policy="none", extra=70, scale=1.0, decay=0.9, shared=False, budget=None):
+        self.F = F
+        mid = [max(0, n - S - (W if rec is None else rec)) for n in lens]
+        evicts = policy != "none"
+        budget = max(mid) if budget is None else budget
+        self.cfg = F.Config(batch=B, num_q_heads=hq, num_kv_heads=h, head_dim=d, n_sink=S,
+                            recent_window=W, int4_budget=budget if evicts else -1,
+                            middle_k_bits=kb, middle_v_bits=vb, mid_capacity=max(mid) + extra,
+                            policy=policy, rope_kind="none", v_codec=codec, ema_decay=decay,
+                            shared_rows=shared)
+        self.L = L = F.TieredLayer(self.cfg, max(1, max(lens)), "cuda")
+        self.cb = None
+        if codec == "pq":
+            self.cb = (scale * rng.standard_normal((d // 4, 256, 4))).astype(np.float16)
+            L.set_pq_codebook(dev(self.cb))
+        P = max(1, max(lens))
+        k = (scale * rng.standard_normal((B, h, P, d))).astype(np.float16)
+        k[..., 3] *= 4
+        v = (scale * rng.standard_normal((B, h, P, d))).astype(np.float16)
+        mass = dev(rng.random((B, h, P)).astype(np.float32)) if policy == "h2o" else None
+        F.fade_cache_reset(L)
+        F.fade_cache_prefill(L, dev(k), dev(v), P, lens, mass, None, 0)
+
+    def unit(self, b, h):
+        """(n_sink, n_mid, n_recent, keys, values, scores) of a unit, cache order, float64."""
+        L, c = self.L, self.cfg
+        m = L.meta[b, h].cpu().numpy()
+        ns, nm, nr, head, cur = (int(x) for x in m[:5])
+        ring = [(head + i) % c.recent_window for i in range(nr)]
+        g = lambda t: t[b, h].cpu().numpy()
+        kq = quant.unpack(g(L.mid_k_codes[cur])[:nm], c.middle_k_bits)
+        mk = quant.dequantize(kq, g(L.mid_k_scales[cur])[:nm])
+        vc = g(L.mid_v_codes[cur])[:nm]
+        if self.cb is not None:
+            mv = pq.decode(vc, self.cb).astype(np.float64)
+        else:
+            mv = quant.dequantize(quant.unpack(vc, c.middle_v_bits), g(L.mid_v_scales[cur])[:nm])
+        cat = lambda s, x, r: np.concatenate([s[:ns].astype(np.float64), x,
+                                              r[ring].astype(np.float64)])
+        return (ns, nm, nr, cat(g(L.sink_k), mk, g(L.recent_k)),
+                cat(g(L.sink_v), mv, g(L.recent_v)),
+                np.concatenate([g(L.sink_scores)[:ns], g(L.mid_scores[cur])[:nm],
+                                g(L.recent_scores)[ring]]))
+
+    def draft(self, rng, T, scale=1.0, fused=True):
+        c = self.cfg
+        B, hq, h, d = c.batch, c.num_q_heads, c.num_kv_heads, c.head_dim
+        self.q = (scale * rng.standard_normal((B, T, hq, d))).astype(np.float16)
+        self.tk = rng.standard_normal((B, T, h, d)).astype(np.float16)
+        self.tv = rng.standard_normal((B, T, h, d)).astype(np.float16)
+        self.dq = dev(self.q)
+        self.out = torch.full(self.q.shape, 7.0, dtype=torch.float16, device="cuda")
+        self.lse = torch.full(self.q.shape[:3], 7.0, device="cuda")
+        self.ws = torch.full((self.F.fade_tree_ws_bytes(c, T),), 0xff, dtype=torch.uint8,
+                             device="cuda")   # NaN patterns: nothing is read before it is written
+        self.fused = fused
+        self.load_tree()
+
+    def load_tree(self):
+        if self.fused:   # slices of a projection, token-major, and a head-major tensor
+            x = torch.zeros((*self.tk.shape[:2], 3 * self.tk.shape[2], self.tk.shape[3]),
+                            dtype=torch.float16, device="cuda")
+            self.dk = x[:, :, self.tk.shape[2]:2 * self.tk.shape[2]]
+            self.dk.copy_(dev(self.tk))
+            self.dv = dev(self.tv.transpose(0, 2, 1, 3)).transpose(1, 2)
+        else:
+            self.dk, self.dv = dev(self.tk), dev(self.tv)
+
+    def attend(self, see, n_nodes=None):
+        self.F.fade_tree_attention(self.L, self.dq, self.dk, self.dv, dev(mask_words(see)),
+                                   None if n_nodes is None else dev(n_nodes), self.out, self.lse,
+                                   self.ws)
+        return self.out.double().cpu().numpy(), self.lse.double().cpu().numpy()
+
+    def check(self, see, n_nodes=None):
+        out, lse = self.attend(see, n_nodes)
+        c = self.cfg
+        G = c.num_q_heads // c.num_kv_heads
+        for b in range(c.batch):
+            n = see.shape[1] if n_nodes is None else int(n_nodes[b])
+            assert (out[b, n:] == 7).all() and (lse[b, n:] == 7).all()
+            for h in range(c.num_kv_heads):
+                _, _, _, K, V, _ = self.unit(b, h)
+                for i in range(n):
+                    js = np.nonzero(see[b, i, :n])[0]
+                    k = np.concatenate([K, self.tk[b, js, h].astype(np.float64)])
+                    v = np.concatenate([V, self.tv[b, js, h].astype(np.float64)])
+                    for g in range(G):
+                        o, l = out[b, i, h * G + g], lse[b, i, h * G + g]
+                        compare(o, l, self.q[b, i, h * G + g].astype(np.float64), k, v,
+                                (b, i, h, g))
+        self.F.fade_check_status(self.L)
+
+
+def compare(o, l, q, k, v, where):
+    if not len(k):
+        assert (o == 0).all() and l == -np.inf, where
+        return
+    d = len(q)
+    scale = 1 / np.sqrt(d)
+    s = k @ q * scale
+    m = s.max()
+    e = np.exp(s - m)
+    p = e / e.sum()
+    ref, ref_l = p @ v, m + np.log(e.sum())
+    delta = U * scale * (np.abs(k) @ np.abs(q)).max()
+    sums = (len(k) + d) * 2.0 ** -24 + 2.0 ** -20
+    tol = (np.expm1(2 * delta) + 2 * U + sums) * (p @ np.abs(v)) * (1 + U) + U * np.abs(ref) \
+        + 2.0 ** -25
+    assert (np.abs(o - ref) <= tol).all(), (where, float((np.abs(o - ref) / tol).max()))
+    assert abs(l - ref_l) <= delta + sums + 2.0 ** -22 * abs(ref_l), (where, l, ref_l)
+
+
+CASES = [
+    # B, hq, h, d, lens, T, kind, options
+    (1, 8, 2, 64, [511], 4, "chain", {}),
+    (2, 16, 2, 128, [701, 64], 16, "tree", dict(vb=4)),
+    (1, 4, 4, 64, [300], 1, "chain", dict(kb=2)),
+    (3, 8, 1, 128, [0, 1, 5], 9, "tree", {}),                     # empty and sink-only rows
+    (2, 4, 1, 64, [130, 200], 64, "tree", dict(codec="pq")),
+    (1, 8, 1, 128, [900], 64, "tree", dict(codec="pq", kb=2)),     # 512 query rows
+    (1, 16, 8, 128, [196], 33, "tree", dict(kb=2, vb=4)),
+    (2, 4, 2, 64, [193, 333], 25, "flat", dict(vb=4)),
+    (1, 2, 1, 128, [2500], 64, "chain", dict(kb=2, vb=2)),
+    (2, 2, 2, 128, [70, 199], 7, "tree", dict(S=0, W=1)),
+    (1, 4, 1, 64, [400], 12, "tree", dict(S=130, W=200)),          # more FP16 tokens than a tile
+    (4, 32, 8, 128, [1030, 517, 1028, 69], 16, "tree", {}),
+]
+
+
+@pytest.mark.parametrize("B,hq,h,d,lens,T,kind,opt", CASES)
+@pytest.mark.parametrize("ragged", [False, True])
+def test_attention(F, B, hq, h, d, lens, T, kind, opt, ragged):
+    rng = np.random.default_rng(sum(lens) + T)
+    c = Cache(F, rng, B, hq, h, d, lens, **opt)
+    c.draft(rng, T, fused=ragged)
+    n = rng.integers(0, T + 1, B).astype(np.int32) if ragged else np.full(B, T, np.int32)
+    n[B - 1] = T
+    par = random_parents(rng, B, T, kind)
+    see = np.stack([plain_layout(par[b], T)[0] for b in range(B)])
+    if ragged:
+        see[:, 0, :] = False     # a node that sees no node, itself included
+        see[:, :, T - 1] = True  # bits past a row's nodes (where it has fewer) are ignored
+        for b in range(B):       # what the padding holds does not matter
+            c.tk[b, n[b]:] = np.nan
+            c.tv[b, n[b]:] = np.inf
+            c.q[b, n[b]:] = np.nan
+        c.dq = dev(c.q)
+        c.load_tree()
+    c.check(see, n if ragged else None)
+
+
+def test_attention_of_an_empty_cache_with_nodes_that_see_nothing(F):
+    rng = np.random.default_rng(5)
+    c = Cache(F, rng, 2, 8, 2, 64, [0, 0])
+    c.draft(rng, 6)
+    see = np.stack([plain_layout(np.arange(6) - 1, 6)[0]] * 2)
+    see[0, 2] = see[1, 5] = False
+    c.check(see)
+
+
+@pytest.mark.parametrize("d,codec", [(64, "int"), (128, "int"), (128, "pq")])
+def test_what_a_node_does_not_see_does_not_reach_it(F, d, codec):
+    """Infinities and NaN in the keys and values of other branches leave a node's bits alone; a
+    node that sees them is not finite."""
+    rng = np.random.default_rng(d)
+    c = Cache(F, rng, 1, 8, 2, d, [300], codec=codec)
+    T = 12
+    c.draft(rng, T)
+    par = np.array([-1, 0, 1, 2, 3, -1, 5, 6, 7, 8, 9, 10])   # two branches
+    see = plain_layout(par, T)[0][None]
+    c.check(see)
+    clean = c.out.clone(), c.lse.clone()
+    c.tv[0, 6, :, 5], c.tv[0, 7, :, 9], c.tk[0, 8] = np.inf, np.nan, np.nan
+    c.load_tree()
+    c.attend(see)
+    assert torch.equal(c.out[:, :6], clean[0][:, :6]) and torch.equal(c.lse[:, :6], clean[1][:, :6])
+    o = c.out.float().cpu().numpy()
+    for node in (6, 7):
+        assert not np.isfinite(o[0, node, :, 5]).any()
+    assert np.isfinite(o[0, 6, :, 9]).all() and np.isnan(o[0, 7, :, 9]).all()
+    assert np.isnan(o[0, 8:]).all()
+
+
+def test_large_logits_and_extreme_scales(F):
+    """Logits hundreds apart (the running maximum moves by whole exponents), keys near fp16's
+    largest value and values among its smallest."""
+    rng = np.random.default_rng(11)
+    c = Cache(F, rng, 1, 4, 1, 64, [600])
+    c.draft(rng, 8, scale=8.0)
+    see = np.tril(np.ones((1, 8, 8), bool))
+    c.check(see)
+    c = Cache(F, rng, 1, 4, 1, 128, [400], scale=1.0)
+    L = c.L
+    cur = int(L.meta[0, 0, 4])
+    L.mid_k_scales[cur][:, :, 7] = 9360.0
+    L.mid_k_codes[cur][:, :, 7] = 0x77
+    L.mid_v_scales[cur][:, :, 9] = 65504.0
+    L.mid_v_scales[cur][:, :, 11:200] = 2.0 ** -24
+    c.draft(rng, 8, scale=2.0 ** -12)
+    c.check(see)
+
+
+def test_attention_runs_the_same_twice_and_beside_another_stream(F):
+    rng = np.random.default_rng(3)
+    c = Cache(F, rng, 2, 8, 2, 128, [1500, 700])
+    c.draft(rng, 16)
+    see = np.stack([plain_layout(p, 16)[0] for p in random_parents(rng, 2, 16)])
+    c.check(see)
+    first = c.out.clone(), c.lse.clone()
+    mask, out2 = dev(mask_words(see)), torch.empty_like(c.out)
+    lse2, ws2 = torch.empty_like(c.lse), torch.empty_like(c.ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):   # two calls at once, each with its own workspace
+        F.fade_tree_attention(c.L, c.dq, c.dk, c.dv, mask, None, c.out, c.lse, c.ws)
+        with torch.cuda.stream(side):
+            F.fade_tree_attention(c.L, c.dq, c.dk, c.dv, mask, None, out2, lse2, ws2)
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
+    assert torch.equal(out2, first[0]) and torch.equal(lse2, first[1])
+
+
+# --------------------------------------------------------------------------- commit
+def state(c):
+    """Every unit's held bytes in cache order (codes as they are)."""
+    L, res = c.L, []
+    for b in range(c.cfg.batch):
+        for h in range(c.cfg.num_kv_heads):
+            m = L.meta[b, h].cpu().numpy()
+            ns, nm, nr, head, cur = (int(x) for x in m[:5])
+            ring = [(head + i) % c.cfg.recent_window for i in range(nr)]
+            g = lambda t: t[b, h].cpu().numpy()
+            res.append([np.array([ns, nm, nr]), g(L.sink_k)[:ns], g(L.sink_v)[:ns],
+                        g(L.mid_k_codes[cur])[:nm], g(L.mid_k_scales[cur])[:nm],
+                        g(L.mid_v_codes[cur])[:nm], g(L.mid_v_scales[cur])[:nm],
+                        g(L.recent_k)[ring], g(L.recent_v)[ring]])
+    return res
+
+
+COMMITS = [
+    # B, hq, h, d, lens, W, S, T, n_path, options
+    (2, 8, 2, 64, [200, 150], 64, 4, 16, [5, 3], {}),
+    (3, 4, 1, 128, [90, 0, 2], 16, 4, 9, [9, 9, 0], dict(vb=4)),        # sinks still filling
+    (2, 4, 4, 64, [30, 7], 3, 2, 20, [20, 1], dict(kb=2)),              # path longer than the ring
+    (1, 8, 1, 128, [300], 1, 0, 64, [64], dict(codec="pq")),
+    (2, 2, 1, 64, [10, 66], 64, 4, 7, [7, 7], dict(kb=2, vb=4)),        # ring with free slots
+]
+
+
+@pytest.mark.parametrize("policy", ["position", "h2o", "ema"])
+@pytest.mark.parametrize("B,hq,h,d,lens,W,S,T,n_path,opt", COMMITS)
+def test_commit(F, B, hq, h, d, lens, W, S, T, n_path, opt, policy):
+    """The tiers are bit for bit what demotions and appends one token at a time make of the same
+    tokens; the scores follow the accumulation in 64 bits."""
+    caches = [Cache(F, np.random.default_rng(sum(lens) + T), B, hq, h, d, lens, W=W, S=S,
+                    policy=policy, **opt) for _ in range(2)]
+    c, step = caches
+    rng = np.random.default_rng(1)
+    c.draft(rng, T)
+    path = np.zeros((B, T), np.int32)
+    par = np.full((B, T), -1, np.int32)
+    for b in range(B):   # increasing nodes, each the parent of the next
+        path[b, :n_path[b]] = np.sort(rng.choice(T, n_path[b], replace=False))
+        for i in range(1, n_path[b]):
+            par[b, path[b, i]] = path[b, i - 1]
+    see = np.stack([plain_layout(par[b], T)[0] for b in range(B)])
+    _, lse = c.attend(see)
+    before = [[c.unit(b, x) for x in range(h)] for b in range(B)]
+    F.fade_tree_commit(c.L, c.dq, c.lse, c.dk, c.dv, dev(path), n_path, c.ws)
+    F.fade_check_status(c.L)
+    # one token at a time, row by row: caches of one row each
+    for b in range(B):
+        one = Cache(F, np.random.default_rng(sum(lens) + T), B, hq, h, d, lens, W=W, S=S,
+                    policy=policy, **opt)
+        for i in range(n_path[b]):
+            F.fade_cache_demote(one.L)
+            kk, vv = (dev(np.repeat(x[b, path[b, i]][None], B, 0)) for x in (c.tk, c.tv))
+            F.fade_cache_append(one.L, kk, vv)
+        for x in range(h):
+            for got, want in zip(state(c)[b * h + x], state(one)[b * h + x]):
+                assert np.array_equal(got.view(np.uint8), want.view(np.uint8)), (b, x)
+        counts = F.fade_tier_counts(c.L)[b]
+        assert np.array_equal(counts, state(one)[b * h][0])
+    G = hq // h
+    for b in range(B):
+        for x in range(h):
+            ns, nm, nr, K, _, old = before[b][x]
+            got = c.unit(b, x)[5]
+            a = n_path[b]
+            if policy == "position" or a == 0:
+                want, tol = np.concatenate([old, np.zeros(a)]), 0.0
+            else:
+                want, tol = scores_reference(c, b, x, G, K, old, path[b, :a], lse, policy)
+            # held order: sinks, middle, recent; new tokens come last in every case
+            assert got.shape == want.shape
+            assert (np.abs(got - want) <= tol).all(), (b, x, float(np.abs(got - want).max()))
+
+
+def scores_reference(c, b, h, G, K, old, path, lse, policy):
+    """Scores in path order, and a bound: every probability moves by its logit's roundings (the key
+    to fp16 once, fp32 sums) and lse's; each update rounds to fp32 three times."""
+    d = K.shape[1]
+    k = np.concatenate([K, c.tk[b, path, h].astype(np.float64)])
+    s = np.concatenate([old, np.zeros(len(path))])
+    tol = np.zeros_like(s)
+    delta_max = 0.0
+    for i, node in enumerate(path):
+        live = len(old) + i + 1
+        q = c.q[b, node, h * G:(h + 1) * G].astype(np.float64)
+        z = q @ k[:live].T / np.sqrt(d)
+        p = np.exp(z - lse[b, node, h * G:(h + 1) * G][:, None])
+        delta = (U + (d + 4) * 2.0 ** -24) / np.sqrt(d) * (np.abs(q) @ np.abs(k[:live]).T)
+        err = (p * (np.expm1(delta) + 2.0 ** -19 + 2.0 ** -23 * np.abs(z))).sum(0)
+        if policy == "h2o":
+            s[:live] += p.sum(0)
+            tol[:live] += err
+        else:
+            dl, g = c.cfg.ema_decay, 1 - c.cfg.ema_decay
+            dl, g = float(np.float32(dl)), float(np.float32(1) - np.float32(dl))
+            s[:live] = dl * s[:live] + g * p.sum(0)
+            tol[:live] = dl * tol[:live] + g * err
+        tol[:live] += 4 * 2.0 ** -24 * np.abs(s[:live])
+        delta_max = max(delta_max, delta.max())
+    return s, tol + 2.0 ** -30
+
+
+def test_commit_of_a_bad_path_is_recorded(F):
+    rng = np.random.default_rng(2)
+    c = Cache(F, rng, 1, 4, 1, 64, [100], policy="position")
+    c.draft(rng, 4)
+    path = dev(np.array([[1, 77, -2, 3]], np.int32))
+    F.fade_tree_commit(c.L, c.dq, None, c.dk, c.dv, path, [3])
+    with pytest.raises(F.FadeError) as e:
+        F.fade_check_status(c.L)
+    assert e.value.status == 6
+    # counts and contents stay consistent: the bad nodes read as node 0
+    assert F.fade_tier_counts(c.L)[0].tolist() == [4, 35, 64]
+    ring = c.unit(0, 0)[3][-3:]
+    assert np.array_equal(ring[1], c.tk[0, 0, 0].astype(np.float64))
+
+
+# --------------------------------------------------------------------------- together
+@pytest.mark.parametrize("policy,codec,norm", [("none", "int", True), ("position", "int", False),
+                                               ("h2o", "int", True), ("ema", "pq", False)])
+def test_draft_steps_together(F, policy, codec, norm):
+    """Draft, attend, commit, evict, draft again, then a plain step, through FadeCache; every
+    attention against the 64-bit form of the state it read, every commit's counts and scores."""
+    from tiered_mixed_precision_gb300.model import FadeCache
+
+    rng = np.random.default_rng(7)
+    B, hq, h, d, T, P, layers = 2, 8, 2, 64, 11, 150, 2
+    cfg = F.Config(batch=B, num_q_heads=hq, num_kv_heads=h, head_dim=d, n_sink=4,
+                   recent_window=16, int4_budget=90 if policy != "none" else -1,
+                   mid_capacity=400, policy=policy, v_codec=codec)
+    fc = FadeCache(cfg, layers, P, 800)
+    cb = None
+    if codec == "pq":
+        cb = rng.standard_normal((d // 4, 256, 4)).astype(np.float16)
+        fc.set_pq_codebook(dev(cb))
+    if norm:
+        fc.set_qk_norm(*(dev((1 + 0.2 * rng.standard_normal(d)).astype(np.float16))
+                         for _ in range(2)))
+    draw = lambda *s: dev(rng.standard_normal(s).astype(np.float16))
+    for layer in range(layers):
+        fc.prefill(layer, draw(B, h, P, d), draw(B, h, P, d), q_raw=draw(B, hq, P, d))
+    view = Cache.__new__(Cache)
+    view.F, view.cfg, view.cb, view.fused = F, cfg, cb, False
+    for step in range(4):
+        par = random_parents(rng, B, T)
+        n = rng.integers(T // 2, T + 1, B).astype(np.int32)
+        want_pos = fc.next_positions()
+        tree = fc.tree_begin(dev(par), dev(n))
+        see = np.stack([plain_layout(par[b], n[b])[0] for b in range(B)])
+        assert np.array_equal(tree.mask.cpu().numpy(), mask_words(see))
+        for b in range(B):
+            assert np.array_equal(tree.pos[b].cpu().numpy(),
+                                  want_pos[b] + plain_layout(par[b], n[b])[1])
+            held = fc.layers[0].h_n_sink[b] + fc.layers[0].h_n_mid[b] + fc.layers[0].h_n_recent[b]
+            assert held == want_pos[b]
+        before = []
+        for layer in range(layers):
+            x = draw(B, T, hq + 2 * h, d)
+            out = torch.full((B, T, hq, d), 7.0, dtype=torch.float16, device="cuda")
+            fc.tree_attend(layer, tree, x[:, :, :hq], x[:, :, hq:hq + h], x[:, :, hq + h:], out)
+            view.L = fc.layers[layer]
+            view.q, view.tk = (t[layer].cpu().numpy() for t in (tree.q_rot, tree.k_rot))
+            view.tv = x[:, :, hq + h:].cpu().numpy()
+            got, lse = out.double().cpu().numpy(), tree.lse[layer].double().cpu().numpy()
+            units = [[view.unit(b, u) for u in range(h)] for b in range(B)]
+            before.append((units, view.q, view.tk, lse))
+            for b in range(B):
+                assert (got[b, n[b]:] == 7).all()
+                for i in range(n[b]):
+                    js = np.nonzero(see[b, i])[0]
+                    for a in range(hq):
+                        u = a // (hq // h)
+                        compare(got[b, i, a], lse[b, i, a], view.q[b, i, a].astype(np.float64),
+                                np.concatenate([units[b][u][3], view.tk[b, js, u]]),
+                                np.concatenate([units[b][u][4], view.tv[b, js, u]]), (step, b, i))
+        path, lens = np.zeros((B, T), np.int32), []
+        for b in range(B):
+            leaf = int(n[b]) - 1
+            nodes = np.nonzero(see[b, leaf])[0]
+            nodes = nodes[:rng.integers(0, len(nodes) + 1)]
+            path[b, :len(nodes)] = nodes
+            lens.append(len(nodes))
+        fc.tree_commit(tree, dev(path), lens)
+        for layer in range(layers):
+            units, view.q, view.tk, lse = before[layer]
+            view.L = fc.layers[layer]
+            F.fade_check_status(view.L)
+            for b in range(B):
+                for u in range(h):
+                    now = view.unit(b, u)
+                    assert sum(now[:3]) == sum(units[b][u][:3]) + lens[b]
+                    if policy in ("h2o", "ema") and lens[b]:
+                        want, tol = scores_reference(view, b, u, hq // h, units[b][u][3],
+                                                     units[b][u][5], path[b, :lens[b]], lse,
+                                                     policy)
+                        assert (np.abs(now[5] - want) <= tol).all()
+    # a plain step goes on from there
+    q, k, v = draw(layers, B, hq, d), draw(layers, B, h, d), draw(layers, B, h, d)
+    out = torch.empty_like(q)
+    fc.step_all(q, k, v, out)
+    for layer in range(layers):
+        F.fade_check_status(fc.layers[layer])
+        assert torch.isfinite(out[layer]).all()
+
+
+def test_a_captured_tree_step_follows_the_cache(F):
+    """norm and attention captured once and replayed while the cache grows: the bits of an eager
+    call on the same state."""
+    rng = np.random.default_rng(9)
+    c = Cache(F, rng, 2, 8, 2, 128, [900, 300], extra=700)
+    T = 6
+    c.draft(rng, T)
+    see = np.stack([plain_layout(p, T)[0] for p in random_parents(rng, 2, T)])
+    mask, path = dev(mask_words(see)), torch.arange(T, dtype=torch.int32, device="cuda").repeat(2, 1)
+    c.check(see)
+    ws2, out2, lse2 = torch.empty_like(c.ws), torch.empty_like(c.out), torch.empty_like(c.lse)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        F.fade_tree_attention(c.L, c.dq, c.dk, c.dv, mask, None, out2, lse2, ws2)
+    for n_path in ([6, 1], [6, 6], [0, 3]):
+        for _ in range(40):
+            F.fade_tree_commit(c.L, c.dq, None, c.dk, c.dv, path, n_path)
+        c.attend(see)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out2, c.out) and torch.equal(lse2, c.lse)
+    c.check(see)

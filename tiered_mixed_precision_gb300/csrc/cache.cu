@@ -305,22 +305,6 @@ __device__ __forceinline__ void store_fp16_key(const WarpKey<D>& k, uint16_t* ro
   }
 }
 
-// Quantise an fp16 row (V, or an unmoved K) with one warp.
-template <int D, int BITS>
-__device__ __forceinline__ void warp_quantize_row(const uint16_t* x, uint8_t* codes,
-                                                  uint16_t* scales) {
-  const int lane = threadIdx.x & 31;
-  constexpr int qmax = (1 << (BITS - 1)) - 1;
-#pragma unroll
-  for (int g = 0; g < D / kGroup; ++g) {
-    uint16_t sb;
-    int q;
-    quant_group_lane(h2f(x[g * kGroup + lane]), qmax, sb, q);
-    pack_group_store<BITS>(q, codes + g * (kGroup * BITS / 8));
-    if (lane == 0) scales[g] = sb;
-  }
-}
-
 template <int BYTES>
 __device__ __forceinline__ void copy_row(const void* src, void* dst) {
   if constexpr (BYTES % 16 == 0) {

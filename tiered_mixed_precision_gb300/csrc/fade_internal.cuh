@@ -51,6 +51,8 @@ enum DevCheck {
   kCheckAppendSlot,                  // append: the recent window is full
   kCheckCompactRow,                  // compaction: a destination row outside the unit (debug)
   kCheckAttnTile,                    // attention: a tile past the unit's capacity (debug)
+  kCheckTreePath,                    // tree commit: a path node outside the tree
+  kCheckTreeSlot,                    // tree commit: the middle tier is full or a bad ring head
 };
 inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
@@ -171,6 +173,22 @@ __device__ __forceinline__ void pack_group_store(int q, uint8_t* dst) {
 #pragma unroll
   for (int o = 1; o < per; o <<= 1) v |= __shfl_xor_sync(0xffffffffu, v, o);
   if (lane % per == 0) reinterpret_cast<uint32_t*>(dst)[lane / per] = v;
+}
+
+// Quantise an fp16 row (V, or an unmoved K) with one warp.
+template <int D, int BITS>
+__device__ __forceinline__ void warp_quantize_row(const uint16_t* x, uint8_t* codes,
+                                                  uint16_t* scales) {
+  const int lane = threadIdx.x & 31;
+  constexpr int qmax = (1 << (BITS - 1)) - 1;
+#pragma unroll
+  for (int g = 0; g < D / kGroup; ++g) {
+    uint16_t sb;
+    int q;
+    quant_group_lane(h2f(x[g * kGroup + lane]), qmax, sb, q);
+    pack_group_store<BITS>(q, codes + g * (kGroup * BITS / 8));
+    if (lane == 0) scales[g] = sb;
+  }
 }
 
 // Sign-extended code of channel c of a packed row.

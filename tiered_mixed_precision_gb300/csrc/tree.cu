@@ -1,0 +1,364 @@
+// Drafted tokens around the attention call: the tree's masks and positions, and the commit of the
+// accepted path (its tokens appended with the demotions they cause, its attention mass added to
+// the scores). Page "FADE：面向LLM推理的注意力感知分层KV缓存压缩技术", §第一层 and §第二层 (FP16 recent
+// window, mid-aged tokens quantised), §四种驱逐策略详解 1 and 2 (H2O, EMA scores).
+#include <math.h>
+
+#include "tree.cuh"
+
+namespace fade {
+
+fade_status_t validate_tree(const fade_config_t* c, int32_t T) {
+  fade_status_t st = validate_config(c);
+  if (st) return st;
+  if (T < 1 || T > FADE_TREE_MAX_NODES)
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "%d tree nodes outside [1, %d]", T,
+                     FADE_TREE_MAX_NODES);
+  return FADE_OK;
+}
+
+fade_status_t validate_heads(const fade_heads_t* h, const char* name) {
+  if (!h || !h->x) return set_error(FADE_ERR_INVALID_ARGUMENT, "NULL %s", name);
+  if ((reinterpret_cast<uintptr_t>(h->x) & 15) || h->row_stride % 8 || h->token_stride % 8 ||
+      h->head_stride % 8)
+    return set_error(FADE_ERR_INVALID_ARGUMENT,
+                     "%s: vectors must start 16-byte aligned (strides in multiples of 8 elements)",
+                     name);
+  return FADE_OK;
+}
+
+namespace {
+
+// One CTA per row, one thread per node. Pointer doubling: after k rounds a node's mask holds its
+// 2^k nearest ancestors and `up` is the 2^k-th, so six rounds reach every root of 64 nodes (a walk
+// up the parents would take 64 dependent shared loads on a chain).
+__global__ void __launch_bounds__(FADE_TREE_MAX_NODES)
+    tree_layout_kernel(int T, const int32_t* __restrict__ parents,
+                       const int32_t* __restrict__ n_nodes, const int32_t* __restrict__ base_pos,
+                       uint64_t* __restrict__ mask, int32_t* __restrict__ pos) {
+  __shared__ unsigned long long sm[FADE_TREE_MAX_NODES];
+  __shared__ int su[FADE_TREE_MAX_NODES];
+  const int b = blockIdx.x, i = threadIdx.x;
+  const int n = n_nodes ? min(max(n_nodes[b], 0), T) : T;
+  const bool live = i < n;
+  int up = live ? parents[(size_t)b * T + i] : -1;
+  if (up < 0 || up >= i) up = -1;
+  unsigned long long m = live ? 1ull << i : 0ull;
+#pragma unroll
+  for (int r = 0; r < 6; ++r) {
+    sm[i] = m;
+    su[i] = up;
+    __syncthreads();
+    if (up >= 0) {
+      m |= sm[up];
+      up = su[up];
+    }
+    __syncthreads();
+  }
+  if (i < T) {
+    mask[(size_t)b * T + i] = m;
+    pos[(size_t)b * T + i] = base_pos[b] + (live ? __popcll(m) - 1 : 0);
+  }
+}
+
+// ----------------------------------------------------------------- commit
+// The path's attention mass: one warp per token the unit holds or commits, lane l owning channels
+// l, l + 32, .. of its key (read once); per path node the G dot products, p = exp(s - lse) summed
+// over the heads and folded into the running score in path order. Path token j (score 0) takes
+// the nodes j, j + 1, .. of the path.
+template <int D, int KB>
+__global__ void __launch_bounds__(256) tree_scores_kernel(TreeArgs a, RowLens lens, int policy,
+                                                          float decay,
+                                                          const float* __restrict__ lse,
+                                                          const int32_t* __restrict__ path,
+                                                          float* __restrict__ path_sc) {
+  const int h = blockIdx.y, b = blockIdx.z, unit = b * a.H + h;
+  const int n_path = lens.v[b];
+  if (n_path == 0) return;
+  const int32_t* m = a.meta + unit * FADE_META_FIELDS;
+  const int n_sink = m[FADE_META_N_SINK], n_mid = m[FADE_META_N_MID];
+  const int n_rec = m[FADE_META_N_RECENT], head = m[FADE_META_HEAD], cur = m[FADE_META_CUR];
+  const int held = n_sink + n_mid + n_rec;
+  const int lane = threadIdx.x & 31;
+  const float scale = rsqrtf((float)D);
+  for (int j = blockIdx.x * 8 + (threadIdx.x >> 5); j < held + n_path; j += gridDim.x * 8) {
+    float k[D / 32];
+    float* sc;
+    int first = 0;
+    if (j >= n_sink && j < n_sink + n_mid) {
+      const size_t r = (size_t)unit * a.C + (j - n_sink);
+      const uint8_t* codes = a.mk[cur] + r * (D * KB / 8);
+      const uint16_t* scl = a.mks[cur] + r * (D / kGroup);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e)
+        k[e] = (float)unpack_code<KB>(codes, 32 * e + lane) * h2f(scl[e]);
+      sc = a.mid_sc[cur] + r;
+    } else {
+      const uint16_t* x;
+      if (j < n_sink) {
+        x = a.sink_k + ((size_t)unit * a.S + j) * D;
+        sc = a.sink_sc + (size_t)unit * a.S + j;
+      } else if (j < held) {
+        const int slot = (head + (j - n_sink - n_mid)) % a.W;
+        x = a.rec_k + ((size_t)unit * a.W + slot) * D;
+        sc = a.rec_sc + (size_t)unit * a.W + slot;
+      } else {
+        first = j - held;
+        x = a.tk.x + b * a.tk.row_stride + tree_node(a, path, b, first) * a.tk.token_stride +
+            h * a.tk.head_stride;
+        sc = path_sc + (size_t)unit * a.T + first;
+      }
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) k[e] = h2f(x[32 * e + lane]);
+    }
+    float score = j < held ? *sc : 0.f;
+    for (int i = first; i < n_path; ++i) {
+      const int node = tree_node(a, path, b, i);
+      const size_t q0 = ((size_t)b * a.T + node) * a.Hq + h * a.G;
+      float mass = 0.f;
+      for (int g = 0; g < a.G; ++g) {
+        const uint16_t* q = a.q + (q0 + g) * D;
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) s = fmaf(h2f(q[32 * e + lane]), k[e], s);
+        s = warp_sum(s);
+        mass += __expf(fmaf(s, scale, -lse[q0 + g]));
+      }
+      score = policy == FADE_EVICT_H2O ? score + mass : decay * score + (1.f - decay) * mass;
+    }
+    if (lane == 0) *sc = score;
+  }
+}
+
+// One CTA of 8 warps per unit. The unit's ring followed by the path's non-sink tokens is one
+// sequence; its first `dem` entries leave for the middle tier (whether they came from the ring or
+// from the path), the rest end in ring slots head, head + 1, ... Demotions first (two warps a
+// token, K and V side by side), then, after a barrier, the new tokens into the slots they freed.
+template <int D, int KB, int VB>
+__global__ void __launch_bounds__(256) tree_commit_kernel(TreeArgs a, RowLens lens,
+                                                          const int32_t* __restrict__ path,
+                                                          const float* __restrict__ path_sc) {
+  const int h = blockIdx.x, b = blockIdx.y, unit = b * a.H + h;
+  const int n_path = lens.v[b];
+  if (n_path == 0) return;   // uniform per CTA, as are the returns below
+  int32_t* m = a.meta + unit * FADE_META_FIELDS;
+  const int n_sink = m[FADE_META_N_SINK], n_mid = m[FADE_META_N_MID];
+  const int n_rec = m[FADE_META_N_RECENT], head = m[FADE_META_HEAD], cur = m[FADE_META_CUR];
+  const int to_sink = min(max(a.S - n_sink, 0), n_path);
+  const int dem = max(0, n_rec + n_path - to_sink - a.W);
+  if (n_sink < 0 || head < 0 || head >= a.W || n_rec < 0 || n_rec > a.W || n_mid < 0 ||
+      n_mid + dem > a.C) {
+    if (threadIdx.x == 0) record_status(a.status, kCheckTreeSlot);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0)
+    for (int i = lane; i < n_path; i += 32) {
+      const int node = path[(size_t)b * a.T + i];
+      if (node < 0 || node >= a.T) record_status(a.status, kCheckTreePath);
+    }
+  auto tree_row = [&](const fade_heads_t& t, int i) {
+    return t.x + b * t.row_stride + tree_node(a, path, b, i) * t.token_stride +
+           h * t.head_stride;
+  };
+  for (int w = warp; w < 2 * dem; w += 8) {
+    const int i = w >> 1, isv = w & 1;
+    const size_t mrow = (size_t)unit * a.C + n_mid + i;
+    const bool old = i < n_rec;
+    const size_t rrow = (size_t)unit * a.W + (head + i) % a.W;
+    const int pi = to_sink + i - n_rec;
+    if (!isv) {
+      warp_quantize_row<D, KB>(old ? a.rec_k + rrow * D : tree_row(a.tk, pi),
+                               a.mk[cur] + mrow * (D * KB / 8), a.mks[cur] + mrow * (D / kGroup));
+      if (lane == 0)
+        a.mid_sc[cur][mrow] =
+            old ? a.rec_sc[rrow] : (path_sc ? path_sc[(size_t)unit * a.T + pi] : 0.f);
+    } else {
+      const uint16_t* x = old ? a.rec_v + rrow * D : tree_row(a.tv, pi);
+      uint16_t* scl = a.mvs[cur] + mrow * (D / kGroup);
+      if (a.pq_cb)
+        warp_pq_encode_row<D>(x, a.pq_cb, a.mv[cur] + mrow * (D / 4), scl);
+      else
+        warp_quantize_row<D, VB>(x, a.mv[cur] + mrow * (D * VB / 8), scl);
+    }
+  }
+  __syncthreads();   // the demoted slots and every count have been read
+  for (int i = warp; i < n_path; i += 8) {
+    const int seq = n_rec + i - to_sink;   // the token's place in the ring's sequence
+    if (i >= to_sink && seq < dem) continue;   // demoted above
+    const size_t row = i < to_sink ? (size_t)unit * a.S + n_sink + i
+                                   : (size_t)unit * a.W + (head + seq) % a.W;
+    uint16_t* dk = (i < to_sink ? a.sink_k : a.rec_k) + row * D;
+    uint16_t* dv = (i < to_sink ? a.sink_v : a.rec_v) + row * D;
+    const uint16_t *sk = tree_row(a.tk, i), *sv = tree_row(a.tv, i);
+    if (lane < D / 8)
+      *reinterpret_cast<uint4*>(dk + 8 * lane) = *reinterpret_cast<const uint4*>(sk + 8 * lane);
+    else if (lane >= 16 && lane - 16 < D / 8)
+      *reinterpret_cast<uint4*>(dv + 8 * (lane - 16)) =
+          *reinterpret_cast<const uint4*>(sv + 8 * (lane - 16));
+    if (lane == 0)
+      (i < to_sink ? a.sink_sc : a.rec_sc)[row] =
+          path_sc ? path_sc[(size_t)unit * a.T + i] : 0.f;
+  }
+  if (threadIdx.x == 0) {
+    m[FADE_META_N_SINK] = n_sink + to_sink;
+    m[FADE_META_N_MID] = n_mid + dem;
+    m[FADE_META_N_RECENT] = n_rec + n_path - to_sink - dem;
+    m[FADE_META_HEAD] = (head + dem) % a.W;
+  }
+}
+
+template <int D, int KB>
+fade_status_t launch_scores(const fade_config_t* c, const TreeArgs& a, const RowLens& lens,
+                            int max_tokens, const float* lse, const int32_t* path, float* path_sc,
+                            cudaStream_t st) {
+  tree_scores_kernel<D, KB><<<dim3(ceil_div(max_tokens, 32), c->num_kv_heads, c->batch), 256, 0,
+                              st>>>(a, lens, c->policy, c->ema_decay, lse, path, path_sc);
+  return launch_status("fade_tree_commit scores");
+}
+
+template <int D, int KB, int VB>
+fade_status_t launch_commit(const fade_config_t* c, const TreeArgs& a, const RowLens& lens,
+                            const int32_t* path, const float* path_sc, cudaStream_t st) {
+  tree_commit_kernel<D, KB, VB>
+      <<<dim3(c->num_kv_heads, c->batch), 256, 0, st>>>(a, lens, path, path_sc);
+  return launch_status("fade_tree_commit");
+}
+
+}  // namespace
+
+TreeArgs make_tree_args(const fade_config_t* c, const fade_layer_t* L, int T, const uint16_t* q,
+                        const fade_heads_t* tk, const fade_heads_t* tv) {
+  TreeArgs a{};
+  a.sink_k = L->sink_k;
+  a.sink_v = L->sink_v;
+  a.rec_k = L->recent_k;
+  a.rec_v = L->recent_v;
+  for (int i = 0; i < 2; ++i) {
+    a.mk[i] = L->mid_k_codes[i];
+    a.mv[i] = L->mid_v_codes[i];
+    a.mks[i] = L->mid_k_scales[i];
+    a.mvs[i] = L->mid_v_scales[i];
+    a.mid_sc[i] = L->mid_scores[i];
+  }
+  a.sink_sc = L->sink_scores;
+  a.rec_sc = L->recent_scores;
+  a.meta = L->meta;
+  a.status = L->status;
+  a.pq_cb = c->v_codec == FADE_V_PQ ? L->pq_codebook : nullptr;
+  a.q = q;
+  a.tk = *tk;
+  a.tv = *tv;
+  a.B = c->batch;
+  a.H = c->num_kv_heads;
+  a.Hq = c->num_q_heads;
+  a.G = c->num_q_heads / c->num_kv_heads;
+  a.S = c->n_sink;
+  a.W = c->recent_window;
+  a.C = mid_stride(c);
+  a.T = T;
+  return a;
+}
+
+}  // namespace fade
+
+using namespace fade;
+
+extern "C" fade_status_t fade_tree_layout(const fade_config_t* c, int32_t T,
+                                          const int32_t* parents, const int32_t* n_nodes,
+                                          const int32_t* base_pos, uint64_t* mask, int32_t* pos,
+                                          void* stream) {
+  clear_error();
+  FADE_RANGE("fade_tree_layout");
+  fade_status_t st = validate_tree(c, T);
+  if (st) return st;
+  if (!parents || !base_pos || !mask || !pos)
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "NULL parents, base_pos, mask or pos");
+  tree_layout_kernel<<<c->batch, FADE_TREE_MAX_NODES, 0, as_stream(stream)>>>(
+      T, parents, n_nodes, base_pos, mask, pos);
+  return launch_status("fade_tree_layout");
+}
+
+extern "C" size_t fade_tree_ws_bytes(const fade_config_t* c, int32_t T) {
+  clear_error();
+  if (validate_tree(c, T)) return 0;
+  const size_t scores = (size_t)c->batch * c->num_kv_heads * T * 4;
+  const size_t attn = tree_attention_ws(c, T);
+  return ((scores > attn ? scores : attn) + 15) / 16 * 16;
+}
+
+extern "C" fade_status_t fade_tree_commit(const fade_config_t* c, fade_layer_t* L, int32_t T,
+                                          const uint16_t* q_rot, const float* lse,
+                                          const fade_heads_t* tree_k, const fade_heads_t* tree_v,
+                                          const int32_t* path, const int32_t* h_n_path, void* ws,
+                                          size_t ws_bytes, void* stream) {
+  clear_error();
+  FADE_RANGE("fade_tree_commit");
+  fade_status_t st = validate_tree(c, T);
+  if (!st) st = validate_layer(c, L);
+  if (!st) st = validate_heads(tree_k, "tree_k");
+  if (!st) st = validate_heads(tree_v, "tree_v");
+  if (st) return st;
+  if (!path || !h_n_path)
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "NULL path or path lengths");
+  const bool scored = c->policy == FADE_EVICT_H2O || c->policy == FADE_EVICT_EMA;
+  if (scored && (!q_rot || !lse || !ws))
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "H2O and EMA need q_rot, lse and a workspace");
+  if (scored && ((reinterpret_cast<uintptr_t>(q_rot) | reinterpret_cast<uintptr_t>(ws)) & 15))
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "q_rot and the workspace must be 16-byte aligned");
+  const size_t need = (size_t)c->batch * c->num_kv_heads * T * 4;
+  if (scored && ws_bytes < need)
+    return set_error(FADE_ERR_CAPACITY, "tree workspace %zu bytes, %zu needed", ws_bytes, need);
+  RowLens lens{}, to_sink{}, dem{};
+  int any = 0, max_tokens = 0;
+  for (int b = 0; b < c->batch; ++b) {
+    const int n = h_n_path[b];
+    if (n < 0 || n > T)
+      return set_error(FADE_ERR_INVALID_ARGUMENT, "row %d: path length %d outside [0, %d]", b, n,
+                       T);
+    if (c->shared_rows && n != h_n_path[0])
+      return set_error(FADE_ERR_INVALID_ARGUMENT,
+                       "rows sharing their tier decisions need equal path lengths (row %d)", b);
+    const int room = c->n_sink - L->h_n_sink[b];
+    to_sink.v[b] = n < room ? n : (room > 0 ? room : 0);
+    const int over = L->h_n_recent[b] + n - to_sink.v[b] - c->recent_window;
+    dem.v[b] = over > 0 ? over : 0;
+    if (n && L->h_n_mid[b] + dem.v[b] > c->mid_capacity)
+      return set_error(FADE_ERR_CAPACITY, "row %d needs %d middle slots, capacity %d", b,
+                       L->h_n_mid[b] + dem.v[b], c->mid_capacity);
+    if (n == 0) dem.v[b] = 0;
+    lens.v[b] = n;
+    any |= n;
+    const int total = L->h_n_sink[b] + L->h_n_mid[b] + L->h_n_recent[b] + n;
+    if (n && total > max_tokens) max_tokens = total;
+  }
+  if (!any) return FADE_OK;
+  const TreeArgs a = make_tree_args(c, L, T, q_rot, tree_k, tree_v);
+  cudaStream_t s = as_stream(stream);
+  float* path_sc = scored ? static_cast<float*>(ws) : nullptr;
+  const int d = c->head_dim, kb = c->middle_k_bits, vb = c->middle_v_bits;
+  if (scored) {
+    st = d == 64 ? (kb == 4 ? launch_scores<64, 4>(c, a, lens, max_tokens, lse, path, path_sc, s)
+                            : launch_scores<64, 2>(c, a, lens, max_tokens, lse, path, path_sc, s))
+                 : (kb == 4 ? launch_scores<128, 4>(c, a, lens, max_tokens, lse, path, path_sc, s)
+                            : launch_scores<128, 2>(c, a, lens, max_tokens, lse, path, path_sc, s));
+    if (st) return st;
+  }
+  if (d == 64)
+    st = kb == 4 ? (vb == 4 ? launch_commit<64, 4, 4>(c, a, lens, path, path_sc, s)
+                            : launch_commit<64, 4, 2>(c, a, lens, path, path_sc, s))
+                 : (vb == 4 ? launch_commit<64, 2, 4>(c, a, lens, path, path_sc, s)
+                            : launch_commit<64, 2, 2>(c, a, lens, path, path_sc, s));
+  else
+    st = kb == 4 ? (vb == 4 ? launch_commit<128, 4, 4>(c, a, lens, path, path_sc, s)
+                            : launch_commit<128, 4, 2>(c, a, lens, path, path_sc, s))
+                 : (vb == 4 ? launch_commit<128, 2, 4>(c, a, lens, path, path_sc, s)
+                            : launch_commit<128, 2, 2>(c, a, lens, path, path_sc, s));
+  if (st) return st;
+  for (int b = 0; b < c->batch; ++b) {
+    L->h_n_sink[b] += to_sink.v[b];
+    L->h_n_mid[b] += dem.v[b];
+    L->h_n_recent[b] += lens.v[b] - to_sink.v[b] - dem.v[b];
+  }
+  return FADE_OK;
+}

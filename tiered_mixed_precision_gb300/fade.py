@@ -35,6 +35,7 @@ META = {"n_sink": 0, "n_mid": 1, "n_recent": 2, "head": 3, "cur": 4, "n_ev": 5, 
 MAX_BATCH = 256
 STATUS_WORDS = 4
 ATTN_TILE_TOKENS = 256   # FADE_ATTN_TILE_TOKENS
+TREE_MAX_NODES = 64      # FADE_TREE_MAX_NODES
 
 
 class FadeError(RuntimeError):
@@ -70,6 +71,11 @@ class LayerT(ctypes.Structure):
                 ("victim_words", c_i32), ("chunk_slots", c_i32), ("status", c_vp),
                 ("h_n_sink", c_vp), ("h_n_mid", c_vp), ("h_n_recent", c_vp),
                 ("pq_codebook", c_vp)]
+
+
+class HeadsT(ctypes.Structure):
+    _fields_ = [("x", c_vp), ("row_stride", c_i64), ("token_stride", c_i64),
+                ("head_stride", c_i64)]
 
 
 class LayoutT(ctypes.Structure):
@@ -126,6 +132,15 @@ def lib():
             "fade_attention_tiled": (c_i32, [S(ConfigT)]),
             "fade_measure_fp32_rate": (c_i32, [c_i32, c_i32, c_vp, ctypes.POINTER(c_f64), c_vp]),
             "fade_selftest_bounded_wait": (c_i32, [c_vp, c_i32, c_i64, c_vp]),
+            "fade_tree_layout": (c_i32, [S(ConfigT), c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+            "fade_qk_norm_rope": (c_i32, [S(ConfigT), c_vp, c_i32, S(HeadsT), S(HeadsT), c_vp,
+                                          S(HeadsT), S(HeadsT), c_vp, c_f32, c_vp, c_i64, c_i32,
+                                          c_vp]),
+            "fade_tree_ws_bytes": (c_sz, [S(ConfigT), c_i32]),
+            "fade_tree_attention": (c_i32, [S(ConfigT), S(LayerT), c_i32, c_vp, S(HeadsT),
+                                            S(HeadsT), c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+            "fade_tree_commit": (c_i32, [S(ConfigT), S(LayerT), c_i32, c_vp, c_vp, S(HeadsT),
+                                         S(HeadsT), c_vp, c_vp, c_vp, c_sz, c_vp]),
             "fade_last_error": (ctypes.c_char_p, []),
         }
         for name, (res, args) in sig.items():
@@ -497,6 +512,118 @@ def fade_measure_fp32_rate(blocks: int, iters: int, sink, stream=None) -> float:
     _check(lib().fade_measure_fp32_rate(int(blocks), int(iters), _ptr(sink), ctypes.byref(ops),
                                         _stream(stream)))
     return ops.value
+
+
+def _tensors(stream, **tensors):
+    """Checks of the drafted-token entry points: every tensor that is given has the dtype, shape
+    and layout asked for (name=(tensor, dtype, shape, strided); strided: only the last dimension
+    has to be contiguous) and, unless the caller passes its own stream, lies on the current CUDA
+    device, whose current stream the call is enqueued on. ValueError otherwise."""
+    import torch
+
+    device = None
+    for name, (t, dtype, shape, strided) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != getattr(torch, dtype) or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not "
+                             f"{str(t.dtype).removeprefix('torch.')} {tuple(t.shape)}")
+        if not (t.is_contiguous() if not strided else
+                t.stride(-1) == 1 or t.shape[-1] == 1 or t.numel() == 0):
+            raise ValueError(f"{name} must be contiguous" + (" in its last dimension" if strided
+                                                             else ""))
+        if stream is None:
+            if device is None:
+                device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+            if t.device.type != "cuda" or t.device.index != device:
+                raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+
+
+def _heads(t):
+    """A [rows][tokens][heads][d] tensor as a fade_heads_t."""
+    return None if t is None else ctypes.byref(HeadsT(t.data_ptr(), t.stride(0), t.stride(1),
+                                                      t.stride(2)))
+
+
+def fade_tree_layout(cfg: Config, parents, n_nodes, base_pos, mask, pos, stream=None):
+    """parents i32 [B][T], n_nodes i32 [B] or None, base_pos i32 [B] -> mask i64 [B][T] (the
+    64 bits of FADE's u64 masks), pos i32 [B][T]."""
+    B, T = parents.shape
+    _tensors(stream, parents=(parents, "int32", (cfg.batch, T), False),
+             n_nodes=(n_nodes, "int32", (B,), False), base_pos=(base_pos, "int32", (B,), False),
+             mask=(mask, "int64", (B, T), False), pos=(pos, "int32", (B, T), False))
+    _check(lib().fade_tree_layout(ctypes.byref(cfg.c()), T, _ptr(parents), _ptr(n_nodes),
+                                  _ptr(base_pos), _ptr(mask), _ptr(pos), _stream(stream)))
+
+
+def fade_qk_norm_rope(cfg: Config, table, max_pos, q, k, q_weight, k_weight, eps, pos, q_rot,
+                      k_rot, stream=None):
+    """q [rows][tokens][Hq][d] and k [rows][tokens][H][d] (fp16, any strides over the first three
+    dimensions; either may be None) normed per head (weights fp16 [d]; None: no norm) and rotated
+    to pos (i32 [rows][tokens]; None: token t at t) into q_rot and k_rot of the same shapes."""
+    n, t = (q if q is not None else k).shape[:2]
+    d, hq, h = cfg.head_dim, cfg.num_q_heads, cfg.num_kv_heads
+    _tensors(stream, q=(q, "float16", (n, t, hq, d), True), k=(k, "float16", (n, t, h, d), True),
+             q_rot=(q_rot, "float16", (n, t, hq, d), True),
+             k_rot=(k_rot, "float16", (n, t, h, d), True),
+             q_weight=(q_weight, "float16", (d,), False),
+             k_weight=(k_weight, "float16", (d,), False), pos=(pos, "int32", (n, t), False))
+    _check(lib().fade_qk_norm_rope(ctypes.byref(cfg.c()), _ptr(table), max_pos, _heads(q),
+                                   _heads(q_rot), _ptr(q_weight), _heads(k), _heads(k_rot),
+                                   _ptr(k_weight), eps, _ptr(pos), n, t, _stream(stream)))
+
+
+def fade_tree_ws_bytes(cfg: Config, T: int) -> int:
+    """Workspace bytes of fade_tree_attention and fade_tree_commit for trees of up to T nodes."""
+    n = lib().fade_tree_ws_bytes(ctypes.byref(cfg.c()), T)
+    if n == 0:
+        raise FadeError(FADE_ERR_INVALID_ARGUMENT, fade_last_error())
+    return n
+
+
+def _tree_tensors(stream, cfg, q_rot, tree_k, tree_v):
+    T, d = q_rot.shape[1], cfg.head_dim
+    kv = (cfg.batch, T, cfg.num_kv_heads, d)
+    _tensors(stream, q_rot=(q_rot, "float16", (cfg.batch, T, cfg.num_q_heads, d), False),
+             tree_k=(tree_k, "float16", kv, True), tree_v=(tree_v, "float16", kv, True))
+    return T
+
+
+def fade_tree_attention(layer: TieredLayer, q_rot, tree_k, tree_v, mask, n_nodes, out, lse, ws,
+                        stream=None):
+    """q_rot fp16 [B][T][Hq][d], tree_k / tree_v fp16 [B][T][H][d] (any strides over the first
+    three dimensions), mask i64 [B][T], n_nodes i32 [B] or None -> out fp16 [B][T][Hq][d], lse
+    f32 [B][T][Hq]. ws: a tensor of fade_tree_ws_bytes(cfg, T) bytes."""
+    cfg = layer.cfg
+    _require_codebook(layer)
+    T = _tree_tensors(stream, cfg, q_rot, tree_k, tree_v)
+    _tensors(stream, mask=(mask, "int64", (cfg.batch, T), False),
+             n_nodes=(n_nodes, "int32", (cfg.batch,), False),
+             out=(out, "float16", q_rot.shape, False), lse=(lse, "float32", q_rot.shape[:3], False))
+    _check(lib().fade_tree_attention(ctypes.byref(cfg.c()), ctypes.byref(layer.c), T, _ptr(q_rot),
+                                     _heads(tree_k), _heads(tree_v), _ptr(mask), _ptr(n_nodes),
+                                     _ptr(out), _ptr(lse), _ptr(ws),
+                                     ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def fade_tree_commit(layer: TieredLayer, q_rot, lse, tree_k, tree_v, path, n_path, ws=None,
+                     stream=None):
+    """Append row b's nodes path[b][:n_path[b]] (path i32 [B][T] on the device, n_path any host
+    int sequence of B lengths); H2O / EMA: their attention mass from q_rot and lse as in
+    fade_tree_attention, with a workspace of fade_tree_ws_bytes(cfg, T) bytes."""
+    cfg = layer.cfg
+    _require_codebook(layer)
+    T = _tree_tensors(stream, cfg, q_rot, tree_k, tree_v)
+    _tensors(stream, path=(path, "int32", (cfg.batch, T), False),
+             lse=(lse, "float32", q_rot.shape[:3], False))
+    lens = np.ascontiguousarray(n_path, np.int32)
+    if lens.shape != (cfg.batch,):
+        raise ValueError(f"n_path must hold {cfg.batch} lengths")
+    _check(lib().fade_tree_commit(ctypes.byref(cfg.c()), ctypes.byref(layer.c), T, _ptr(q_rot),
+                                  _ptr(lse), _heads(tree_k), _heads(tree_v), _ptr(path),
+                                  lens.ctypes.data, _ptr(ws),
+                                  0 if ws is None else ws.numel() * ws.element_size(),
+                                  _stream(stream)))
 
 
 def fade_attention_tiled(cfg: Config) -> bool:

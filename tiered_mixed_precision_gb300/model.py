@@ -9,6 +9,7 @@ CUDA library on the caller's stream; this module only allocates buffers and pass
 from __future__ import annotations
 
 import ctypes
+from dataclasses import dataclass
 
 import numpy as np
 import torch
@@ -36,6 +37,20 @@ def _record_event(ev):
                                           1)  # cudaEventRecordExternal
     if rc != 0:
         raise RuntimeError(f"cudaEventRecordWithFlags failed ({rc})")
+
+
+@dataclass
+class DraftTree:
+    """A step's drafted tree (``FadeCache.tree_begin``): masks and positions for every layer, and
+    what the layers' attention left for the commit."""
+    n_nodes: torch.Tensor | None   # i32 [B]: nodes of every row (None: all of them)
+    mask: torch.Tensor             # i64 [B][T]: ancestor bits
+    pos: torch.Tensor              # i32 [B][T]
+    q_rot: torch.Tensor            # fp16 [L][B][T][Hq][d]
+    k_rot: torch.Tensor            # fp16 [L][B][T][H][d]
+    lse: torch.Tensor              # f32 [L][B][T][Hq]
+    ws: torch.Tensor
+    v: list                        # per layer: the values its attention read
 
 
 class FadeCache:
@@ -73,6 +88,8 @@ class FadeCache:
         self._pos_ring, self._pos_ring_ev, self._pos_ring_i = None, None, 0
         self._growing = None        # (key, graph) of growing_step
         self.growing_captures = 0   # captures made by growing_step
+        self.qk_norm = [None] * num_layers   # per layer (q weight, k weight, eps): set_qk_norm
+        self._tree_bufs = {}        # per tree size: the buffers of a DraftTree
 
     # ------------------------------------------------------------------ session persistence
     # Page "FADE：面向LLM推理的注意力感知分层KV缓存压缩技术", §会话持久化: the compressed cache is
@@ -151,6 +168,26 @@ class FadeCache:
         self.set_pq_codebook(cb, layer)
         return cb
 
+    # ------------------------------------------------------------------ per-head norms
+    def set_qk_norm(self, q_weight, k_weight, eps: float = 1e-6, layer=None):
+        """Models that norm each head of q and k before the rotation: fp16 [d] weights (None: that
+        side is not normed) for one layer, or every layer. Prefill, decode steps and drafted trees
+        of the layer then norm and rotate in one pass (``fade_qk_norm_rope``). Captured steps keep
+        the weights they were captured with."""
+        for w in (q_weight, k_weight):
+            if w is not None and (w.dtype != torch.float16 or tuple(w.shape) != (
+                    self.cfg.head_dim,) or not w.is_contiguous()):
+                raise ValueError(f"norm weights must be contiguous float16 [{self.cfg.head_dim}]")
+        for i in (range(len(self.layers)) if layer is None else [layer]):
+            self.qk_norm[i] = (None if q_weight is None and k_weight is None
+                               else (q_weight, k_weight, eps))
+
+    def _norm_rope(self, layer: int, q, k, pos, q_rot, k_rot):
+        """q [B][n][Hq][d], k [B][n][H][d] normed (if the layer norms) and rotated to pos."""
+        qw, kw, eps = self.qk_norm[layer] or (None, None, 1.0)
+        F.fade_qk_norm_rope(self.cfg, self.table, self.max_pos, q, k, qw, kw, eps, pos, q_rot,
+                            k_rot)
+
     # ------------------------------------------------------------------ pieces
     def rope_(self, x: torch.Tensor, n_groups: int, group_len: int, pos_start=None, pos_step=1):
         """Rotate x in place (fp16 [n_groups][group_len][d])."""
@@ -169,9 +206,18 @@ class FadeCache:
         B, H, P, d = k_raw.shape
         if prompt_len is None:
             prompt_len = np.full(B, P, np.int32)
-        self.rope_(k_raw, B * H, P, None, 1)
+        normed = self.qk_norm[layer] is not None
+        if normed:
+            kt = k_raw.transpose(1, 2)
+            self._norm_rope(layer, None, kt, None, None, kt)
+        else:
+            self.rope_(k_raw, B * H, P, None, 1)
         if mass is None and q_raw is not None and c.policy == "h2o":
-            self.rope_(q_raw, B * c.num_q_heads, P, None, 1)
+            if normed:
+                qt = q_raw.transpose(1, 2)
+                self._norm_rope(layer, qt, None, None, qt, None)
+            else:
+                self.rope_(q_raw, B * c.num_q_heads, P, None, 1)
             mass = torch.empty((B, H, P), dtype=torch.float32, device=k_raw.device)
             F.fade_prefill_mass(c, q_raw, k_raw, P, prompt_len, mass)
         L = self.layers[layer]
@@ -211,7 +257,15 @@ class FadeCache:
         accumulation."""
         c = self.cfg
         L = self.layers[layer]
-        if self.fused_prologue:
+        if self.qk_norm[layer] is not None:
+            if demote:
+                F.fade_cache_demote(L)
+            one = lambda x: x.unsqueeze(1)   # one token a row
+            self._norm_rope(layer, one(q_raw), one(k_raw), one(self.pos), one(self.q_rot),
+                            one(self.k_rot))
+            F.fade_cache_append(L, self.k_rot, v)
+            n = (1 if demote else 0) + 2
+        elif self.fused_prologue:
             F.fade_rope_append(L, self.table, self.max_pos, q_raw, k_raw, v, self.pos,
                                self.q_rot, demote=demote)
             n = 1
@@ -313,6 +367,56 @@ class FadeCache:
             if any((x != y).any() for x, y in zip(a, b)):
                 raise RuntimeError("capture_step needs a steady-state cache (tier counts changed)")
         return g
+
+    # ------------------------------------------------------------------ drafted trees
+    def tree_begin(self, parents: torch.Tensor, n_nodes: torch.Tensor | None = None) -> DraftTree:
+        """Start a step that verifies a tree of T drafted tokens per row (parents: device i32
+        [B][T], n_nodes: device i32 [B] or None): every layer's maintenance is done, and the
+        tree's masks and positions are built. Then ``tree_attend`` every layer and
+        ``tree_commit`` the accepted paths (or begin again, which leaves the cache as it is). A
+        cache that evicts needs mid_capacity >= int4_budget + T. The tree's buffers are reused by
+        the next tree of as many nodes."""
+        c, L = self.cfg, len(self.layers)
+        if parents.dim() != 2 or parents.shape[0] != c.batch:
+            raise ValueError(f"parents must be [{c.batch}][nodes]")
+        T = parents.shape[1]
+        ws_bytes = F.fade_tree_ws_bytes(c, T)
+        b = self._tree_bufs.get(T)
+        if b is None:
+            e = lambda dt, *s: torch.empty(s, dtype=dt, device=self.device)
+            b = self._tree_bufs[T] = dict(
+                mask=e(torch.int64, c.batch, T), pos=e(torch.int32, c.batch, T),
+                q_rot=e(torch.float16, L, c.batch, T, c.num_q_heads, c.head_dim),
+                k_rot=e(torch.float16, L, c.batch, T, c.num_kv_heads, c.head_dim),
+                lse=e(torch.float32, L, c.batch, T, c.num_q_heads),
+                ws=e(torch.uint8, ws_bytes))
+        # from pageable memory: the copy has left the host array when the call returns
+        self.pos.copy_(torch.from_numpy(self.next_positions()))
+        self.maintain_all()
+        F.fade_tree_layout(c, parents, n_nodes, self.pos, b["mask"], b["pos"])
+        self.launches += 1
+        return DraftTree(n_nodes=n_nodes, v=[None] * L, **b)
+
+    def tree_attend(self, layer: int, tree: DraftTree, q_raw: torch.Tensor, k_raw: torch.Tensor,
+                    v: torch.Tensor, out: torch.Tensor):
+        """One layer's attention of the tree: q_raw [B][T][Hq][d], k_raw and v [B][T][H][d] (fp16,
+        any strides over the first three dimensions; v is read again by the commit); out fp16
+        [B][T][Hq][d], left as it is past a row's nodes."""
+        self._norm_rope(layer, q_raw, k_raw, tree.pos, tree.q_rot[layer], tree.k_rot[layer])
+        F.fade_tree_attention(self.layers[layer], tree.q_rot[layer], tree.k_rot[layer], v,
+                              tree.mask, tree.n_nodes, out, tree.lse[layer], tree.ws)
+        tree.v[layer] = v
+        self.launches += 3
+
+    def tree_commit(self, tree: DraftTree, path: torch.Tensor, n_path):
+        """Append every row's accepted path (path: device i32 [B][T], n_path: B host lengths) to
+        every layer, each of which has attended to the tree."""
+        if any(v is None for v in tree.v):
+            raise ValueError("tree_attend every layer before the commit")
+        for i, L in enumerate(self.layers):
+            F.fade_tree_commit(L, tree.q_rot[i], tree.lse[i], tree.k_rot[i], tree.v[i], path,
+                               n_path, tree.ws)
+            self.launches += 2 if self.needs_logits else 1
 
     # ------------------------------------------------------------------ host-fed steps
     def prepare_host_pipeline(self, side=None):
