@@ -4,7 +4,8 @@ Tolerances count roundings. u = 2^-11 is half a step of fp16 relative to the val
 Attention: a dequantised middle key rounds to fp16 once, which moves a logit by at most
 delta = u * scale * sum_c |q_c k_c|; the softmax then moves every probability by a factor within
 e^(+-2 delta); probabilities and dequantised values round to fp16 once each (u each), the output
-once (u |out|); fp32 sums over d channels and N tokens add (N + d) 2^-24, the fast exponential and
+once (u |out|); a probability's rounding is off by half a subnormal step, 2^-25, at least, where
+the largest one is held as 2^6 or more: 2^-31 of the largest, sum |v| times over the sum of e; fp32 sums over d channels and N tokens add (N + d) 2^-24, the fast exponential and
 logarithm 2^-20.
 """
 
@@ -291,7 +292,7 @@ def compare(o, l, q, k, v, where):
     delta = U * scale * (np.abs(k) @ np.abs(q)).max()
     sums = (len(k) + d) * 2.0 ** -24 + 2.0 ** -20
     tol = (np.expm1(2 * delta) + 2 * U + sums) * (p @ np.abs(v)) * (1 + U) + U * np.abs(ref) \
-        + 2.0 ** -25
+        + 2.0 ** -25 + 2.0 ** -31 / e.sum() * np.abs(v).sum(0)
     assert (np.abs(o - ref) <= tol).all(), (where, float((np.abs(o - ref) / tol).max()))
     assert abs(l - ref_l) <= delta + sums + 2.0 ** -22 * abs(ref_l), (where, l, ref_l)
 

@@ -27,6 +27,20 @@ fade_status_t validate_heads(const fade_heads_t* h, const char* name) {
   return FADE_OK;
 }
 
+fade_status_t validate_tree_layer(const fade_config_t* c, const fade_layer_t* L) {
+  fade_status_t st = validate_layer(c, L);
+  if (st) return st;
+  uintptr_t any = 0;
+  for (const void* p : {(const void*)L->sink_k, (const void*)L->sink_v, (const void*)L->recent_k,
+                        (const void*)L->recent_v, (const void*)L->mid_k_codes[0],
+                        (const void*)L->mid_k_codes[1], (const void*)L->mid_v_codes[0],
+                        (const void*)L->mid_v_codes[1]})
+    any |= reinterpret_cast<uintptr_t>(p);
+  if (any & 15)
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "the layer's K and V buffers must be 16-byte aligned");
+  return FADE_OK;
+}
+
 namespace {
 
 // One CTA per row, one thread per node. Pointer doubling: after k rounds a node's mask holds its
@@ -295,7 +309,7 @@ extern "C" fade_status_t fade_tree_commit(const fade_config_t* c, fade_layer_t* 
   clear_error();
   FADE_RANGE("fade_tree_commit");
   fade_status_t st = validate_tree(c, T);
-  if (!st) st = validate_layer(c, L);
+  if (!st) st = validate_tree_layer(c, L);
   if (!st) st = validate_heads(tree_k, "tree_k");
   if (!st) st = validate_heads(tree_v, "tree_v");
   if (st) return st;

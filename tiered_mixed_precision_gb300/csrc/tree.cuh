@@ -24,6 +24,8 @@ __device__ __forceinline__ int tree_node(const TreeArgs& a, const int32_t* path,
 }
 
 fade_status_t validate_tree(const fade_config_t* c, int32_t T);
+// validate_layer, and the 16-byte alignment that vector loads of the tiers need.
+fade_status_t validate_tree_layer(const fade_config_t* c, const fade_layer_t* L);
 fade_status_t validate_heads(const fade_heads_t* h, const char* name);
 TreeArgs make_tree_args(const fade_config_t* c, const fade_layer_t* L, int T, const uint16_t* q,
                         const fade_heads_t* tk, const fade_heads_t* tv);
