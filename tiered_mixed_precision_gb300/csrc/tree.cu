@@ -31,7 +31,9 @@ fade_status_t validate_tree_layer(const fade_config_t* c, const fade_layer_t* L)
   fade_status_t st = validate_layer(c, L);
   if (st) return st;
   uintptr_t any = 0;
-  for (const void* p : {(const void*)L->sink_k, (const void*)L->sink_v, (const void*)L->recent_k,
+  for (const void* p : {(const void*)L->mid_k_scales[0], (const void*)L->mid_k_scales[1],
+                        (const void*)L->mid_v_scales[0], (const void*)L->mid_v_scales[1],
+                        (const void*)L->sink_k, (const void*)L->sink_v, (const void*)L->recent_k,
                         (const void*)L->recent_v, (const void*)L->mid_k_codes[0],
                         (const void*)L->mid_k_codes[1], (const void*)L->mid_v_codes[0],
                         (const void*)L->mid_v_codes[1]})
@@ -267,6 +269,7 @@ TreeArgs make_tree_args(const fade_config_t* c, const fade_layer_t* L, int T, co
   a.H = c->num_kv_heads;
   a.Hq = c->num_q_heads;
   a.G = c->num_q_heads / c->num_kv_heads;
+  while ((1 << a.log_g) < a.G) ++a.log_g;   // G is 1, 2, 4 or 8
   a.S = c->n_sink;
   a.W = c->recent_window;
   a.C = mid_stride(c);

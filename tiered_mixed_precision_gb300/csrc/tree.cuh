@@ -14,7 +14,7 @@ struct TreeArgs {
   const uint16_t* pq_cb;   // nullptr: integer-coded V
   const uint16_t* q;       // [B][T][Hq][D]
   fade_heads_t tk, tv;     // the nodes' keys and values, H heads
-  int B, H, Hq, G, S, W, C, T;
+  int B, H, Hq, G, log_g, S, W, C, T;   // G = 1 << log_g
 };
 
 // The i-th node of row b's path; a node outside the tree reads as node 0 (the commit records it).
