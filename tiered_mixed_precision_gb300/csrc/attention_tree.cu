@@ -52,22 +52,25 @@ struct Shape {
   static constexpr int LOWB = LOW ? kBlk : 0;                 // of Q or K in E5M2: 128-byte rows
   static constexpr int CODEBOOK = PQ ? 256 * D * 2 : 0;
   static constexpr int STAGE = 2 * TILE + LOWB;               // K, V, K's remainders
-  static constexpr int FIXED = TILE + LOWB + CODEBOOK + 2048 + 1024;   // Q, small arrays, alignment
+  static constexpr int FIXED = TILE + LOWB + CODEBOOK + 11264 + 1024;   // Q, small arrays, alignment
   static constexpr int STAGES = FIXED + 2 * STAGE <= 226 * 1024 ? 2 : 1;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
-  static constexpr int SOFT = 128 * R;                        // softmax threads: 16 rows a warp
-  static constexpr int UNPACK = 4 * D;                        // one group of 32 channels a thread
-  static constexpr int THREADS = SOFT + UNPACK + 128;         // and four warps, one issues products
+  static constexpr int SOFT = 256 * R;                        // softmax threads
+  static constexpr int SIDE = R == 1 ? 2 * D : D;             // threads that unpack K, and V
+  static constexpr int ITEMS = kTok * (D / 32) / SIDE;        // groups of 32 channels a thread
+  static constexpr int UNPACK = 2 * SIDE;
+  static constexpr int THREADS = SOFT + UNPACK + 128;         // and four warps: two issue, one prefetches
   // Registers a thread: at the launch, then by role (multiples of 8; the sum over the roles stays
   // within the launch's).
   static constexpr int REGS = 65536 / THREADS / 8 * 8;
   static constexpr int REGS_MMA = 40;
-  static constexpr int REGS_UNPACK = THREADS == 896 ? 64 : REGS > 128 ? 128 : REGS;
+  static constexpr int REGS_UNPACK_ = R == 1 ? 64 : 88;
+  static constexpr int REGS_UNPACK = REGS > REGS_UNPACK_ ? (REGS > 96 ? 96 : REGS) : REGS_UNPACK_;
   static constexpr int REGS_SOFT_ =
       (REGS * THREADS - REGS_MMA * 128 - REGS_UNPACK * UNPACK) / SOFT / 8 * 8;
-  static constexpr int REGS_SOFT = REGS_SOFT_ > 160 ? 160 : REGS_SOFT_;
+  static constexpr int REGS_SOFT = REGS_SOFT_ > 128 ? 128 : REGS_SOFT_;
   static_assert(REGS_SOFT * SOFT + REGS_UNPACK * UNPACK + REGS_MMA * 128 <= REGS * THREADS, "");
-  static constexpr int TMEM = 512;                            // columns: S 2 x 128, O D
+  static constexpr int TMEM = 512;                            // columns: S (and P) 2 x 128, O 2 x D
 };
 
 struct AttnTreeArgs {
@@ -170,6 +173,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok));
+  return ok != 0;
+}
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    bar)
@@ -225,31 +234,43 @@ __device__ __forceinline__ float ex2(float x) {
 
 // ---------------------------------------------------------------- tiles in shared memory
 // Rows of 64 channels (128 bytes) under the 128-byte swizzle, one [128][64] block per 64 channels.
-__device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {   // chunk: 8 channels
-  return (uint32_t)((chunk >> 3) * kBlk + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+// An unpacking thread always writes the same group of 32 channels of the same row: four 16-byte
+// chunks, chunk c at `at` ^ 16 c (`at`: the tile's address plus the thread's offset, whose bits 4..6
+// already hold the swizzle).
+__device__ __forceinline__ uint32_t group_at(int row, int g) {
+  return (uint32_t)((g >> 1) * kBlk + row * 128 + (((4 * (g & 1)) ^ (row & 7)) << 4));
 }
-__device__ __forceinline__ void st_chunk(char* tile, int row, int chunk, uint32_t x, uint32_t y,
-                                         uint32_t z, uint32_t w) {
-  *reinterpret_cast<uint4*>(tile + chunk_at(row, chunk)) = make_uint4(x, y, z, w);
+// The same in a tile of E5M2 (32 bytes a group): chunks 0 and 1.
+__device__ __forceinline__ uint32_t low_at(int row, int g) {
+  return (uint32_t)(row * 128 + (((2 * g) ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ void st_shared8(uint32_t at, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void st_chunk(uint32_t at, int c, uint32_t x, uint32_t y, uint32_t z,
+                                         uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (16 * c)), "r"(x), "r"(y),
+               "r"(z), "r"(w)
+               : "memory");
 }
 // 32 fp16 channels (one quantisation group) of a row, stored in ORDER.
 template <int ORDER>
-__device__ __forceinline__ void store_f16(char* tile, int row, int g, const uint4 (&x)[4]) {
+__device__ __forceinline__ void store_f16(uint32_t at, const uint4 (&x)[4]) {
   if constexpr (ORDER == kNatural) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) st_chunk(tile, row, 4 * g + c, x[c].x, x[c].y, x[c].z, x[c].w);
+    for (int c = 0; c < 4; ++c) st_chunk(at, c, x[c].x, x[c].y, x[c].z, x[c].w);
   } else if constexpr (ORDER == kPair4) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      st_chunk(tile, row, 4 * g + c, prmt(x[c].x, x[c].z, 0x5410), prmt(x[c].x, x[c].z, 0x7632),
+      st_chunk(at, c, prmt(x[c].x, x[c].z, 0x5410), prmt(x[c].x, x[c].z, 0x7632),
                prmt(x[c].y, x[c].w, 0x5410), prmt(x[c].y, x[c].w, 0x7632));
   } else {
 #pragma unroll
     for (int c = 0; c < 4; c += 2) {
       const uint4 &p = x[c], &q = x[c + 1];
-      st_chunk(tile, row, 4 * g + c, prmt(p.x, q.x, 0x5410), prmt(p.x, q.x, 0x7632),
-               prmt(p.y, q.y, 0x5410), prmt(p.y, q.y, 0x7632));
-      st_chunk(tile, row, 4 * g + c + 1, prmt(p.z, q.z, 0x5410), prmt(p.z, q.z, 0x7632),
+      st_chunk(at, c, prmt(p.x, q.x, 0x5410), prmt(p.x, q.x, 0x7632), prmt(p.y, q.y, 0x5410),
+               prmt(p.y, q.y, 0x7632));
+      st_chunk(at, c + 1, prmt(p.z, q.z, 0x5410), prmt(p.z, q.z, 0x7632),
                prmt(p.w, q.w, 0x5410), prmt(p.w, q.w, 0x7632));
     }
   }
@@ -270,10 +291,23 @@ __device__ __forceinline__ uint32_t scaled(uint32_t u, uint32_t off, __half2 s, 
   }
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Masks of the code fields in registers the compiler does not see through: a logic operation takes
+// one literal, and the offsets are it.
+template <int BITS>
+struct Fields {
+  uint32_t m[BITS == 4 ? 2 : 5];
+  __device__ __forceinline__ Fields() {
+#pragma unroll
+    for (int i = 0; i < (BITS == 4 ? 2 : 5); ++i) {
+      m[i] = BITS == 4 ? 0x000f000fu << (4 * i) : 0x00030003u << (2 * i);
+      asm volatile("" : "+r"(m[i]));
+    }
+  }
+};
 // A group of 32 codes: INT4 in four words (x), INT2 in two. LOW (INT4): the remainders as E5M2, the
 // upper bytes of their fp16 form, in the same order.
 template <int BITS, bool LOW>
-__device__ __forceinline__ void store_codes(char* tile, char* low, int row, int g,
+__device__ __forceinline__ void store_codes(uint32_t at, uint32_t low, const Fields<BITS>& f,
                                             const uint32_t* x, uint16_t scale) {
   const __half2 s = __half2half2(__ushort_as_half(scale));
   if constexpr (BITS == 4) {
@@ -283,17 +317,17 @@ __device__ __forceinline__ void store_codes(char* tile, char* low, int row, int 
       // nibbles at bits 0..3: 512 + u/2; at bits 4..7: 32 + u/2 (u = code + 8)
       const uint32_t w = x[c], h = w >> 8;
       uint32_t r[4] = {};
-      const uint32_t a = scaled<LOW>((w & 0x000f000fu) ^ 0x60086008u, 0x60086008u, s, r[0]);
-      const uint32_t b = scaled<LOW>((w & 0x00f000f0u) ^ 0x50805080u, 0x50805080u, s, r[1]);
-      const uint32_t d = scaled<LOW>((h & 0x000f000fu) ^ 0x60086008u, 0x60086008u, s, r[2]);
-      const uint32_t e = scaled<LOW>((h & 0x00f000f0u) ^ 0x50805080u, 0x50805080u, s, r[3]);
-      st_chunk(tile, row, 4 * g + c, a, b, d, e);
+      const uint32_t a = scaled<LOW>((w & f.m[0]) ^ 0x60086008u, 0x60086008u, s, r[0]);
+      const uint32_t b = scaled<LOW>((w & f.m[1]) ^ 0x50805080u, 0x50805080u, s, r[1]);
+      const uint32_t d = scaled<LOW>((h & f.m[0]) ^ 0x60086008u, 0x60086008u, s, r[2]);
+      const uint32_t e = scaled<LOW>((h & f.m[1]) ^ 0x50805080u, 0x50805080u, s, r[3]);
+      st_chunk(at, c, a, b, d, e);
       lo[2 * c] = prmt(r[0], r[1], 0x7531);
       lo[2 * c + 1] = prmt(r[2], r[3], 0x7531);
     }
     if constexpr (LOW) {
-      st_chunk(low, row, 2 * g, lo[0], lo[1], lo[2], lo[3]);
-      st_chunk(low, row, 2 * g + 1, lo[4], lo[5], lo[6], lo[7]);
+      st_chunk(low, 0, lo[0], lo[1], lo[2], lo[3]);
+      st_chunk(low, 1, lo[4], lo[5], lo[6], lo[7]);
     }
   } else {
     uint32_t none;
@@ -302,14 +336,14 @@ __device__ __forceinline__ void store_codes(char* tile, char* low, int row, int 
       // crumbs at bits 0, 2, 4, 6, 8 of a half: 512, 128, 32, 8, 2 + u/2 (u = code + 2)
       const uint32_t w = x[c], h = w >> 8;
       auto sc = [&](uint32_t u, uint32_t off) { return scaled<false>(u, off, s, none); };
-      st_chunk(tile, row, 4 * g + 2 * c, sc((w & 0x00030003u) ^ 0x60026002u, 0x60026002u),
-               sc((w & 0x000c000cu) ^ 0x58085808u, 0x58085808u),
-               sc((w & 0x00300030u) ^ 0x50205020u, 0x50205020u),
-               sc((w & 0x00c000c0u) ^ 0x48804880u, 0x48804880u));
-      st_chunk(tile, row, 4 * g + 2 * c + 1, sc((w & 0x03000300u) ^ 0x42004200u, 0x42004200u),
-               sc((h & 0x000c000cu) ^ 0x58085808u, 0x58085808u),
-               sc((h & 0x00300030u) ^ 0x50205020u, 0x50205020u),
-               sc((h & 0x00c000c0u) ^ 0x48804880u, 0x48804880u));
+      st_chunk(at, 2 * c, sc((w & f.m[0]) ^ 0x60026002u, 0x60026002u),
+               sc((w & f.m[1]) ^ 0x58085808u, 0x58085808u),
+               sc((w & f.m[2]) ^ 0x50205020u, 0x50205020u),
+               sc((w & f.m[3]) ^ 0x48804880u, 0x48804880u));
+      st_chunk(at, 2 * c + 1, sc((w & f.m[4]) ^ 0x42004200u, 0x42004200u),
+               sc((h & f.m[1]) ^ 0x58085808u, 0x58085808u),
+               sc((h & f.m[2]) ^ 0x50205020u, 0x50205020u),
+               sc((h & f.m[3]) ^ 0x48804880u, 0x48804880u));
     }
   }
 }
@@ -320,7 +354,7 @@ __device__ __forceinline__ uint32_t to_e5m2(uint32_t x) {
   return y;
 }
 // The E5M2 copy of 32 fp16 channels in the order of INT4 keys.
-__device__ __forceinline__ void store_low(char* low, int row, int g, const uint4 (&x)[4]) {
+__device__ __forceinline__ void store_low(uint32_t low, const uint4 (&x)[4]) {
 #pragma unroll
   for (int c = 0; c < 4; c += 2) {
     uint32_t w[4];
@@ -330,7 +364,7 @@ __device__ __forceinline__ void store_low(char* low, int row, int g, const uint4
       w[2 * i] = to_e5m2(prmt(y.x, y.z, 0x5410)) | (to_e5m2(prmt(y.x, y.z, 0x7632)) << 16);
       w[2 * i + 1] = to_e5m2(prmt(y.y, y.w, 0x5410)) | (to_e5m2(prmt(y.y, y.w, 0x7632)) << 16);
     }
-    st_chunk(low, row, 2 * g + (c >> 1), w[0], w[1], w[2], w[3]);
+    st_chunk(low, c >> 1, w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -348,8 +382,9 @@ __device__ __forceinline__ bool clear_nonfinite(uint4 (&x)[4]) {
   return bad;
 }
 
-// The (token, group of 32 channels) of a tile that an unpacking thread takes: a quarter warp holds
-// eight tokens of one group, so its 16-byte stores hit eight different chunks of the swizzle.
+// The (token, group of 32 channels) of a tile that an unpacking thread takes first (the others lie
+// 128 / ITEMS tokens on): a quarter warp holds eight tokens of one group, so its 16-byte stores hit
+// eight different chunks of the swizzle.
 template <int D>
 __device__ __forceinline__ void item_of(int thread, int& tok, int& g) {
   const int lane = thread & 31, w = thread >> 5;
@@ -362,13 +397,6 @@ __device__ __forceinline__ void item_of(int thread, int& tok, int& g) {
   }
 }
 
-// A thread's codes and scales of a middle tile on their way to shared memory.
-template <int D, int KB, int VB>
-struct Codes {
-  static constexpr int KW = KB, VW = VB == kPQ ? 2 : VB;   // 32-bit words of a group
-  uint32_t k[KW], v[VW];
-  uint16_t ks, vs;
-};
 template <int W>
 __device__ __forceinline__ void ld_words(const uint8_t* p, uint32_t* w) {
   if constexpr (W == 4) {
@@ -379,48 +407,44 @@ __device__ __forceinline__ void ld_words(const uint8_t* p, uint32_t* w) {
     w[0] = x.x; w[1] = x.y;
   }
 }
-// Where a thread's codes of a segment's middle tiles lie (token `tok` of tile 0, group g).
-template <int D, int KB, int VB>
-struct CodePtrs {
-  static constexpr int G = D / 32, KW = Codes<D, KB, VB>::KW, VW = Codes<D, KB, VB>::VW;
-  const uint8_t *k, *v;
-  const uint16_t *ks, *vs;
-  int last;   // tokens from `tok` to the tier's last
-  __device__ __forceinline__ CodePtrs(const TreeArgs& a, int unit, int cur, int n_mid, int tok,
-                                      int g) {
-    const size_t r = ((size_t)unit * a.C + tok) * G + g;
-    k = a.mk[cur] + r * (4 * KW);
-    v = a.mv[cur] + r * (4 * VW);
-    ks = a.mks[cur] + r;
-    vs = a.mvs[cur] + r;
+// A thread's codes and scales of middle tiles, K's or V's (W 32-bit words a group): the next
+// tile's on their way while the present one's are unpacked.
+template <int D, int W, bool SCALED, int ITEMS>
+struct Codes {
+  static constexpr int G = D / 32, APART = kTok / ITEMS;
+  uint32_t w[2][ITEMS][W];   // [present or next tile][row]
+  uint16_t sc[2][ITEMS];
+  const uint8_t* codes;
+  const uint16_t* scales;
+  int last;   // tokens from the coming tile's row to the tier's last
+  __device__ __forceinline__ void start(const uint8_t* c, const uint16_t* s, size_t unit_row,
+                                        int n_mid, int tok, int g) {
+    const size_t r = (unit_row + tok) * G + g;
+    codes = c + r * (4 * W);
+    scales = s + r;
     last = n_mid - 1 - tok;
   }
-  // Tokens past the tier read its last row (masked in S); their V is zeroed by the caller.
-  __device__ __forceinline__ void load(int tile, Codes<D, KB, VB>& c) const {
-    const int r = min(tile * kTok, last) * G;
-    ld_words<KW>(k + r * (4LL * KW), c.k);
-    ld_words<VW>(v + r * (4LL * VW), c.v);
-    c.ks = __ldg(ks + r);
-    if (VB != kPQ) c.vs = __ldg(vs + r);
+  // Tokens past the tier read its last row: their keys are masked in S, their values zeroed.
+  __device__ __forceinline__ void load(int buf) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int at = (APART * i + min(last - APART * i, 0)) * G;
+      ld_words<W>(codes + (long long)at * (4 * W), w[buf][i]);
+      if constexpr (SCALED) sc[buf][i] = __ldg(scales + at);
+    }
+    codes += kTok * G * 4 * W;
+    scales += kTok * G;
+    last -= kTok;
+  }
+  __device__ __forceinline__ void advance() {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[0][i][j] = w[1][i][j];
+      if constexpr (SCALED) sc[0][i] = sc[1][i];
+    }
   }
 };
-
-// Ask for a tile's codes and scales to be in L2 (contiguous runs of 16-byte multiples; the stride of
-// a unit is a multiple of 64 rows, so a run may pass the tier's end but not the buffer's).
-template <int D, int KB, int VB>
-__device__ __forceinline__ void prefetch_codes(const TreeArgs& a, int unit, int cur, int n_mid,
-                                               int t0) {
-  constexpr int G = D / 32, VW = Codes<D, KB, VB>::VW;
-  const int rows = min(kTok, (n_mid - t0 + 7) & ~7);   // scales: 2 G bytes a row
-  const size_t r = (size_t)unit * a.C + t0;
-  auto run = [](const void* x, int bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(x), "r"(bytes) : "memory");
-  };
-  run(a.mk[cur] + r * (G * 4 * KB), rows * G * 4 * KB);
-  run(a.mv[cur] + r * (G * 4 * VW), rows * G * 4 * VW);
-  run(a.mks[cur] + r * G, rows * G * 2);
-  if (VB != kPQ) run(a.mvs[cur] + r * G, rows * G * 2);
-}
 
 // The key or value row of FP16 token j of a unit (sinks, then the ring oldest first, then nodes).
 __device__ __forceinline__ const uint16_t* f16_row(const TreeArgs& a, int D, int b, int h, int unit,
@@ -442,22 +466,20 @@ __device__ __forceinline__ void reg_set() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Waits for the phase-th completion of an mbarrier, suspended by the hardware for up to 1 ms at a
-// time and bounded to about 2 s; false, with the layer's status set, when it gives up.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, int phase, int32_t* status) {
-#pragma unroll 1
-  for (int i = 0; i < 2000; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"((uint32_t)phase & 1), "r"(1000000)
-        : "memory");
-    if (ok) return true;
-  }
-  record_status(status, 1);
-  return false;
+// Waits for the phase-th completion of an mbarrier, for `limit` cycles at most; false when it gives up.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, int phase, long long limit) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .s64 t0, t1;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
+      " mov.u64 t0, %%clock64;\n"
+      "WAIT:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
+      " mov.u64 t1, %%clock64;\n sub.s64 t1, t1, t0;\n setp.lt.s64 q, t1, %3;\n @q bra WAIT;\n"
+      "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"((uint32_t)phase & 1), "l"(limit)
+      : "memory");
+  return ok != 0;
 }
 
 // The lowest n bits; x moved up by n places (down for a negative n). Any n.
@@ -468,77 +490,146 @@ __device__ __forceinline__ uint64_t shifted(uint64_t x, int n) {
   return n >= 64 || n <= -64 ? 0ull : n >= 0 ? x << n : x >> -n;
 }
 
-// One segment of a CTA's tiles: consecutive tiles of one block of query rows. Every role walks the
-// same segments.
+// One segment of a CTA's tiles: consecutive tiles of one block of query rows. The list of a CTA's
+// segments is made once, in shared memory, a thread a segment.
 struct Segment {
   int b, h, unit, r0, rows, n, f16, tiles;   // f16, tiles: of the whole block
   int begin, end;                            // its tiles in this segment
   int n_sink, n_mid, n_rec, head, cur;
 };
+constexpr int kMaxSeg = 128;   // segments of a CTA at most (the grid is sized for it)
 template <int ROWS>
-__device__ __forceinline__ Segment segment_at(const AttnTreeArgs& p, const int* pre, int g,
-                                              int g_end) {
+__device__ __forceinline__ int list_segments(const AttnTreeArgs& p, const int* pre, int g_first,
+                                             int g_end, Segment* list) {
   const TreeArgs& a = p.a;
-  Segment s;
-  s.b = row_of(pre, a.B, g);
-  const RowTiles rt = row_tiles<ROWS>(a, p.n_nodes, s.b);
-  const int rel = g - pre[s.b], blk = rel / rt.tiles;
-  s.begin = rel % rt.tiles;
-  s.end = min(rt.tiles, s.begin + (g_end - g));
-  s.h = blk / rt.blocks;
-  s.r0 = (blk % rt.blocks) * ROWS;
-  s.rows = min(ROWS, rt.n * a.G - s.r0);
-  s.n = rt.n;
-  s.f16 = rt.f16;
-  s.tiles = rt.tiles;
-  s.unit = s.b * a.H + s.h;
-  const int32_t* m = a.meta + (size_t)s.unit * FADE_META_FIELDS;
-  s.n_sink = m[FADE_META_N_SINK];
-  s.n_mid = m[FADE_META_N_MID];
-  s.n_rec = m[FADE_META_N_RECENT];
-  s.head = m[FADE_META_HEAD];
-  s.cur = m[FADE_META_CUR];
-  return s;
+  __shared__ int count;
+  if (threadIdx.x == 0) count = 0;
+  __syncthreads();
+  if (threadIdx.x < kMaxSeg) {
+    // the k-th block from the one that holds g_first
+    int k = threadIdx.x;
+    int b = row_of(pre, a.B, g_first);
+    RowTiles rt = row_tiles<ROWS>(a, p.n_nodes, b);
+    int blk = (g_first - pre[b]) / rt.tiles;
+    while (b < a.B && blk + k >= a.H * rt.blocks) {   // on to the row that holds it
+      k -= a.H * rt.blocks - blk;
+      blk = 0;
+      if (++b < a.B) rt = row_tiles<ROWS>(a, p.n_nodes, b);
+    }
+    blk += k;
+    const int g0 = b < a.B ? pre[b] + blk * rt.tiles : g_end;
+    if (g0 < g_end) {
+      Segment s;
+      s.b = b;
+      s.begin = max(g_first - g0, 0);
+      s.end = min(rt.tiles, g_end - g0);
+      s.h = blk / rt.blocks;
+      s.r0 = (blk % rt.blocks) * ROWS;
+      s.rows = min(ROWS, rt.n * a.G - s.r0);
+      s.n = rt.n;
+      s.f16 = rt.f16;
+      s.tiles = rt.tiles;
+      s.unit = s.b * a.H + s.h;
+      const int32_t* m = a.meta + (size_t)s.unit * FADE_META_FIELDS;
+      s.n_sink = m[FADE_META_N_SINK];
+      s.n_mid = m[FADE_META_N_MID];
+      s.n_rec = m[FADE_META_N_RECENT];
+      s.head = m[FADE_META_HEAD];
+      s.cur = m[FADE_META_CUR];
+      list[threadIdx.x] = s;
+      atomicMax(&count, threadIdx.x + 1);
+    }
+  }
+  __syncthreads();
+  return count;
 }
 
-// One CTA per SM, three roles that meet at mbarriers. D / 8 warps unpack tiles into a ring of STAGES
-// (the next tile's codes already in registers); one thread issues the products, S of the
-// next tile before O of the present one, so that S is computed under the softmax; 4 R warps do the
-// softmax, 16 query rows each (two rows a thread, a row spread over four lanes: no exchange between
-// warps). S has two buffers; P overwrites the first columns of its own. R: 16-row halves of each
-// 32-lane quarter of tensor memory in use: up to 64 query rows take lanes 0..15 of every quarter
-// (R = 1), which gives each scheduler of the SM a share of the softmax; otherwise 128 (R = 2).
+// What tile t of a segment needs, asked for in L2 by one warp; with a segment's first tile, its Q.
+template <int D, int KB, int VB>
+__device__ __forceinline__ void tile_to_l2(const AttnTreeArgs& p, const Segment& s, int t) {
+  const TreeArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  auto line = [](const void* x) { asm volatile("prefetch.global.L2 [%0];" ::"l"(x)); };
+  if (t == s.begin)
+    for (int i = lane; i < s.rows; i += 32) {
+      const int r = s.r0 + i;
+      const uint16_t* q = a.q + (((size_t)s.b * a.T + (r >> a.log_g)) * a.Hq + s.h * a.G +
+                                 (r & (a.G - 1))) * D;
+      line(q);
+      if (D == 128) line(q + 64);
+    }
+  if (t < s.f16) {
+    const int end = min((t + 1) * kTok, s.n_sink + s.n_rec + s.n);
+    for (int j = t * kTok + lane; j < end; j += 32)
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        const uint16_t* x =
+            f16_row(a, D, s.b, s.h, s.unit, s.n_sink, s.n_rec, s.head, j, v != 0);
+        line(x);
+        if (D == 128) line(x + 64);
+      }
+  } else {
+    // contiguous runs of codes and scales, a 128-byte line a lane; the stride of a unit is a multiple
+    // of 64 rows, so a run may pass the tier's end but not the buffer's
+    constexpr int G = D / 32, KW = KB, VW = VB == kPQ ? 2 : VB;   // 32-bit words of a group
+    const int t0 = (t - s.f16) * kTok, rows = min(kTok, (s.n_mid - t0 + 63) & ~63);
+    const size_t r = ((size_t)s.unit * a.C + t0) * G;
+    const int cur = s.cur;
+    auto run = [&](const void* x, int bytes) {
+      for (int i = lane * 128; i < bytes; i += 32 * 128) line(static_cast<const char*>(x) + i);
+    };
+    run(a.mk[cur] + r * (4 * KW), rows * G * 4 * KW);
+    run(a.mv[cur] + r * (4 * VW), rows * G * 4 * VW);
+    run(a.mks[cur] + r, rows * G * 2);
+    if (VB != kPQ) run(a.mvs[cur] + r, rows * G * 2);
+  }
+}
+
+// One CTA per SM, roles that meet at mbarriers. Some warps unpack K and as many V, each into a ring
+// of STAGES (the next tile's codes already in registers); one warp issues S = Q K^T, one O += P V,
+// one asks for coming tiles in L2; 8 R warps do the softmax, 16 query rows each (a thread: two rows,
+// spread over four lanes). A tile's chain (S, softmax, P V) is long and mostly waiting, so even and
+// odd tiles run as two streams, each with its softmax warps, its S (over which P is written), its
+// references and its own O; the segment's end joins them. R: 16-row halves of each 32-lane quarter
+// of tensor memory in use: up to 64 query rows take lanes 0..15 of every quarter (R = 1), which
+// gives each scheduler of the SM a share of the softmax; otherwise 128 (R = 2).
 template <int D, int KB, int VB, int R>
 __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
     tree_attention_kernel(const __grid_constant__ AttnTreeArgs p) {
   using Sh = Shape<D, KB, VB, R>;
-  using Cd = Codes<D, KB, VB>;
   constexpr int ROWS = 64 * R, KO = order_of(KB), VO = order_of(VB), ST = Sh::STAGES;
   constexpr float kLog2e = 1.4426950408889634f;
   extern __shared__ char raw[];
   char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  char *sQ = base, *sQL = base + Sh::TILE, *stages = sQL + Sh::LOWB;
-  uint2* sCB = reinterpret_cast<uint2*>(stages + ST * Sh::STAGE);   // [256][D/4], centroid-major
-  char* small = stages + ST * Sh::STAGE + Sh::CODEBOOK;
+  constexpr int kStages = Sh::TILE + Sh::LOWB;   // after Q
+  const uint32_t sQ = smem_u32(base), sQL = sQ + Sh::TILE, stages = sQ + kStages;
+  uint2* sCB = reinterpret_cast<uint2*>(base + kStages + ST * Sh::STAGE);   // [256][D/4]: centroid-major
+  char* small = base + kStages + ST * Sh::STAGE + Sh::CODEBOOK;
   uint64_t* bars = reinterpret_cast<uint64_t*>(small);
   uint32_t* sTm = reinterpret_cast<uint32_t*>(small + 128);
+  volatile int* sDone = reinterpret_cast<volatile int*>(small + 136);   // tiles unpacked
   uint32_t* sBad = reinterpret_cast<uint32_t*>(small + 160);   // [8 segments][2] see below
   int* sPre = reinterpret_cast<int*>(small + 256);             // [257]
+  float* sMax = reinterpret_cast<float*>(small + 1536);        // [softmax warps][2][16 rows]
+  Segment* sSeg = reinterpret_cast<Segment*>(small + 3584);    // [kMaxSeg]
   auto kTile = [&](int st) { return stages + st * Sh::STAGE; };
   auto vTile = [&](int st) { return stages + st * Sh::STAGE + Sh::TILE; };
   auto kLow = [&](int st) { return stages + st * Sh::STAGE + 2 * Sh::TILE; };
   const uint32_t bar0 = smem_u32(bars);
   const uint32_t kFull = bar0, kFree = bar0 + 16, vFull = bar0 + 32, vFree = bar0 + 48;   // [2]
   const uint32_t sFull = bar0 + 64, pFull = bar0 + 80;                                    // [2]
-  const uint32_t oFull = bar0 + 96, oRead = bar0 + 104;
+  const uint32_t oFull = bar0 + 96, oRead = bar0 + 112;                                   // [2], 1
   const TreeArgs& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
+  // the combine kernel may be scheduled as this one drains
+  asm volatile("griddepcontrol.launch_dependents;");
   tile_prefix<ROWS>(a, p.n_nodes, sPre);
   const int N = sPre[a.B];
   const int g_first = cta_start(N, gridDim.x, blockIdx.x);
   const int g_end = cta_start(N, gridDim.x, blockIdx.x + 1);
   if (g_first >= g_end) return;   // uniform over the CTA; nothing allocated yet
+  const int n_seg = list_segments<ROWS>(p, sPre, g_first, g_end, sSeg);
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(sTm)),
@@ -547,15 +638,16 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid == 0) {
+    *sDone = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(kFull + 8 * i, Sh::UNPACK / 32);
-      mbar_init(vFull + 8 * i, Sh::UNPACK / 32);
+      mbar_init(kFull + 8 * i, Sh::SIDE / 32);
+      mbar_init(vFull + 8 * i, Sh::SIDE / 32);
       mbar_init(kFree + 8 * i, 1);
       mbar_init(vFree + 8 * i, 1);
       mbar_init(sFull + 8 * i, 1);
-      mbar_init(pFull + 8 * i, Sh::SOFT / 32);
+      mbar_init(pFull + 8 * i, Sh::SOFT / 64);
+      mbar_init(oFull + 8 * i, 1);
     }
-    mbar_init(oFull, 1);
     mbar_init(oRead, Sh::SOFT / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -569,9 +661,15 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
   __syncthreads();
   fence_after();
   const uint32_t tm = *sTm, tmO = tm + 256;
-  bool dead = false;   // a wait gave up: later ones are skipped, the flow stays the same
+  auto pair_sync = [&](int pair) {   // the two softmax warps of the same rows
+    __syncwarp();
+    asm volatile("bar.sync %0, 64;" ::"r"(4 + pair) : "memory");
+  };
+  // a wait that gives up makes the later ones of its thread end at once, the flow stays the same,
+  // and the layer's status tells
+  long long limit = kWaitCycles;
   auto wait = [&](uint32_t bar, int phase) {   // until the bar's phase-th completion
-    if (!dead && !wait_phase(bar, phase, a.status)) dead = true;
+    if (!wait_phase(bar, phase, limit)) limit = 0;
   };
   auto arrive = [&](uint32_t bar) {   // once per warp
     __syncwarp();
@@ -581,263 +679,323 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
   if (warp >= Sh::SOFT / 32 && warp < (Sh::SOFT + Sh::UNPACK) / 32) {
     // ================================================================ unpacking
     reg_set<Sh::REGS_UNPACK, Sh::REGS>();
+    const bool is_v = warp >= (Sh::SOFT + Sh::SIDE) / 32;
     int it = 0, seg = 0, tok, gq;
-    item_of<D>(tid - Sh::SOFT, tok, gq);
-    for (int g = g_first; g < g_end; ++seg) {
-      const Segment s = segment_at<ROWS>(p, sPre, g, g_end);
-      const int n16 = s.n_sink + s.n_rec;   // cached FP16 tokens, then the nodes
-      uint32_t* bad = sBad + 2 * (seg & 7);
-      const CodePtrs<D, KB, VB> ptrs(a, s.unit, s.cur, s.n_mid, tok, gq);
-      Cd codes, next;
-      auto fetch = [&](int t, Cd& c) {   // the codes of middle tile t of the segment
-        if (t >= s.f16 && t < s.end)
-          ptrs.load(t - s.f16, c);
-      };
-      auto ahead = [&](int t) {   // tile t into L2
-        if (tid == Sh::SOFT && t >= s.f16 && t < s.end)
-          prefetch_codes<D, KB, VB>(a, s.unit, s.cur, s.n_mid, (t - s.f16) * kTok);
-      };
-      fetch(s.begin, codes);
-      for (int t = 1; t < kAhead; ++t) ahead(s.begin + t);
-      // Q, once the last product that reads the old one is done: matrix row 32 q + i holds query
-      // row 16 q + i (R = 1, i < 16) or 32 q + i
-      if (it > 0) wait(kFree + 8 * ((it - 1) % ST), (it - 1) / ST);
-      if (tid == Sh::SOFT) bad[0] = bad[1] = 0;
-      {
-        const int in = tok & 31, r = (tok >> 5) * (16 * R) + in;
-        uint4 x[4] = {};
-        if (in < 16 * R && r < s.rows) {
-          const int node = (s.r0 + r) >> a.log_g, gh = (s.r0 + r) & (a.G - 1);
-          const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + (((size_t)s.b * a.T + node) * a.Hq + s.h * a.G + gh) * D + 32 * gq);
+    item_of<D>((tid - Sh::SOFT) & (Sh::SIDE - 1), tok, gq);
+    const uint32_t at16 = group_at(tok, gq), at8 = low_at(tok, gq);
+    // one warp of the side watches the mbarrier, the others block at a named barrier: eight
+    // watching warps would take the softmax's issue slots
+    auto side_wait = [&](uint32_t bar, int phase) {
+      if (((tid - Sh::SOFT) & (Sh::SIDE - 1)) < 32) wait(bar, phase);
+      __syncwarp();
+      asm volatile("bar.sync %0, %1;" ::"r"(2 + (int)is_v), "n"(Sh::SIDE) : "memory");
+    };
+    // an FP16 token's share of a row (zeros past the nodes)
+    auto f16_load = [&](const Segment& s, int j, bool v, uint4 (&x)[4]) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) x[c] = __ldg(src + c);
-        }
-        store_f16<KO>(sQ, tok, gq, x);
-        if constexpr (Sh::LOW) store_low(sQL, tok, gq, x);
+      for (int c = 0; c < 4; ++c) x[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (j < s.n_sink + s.n_rec + s.n) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            f16_row(a, D, s.b, s.h, s.unit, s.n_sink, s.n_rec, s.head, j, v) + 32 * gq);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = src[c];
       }
-      for (int t = s.begin; t < s.end; ++t, ++it) {
-        const bool f16 = t < s.f16;
-        const int st = it % ST, use = it / ST;
-        const int tok0 = (f16 ? t : t - s.f16) * kTok;
-        const int count = min(kTok, (f16 ? n16 + s.n : s.n_mid) - tok0);   // tokens of the tile
-        ahead(t + kAhead);
-        fetch(t + 1, next);
-        if (use > 0) wait(kFree + 8 * st, use - 1);
-        {
-          if (f16) {
-            uint4 x[4] = {};
-            if (tok < count) {
-              const uint4* src = reinterpret_cast<const uint4*>(
-                  f16_row(a, D, s.b, s.h, s.unit, s.n_sink, s.n_rec, s.head, tok0 + tok, false) +
-                  32 * gq);
+    };
+    constexpr int NI = Sh::ITEMS, APART = kTok / NI, ROWB = APART * 128;   // rows apart, bytes
+    if (!is_v) {   // -------------------------------------------- keys, and Q
+      const Fields<KB> kf;
+      for (; seg < n_seg; ++seg) {
+        const Segment& s = sSeg[seg];
+        const int f16 = s.f16, t_end = s.end;
+        int t = s.begin;
+        Codes<D, KB, true, NI> c;
+        c.start(a.mk[s.cur], a.mks[s.cur], (size_t)s.unit * a.C, s.n_mid,
+                max(t - f16, 0) * kTok + tok, gq);
+        if (t >= f16) c.load(0);
+        // Q, once the last product that reads the old one is done: matrix row 32 q + i holds query
+        // row 16 q + i (R = 1, i < 16) or 32 q + i
+        if (it > 0) side_wait(kFree + 8 * ((it - 1) % ST), (it - 1) / ST);
+#pragma unroll 1
+        for (int i = 0; i < NI; ++i) {
+          const int row = tok + APART * i, in = row & 31, qr = (row >> 5) * (16 * R) + in;
+          uint4 x[4] = {};
+          if (in < 16 * R && qr < s.rows) {
+            const int node = (s.r0 + qr) >> a.log_g, gh = (s.r0 + qr) & (a.G - 1);
+            const uint4* src = reinterpret_cast<const uint4*>(
+                a.q + (((size_t)s.b * a.T + node) * a.Hq + s.h * a.G + gh) * D + 32 * gq);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) x[c] = src[c];
-            }
-            store_f16<KO>(kTile(st), tok, gq, x);
-          } else {
-            store_codes<KB, Sh::LOW>(kTile(st), kLow(st), tok, gq, codes.k, codes.ks);
+            for (int e = 0; e < 4; ++e) x[e] = __ldg(src + e);
           }
+          store_f16<KO>(sQ + at16 + i * ROWB, x);
+          if constexpr (Sh::LOW) store_low(sQL + at8 + i * ROWB, x);
         }
-        fence_proxy_async_smem();
-        arrive(kFull + 8 * st);
-        if (use > 0) wait(vFree + 8 * st, use - 1);
-        {
-          if (f16) {
-            uint4 x[4] = {};
-            if (tok < count) {
-              const uint4* src = reinterpret_cast<const uint4*>(
-                  f16_row(a, D, s.b, s.h, s.unit, s.n_sink, s.n_rec, s.head, tok0 + tok, true) +
-                  32 * gq);
-#pragma unroll
-              for (int c = 0; c < 4; ++c) x[c] = src[c];
-              // a node's infinities and NaN would reach the rows that do not see it (0 * inf):
-              // they are left out of the product and put into the rows that see it at the end
-              const int node = tok0 + tok - n16;
-              if (node >= 0 && clear_nonfinite(x)) atomicOr(bad + (node >> 5), 1u << (node & 31));
-            }
-            store_f16<VO>(vTile(st), tok, gq, x);
-          } else if constexpr (Sh::PQ) {
-            // lane-dependent order of the eight sub-spaces: the 32 lanes of a warp read 32
-            // different sub-spaces of the centroid-major codebook, two wavefronts whatever the
-            // codes
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int ss = (e + tok) & 7;
-              const uint32_t w = (ss & 4) ? codes.v[1] : codes.v[0];
-              const int code = (w >> (8 * (ss & 3))) & 255;
-              const uint2 x = tok < count ? sCB[code * (D / 4) + 8 * gq + ss] : make_uint2(0u, 0u);
-              *reinterpret_cast<uint2*>(vTile(st) + chunk_at(tok, 4 * gq + (ss >> 1)) +
-                                        8 * (ss & 1)) = x;
-            }
-          } else {
-            store_codes<VB, false>(vTile(st), nullptr, tok, gq, codes.v,
-                                   tok < count ? codes.vs : (uint16_t)0);
+        for (; t < t_end && t < f16; ++t, ++it) {
+          const int st = it % ST, use = it / ST;
+          if (use > 0) side_wait(kFree + 8 * st, use - 1);
+          if (t + 1 == f16 && t + 1 < t_end) c.load(0);
+#pragma unroll 1
+          for (int i = 0; i < NI; i += 2) {
+            uint4 x[4], y[4];
+            f16_load(s, t * kTok + tok + APART * i, false, x);
+            f16_load(s, t * kTok + tok + APART * (i + 1), false, y);
+            store_f16<KO>(kTile(st) + at16 + i * ROWB, x);
+            store_f16<KO>(kTile(st) + at16 + (i + 1) * ROWB, y);
           }
+          fence_proxy_async_smem();
+          arrive(kFull + 8 * st);
         }
-        fence_proxy_async_smem();
-        arrive(vFull + 8 * st);
-        codes = next;
+        for (; t < t_end; ++t, ++it) {
+          const int st = it % ST, use = it / ST;
+          if (t + 1 < t_end) c.load(1);
+          if (use > 0) side_wait(kFree + 8 * st, use - 1);
+          const uint32_t k = kTile(st) + at16, l = kLow(st) + at8;
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+            store_codes<KB, Sh::LOW>(k + i * ROWB, l + i * ROWB, kf, c.w[0][i], c.sc[0][i]);
+          fence_proxy_async_smem();
+          arrive(kFull + 8 * st);
+          if (tid == Sh::SOFT) *sDone = it + 1;
+          c.advance();
+        }
       }
-      g += s.end - s.begin;
+    } else {   // ------------------------------------------------ values
+      const Fields<Sh::PQ ? 4 : VB> vf;
+      for (; seg < n_seg; ++seg) {
+        const Segment& s = sSeg[seg];
+        const int f16 = s.f16, t_end = s.end, n_mid = s.n_mid, n16 = s.n_sink + s.n_rec;
+        uint32_t* bad = sBad + 2 * (seg & 7);
+        int t = s.begin;
+        Codes<D, Sh::PQ ? 2 : VB, !Sh::PQ, NI> c;
+        c.start(a.mv[s.cur], a.mvs[s.cur], (size_t)s.unit * a.C, n_mid,
+                max(t - f16, 0) * kTok + tok, gq);
+        if (t >= f16) c.load(0);
+        if (tid == Sh::SOFT + Sh::SIDE) bad[0] = bad[1] = 0;
+        asm volatile("bar.sync 1, %0;" ::"n"(Sh::SIDE) : "memory");   // cleared before any is set
+        for (; t < t_end && t < f16; ++t, ++it) {
+          const int st = it % ST, use = it / ST;
+          if (use > 0) side_wait(vFree + 8 * st, use - 1);
+          if (t + 1 == f16 && t + 1 < t_end) c.load(0);
+#pragma unroll 1
+          for (int i = 0; i < NI; i += 2) {
+            uint4 x[4], y[4];
+            f16_load(s, t * kTok + tok + APART * i, true, x);
+            f16_load(s, t * kTok + tok + APART * (i + 1), true, y);
+            // a node's infinities and NaN would reach the rows that do not see it (0 * inf): they
+            // are left out of the product and put into the rows that see it at the end
+            const int node = t * kTok + tok + APART * i - n16, next = node + APART;
+            if (node >= 0 && clear_nonfinite(x)) atomicOr(bad + (node >> 5), 1u << (node & 31));
+            if (next >= 0 && clear_nonfinite(y)) atomicOr(bad + (next >> 5), 1u << (next & 31));
+            store_f16<VO>(vTile(st) + at16 + i * ROWB, x);
+            store_f16<VO>(vTile(st) + at16 + (i + 1) * ROWB, y);
+          }
+          fence_proxy_async_smem();
+          arrive(vFull + 8 * st);
+        }
+        for (; t < t_end; ++t, ++it) {
+          const int st = it % ST, use = it / ST;
+          if (t + 1 < t_end) c.load(1);
+          if (use > 0) side_wait(vFree + 8 * st, use - 1);
+          const int left = n_mid - (t - f16) * kTok - tok;   // tokens from this row on
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const uint32_t v = vTile(st) + at16 + i * ROWB;
+            const bool in = left > APART * i;
+            if constexpr (Sh::PQ) {
+              // lane-dependent order of the eight sub-spaces: the 32 lanes of a warp read 32
+              // different sub-spaces of the centroid-major codebook, two wavefronts whatever the
+              // codes
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int ss = (e + tok) & 7;
+                const uint32_t w = (ss & 4) ? c.w[0][i][1] : c.w[0][i][0];
+                const int code = (w >> (8 * (ss & 3))) & 255;
+                const uint2 x = in ? sCB[code * (D / 4) + 8 * gq + ss] : make_uint2(0u, 0u);
+                st_shared8((v ^ (16 * (ss >> 1))) + 8 * (ss & 1), x.x, x.y);
+              }
+            } else {
+              store_codes<VB, false>(v, 0, vf, c.w[0][i], in ? c.sc[0][i] : (uint16_t)0);
+            }
+          }
+          fence_proxy_async_smem();
+          arrive(vFull + 8 * st);
+          c.advance();
+        }
+      }
     }
   } else if (warp >= (Sh::SOFT + Sh::UNPACK) / 32) {
     // ================================================================ products
     reg_set<Sh::REGS_MMA, Sh::REGS>();
-    if (warp == (Sh::SOFT + Sh::UNPACK) / 32 && lane == 0) {
-      // two walks over the same tiles: S runs one tile ahead of O
-      int s_left = 0, s_f16 = 0, o_left = 0, gs = g_first, go = g_first, seg = -1;
-      const int total = g_end - g_first;
-      for (int it = 0; it <= total; ++it) {
-        if (it < total) {   // S of tile `it`
+    const int role = warp - (Sh::SOFT + Sh::UNPACK) / 32;
+    // a warp walks as one and elects the thread that issues, so that addresses and descriptors stay
+    // in uniform registers
+    const bool issuer = elect_one();
+    constexpr uint32_t kStage = Sh::STAGE >> 4;
+    if (role == 0) {   // S = Q K^T
+      const uint64_t dQ = smem_desc(sQ, 16, 1024);
+      const uint64_t dK = smem_desc(kTile(0), 16, 1024);
+      const uint64_t dQL = smem_desc(sQL, 16, 1024);
+      const uint64_t dKL = smem_desc(kLow(0), 16, 1024);
+      int it = 0;
+      for (int seg = 0; seg < n_seg; ++seg) {
+        const Segment& s = sSeg[seg];
+        int f16 = s.f16 - s.begin;   // FP16 tiles left
+        const int n = s.end - s.begin;
+        for (int i = 0; i < n; ++i, --f16, ++it) {
           const int st = it % ST;
-          if (s_left == 0) {   // s_left tiles of the segment, s_f16 of them FP16 tiles
-            const Segment s = segment_at<ROWS>(p, sPre, gs, g_end);
-            s_left = s.end - s.begin;
-            s_f16 = s.f16 - s.begin;
-            gs += s_left;
-          }
+          if (it >= 2) wait(oFull + 8 * (it & 1), (it >> 1) - 1);   // the buffer's P has been read
           wait(kFull + 8 * st, it / ST);
-          if (it >= 2) wait(oFull, it - 2);   // P of this buffer has been read
+          __syncwarp();
           fence_after();
-          const uint32_t d = tm + 128 * (it & 1);
-          const uint32_t q = smem_u32(sQ), k = smem_u32(kTile(st));
+          if (issuer) {
+            const uint32_t d = tm + 128 * (it & 1);
+            const uint64_t k = dK + st * kStage;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t off = (i >> 2) * kBlk + (i & 3) * 32;
-            mma_ss(d, smem_desc(q + off, 16, 1024), smem_desc(k + off, 16, 1024),
-                   instr_desc(kTok, false), i > 0);
-          }
-          if constexpr (Sh::LOW)
-            if (s_f16 <= 0) {   // the remainders of a middle tile's keys
-              const uint32_t ql = smem_u32(sQL), kl = smem_u32(kLow(st));
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i)
-                mma_low(d, smem_desc(ql + 32 * i, 16, 1024), smem_desc(kl + 32 * i, 16, 1024),
-                        instr_desc_low(kTok));
+            for (int j = 0; j < D / 16; ++j) {
+              const uint32_t off = ((j >> 2) * kBlk + (j & 3) * 32) >> 4;
+              mma_ss(d, dQ + off, k + off, instr_desc(kTok, false), j > 0);
             }
-          mma_commit(kFree + 8 * st);
-          mma_commit(sFull + 8 * (it & 1));
-          --s_left;
-          --s_f16;
-        }
-        if (it > 0) {   // O of the tile before
-          const int jt = it - 1, st = jt % ST;
-          const bool first = o_left == 0;
-          if (first) {
-            const Segment o = segment_at<ROWS>(p, sPre, go, g_end);
-            o_left = o.end - o.begin;
-            go += o_left;
-            ++seg;
-          }
-          --o_left;
-          wait(vFull + 8 * st, jt / ST);
-          wait(pFull + 8 * (jt & 1), jt >> 1);
-          if (first && seg > 0) wait(oRead, seg - 1);   // the last segment's O has been read
-          fence_after();
-          const uint32_t v = smem_u32(vTile(st)), pt = tm + 128 * (jt & 1);
+            if constexpr (Sh::LOW)
+              if (f16 <= 0) {   // the remainders of a middle tile's keys
+                const uint64_t kl = dKL + st * kStage;
 #pragma unroll
-          for (int i = 0; i < kTok / 16; ++i)
-            mma_ts(tmO, pt + 8 * i, smem_desc(v + i * 2048, kBlk, 1024), instr_desc(D, true),
-                   !(first && i == 0));
-          mma_commit(vFree + 8 * st);
-          mma_commit(oFull);
+                for (int j = 0; j < D / 32; ++j)
+                  mma_low(d, dQL + 2 * j, kl + 2 * j, instr_desc_low(kTok));
+              }
+            mma_commit(kFree + 8 * st);
+            mma_commit(sFull + 8 * (it & 1));
+          }
+          __syncwarp();
+        }
+      }
+    } else if (role == 1) {   // O += P V
+      const uint64_t dV = smem_desc(vTile(0), kBlk, 1024);
+      int it = 0, seg = 0;
+      for (; seg < n_seg; ++seg) {
+        const Segment& s = sSeg[seg];
+        const int n = s.end - s.begin;
+        for (int i = 0; i < n; ++i, ++it) {
+          const int st = it % ST, stream = it & 1;
+          wait(vFull + 8 * st, it / ST);
+          wait(pFull + 8 * stream, it >> 1);
+          if (i == 0 && seg > 0) wait(oRead, seg - 1);   // the last segment's O has been read
+          __syncwarp();
+          fence_after();
+          if (issuer) {
+            const uint64_t v = dV + st * kStage;
+            const uint32_t pt = tm + 128 * stream, o = tmO + D * stream;
+#pragma unroll
+            for (int j = 0; j < kTok / 16; ++j)
+              mma_ts(o, pt + 8 * j, v + ((j * 2048) >> 4), instr_desc(D, true), i > 1 || j > 0);
+            mma_commit(vFree + 8 * st);
+            mma_commit(oFull + 8 * stream);
+          }
+          __syncwarp();
+        }
+      }
+    } else if (role == 2) {   // L2, kAhead tiles ahead of the unpacking
+      int it = 0;
+      for (int seg = 0; seg < n_seg; ++seg) {
+        const Segment& s = sSeg[seg];
+        for (int t = s.begin; t < s.end; ++t, ++it) {
+          // no more than kAhead tiles before the unpacking (a pace, not an order: bounded)
+          for (int i = 0; *sDone + kAhead < it && i < 1000; ++i) __nanosleep(200);
+          tile_to_l2<D, KB, VB>(p, s, t);
         }
       }
     }
-    __syncwarp();
   } else {
     // ================================================================ softmax
     reg_set<Sh::REGS_SOFT, Sh::REGS>();
-    const int quarter = warp & 3, f = warp >> 2;
+    const int quarter = warp & 3, stream = (warp >> 2) & 1, f = warp >> 3;
     const uint32_t lanes = (uint32_t)(quarter * 32 + 16 * f) << 16;
+    const uint32_t tS = tm + 128 * stream + lanes, tO = tmO + lanes;
     const int row0 = quarter * (16 * R) + 16 * f + (lane >> 2);   // this thread's rows: row0, + 8
     const float cscale = kLog2e * rsqrtf((float)D);
-    int it = 0, seg = 0;
-    for (int g = g_first; g < g_end; ++seg) {
-      const Segment s = segment_at<ROWS>(p, sPre, g, g_end);
-      const int n16 = s.n_sink + s.n_rec;
+    int it0 = 0, seg = 0;   // the segment's first tile
+    for (; seg < n_seg; ++seg) {
+      const Segment& s = sSeg[seg];
+      const int f16_tiles = s.f16, t_begin = s.begin, t_end = s.end, n_mid = s.n_mid, rows = s.rows;
+      const int n16 = s.n_sink + s.n_rec, n_f16 = n16 + s.n;
       // a warp whose rows are all past the block's takes no part
-      const bool active = quarter * (16 * R) + 16 * f < s.rows;
+      const bool active = quarter * (16 * R) + 16 * f < rows;
+      const int t0 = t_begin + ((it0 ^ stream) & 1);   // this stream's first tile, and every other
       float mref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
-      for (int t = s.begin; t < s.end; ++t, ++it) {
-        const uint32_t tS = tm + 128 * (it & 1) + lanes;
-        wait(sFull + 8 * (it & 1), it >> 1);
+      for (int t = t0; t < t_end; t += 2) {
+        // S of the tile; the stream's last O += P V is then complete, too
+        wait(sFull + 8 * stream, (it0 + t - t_begin) >> 1);
         __syncwarp();
         fence_after();
         if (active) {
-          const bool f16 = t < s.f16;
-          const int tok0 = (f16 ? t : t - s.f16) * kTok;
-          const int count = min(kTok, (f16 ? n16 + s.n : s.n_mid) - tok0);
+          const bool f16 = t < f16_tiles;
+          const int tok0 = (f16 ? t : t - f16_tiles) * kTok;
+          const int count = min(kTok, (f16 ? n_f16 : n_mid) - tok0);
           const float c = f16 ? cscale : 2.f * cscale;   // middle keys are stored halved
-          // what this thread's rows attend to of a tile that is not wholly visible, a bit a column
-          const bool masked = f16 || count < kTok;
-          uint64_t vis[2][2];   // [row][half of the columns]
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint64_t see = 0;
-              if (f16 && row0 + 8 * e < s.rows)
-                see = p.mask[(size_t)s.b * a.T + ((s.r0 + row0 + 8 * e) >> a.log_g)];
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const int c0 = tok0 + 64 * half;   // column 0 of the half as a token
-                uint64_t v = low_bits(f16 ? n16 - c0 : 64) | shifted(see, f16 ? n16 - c0 : 64);
-                vis[e][half] = (v & low_bits(count - 64 * half)) >> (2 * (lane & 3));
-              }
-            }
-          }
-          // 64 columns of S; -inf where a row does not attend
-          auto load = [&](int half, float (&x)[32]) {
+          auto load = [&](int half, float (&x)[32]) {   // 64 columns of S
             tm_ld32(tS + 64 * half, x);
             tm_ld32(tS + 64 * half + 32, x + 16);
             tm_wait_ld();
-            if (masked) {
+          };
+          float x[32], m8[8];
+          if (f16 || count < kTok) {   // -inf where a row does not attend, written back into S
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              load(half, x);
+              const int c0 = tok0 + 64 * half;   // the half's first column as a token
+              uint64_t vis[2];                   // what the rows attend to, a bit a column
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint64_t see = 0;
+                if (f16 && row0 + 8 * e < rows)
+                  see = p.mask[(size_t)s.b * a.T + ((s.r0 + row0 + 8 * e) >> a.log_g)];
+                const uint64_t v =
+                    low_bits(f16 ? n16 - c0 : 64) | shifted(see, f16 ? n16 - c0 : 64);
+                vis[e] = (v & low_bits(count - 64 * half)) >> (2 * (lane & 3));
+              }
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (!((vis[(i >> 1) & 1][half] >> (8 * (i >> 2) + (i & 1))) & 1)) x[i] = -INFINITY;
+                if (!((vis[(i >> 1) & 1] >> (8 * (i >> 2) + (i & 1))) & 1)) x[i] = -INFINITY;
+              tm_st32(tS + 64 * half, x);
+              tm_st32(tS + 64 * half + 32, x + 16);
             }
-          };
+            tm_wait_st();
+          }
           // the upper half is read twice, so that only 32 logits are held at a time
-          float x[32], mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m8[i] = -INFINITY;
 #pragma unroll
           for (int half = 1; half >= 0; --half) {
             load(half, x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mx[(i >> 1) & 1] = fmaxf(mx[(i >> 1) & 1], x[i]);
+            for (int i = 0; i < 32; ++i) m8[i & 7] = fmaxf(m8[i & 7], x[i]);
           }
           float ref[2], fac[2];
           bool move = false;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2)) * c;
-            const bool up = mx[e] > mref[e] + kRefSlack;   // true from -inf
-            const float to = up ? mx[e] - kRefBelow : mref[e];
+            float mx = fmaxf(fmaxf(m8[2 * e], m8[2 * e + 1]), fmaxf(m8[2 * e + 4], m8[2 * e + 5]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * c;
+            const bool up = mx > mref[e] + kRefSlack;   // true from -inf
+            const float to = up ? mx - kRefBelow : mref[e];
             fac[e] = up ? ex2(mref[e] - to) : 1.f;
             mref[e] = to;
             lsum[e] *= fac[e];
             ref[e] = to == -INFINITY ? 0.f : to;
             move |= up;
           }
-          // O of the last tile: waited for at every tile, so that no wait is two phases behind
-          if (t > s.begin) {
-            wait(oFull, it - 1);
-            __syncwarp();
-          }
-          if (t > s.begin && __any_sync(0xffffffffu, move)) {
-            fence_after();
+          if (t > t0 && __any_sync(0xffffffffu, move)) {
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
               float o[16];
-              tm_ld32(tmO + lanes + 32 * q, o);
+              const uint32_t ao = tO + D * stream + 32 * q;
+              tm_ld32(ao, o);
               tm_wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] *= fac[(i >> 1) & 1];
-              tm_st32(tmO + lanes + 32 * q, o);
+              tm_st32(ao, o);
             }
           }
-          // P: twice the probability where V is stored halved
+          // P over S's lower columns: twice the probability where V is stored halved
           const float add = (!f16 && !Sh::PQ) ? 1.f : 0.f;
           float sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -855,53 +1013,85 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
                 const __half2 h2 = __floats2half2_rn(y, z);
                 pk[i] = *reinterpret_cast<const uint32_t*>(&h2);
               }
-              // over S's lower columns, which this warp has read for its rows
               tm_st16(tS + 32 * half + 16 * q, pk);
             }
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) lsum[e] = fmaf(sum[e], add != 0.f ? 0.5f : 1.f, lsum[e]);
           tm_wait_st();
-        } else if (t > s.begin) {
-          wait(oFull, it - 1);
         }
         fence_before();
-        arrive(pFull + 8 * (it & 1));
+        arrive(pFull + 8 * stream);
       }
-      wait(oFull, it - 1);
+      // the stream's last O (S of its last tile said that the one before is complete)
+      const int last = it0 + t_end - t_begin - 1;
+      if (t0 < t_end) wait(oFull + 8 * stream, (last - ((last ^ stream) & 1)) >> 1);
       __syncwarp();
       fence_after();
 
-      // ---------------------------------------------- the segment's result
+      // ---------------------------------------------- the segment's result: both streams joined
       const bool whole = s.begin == 0 && s.end == s.tiles;
       if (active) {
-        const unsigned long long bad = *reinterpret_cast<volatile unsigned long long*>(
-            sBad + 2 * (seg & 7));
-        float* part = p.part + ((size_t)blockIdx.x * 2 + (g == g_first ? 0 : 1)) * ROWS * (D + 2);
+        // rows' references and sums, over the quad and exchanged with the other stream's warp
+        float* mine16 = sMax + warp * 32;
+        const float* other16 = sMax + (warp ^ 4) * 32;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          lsum[e] += __shfl_xor_sync(0xffffffffu, lsum[e], 1);
+          lsum[e] += __shfl_xor_sync(0xffffffffu, lsum[e], 2);
+          if ((lane & 3) == 0) {
+            mine16[(lane >> 2) + 8 * e] = mref[e];
+            mine16[(lane >> 2) + 8 * e + 16] = lsum[e];
+          }
+        }
+        fence_before();
+        pair_sync(quarter + 4 * f);
+        fence_after();
+        const unsigned long long bad =
+            *reinterpret_cast<volatile unsigned long long*>(sBad + 2 * (seg & 7));
+        float* part = p.part + ((size_t)blockIdx.x * 2 + (seg == 0 ? 0 : 1)) * ROWS * (D + 2);
         size_t vec[2];
+        float w[2][2];   // [row][stream]: what its O counts for
         float inv[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float L = lsum[e];
-          L += __shfl_xor_sync(0xffffffffu, L, 1);
-          L += __shfl_xor_sync(0xffffffffu, L, 2);
-          const int r = row0 + 8 * e, rr = s.r0 + min(r, s.rows - 1);
-          vec[e] = ((size_t)s.b * a.T + (rr >> a.log_g)) * a.Hq + s.h * a.G + (rr & (a.G - 1));
-          inv[e] = mref[e] == -INFINITY ? 0.f : 1.f / L;
-          if ((lane & 3) == 0 && r < s.rows) {
+          const float m1 = other16[(lane >> 2) + 8 * e], l1 = other16[(lane >> 2) + 8 * e + 16];
+          const float M = fmaxf(mref[e], m1);
+          const float w0 = mref[e] == -INFINITY ? 0.f : ex2(mref[e] - M);
+          const float w1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+          // the same order of the sum in both warps
+          const float L = stream ? fmaf(l1, w1, lsum[e] * w0) : fmaf(lsum[e], w0, l1 * w1);
+          w[e][0] = stream ? w1 : w0;
+          w[e][1] = stream ? w0 : w1;
+          const int r = row0 + 8 * e, rr = s.r0 + min(r, rows - 1);
+          vec[e] =
+              ((size_t)s.b * a.T + (rr >> a.log_g)) * a.Hq + s.h * a.G + (rr & (a.G - 1));
+          inv[e] = M == -INFINITY ? 0.f : 1.f / L;
+          if (stream == 0 && (lane & 3) == 0 && r < rows) {
             if (whole)
-              p.lse[vec[e]] = mref[e] == -INFINITY
-                                  ? -INFINITY
-                                  : (mref[e] + log2f(L)) * 0.6931471805599453f;
+              p.lse[vec[e]] =
+                  M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
             else
-              *reinterpret_cast<float2*>(part + 2 * r) = make_float2(mref[e], L);
+              *reinterpret_cast<float2*>(part + 2 * r) = make_float2(M, L);
           }
         }
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          float o[16];
-          tm_ld32(tmO + lanes + 32 * q, o);
+        for (int q = 0; q < D / 64; ++q) {   // each stream's warp joins half of the columns
+          float o[16], o1[16];
+          const int c0 = stream * (D / 2) + 32 * q;
+          tm_ld32(tO + c0, o);
+          tm_ld32(tO + D + c0, o1);
           tm_wait_ld();
+          if (q == D / 64 - 1) {
+            fence_before();
+            arrive(oRead);
+          }
+          // (a stream without a tile, or a row that saw nothing, may hold anything)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int e = (i >> 1) & 1;
+            o[i] = (w[e][0] == 0.f ? 0.f : o[i] * w[e][0]) + (w[e][1] == 0.f ? 0.f : o1[i] * w[e][1]);
+          }
           for (unsigned long long left = bad; left; left &= left - 1) {
             const int node = __ffsll((long long)left) - 1;
             const uint16_t* v = a.tv.x + s.b * a.tv.row_stride + node * a.tv.token_stride +
@@ -909,17 +1099,16 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int r = row0 + 8 * ((i >> 1) & 1);
-              if (r >= s.rows || !((p.mask[(size_t)s.b * a.T + ((s.r0 + r) >> a.log_g)] >> node) & 1))
+              if (r >= rows || !((p.mask[(size_t)s.b * a.T + ((s.r0 + r) >> a.log_g)] >> node) & 1))
                 continue;
-              const float y =
-                  h2f(v[channel_of<VO>(32 * q + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1))]);
+              const float y = h2f(v[channel_of<VO>(c0 + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1))]);
               if (!isfinite(y)) o[i] += y;
             }
           }
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const int e = (i >> 1) & 1, col = 32 * q + 8 * (i >> 2) + 2 * (lane & 3);
-            if (row0 + 8 * e >= s.rows) continue;
+            const int e = (i >> 1) & 1, col = c0 + 8 * (i >> 2) + 2 * (lane & 3);
+            if (row0 + 8 * e >= rows) continue;
             if (whole) {
               p.out[vec[e] * D + channel_of<VO>(col)] = f2h(o[i] * inv[e]);
               p.out[vec[e] * D + channel_of<VO>(col + 1)] = f2h(o[i + 1] * inv[e]);
@@ -929,12 +1118,13 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
             }
           }
         }
+        pair_sync(quarter + 4 * f);   // the exchange has been read
       }
-      fence_before();
-      arrive(oRead);
-      g += s.end - s.begin;
+      if (!active) arrive(oRead);
+      it0 += t_end - t_begin;
     }
   }
+  if (limit == 0) record_status(a.status, 1);
   fence_before();
   __syncthreads();
   if (warp == 0)
@@ -942,53 +1132,61 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
 }
 
 // Joins the partials of a block of query rows that several CTAs shared, in the order of their
-// tiles: one warp a row, lane l its channels (in V's order) 2l + 64 i and the next.
+// tiles. CTA x takes the block in which the tiles of CTA x end and those of x + 1 begin, if x is
+// the first to share it: one warp a row, lane l its channels (in V's order) 2l + 64 i and the next.
 template <int D, int VB, int R>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ AttnTreeArgs p,
-                                                            int P) {
+                                                           int P) {
   constexpr int ROWS = 64 * R, VO = order_of(VB);
   __shared__ int pre[257];
   const TreeArgs& a = p.a;
   tile_prefix<ROWS>(a, p.n_nodes, pre);
-  const int N = pre[a.B], b = blockIdx.z;
+  const int N = pre[a.B];
+  const int g = cta_start(N, P, blockIdx.x + 1);
+  // a programmatic dependent of the attention kernel: its partials are complete from here on (and
+  // no CTA ends before it, so that what follows on the stream finds it done)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (g >= N) return;
+  const int b = row_of(pre, a.B, g);
   const RowTiles rt = row_tiles<ROWS>(a, p.n_nodes, b);
-  const int h = blockIdx.y, qb = blockIdx.x / (ROWS / 8);
-  if (qb >= rt.blocks) return;
-  const int begin = pre[b] + (h * rt.blocks + qb) * rt.tiles, end = begin + rt.tiles;
-  const int c0 = cta_of(N, P, begin), c1 = cta_of(N, P, end - 1);
-  if (c0 == c1) return;   // written by its CTA
+  const int blk = (g - pre[b]) / rt.tiles, h = blk / rt.blocks, qb = blk % rt.blocks;
+  const int begin = pre[b] + blk * rt.tiles, end = begin + rt.tiles;
+  if (g == begin || cta_start(N, P, blockIdx.x) > begin) return;
+  const int c1 = cta_of(N, P, end - 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = (blockIdx.x % (ROWS / 8)) * 8 + warp, rr = qb * ROWS + row;
-  if (rr >= rt.n * a.G) return;
-  float M = -INFINITY, L = 0.f, o[D / 32];
+  for (int row = blockIdx.y * 16 + warp; row < blockIdx.y * 16 + 16; row += 8) {
+    const int rr = qb * ROWS + row;
+    if (rr >= rt.n * a.G) return;
+    float M = -INFINITY, L = 0.f, o[D / 32];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-  for (int c = c0; c <= c1; ++c) {
-    const int g0 = cta_start(N, P, c);
-    if (g0 == cta_start(N, P, c + 1)) continue;   // a CTA without tiles
-    const float* part =
-        p.part + ((size_t)c * 2 + (g0 >= begin ? 0 : 1)) * ROWS * (D + 2);
-    const float2 ml = *reinterpret_cast<const float2*>(part + 2 * row);
-    const float Mn = fmaxf(M, ml.x);
-    const float fo = M == -INFINITY ? 0.f : ex2(M - Mn);
-    const float fn = ml.x == -INFINITY ? 0.f : ex2(ml.x - Mn);
-    L = fmaf(L, fo, ml.y * fn);
+    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+    for (int c = blockIdx.x; c <= c1; ++c) {
+      const int g0 = cta_start(N, P, c);
+      if (g0 == cta_start(N, P, c + 1)) continue;   // a CTA without tiles
+      const float* part = p.part + ((size_t)c * 2 + (g0 >= begin ? 0 : 1)) * ROWS * (D + 2);
+      const float2 ml = *reinterpret_cast<const float2*>(part + 2 * row);
+      const float Mn = fmaxf(M, ml.x);
+      const float fo = M == -INFINITY ? 0.f : ex2(M - Mn);
+      const float fn = ml.x == -INFINITY ? 0.f : ex2(ml.x - Mn);
+      L = fmaf(L, fo, ml.y * fn);
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const float2 x =
-          *reinterpret_cast<const float2*>(part + 2 * ROWS + (size_t)row * D + 64 * i + 2 * lane);
-      o[2 * i] = fmaf(o[2 * i], fo, x.x * fn);
-      o[2 * i + 1] = fmaf(o[2 * i + 1], fo, x.y * fn);
+      for (int i = 0; i < D / 64; ++i) {
+        const float2 x =
+            *reinterpret_cast<const float2*>(part + 2 * ROWS + (size_t)row * D + 64 * i + 2 * lane);
+        o[2 * i] = fmaf(o[2 * i], fo, x.x * fn);
+        o[2 * i + 1] = fmaf(o[2 * i + 1], fo, x.y * fn);
+      }
+      M = Mn;
     }
-    M = Mn;
-  }
-  const size_t vec = ((size_t)b * a.T + rr / a.G) * a.Hq + h * a.G + rr % a.G;
-  const float inv = M == -INFINITY ? 0.f : 1.f / L;
+    const size_t vec =
+        ((size_t)b * a.T + (rr >> a.log_g)) * a.Hq + h * a.G + (rr & (a.G - 1));
+    const float inv = M == -INFINITY ? 0.f : 1.f / L;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-    p.out[vec * D + channel_of<VO>(64 * (i >> 1) + 2 * lane + (i & 1))] = f2h(o[i] * inv);
-  if (lane == 0)
-    p.lse[vec] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    for (int i = 0; i < D / 32; ++i)
+      p.out[vec * D + channel_of<VO>(64 * (i >> 1) + 2 * lane + (i & 1))] = f2h(o[i] * inv);
+    if (lane == 0)
+      p.lse[vec] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  }
 }
 
 int sm_count() {
@@ -997,6 +1195,13 @@ int sm_count() {
       cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
   return n < kMaxSM ? n : kMaxSM;
+}
+
+// One CTA per SM, more where a CTA's list of segments (one more than its blocks of query rows) would
+// not hold them.
+int tree_ctas(long long blocks, int sms) {
+  const long long least = (blocks + kMaxSeg - 3) / (kMaxSeg - 2);
+  return (int)(least > sms ? least : sms);
 }
 
 int rows_of(const fade_config_t* c, int T) {   // query rows of a block: 64 where they are enough
@@ -1012,7 +1217,8 @@ fade_status_t launch(const fade_config_t* c, const AttnTreeArgs& p, cudaStream_t
   const long long blocks = ceil_div((long long)p.a.T * p.a.G, 64 * R);
   const long long most = (long long)p.a.B * p.a.H * blocks *
                          (ceil_div(p.a.C, kTok) + ceil_div(p.a.S + p.a.W + p.a.T, kTok));
-  const int P = (int)(most < sms ? most : sms);
+  const long long all = (long long)p.a.B * p.a.H * blocks;
+  const int P = tree_ctas(all, most < sms ? (int)most : sms);
   auto kern = tree_attention_kernel<D, KB, VB, R>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM) !=
       cudaSuccess)
@@ -1028,8 +1234,19 @@ fade_status_t launch(const fade_config_t* c, const AttnTreeArgs& p, cudaStream_t
   kern<<<P, Sh::THREADS, Sh::SMEM, st>>>(p);
   fade_status_t s = launch_status("fade_tree_attention");
   if (s) return s;
-  tree_combine_kernel<D, VB, R>
-      <<<dim3((unsigned)(blocks * 8 * R), p.a.H, p.a.B), 256, 0, st>>>(p, P);
+  if (P == 1) return FADE_OK;
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3(P - 1, 4 * R);
+  lc.blockDim = dim3(256);
+  lc.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&lc, tree_combine_kernel<D, VB, R>, p, P);
+  if (e != cudaSuccess)
+    return set_error(FADE_ERR_CUDA, "fade_tree_attention combine: %s", cudaGetErrorString(e));
   return launch_status("fade_tree_attention combine");
 }
 
@@ -1041,7 +1258,10 @@ fade_status_t launch_rows(const fade_config_t* c, const AttnTreeArgs& p, cudaStr
 }  // namespace
 
 size_t tree_attention_ws(const fade_config_t* c, int T) {
-  return (size_t)kMaxSM * 2 * rows_of(c, T) * (c->head_dim + 2) * 4;
+  const int rows = rows_of(c, T);
+  const long long blocks = (long long)c->batch * c->num_kv_heads *
+                           ceil_div((long long)T * (c->num_q_heads / c->num_kv_heads), rows);
+  return (size_t)tree_ctas(blocks, kMaxSM) * 2 * rows * (c->head_dim + 2) * 4;
 }
 
 }  // namespace fade
