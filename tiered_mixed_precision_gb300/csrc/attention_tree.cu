@@ -55,21 +55,10 @@ struct Shape {
   static constexpr int FIXED = TILE + LOWB + CODEBOOK + 11264 + 1024;   // Q, small arrays, alignment
   static constexpr int STAGES = FIXED + 2 * STAGE <= 226 * 1024 ? 2 : 1;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
-  static constexpr int SOFT = 256 * R;                        // softmax threads
-  static constexpr int SIDE = R == 1 ? 2 * D : D;             // threads that unpack K, and V
-  static constexpr int ITEMS = kTok * (D / 32) / SIDE;        // groups of 32 channels a thread
-  static constexpr int UNPACK = 2 * SIDE;
+  static constexpr int SOFT = 256;                            // softmax threads
+  static constexpr int KT = 128, VT = 128;                    // threads that unpack K, and V
+  static constexpr int UNPACK = KT + VT;
   static constexpr int THREADS = SOFT + UNPACK + 128;         // and four warps: two issue, one prefetches
-  // Registers a thread: at the launch, then by role (multiples of 8; the sum over the roles stays
-  // within the launch's).
-  static constexpr int REGS = 65536 / THREADS / 8 * 8;
-  static constexpr int REGS_MMA = 40;
-  static constexpr int REGS_UNPACK_ = R == 1 ? 64 : 88;
-  static constexpr int REGS_UNPACK = REGS > REGS_UNPACK_ ? (REGS > 96 ? 96 : REGS) : REGS_UNPACK_;
-  static constexpr int REGS_SOFT_ =
-      (REGS * THREADS - REGS_MMA * 128 - REGS_UNPACK * UNPACK) / SOFT / 8 * 8;
-  static constexpr int REGS_SOFT = REGS_SOFT_ > 128 ? 128 : REGS_SOFT_;
-  static_assert(REGS_SOFT * SOFT + REGS_UNPACK * UNPACK + REGS_MMA * 128 <= REGS * THREADS, "");
   static constexpr int TMEM = 512;                            // columns: S (and P) 2 x 128, O 2 x D
 };
 
@@ -397,26 +386,32 @@ __device__ __forceinline__ void item_of(int thread, int& tok, int& g) {
   }
 }
 
+// Loads that stay where they are written: the compiler would sink them to their use, a tile later.
 template <int W>
 __device__ __forceinline__ void ld_words(const uint8_t* p, uint32_t* w) {
-  if constexpr (W == 4) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
-    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-  } else {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-    w[0] = x.x; w[1] = x.y;
-  }
+  if constexpr (W == 4)
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p));
+  else
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
 }
-// A thread's codes and scales of middle tiles, K's or V's (W 32-bit words a group): the next
-// tile's on their way while the present one's are unpacked.
+__device__ __forceinline__ uint16_t ld_half(const uint16_t* p) {
+  uint16_t x;
+  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(x) : "l"(p));
+  return x;
+}
+
+// A thread's codes and scales of a middle tile, K's or V's (W 32-bit words a group). An item's
+// registers take the next tile's codes as soon as they have been unpacked.
 template <int D, int W, bool SCALED, int ITEMS>
 struct Codes {
   static constexpr int G = D / 32, APART = kTok / ITEMS;
-  uint32_t w[2][ITEMS][W];   // [present or next tile][row]
-  uint16_t sc[2][ITEMS];
+  uint32_t w[ITEMS][W];
+  uint16_t sc[ITEMS];
   const uint8_t* codes;
   const uint16_t* scales;
-  int last;   // tokens from the coming tile's row to the tier's last
+  int last;   // tokens from the thread's first row of the tile to come to the tier's last
   __device__ __forceinline__ void start(const uint8_t* c, const uint16_t* s, size_t unit_row,
                                         int n_mid, int tok, int g) {
     const size_t r = (unit_row + tok) * G + g;
@@ -424,25 +419,22 @@ struct Codes {
     scales = s + r;
     last = n_mid - 1 - tok;
   }
-  // Tokens past the tier read its last row: their keys are masked in S, their values zeroed.
-  __device__ __forceinline__ void load(int buf) {
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int at = (APART * i + min(last - APART * i, 0)) * G;
-      ld_words<W>(codes + (long long)at * (4 * W), w[buf][i]);
-      if constexpr (SCALED) sc[buf][i] = __ldg(scales + at);
-    }
+  // Item i of the tile to come. Tokens past the tier read its last row: their keys are masked in S,
+  // their values zeroed.
+  __device__ __forceinline__ void load(int i) {
+    const int at = min(APART * i, last) * G;
+    ld_words<W>(codes + (long long)at * (4 * W), w[i]);
+    if constexpr (SCALED) sc[i] = ld_half(scales + at);
+  }
+  __device__ __forceinline__ void next_tile() {
     codes += kTok * G * 4 * W;
     scales += kTok * G;
     last -= kTok;
   }
-  __device__ __forceinline__ void advance() {
+  __device__ __forceinline__ void load_all() {
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-#pragma unroll
-      for (int j = 0; j < W; ++j) w[0][i][j] = w[1][i][j];
-      if constexpr (SCALED) sc[0][i] = sc[1][i];
-    }
+    for (int i = 0; i < ITEMS; ++i) load(i);
+    next_tile();
   }
 };
 
@@ -455,15 +447,6 @@ __device__ __forceinline__ const uint16_t* f16_row(const TreeArgs& a, int D, int
   j -= n_rec;
   const fade_heads_t& t = v ? a.tv : a.tk;
   return t.x + b * t.row_stride + j * t.token_stride + h * t.head_stride;
-}
-
-// The calling warpgroup's share of the CTA's registers (HAVE a thread at the launch).
-template <int N, int HAVE>
-__device__ __forceinline__ void reg_set() {
-  if constexpr (N > HAVE)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-  else if constexpr (N < HAVE)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Waits for the phase-th completion of an mbarrier, for `limit` cycles at most; false when it gives up.
@@ -586,9 +569,9 @@ __device__ __forceinline__ void tile_to_l2(const AttnTreeArgs& p, const Segment&
 }
 
 // One CTA per SM, roles that meet at mbarriers. Some warps unpack K and as many V, each into a ring
-// of STAGES (the next tile's codes already in registers); one warp issues S = Q K^T, one O += P V,
-// one asks for coming tiles in L2; 8 R warps do the softmax, 16 query rows each (a thread: two rows,
-// spread over four lanes). A tile's chain (S, softmax, P V) is long and mostly waiting, so even and
+// of STAGES (the next tile's codes on their way into the registers); one warp issues S = Q K^T, one O += P V,
+// one asks for coming tiles in L2; 8 warps do the softmax, 16 query rows at a time (a thread: two
+// rows, spread over four lanes). A tile's chain (S, softmax, P V) is long and mostly waiting, so even and
 // odd tiles run as two streams, each with its softmax warps, its S (over which P is written), its
 // references and its own O; the segment's end joins them. R: 16-row halves of each 32-lane quarter
 // of tensor memory in use: up to 64 query rows take lanes 0..15 of every quarter (R = 1), which
@@ -618,7 +601,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
   const uint32_t bar0 = smem_u32(bars);
   const uint32_t kFull = bar0, kFree = bar0 + 16, vFull = bar0 + 32, vFree = bar0 + 48;   // [2]
   const uint32_t sFull = bar0 + 64, pFull = bar0 + 80;                                    // [2]
-  const uint32_t oFull = bar0 + 96, oRead = bar0 + 112;                                   // [2], 1
+  const uint32_t oFull = bar0 + 96, oRead = bar0 + 112, qFull = bar0 + 120;               // [2], 1, 1
   const TreeArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
@@ -640,8 +623,8 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
   if (tid == 0) {
     *sDone = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(kFull + 8 * i, Sh::SIDE / 32);
-      mbar_init(vFull + 8 * i, Sh::SIDE / 32);
+      mbar_init(kFull + 8 * i, Sh::KT / 32);
+      mbar_init(vFull + 8 * i, Sh::VT / 32);
       mbar_init(kFree + 8 * i, 1);
       mbar_init(vFree + 8 * i, 1);
       mbar_init(sFull + 8 * i, 1);
@@ -649,6 +632,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
       mbar_init(oFull + 8 * i, 1);
     }
     mbar_init(oRead, Sh::SOFT / 32);
+    mbar_init(qFull, Sh::VT / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if constexpr (Sh::PQ) {
@@ -678,17 +662,19 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
 
   if (warp >= Sh::SOFT / 32 && warp < (Sh::SOFT + Sh::UNPACK) / 32) {
     // ================================================================ unpacking
-    reg_set<Sh::REGS_UNPACK, Sh::REGS>();
-    const bool is_v = warp >= (Sh::SOFT + Sh::SIDE) / 32;
+    const bool is_v = warp >= (Sh::SOFT + Sh::KT) / 32;
     int it = 0, seg = 0, tok, gq;
-    item_of<D>((tid - Sh::SOFT) & (Sh::SIDE - 1), tok, gq);
+    item_of<D>(is_v ? tid - Sh::SOFT - Sh::KT : tid - Sh::SOFT, tok, gq);
     const uint32_t at16 = group_at(tok, gq), at8 = low_at(tok, gq);
     // one warp of the side watches the mbarrier, the others block at a named barrier: eight
     // watching warps would take the softmax's issue slots
     auto side_wait = [&](uint32_t bar, int phase) {
-      if (((tid - Sh::SOFT) & (Sh::SIDE - 1)) < 32) wait(bar, phase);
+      if (warp == Sh::SOFT / 32 || warp == (Sh::SOFT + Sh::KT) / 32) wait(bar, phase);
       __syncwarp();
-      asm volatile("bar.sync %0, %1;" ::"r"(2 + (int)is_v), "n"(Sh::SIDE) : "memory");
+      if (is_v)
+        asm volatile("bar.sync 3, %0;" ::"n"(Sh::VT) : "memory");
+      else
+        asm volatile("bar.sync 2, %0;" ::"n"(Sh::KT) : "memory");
     };
     // an FP16 token's share of a row (zeros past the nodes)
     auto f16_load = [&](const Segment& s, int j, bool v, uint4 (&x)[4]) {
@@ -701,8 +687,8 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         for (int c = 0; c < 4; ++c) x[c] = src[c];
       }
     };
-    constexpr int NI = Sh::ITEMS, APART = kTok / NI, ROWB = APART * 128;   // rows apart, bytes
-    if (!is_v) {   // -------------------------------------------- keys, and Q
+    if (!is_v) {   // -------------------------------------------- keys
+      constexpr int NI = kTok * (D / 32) / Sh::KT, APART = kTok / NI, ROWB = APART * 128;
       const Fields<KB> kf;
       for (; seg < n_seg; ++seg) {
         const Segment& s = sSeg[seg];
@@ -711,28 +697,11 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         Codes<D, KB, true, NI> c;
         c.start(a.mk[s.cur], a.mks[s.cur], (size_t)s.unit * a.C, s.n_mid,
                 max(t - f16, 0) * kTok + tok, gq);
-        if (t >= f16) c.load(0);
-        // Q, once the last product that reads the old one is done: matrix row 32 q + i holds query
-        // row 16 q + i (R = 1, i < 16) or 32 q + i
-        if (it > 0) side_wait(kFree + 8 * ((it - 1) % ST), (it - 1) / ST);
-#pragma unroll 1
-        for (int i = 0; i < NI; ++i) {
-          const int row = tok + APART * i, in = row & 31, qr = (row >> 5) * (16 * R) + in;
-          uint4 x[4] = {};
-          if (in < 16 * R && qr < s.rows) {
-            const int node = (s.r0 + qr) >> a.log_g, gh = (s.r0 + qr) & (a.G - 1);
-            const uint4* src = reinterpret_cast<const uint4*>(
-                a.q + (((size_t)s.b * a.T + node) * a.Hq + s.h * a.G + gh) * D + 32 * gq);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = __ldg(src + e);
-          }
-          store_f16<KO>(sQ + at16 + i * ROWB, x);
-          if constexpr (Sh::LOW) store_low(sQL + at8 + i * ROWB, x);
-        }
+        if (t >= f16) c.load_all();
         for (; t < t_end && t < f16; ++t, ++it) {
           const int st = it % ST, use = it / ST;
           if (use > 0) side_wait(kFree + 8 * st, use - 1);
-          if (t + 1 == f16 && t + 1 < t_end) c.load(0);
+          if (t + 1 == f16 && t + 1 < t_end) c.load_all();
 #pragma unroll 1
           for (int i = 0; i < NI; i += 2) {
             uint4 x[4], y[4];
@@ -746,19 +715,21 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         }
         for (; t < t_end; ++t, ++it) {
           const int st = it % ST, use = it / ST;
-          if (t + 1 < t_end) c.load(1);
           if (use > 0) side_wait(kFree + 8 * st, use - 1);
           const uint32_t k = kTile(st) + at16, l = kLow(st) + at8;
 #pragma unroll
-          for (int i = 0; i < NI; ++i)
-            store_codes<KB, Sh::LOW>(k + i * ROWB, l + i * ROWB, kf, c.w[0][i], c.sc[0][i]);
+          for (int i = 0; i < NI; ++i) {
+            store_codes<KB, Sh::LOW>(k + i * ROWB, l + i * ROWB, kf, c.w[i], c.sc[i]);
+            if (t + 1 < t_end) c.load(i);
+          }
           fence_proxy_async_smem();
           arrive(kFull + 8 * st);
           if (tid == Sh::SOFT) *sDone = it + 1;
-          c.advance();
+          c.next_tile();
         }
       }
-    } else {   // ------------------------------------------------ values
+    } else {   // ------------------------------------------------ values, and Q
+      constexpr int NI = kTok * (D / 32) / Sh::VT, APART = kTok / NI, ROWB = APART * 128;
       const Fields<Sh::PQ ? 4 : VB> vf;
       for (; seg < n_seg; ++seg) {
         const Segment& s = sSeg[seg];
@@ -768,13 +739,39 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         Codes<D, Sh::PQ ? 2 : VB, !Sh::PQ, NI> c;
         c.start(a.mv[s.cur], a.mvs[s.cur], (size_t)s.unit * a.C, n_mid,
                 max(t - f16, 0) * kTok + tok, gq);
-        if (t >= f16) c.load(0);
-        if (tid == Sh::SOFT + Sh::SIDE) bad[0] = bad[1] = 0;
-        asm volatile("bar.sync 1, %0;" ::"n"(Sh::SIDE) : "memory");   // cleared before any is set
+        if (t >= f16) c.load_all();
+        if (tid == Sh::SOFT + Sh::KT) bad[0] = bad[1] = 0;
+        // Q: matrix row 32 q + i holds query row 16 q + i (R = 1, i < 16) or 32 q + i; stored once
+        // the last product that reads the old one is done
+#pragma unroll 1
+        for (int i = 0; i < NI; i += 2) {
+          uint4 x[2][4] = {};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int row = tok + APART * (i + j), in = row & 31, qr = (row >> 5) * (16 * R) + in;
+            if (in < 16 * R && qr < s.rows) {
+              const int node = (s.r0 + qr) >> a.log_g, gh = (s.r0 + qr) & (a.G - 1);
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  a.q + (((size_t)s.b * a.T + node) * a.Hq + s.h * a.G + gh) * D + 32 * gq);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[j][e] = __ldg(src + e);
+            }
+          }
+          if (i == 0 && it > 0) wait(kFree + 8 * ((it - 1) % ST), (it - 1) / ST);
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            store_f16<KO>(sQ + at16 + (i + j) * ROWB, x[j]);
+            if constexpr (Sh::LOW) store_low(sQL + at8 + (i + j) * ROWB, x[j]);
+          }
+        }
+        fence_proxy_async_smem();
+        arrive(qFull);
+        asm volatile("bar.sync 3, %0;" ::"n"(Sh::VT) : "memory");   // the nodes' bits are cleared
         for (; t < t_end && t < f16; ++t, ++it) {
           const int st = it % ST, use = it / ST;
           if (use > 0) side_wait(vFree + 8 * st, use - 1);
-          if (t + 1 == f16 && t + 1 < t_end) c.load(0);
+          if (t + 1 == f16 && t + 1 < t_end) c.load_all();
 #pragma unroll 1
           for (int i = 0; i < NI; i += 2) {
             uint4 x[4], y[4];
@@ -793,7 +790,6 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         }
         for (; t < t_end; ++t, ++it) {
           const int st = it % ST, use = it / ST;
-          if (t + 1 < t_end) c.load(1);
           if (use > 0) side_wait(vFree + 8 * st, use - 1);
           const int left = n_mid - (t - f16) * kTok - tok;   // tokens from this row on
 #pragma unroll
@@ -807,24 +803,24 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const int ss = (e + tok) & 7;
-                const uint32_t w = (ss & 4) ? c.w[0][i][1] : c.w[0][i][0];
+                const uint32_t w = (ss & 4) ? c.w[i][1] : c.w[i][0];
                 const int code = (w >> (8 * (ss & 3))) & 255;
                 const uint2 x = in ? sCB[code * (D / 4) + 8 * gq + ss] : make_uint2(0u, 0u);
                 st_shared8((v ^ (16 * (ss >> 1))) + 8 * (ss & 1), x.x, x.y);
               }
             } else {
-              store_codes<VB, false>(v, 0, vf, c.w[0][i], in ? c.sc[0][i] : (uint16_t)0);
+              store_codes<VB, false>(v, 0, vf, c.w[i], in ? c.sc[i] : (uint16_t)0);
             }
+            if (t + 1 < t_end) c.load(i);
           }
           fence_proxy_async_smem();
           arrive(vFull + 8 * st);
-          c.advance();
+          c.next_tile();
         }
       }
     }
   } else if (warp >= (Sh::SOFT + Sh::UNPACK) / 32) {
     // ================================================================ products
-    reg_set<Sh::REGS_MMA, Sh::REGS>();
     const int role = warp - (Sh::SOFT + Sh::UNPACK) / 32;
     // a warp walks as one and elects the thread that issues, so that addresses and descriptors stay
     // in uniform registers
@@ -843,6 +839,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         for (int i = 0; i < n; ++i, --f16, ++it) {
           const int st = it % ST;
           if (it >= 2) wait(oFull + 8 * (it & 1), (it >> 1) - 1);   // the buffer's P has been read
+          if (i == 0) wait(qFull, seg);
           wait(kFull + 8 * st, it / ST);
           __syncwarp();
           fence_after();
@@ -905,28 +902,39 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
     }
   } else {
     // ================================================================ softmax
-    reg_set<Sh::REGS_SOFT, Sh::REGS>();
-    const int quarter = warp & 3, stream = (warp >> 2) & 1, f = warp >> 3;
-    const uint32_t lanes = (uint32_t)(quarter * 32 + 16 * f) << 16;
-    const uint32_t tS = tm + 128 * stream + lanes, tO = tmO + lanes;
-    const int row0 = quarter * (16 * R) + 16 * f + (lane >> 2);   // this thread's rows: row0, + 8
+    const int quarter = warp & 3, stream = warp >> 2;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const float cscale = kLog2e * rsqrtf((float)D);
     int it0 = 0, seg = 0;   // the segment's first tile
     for (; seg < n_seg; ++seg) {
       const Segment& s = sSeg[seg];
       const int f16_tiles = s.f16, t_begin = s.begin, t_end = s.end, n_mid = s.n_mid, rows = s.rows;
       const int n16 = s.n_sink + s.n_rec, n_f16 = n16 + s.n;
-      // a warp whose rows are all past the block's takes no part
-      const bool active = quarter * (16 * R) + 16 * f < rows;
+      // 16-row groups of this warp with rows of the block
+      const int groups = min(R, max(0, (rows - quarter * (16 * R) + 15) / 16));
       const int t0 = t_begin + ((it0 ^ stream) & 1);   // this stream's first tile, and every other
+      // this thread's two rows' references and sums: the present group's, and the other one's (R = 2)
       float mref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
+      float mref_[2] = {-INFINITY, -INFINITY}, lsum_[2] = {0.f, 0.f};
+      auto other_group = [&]() {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float m = mref[e], l = lsum[e];
+          mref[e] = mref_[e], lsum[e] = lsum_[e];
+          mref_[e] = m, lsum_[e] = l;
+        }
+      };
       for (int t = t0; t < t_end; t += 2) {
         // S of the tile; the stream's last O += P V is then complete, too
         wait(sFull + 8 * stream, (it0 + t - t_begin) >> 1);
         __syncwarp();
         fence_after();
-        if (active) {
-          const bool f16 = t < f16_tiles;
+        const bool f16 = t < f16_tiles;
+#pragma unroll 1
+        for (int f = 0; f < groups; ++f) {
+          const uint32_t at = lanes + ((uint32_t)(16 * f) << 16);
+          const uint32_t tS = tm + 128 * stream + at;
+          const int row0 = quarter * (16 * R) + 16 * f + (lane >> 2);   // the thread's rows: row0, + 8
           const int tok0 = (f16 ? t : t - f16_tiles) * kTok;
           const int count = min(kTok, (f16 ? n_f16 : n_mid) - tok0);
           const float c = f16 ? cscale : 2.f * cscale;   // middle keys are stored halved
@@ -987,7 +995,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
               float o[16];
-              const uint32_t ao = tO + D * stream + 32 * q;
+              const uint32_t ao = tmO + at + D * stream + 32 * q;
               tm_ld32(ao, o);
               tm_wait_ld();
 #pragma unroll
@@ -1018,8 +1026,10 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) lsum[e] = fmaf(sum[e], add != 0.f ? 0.5f : 1.f, lsum[e]);
-          tm_wait_st();
+          if (R == 2) other_group();
         }
+        if (R == 2 && groups == 1) other_group();
+        tm_wait_st();
         fence_before();
         arrive(pFull + 8 * stream);
       }
@@ -1031,7 +1041,10 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
 
       // ---------------------------------------------- the segment's result: both streams joined
       const bool whole = s.begin == 0 && s.end == s.tiles;
-      if (active) {
+#pragma unroll 1
+      for (int f = 0; f < groups; ++f) {
+        const uint32_t at = lanes + ((uint32_t)(16 * f) << 16);
+        const int row0 = quarter * (16 * R) + 16 * f + (lane >> 2);
         // rows' references and sums, over the quad and exchanged with the other stream's warp
         float* mine16 = sMax + warp * 32;
         const float* other16 = sMax + (warp ^ 4) * 32;
@@ -1045,7 +1058,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
           }
         }
         fence_before();
-        pair_sync(quarter + 4 * f);
+        pair_sync(quarter);
         fence_after();
         const unsigned long long bad =
             *reinterpret_cast<volatile unsigned long long*>(sBad + 2 * (seg & 7));
@@ -1079,10 +1092,10 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         for (int q = 0; q < D / 64; ++q) {   // each stream's warp joins half of the columns
           float o[16], o1[16];
           const int c0 = stream * (D / 2) + 32 * q;
-          tm_ld32(tO + c0, o);
-          tm_ld32(tO + D + c0, o1);
+          tm_ld32(tmO + at + c0, o);
+          tm_ld32(tmO + at + D + c0, o1);
           tm_wait_ld();
-          if (q == D / 64 - 1) {
+          if (q == D / 64 - 1 && f == groups - 1) {
             fence_before();
             arrive(oRead);
           }
@@ -1118,9 +1131,10 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
             }
           }
         }
-        pair_sync(quarter + 4 * f);   // the exchange has been read
+        pair_sync(quarter);   // the exchange has been read
+        if (R == 2) other_group();
       }
-      if (!active) arrive(oRead);
+      if (groups == 0) arrive(oRead);
       it0 += t_end - t_begin;
     }
   }
@@ -1223,14 +1237,6 @@ fade_status_t launch(const fade_config_t* c, const AttnTreeArgs& p, cudaStream_t
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM) !=
       cudaSuccess)
     return launch_status("fade_tree_attention shared-memory opt-in");
-  // the kernel's register split counts on the registers it is launched with
-  static const int regs = [&] {
-    cudaFuncAttributes at{};
-    return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
-  }();
-  if (regs < Sh::REGS)
-    return set_error(FADE_ERR_UNSUPPORTED, "fade_tree_attention built with %d registers, not %d",
-                     regs, Sh::REGS);
   kern<<<P, Sh::THREADS, Sh::SMEM, st>>>(p);
   fade_status_t s = launch_status("fade_tree_attention");
   if (s) return s;
