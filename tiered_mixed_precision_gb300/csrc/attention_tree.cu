@@ -534,6 +534,7 @@ __device__ __forceinline__ void tile_to_l2(const AttnTreeArgs& p, const Segment&
   const int lane = threadIdx.x & 31;
   auto line = [](const void* x) { asm volatile("prefetch.global.L2 [%0];" ::"l"(x)); };
   if (t == s.begin)
+#pragma unroll 1
     for (int i = lane; i < s.rows; i += 32) {
       const int r = s.r0 + i;
       const uint16_t* q = a.q + (((size_t)s.b * a.T + (r >> a.log_g)) * a.Hq + s.h * a.G +
@@ -543,6 +544,7 @@ __device__ __forceinline__ void tile_to_l2(const AttnTreeArgs& p, const Segment&
     }
   if (t < s.f16) {
     const int end = min((t + 1) * kTok, s.n_sink + s.n_rec + s.n);
+#pragma unroll 1
     for (int j = t * kTok + lane; j < end; j += 32)
 #pragma unroll 1
       for (int v = 0; v < 2; ++v) {
@@ -559,6 +561,7 @@ __device__ __forceinline__ void tile_to_l2(const AttnTreeArgs& p, const Segment&
     const size_t r = ((size_t)s.unit * a.C + t0) * G;
     const int cur = s.cur;
     auto run = [&](const void* x, int bytes) {
+#pragma unroll 1
       for (int i = lane * 128; i < bytes; i += 32 * 128) line(static_cast<const char*>(x) + i);
     };
     run(a.mk[cur] + r * (4 * KW), rows * G * 4 * KW);
@@ -690,6 +693,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
     if (!is_v) {   // -------------------------------------------- keys
       constexpr int NI = kTok * (D / 32) / Sh::KT, APART = kTok / NI, ROWB = APART * 128;
       const Fields<KB> kf;
+#pragma unroll 1
       for (; seg < n_seg; ++seg) {
         const Segment& s = sSeg[seg];
         const int f16 = s.f16, t_end = s.end;
@@ -698,6 +702,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         c.start(a.mk[s.cur], a.mks[s.cur], (size_t)s.unit * a.C, s.n_mid,
                 max(t - f16, 0) * kTok + tok, gq);
         if (t >= f16) c.load_all();
+#pragma unroll 1
         for (; t < t_end && t < f16; ++t, ++it) {
           const int st = it % ST, use = it / ST;
           if (use > 0) side_wait(kFree + 8 * st, use - 1);
@@ -713,6 +718,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
           fence_proxy_async_smem();
           arrive(kFull + 8 * st);
         }
+#pragma unroll 1
         for (; t < t_end; ++t, ++it) {
           const int st = it % ST, use = it / ST;
           if (use > 0) side_wait(kFree + 8 * st, use - 1);
@@ -731,6 +737,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
     } else {   // ------------------------------------------------ values, and Q
       constexpr int NI = kTok * (D / 32) / Sh::VT, APART = kTok / NI, ROWB = APART * 128;
       const Fields<Sh::PQ ? 4 : VB> vf;
+#pragma unroll 1
       for (; seg < n_seg; ++seg) {
         const Segment& s = sSeg[seg];
         const int f16 = s.f16, t_end = s.end, n_mid = s.n_mid, n16 = s.n_sink + s.n_rec;
@@ -768,6 +775,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         fence_proxy_async_smem();
         arrive(qFull);
         asm volatile("bar.sync 3, %0;" ::"n"(Sh::VT) : "memory");   // the nodes' bits are cleared
+#pragma unroll 1
         for (; t < t_end && t < f16; ++t, ++it) {
           const int st = it % ST, use = it / ST;
           if (use > 0) side_wait(vFree + 8 * st, use - 1);
@@ -788,6 +796,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
           fence_proxy_async_smem();
           arrive(vFull + 8 * st);
         }
+#pragma unroll 1
         for (; t < t_end; ++t, ++it) {
           const int st = it % ST, use = it / ST;
           if (use > 0) side_wait(vFree + 8 * st, use - 1);
@@ -832,10 +841,12 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
       const uint64_t dQL = smem_desc(sQL, 16, 1024);
       const uint64_t dKL = smem_desc(kLow(0), 16, 1024);
       int it = 0;
+#pragma unroll 1
       for (int seg = 0; seg < n_seg; ++seg) {
         const Segment& s = sSeg[seg];
         int f16 = s.f16 - s.begin;   // FP16 tiles left
         const int n = s.end - s.begin;
+#pragma unroll 1
         for (int i = 0; i < n; ++i, --f16, ++it) {
           const int st = it % ST;
           if (it >= 2) wait(oFull + 8 * (it & 1), (it >> 1) - 1);   // the buffer's P has been read
@@ -867,9 +878,11 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
     } else if (role == 1) {   // O += P V
       const uint64_t dV = smem_desc(vTile(0), kBlk, 1024);
       int it = 0, seg = 0;
+#pragma unroll 1
       for (; seg < n_seg; ++seg) {
         const Segment& s = sSeg[seg];
         const int n = s.end - s.begin;
+#pragma unroll 1
         for (int i = 0; i < n; ++i, ++it) {
           const int st = it % ST, stream = it & 1;
           wait(vFull + 8 * st, it / ST);
@@ -891,10 +904,13 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
       }
     } else if (role == 2) {   // L2, kAhead tiles ahead of the unpacking
       int it = 0;
+#pragma unroll 1
       for (int seg = 0; seg < n_seg; ++seg) {
         const Segment& s = sSeg[seg];
+#pragma unroll 1
         for (int t = s.begin; t < s.end; ++t, ++it) {
           // no more than kAhead tiles before the unpacking (a pace, not an order: bounded)
+#pragma unroll 1
           for (int i = 0; *sDone + kAhead < it && i < 1000; ++i) __nanosleep(200);
           tile_to_l2<D, KB, VB>(p, s, t);
         }
@@ -906,6 +922,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const float cscale = kLog2e * rsqrtf((float)D);
     int it0 = 0, seg = 0;   // the segment's first tile
+#pragma unroll 1
     for (; seg < n_seg; ++seg) {
       const Segment& s = sSeg[seg];
       const int f16_tiles = s.f16, t_begin = s.begin, t_end = s.end, n_mid = s.n_mid, rows = s.rows;
@@ -924,6 +941,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
           mref_[e] = m, lsum_[e] = l;
         }
       };
+#pragma unroll 1
       for (int t = t0; t < t_end; t += 2) {
         // S of the tile; the stream's last O += P V is then complete, too
         wait(sFull + 8 * stream, (it0 + t - t_begin) >> 1);
@@ -1105,6 +1123,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
             const int e = (i >> 1) & 1;
             o[i] = (w[e][0] == 0.f ? 0.f : o[i] * w[e][0]) + (w[e][1] == 0.f ? 0.f : o1[i] * w[e][1]);
           }
+#pragma unroll 1
           for (unsigned long long left = bad; left; left &= left - 1) {
             const int node = __ffsll((long long)left) - 1;
             const uint16_t* v = a.tv.x + s.b * a.tv.row_stride + node * a.tv.token_stride +
