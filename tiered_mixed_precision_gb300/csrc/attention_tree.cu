@@ -449,20 +449,20 @@ __device__ __forceinline__ const uint16_t* f16_row(const TreeArgs& a, int D, int
   return t.x + b * t.row_stride + j * t.token_stride + h * t.head_stride;
 }
 
-// Waits for the phase-th completion of an mbarrier, for `limit` cycles at most; false when it gives up.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, int phase, long long limit) {
-  uint32_t ok;
+// Waits for the phase-th completion of an mbarrier, for kWaitCycles at most: a wait that gives up sets
+// the CTA's word `dead`, which ends every other wait at once; the flow stays the same.
+__device__ __forceinline__ void wait_phase(uint32_t bar, int phase, uint32_t dead) {
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .s64 t0, t1;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
+      "{\n .reg .pred p, q;\n .reg .s64 t0, t1;\n .reg .u32 d;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n @p bra DONE;\n"
       " mov.u64 t0, %%clock64;\n"
-      "WAIT:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
+      "WAIT:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n @p bra DONE;\n"
+      " ld.volatile.shared.u32 d, [%2];\n setp.ne.u32 q, d, 0;\n @q bra DONE;\n"
       " mov.u64 t1, %%clock64;\n sub.s64 t1, t1, t0;\n setp.lt.s64 q, t1, %3;\n @q bra WAIT;\n"
-      "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"((uint32_t)phase & 1), "l"(limit)
+      " st.volatile.shared.u32 [%2], 1;\n"
+      "DONE:\n}\n" ::"r"(bar),
+      "r"((uint32_t)phase & 1), "r"(dead), "n"(kWaitCycles)
       : "memory");
-  return ok != 0;
 }
 
 // The lowest n bits; x moved up by n places (down for a negative n). Any n.
@@ -594,6 +594,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(small);
   uint32_t* sTm = reinterpret_cast<uint32_t*>(small + 128);
   volatile int* sDone = reinterpret_cast<volatile int*>(small + 136);   // tiles unpacked
+  volatile int* sDead = reinterpret_cast<volatile int*>(small + 140);   // a wait gave up
   uint32_t* sBad = reinterpret_cast<uint32_t*>(small + 160);   // [8 segments][2] see below
   int* sPre = reinterpret_cast<int*>(small + 256);             // [257]
   float* sMax = reinterpret_cast<float*>(small + 1536);        // [softmax warps][2][16 rows]
@@ -625,6 +626,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
   }
   if (tid == 0) {
     *sDone = 0;
+    *sDead = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(kFull + 8 * i, Sh::KT / 32);
       mbar_init(vFull + 8 * i, Sh::VT / 32);
@@ -652,12 +654,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
     __syncwarp();
     asm volatile("bar.sync %0, 64;" ::"r"(4 + pair) : "memory");
   };
-  // a wait that gives up makes the later ones of its thread end at once, the flow stays the same,
-  // and the layer's status tells
-  long long limit = kWaitCycles;
-  auto wait = [&](uint32_t bar, int phase) {   // until the bar's phase-th completion
-    if (!wait_phase(bar, phase, limit)) limit = 0;
-  };
+  auto wait = [&](uint32_t bar, int phase) { wait_phase(bar, phase, bar0 + 140); };
   auto arrive = [&](uint32_t bar) {   // once per warp
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -1157,9 +1154,9 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
       it0 += t_end - t_begin;
     }
   }
-  if (limit == 0) record_status(a.status, 1);
   fence_before();
   __syncthreads();
+  if (tid == 0 && *sDead) record_status(a.status, 1);
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(Sh::TMEM));
 }
@@ -1193,21 +1190,34 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
     float M = -INFINITY, L = 0.f, o[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-    for (int c = blockIdx.x; c <= c1; ++c) {
-      const int g0 = cta_start(N, P, c);
-      if (g0 == cta_start(N, P, c + 1)) continue;   // a CTA without tiles
-      const float* part = p.part + ((size_t)c * 2 + (g0 >= begin ? 0 : 1)) * ROWS * (D + 2);
-      const float2 ml = *reinterpret_cast<const float2*>(part + 2 * row);
-      const float Mn = fmaxf(M, ml.x);
+    // up to 32 partials at a time: lane l reads the (m, L) of the l-th and weighs it, then every
+    // lane adds its channels of all of them, the loads independent of each other
+    for (int base = blockIdx.x; base <= c1; base += 32) {
+      const int c = base + lane;
+      const int g0 = c <= c1 ? cta_start(N, P, c) : 0;
+      const bool in = c <= c1 && g0 < cta_start(N, P, c + 1);   // a CTA with tiles
+      const int slot = 2 * c + (g0 >= begin ? 0 : 1);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (in) ml = *reinterpret_cast<const float2*>(p.part + (size_t)slot * ROWS * (D + 2) + 2 * row);
+      const float Mn = fmaxf(M, warp_max(ml.x));
       const float fo = M == -INFINITY ? 0.f : ex2(M - Mn);
-      const float fn = ml.x == -INFINITY ? 0.f : ex2(ml.x - Mn);
-      L = fmaf(L, fo, ml.y * fn);
+      const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - Mn);
+      L = fmaf(L, fo, warp_sum(ml.y * w));
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        const float2 x =
-            *reinterpret_cast<const float2*>(part + 2 * ROWS + (size_t)row * D + 64 * i + 2 * lane);
-        o[2 * i] = fmaf(o[2 * i], fo, x.x * fn);
-        o[2 * i + 1] = fmaf(o[2 * i + 1], fo, x.y * fn);
+      for (int i = 0; i < D / 32; ++i) o[i] *= fo;
+      const int n = min(32, c1 - base + 1);
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        const int sj = __shfl_sync(0xffffffffu, slot, j);
+        if (wj == 0.f) continue;   // nothing seen, or no tiles: what lies there does not matter
+        const float* part = p.part + (size_t)sj * ROWS * (D + 2) + 2 * ROWS + (size_t)row * D;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const float2 x = *reinterpret_cast<const float2*>(part + 64 * i + 2 * lane);
+          o[2 * i] = fmaf(x.x, wj, o[2 * i]);
+          o[2 * i + 1] = fmaf(x.y, wj, o[2 * i + 1]);
+        }
       }
       M = Mn;
     }
@@ -1222,12 +1232,18 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
   }
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return n < kMaxSM ? n : kMaxSM;
+// SMs of the current device (cached: the query is not free); 0 on an error.
+int sm_count(int* device) {
+  static int known[64];
+  if (cudaGetDevice(device) != cudaSuccess || *device >= 64) return 0;
+  const int d = *device;
+  if (known[d] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *device) != cudaSuccess)
+      return 0;
+    known[d] = n < kMaxSM ? n : kMaxSM;
+  }
+  return known[d];
 }
 
 // One CTA per SM, more where a CTA's list of segments (one more than its blocks of query rows) would
@@ -1244,7 +1260,8 @@ int rows_of(const fade_config_t* c, int T) {   // query rows of a block: 64 wher
 template <int D, int KB, int VB, int R>
 fade_status_t launch(const fade_config_t* c, const AttnTreeArgs& p, cudaStream_t st) {
   using Sh = Shape<D, KB, VB, R>;
-  const int sms = sm_count();
+  int device = 0;
+  const int sms = sm_count(&device);
   if (sms == 0) return launch_status("fade_tree_attention device query");
   // no more CTAs than the configuration can have tiles (not the present counts: see the header)
   const long long blocks = ceil_div((long long)p.a.T * p.a.G, 64 * R);
@@ -1253,9 +1270,13 @@ fade_status_t launch(const fade_config_t* c, const AttnTreeArgs& p, cudaStream_t
   const long long all = (long long)p.a.B * p.a.H * blocks;
   const int P = tree_ctas(all, most < sms ? (int)most : sms);
   auto kern = tree_attention_kernel<D, KB, VB, R>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM) !=
-      cudaSuccess)
-    return launch_status("fade_tree_attention shared-memory opt-in");
+  static bool opted[64];   // per device: the kernel has its shared memory
+  if (!opted[device]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM) !=
+        cudaSuccess)
+      return launch_status("fade_tree_attention shared-memory opt-in");
+    opted[device] = true;
+  }
   kern<<<P, Sh::THREADS, Sh::SMEM, st>>>(p);
   fade_status_t s = launch_status("fade_tree_attention");
   if (s) return s;

@@ -514,29 +514,38 @@ def fade_measure_fp32_rate(blocks: int, iters: int, sink, stream=None) -> float:
     return ops.value
 
 
-def _tensors(stream, **tensors):
-    """Checks of the drafted-token entry points: every tensor that is given has the dtype, shape
-    and layout asked for (name=(tensor, dtype, shape, strided); strided: only the last dimension
-    has to be contiguous) and, unless the caller passes its own stream, lies on the current CUDA
-    device, whose current stream the call is enqueued on. ValueError otherwise."""
-    import torch
+_torch = None
 
-    device = None
-    for name, (t, dtype, shape, strided) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != getattr(torch, dtype) or tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not "
-                             f"{str(t.dtype).removeprefix('torch.')} {tuple(t.shape)}")
-        if not (t.is_contiguous() if not strided else
-                t.stride(-1) == 1 or t.shape[-1] == 1 or t.numel() == 0):
-            raise ValueError(f"{name} must be contiguous" + (" in its last dimension" if strided
-                                                             else ""))
-        if stream is None:
-            if device is None:
-                device = torch.cuda.current_device() if torch.cuda.is_available() else -1
-            if t.device.type != "cuda" or t.device.index != device:
-                raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+
+def _device(stream):
+    """The device the tensors of a call have to lie on: the current CUDA device, whose current
+    stream the call is enqueued on; None if the caller passes its own stream (and answers for
+    it)."""
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch = torch
+    if stream is not None:
+        return None
+    return _torch.cuda.current_device() if _torch.cuda.is_available() else -2
+
+
+def _tensor(device, name, t, dtype, shape, strided=False):
+    """ValueError unless t (None: not given) has the dtype, shape and layout asked for (strided:
+    only the last dimension has to be contiguous) and lies on the device."""
+    if t is None:
+        return
+    if t.dtype != getattr(_torch, dtype) or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not "
+                         f"{str(t.dtype).removeprefix('torch.')} {tuple(t.shape)}")
+    if strided:
+        if t.stride(-1) != 1 and t.numel():
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
 
 
 def _heads(t):
@@ -549,9 +558,12 @@ def fade_tree_layout(cfg: Config, parents, n_nodes, base_pos, mask, pos, stream=
     """parents i32 [B][T], n_nodes i32 [B] or None, base_pos i32 [B] -> mask i64 [B][T] (the
     64 bits of FADE's u64 masks), pos i32 [B][T]."""
     B, T = parents.shape
-    _tensors(stream, parents=(parents, "int32", (cfg.batch, T), False),
-             n_nodes=(n_nodes, "int32", (B,), False), base_pos=(base_pos, "int32", (B,), False),
-             mask=(mask, "int64", (B, T), False), pos=(pos, "int32", (B, T), False))
+    dev = _device(stream)
+    _tensor(dev, "parents", parents, "int32", (cfg.batch, T))
+    _tensor(dev, "n_nodes", n_nodes, "int32", (B,))
+    _tensor(dev, "base_pos", base_pos, "int32", (B,))
+    _tensor(dev, "mask", mask, "int64", (B, T))
+    _tensor(dev, "pos", pos, "int32", (B, T))
     _check(lib().fade_tree_layout(ctypes.byref(cfg.c()), T, _ptr(parents), _ptr(n_nodes),
                                   _ptr(base_pos), _ptr(mask), _ptr(pos), _stream(stream)))
 
@@ -563,11 +575,14 @@ def fade_qk_norm_rope(cfg: Config, table, max_pos, q, k, q_weight, k_weight, eps
     to pos (i32 [rows][tokens]; None: token t at t) into q_rot and k_rot of the same shapes."""
     n, t = (q if q is not None else k).shape[:2]
     d, hq, h = cfg.head_dim, cfg.num_q_heads, cfg.num_kv_heads
-    _tensors(stream, q=(q, "float16", (n, t, hq, d), True), k=(k, "float16", (n, t, h, d), True),
-             q_rot=(q_rot, "float16", (n, t, hq, d), True),
-             k_rot=(k_rot, "float16", (n, t, h, d), True),
-             q_weight=(q_weight, "float16", (d,), False),
-             k_weight=(k_weight, "float16", (d,), False), pos=(pos, "int32", (n, t), False))
+    dev = _device(stream)
+    _tensor(dev, "q", q, "float16", (n, t, hq, d), True)
+    _tensor(dev, "k", k, "float16", (n, t, h, d), True)
+    _tensor(dev, "q_rot", q_rot, "float16", (n, t, hq, d), True)
+    _tensor(dev, "k_rot", k_rot, "float16", (n, t, h, d), True)
+    _tensor(dev, "q_weight", q_weight, "float16", (d,))
+    _tensor(dev, "k_weight", k_weight, "float16", (d,))
+    _tensor(dev, "pos", pos, "int32", (n, t))
     _check(lib().fade_qk_norm_rope(ctypes.byref(cfg.c()), _ptr(table), max_pos, _heads(q),
                                    _heads(q_rot), _ptr(q_weight), _heads(k), _heads(k_rot),
                                    _ptr(k_weight), eps, _ptr(pos), n, t, _stream(stream)))
@@ -581,11 +596,16 @@ def fade_tree_ws_bytes(cfg: Config, T: int) -> int:
     return n
 
 
-def _tree_tensors(stream, cfg, q_rot, tree_k, tree_v):
+def _tree_tensors(dev, layer, q_rot, tree_k, tree_v, ws):
+    cfg = layer.cfg
     T, d = q_rot.shape[1], cfg.head_dim
     kv = (cfg.batch, T, cfg.num_kv_heads, d)
-    _tensors(stream, q_rot=(q_rot, "float16", (cfg.batch, T, cfg.num_q_heads, d), False),
-             tree_k=(tree_k, "float16", kv, True), tree_v=(tree_v, "float16", kv, True))
+    _tensor(dev, "q_rot", q_rot, "float16", (cfg.batch, T, cfg.num_q_heads, d))
+    _tensor(dev, "tree_k", tree_k, "float16", kv, True)
+    _tensor(dev, "tree_v", tree_v, "float16", kv, True)
+    for name, t in (("the layer", layer.meta), ("ws", ws)):
+        if dev is not None and t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
     return T
 
 
@@ -596,10 +616,12 @@ def fade_tree_attention(layer: TieredLayer, q_rot, tree_k, tree_v, mask, n_nodes
     f32 [B][T][Hq]. ws: a tensor of fade_tree_ws_bytes(cfg, T) bytes."""
     cfg = layer.cfg
     _require_codebook(layer)
-    T = _tree_tensors(stream, cfg, q_rot, tree_k, tree_v)
-    _tensors(stream, mask=(mask, "int64", (cfg.batch, T), False),
-             n_nodes=(n_nodes, "int32", (cfg.batch,), False),
-             out=(out, "float16", q_rot.shape, False), lse=(lse, "float32", q_rot.shape[:3], False))
+    dev = _device(stream)
+    T = _tree_tensors(dev, layer, q_rot, tree_k, tree_v, ws)
+    _tensor(dev, "mask", mask, "int64", (cfg.batch, T))
+    _tensor(dev, "n_nodes", n_nodes, "int32", (cfg.batch,))
+    _tensor(dev, "out", out, "float16", q_rot.shape)
+    _tensor(dev, "lse", lse, "float32", q_rot.shape[:3])
     _check(lib().fade_tree_attention(ctypes.byref(cfg.c()), ctypes.byref(layer.c), T, _ptr(q_rot),
                                      _heads(tree_k), _heads(tree_v), _ptr(mask), _ptr(n_nodes),
                                      _ptr(out), _ptr(lse), _ptr(ws),
@@ -613,9 +635,10 @@ def fade_tree_commit(layer: TieredLayer, q_rot, lse, tree_k, tree_v, path, n_pat
     fade_tree_attention, with a workspace of fade_tree_ws_bytes(cfg, T) bytes."""
     cfg = layer.cfg
     _require_codebook(layer)
-    T = _tree_tensors(stream, cfg, q_rot, tree_k, tree_v)
-    _tensors(stream, path=(path, "int32", (cfg.batch, T), False),
-             lse=(lse, "float32", q_rot.shape[:3], False))
+    dev = _device(stream)
+    T = _tree_tensors(dev, layer, q_rot, tree_k, tree_v, ws)
+    _tensor(dev, "path", path, "int32", (cfg.batch, T))
+    _tensor(dev, "lse", lse, "float32", q_rot.shape[:3])
     lens = np.ascontiguousarray(n_path, np.int32)
     if lens.shape != (cfg.batch,):
         raise ValueError(f"n_path must hold {cfg.batch} lengths")
