@@ -27,146 +27,151 @@ struct NormArgs {
   long long n_items;   // tokens x chunks of both sides
 };
 
-// A group of D/8 lanes takes one vector, lane l its rotation slots 4l .. 4l+3: slot s < rh is the
-// pair (s, s + rh), a slot s >= rh the two unrotated channels 2s and 2s + 1. FULL (rh = D/2): a
-// lane's eight channels are two runs of four, read and written as 8-byte words; otherwise (rh
-// even) as 4-byte words. A pair never leaves its lane, so only the sum of squares is exchanged.
-template <int D, bool FULL>
-__device__ __forceinline__ void load_slots(const uint16_t* x, int l, int rh, float (&a)[4],
-                                           float (&b)[4]) {
-  if constexpr (FULL) {
-    const uint2 lo = *reinterpret_cast<const uint2*>(x + 4 * l);
-    const uint2 hi = *reinterpret_cast<const uint2*>(x + D / 2 + 4 * l);
-    const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(&lo.x));
-    const float2 l1 = __half22float2(*reinterpret_cast<const __half2*>(&lo.y));
-    const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&hi.x));
-    const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&hi.y));
-    a[0] = l0.x; a[1] = l0.y; a[2] = l1.x; a[3] = l1.y;
-    b[0] = h0.x; b[1] = h0.y; b[2] = h1.x; b[3] = h1.y;
-  } else {
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {   // two slots: both rotated or neither (rh is even)
-      const int s = 4 * l + 2 * p;
-      const uint32_t u = *reinterpret_cast<const uint32_t*>(x + (s < rh ? s : 2 * s));
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(x + (s < rh ? s + rh : 2 * s + 2));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
-      const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&v));
-      a[2 * p] = f.x; a[2 * p + 1] = f.y;
-      b[2 * p] = g.x; b[2 * p + 1] = g.y;
-    }
-  }
-}
-
 __device__ __forceinline__ uint32_t pack_h2(float x, float y) {
   return f2h(x) | ((uint32_t)f2h(y) << 16);
 }
+__device__ __forceinline__ void unpack_h2(uint32_t u, float* f) {
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&u));
+  f[0] = v.x;
+  f[1] = v.y;
+}
 
-template <int D, bool FULL>
-__device__ __forceinline__ void store_slots(uint16_t* y, int l, int rh, const float (&a)[4],
-                                            const float (&b)[4]) {
-  if constexpr (FULL) {
-    *reinterpret_cast<uint2*>(y + 4 * l) = make_uint2(pack_h2(a[0], a[1]), pack_h2(a[2], a[3]));
-    *reinterpret_cast<uint2*>(y + D / 2 + 4 * l) =
-        make_uint2(pack_h2(b[0], b[1]), pack_h2(b[2], b[3]));
+// A group of D / (2 SL) lanes takes one vector, lane l its rotation slots SL l .. SL l + SL - 1: slot
+// s < rh is the pair (s, s + rh), a slot s >= rh the two unrotated channels 2s and 2s + 1. A pair
+// never leaves its lane, so only the sum of squares is exchanged. SL = 8 (rh a multiple of 8): a
+// lane's slots are all rotated or all not, its 16 channels two 16-byte words; SL = 4 (rh even): slots
+// go by twos, in 4-byte words.
+template <int SL>
+__device__ __forceinline__ void load_slots(const uint16_t* x, int l, int rh, float (&a)[SL],
+                                           float (&b)[SL]) {
+  if constexpr (SL == 8) {
+    const int s = 8 * l;
+    const uint4 lo = *reinterpret_cast<const uint4*>(x + (s < rh ? s : 2 * s));
+    const uint4 hi = *reinterpret_cast<const uint4*>(x + (s < rh ? s + rh : 2 * s + 8));
+    unpack_h2(lo.x, a); unpack_h2(lo.y, a + 2); unpack_h2(lo.z, a + 4); unpack_h2(lo.w, a + 6);
+    unpack_h2(hi.x, b); unpack_h2(hi.y, b + 2); unpack_h2(hi.z, b + 4); unpack_h2(hi.w, b + 6);
   } else {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int s = 4 * l + 2 * p;
-      *reinterpret_cast<uint32_t*>(y + (s < rh ? s : 2 * s)) = pack_h2(a[2 * p], a[2 * p + 1]);
-      *reinterpret_cast<uint32_t*>(y + (s < rh ? s + rh : 2 * s + 2)) =
-          pack_h2(b[2 * p], b[2 * p + 1]);
+    for (int p = 0; p < SL; p += 2) {   // two slots: both rotated or neither
+      const int s = SL * l + p;
+      unpack_h2(*reinterpret_cast<const uint32_t*>(x + (s < rh ? s : 2 * s)), a + p);
+      unpack_h2(*reinterpret_cast<const uint32_t*>(x + (s < rh ? s + rh : 2 * s + 2)), b + p);
+    }
+  }
+}
+template <int SL>
+__device__ __forceinline__ void store_slots(uint16_t* y, int l, int rh, const float (&a)[SL],
+                                            const float (&b)[SL]) {
+  if constexpr (SL == 8) {
+    const int s = 8 * l;
+    *reinterpret_cast<uint4*>(y + (s < rh ? s : 2 * s)) =
+        make_uint4(pack_h2(a[0], a[1]), pack_h2(a[2], a[3]), pack_h2(a[4], a[5]), pack_h2(a[6], a[7]));
+    *reinterpret_cast<uint4*>(y + (s < rh ? s + rh : 2 * s + 8)) =
+        make_uint4(pack_h2(b[0], b[1]), pack_h2(b[2], b[3]), pack_h2(b[4], b[5]), pack_h2(b[6], b[7]));
+  } else {
+#pragma unroll
+    for (int p = 0; p < SL; p += 2) {
+      const int s = SL * l + p;
+      *reinterpret_cast<uint32_t*>(y + (s < rh ? s : 2 * s)) = pack_h2(a[p], a[p + 1]);
+      *reinterpret_cast<uint32_t*>(y + (s < rh ? s + rh : 2 * s + 2)) = pack_h2(b[p], b[p + 1]);
     }
   }
 }
 
-// One warp per (token, chunk): a chunk is U rounds of 256/D vectors of one side. The table row and
-// the weights stay in registers over the rounds, and every round's loads are issued first.
-template <int D, bool FULL, int U>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int LV = D / 8, NV = 32 / LV;   // lanes a vector, vectors a round
-  const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (item >= a.n_items) return;   // uniform over the warp
+// One warp per (token, chunk): a chunk is U rounds of 64 SL / D vectors of one side, which share the
+// token's table row and the weights. Bound by DRAM (2 bytes read and written a channel), so what
+// counts is bytes in flight: every load of a warp is issued before the first is waited for, 64
+// registers keep 32 warps an SM. 4 x 8191 tokens of 32 + 8 heads of 128 (684 MB): 150 us, 4.56 TB/s,
+// 0.68 of the copy rate; one round a warp 166 us, four (2 CTAs' registers) 210 us, CTAs of 256
+// threads 155 us, 8-byte loads (4 slots a lane) 185 us.
+constexpr int kNormThreads = 128, kNormRounds = 2;
+template <int D, int SL, int U>
+__global__ void __launch_bounds__(kNormThreads, 8) qk_norm_rope_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int LV = D / (2 * SL), NV = 32 / LV;   // lanes a vector, vectors a round
+  const uint32_t item = blockIdx.x * (kNormThreads / 32u) + (threadIdx.x >> 5);   // below 2^31 (the host checks)
+  if (item >= (uint32_t)a.n_items) return;   // uniform over the warp
   const int lane = threadIdx.x & 31, l = lane % LV, sub = lane / LV;
-  const int per = a.q.chunks + a.k.chunks;
-  const long long tok = item / per;
-  const int c = (int)(item % per);
+  const uint32_t per = a.q.chunks + a.k.chunks;
+  const uint32_t tok = item / per;
+  const int c = (int)(item - tok * per);
   const bool isq = c < a.q.chunks;
   const NormSide& s = isq ? a.q : a.k;
-  const long long row = tok / a.n_tokens, t = tok % a.n_tokens;
+  const uint32_t row = tok / (uint32_t)a.n_tokens, t = tok - row * (uint32_t)a.n_tokens;
   const int h0 = (isq ? c : c - a.q.chunks) * (U * NV) + sub;
   const uint16_t* x = s.x + row * s.xr + t * s.xt;
   uint16_t* y = s.y + row * s.yr + t * s.yt;
-  float A[U][4], B[U][4];
+  // the position and the lane's part of the table row are asked for before anything is waited for
+  const float* tab = nullptr;
+  if (a.table) {
+    const int p = min(max(a.pos ? a.pos[tok] : (int)t, 0), a.max_pos - 1);
+    tab = a.table + (size_t)p * D + 2 * SL * l;
+  }
+  float A[U][SL], B[U][SL];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int h = h0 + u * NV;
     if (h < s.heads) {
-      load_slots<D, FULL>(x + h * s.xh, l, a.rh, A[u], B[u]);
+      load_slots<SL>(x + h * s.xh, l, a.rh, A[u], B[u]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) A[u][e] = B[u][e] = 0.f;
+      for (int e = 0; e < SL; ++e) A[u][e] = B[u][e] = 0.f;
     }
   }
-  float wa[4], wb[4], cs[4], sn[4];
-  if (s.w) load_slots<D, FULL>(s.w, l, a.rh, wa, wb);
-  if (a.table) {
-    long long p = a.pos ? a.pos[tok] : t;
-    p = min(max(p, 0LL), (long long)a.max_pos - 1);
+  if (tab && SL * l < a.rh) asm volatile("prefetch.global.L1 [%0];" ::"l"(tab));
+  if (s.w) {
+    float wa[SL], wb[SL];
+    load_slots<SL>(s.w, l, a.rh, wa, wb);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {   // block 2l + e of the table row: two pairs
-      const int sl = 4 * l + 2 * e;
-      float4 r = make_float4(1.f, 1.f, 0.f, 0.f);
-      if (FULL || sl < a.rh)
-        r = *reinterpret_cast<const float4*>(a.table + p * D + 2 * sl);
-      cs[2 * e] = r.x; cs[2 * e + 1] = r.y;
-      sn[2 * e] = r.z; sn[2 * e + 1] = r.w;
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * NV;
-    if (s.w) {
+    for (int u = 0; u < U; ++u) {
       float q = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) q = fmaf(A[u][e], A[u][e], fmaf(B[u][e], B[u][e], q));
+      for (int e = 0; e < SL; ++e) q = fmaf(A[u][e], A[u][e], fmaf(B[u][e], B[u][e], q));
 #pragma unroll
       for (int o = LV / 2; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
       const float r = rsqrtf(fmaf(q, 1.0f / D, a.eps));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < SL; ++e) {
         A[u][e] *= r * wa[e];
         B[u][e] *= r * wb[e];
       }
     }
-    if (a.table) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (FULL || 4 * l + e < a.rh) {
-          const float p = A[u][e], q = B[u][e];
-          rotate_pair(p, q, cs[e], sn[e], A[u][e], B[u][e]);
-        }
-    }
-    if (h < s.heads) store_slots<D, FULL>(y + h * s.yh, l, a.rh, A[u], B[u]);
   }
+  if (tab) {
+#pragma unroll
+    for (int e = 0; e < SL; e += 2) {   // a block of the table row: two pairs
+      if ((SL == 8 ? SL * l : SL * l + e) >= a.rh) continue;
+      const float4 cs = *reinterpret_cast<const float4*>(tab + 2 * e);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float p0 = A[u][e], q0 = B[u][e], p1 = A[u][e + 1], q1 = B[u][e + 1];
+        rotate_pair(p0, q0, cs.x, cs.z, A[u][e], B[u][e]);
+        rotate_pair(p1, q1, cs.y, cs.w, A[u][e + 1], B[u][e + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (h0 + u * NV < s.heads) store_slots<SL>(y + (h0 + u * NV) * s.yh, l, a.rh, A[u], B[u]);
 }
 
-template <int D, bool FULL>
+template <int D, int SL>
 void launch(const NormArgs& a0, long long tokens, cudaStream_t st) {
-  constexpr int NV = 256 / D;
+  constexpr int NV = 64 * SL / D;
   NormArgs a = a0;
   auto items = [&](int per) {
     a.q.chunks = a.q.x ? ceil_div(a.q.heads, per) : 0;
     a.k.chunks = a.k.x ? ceil_div(a.k.heads, per) : 0;
     a.n_items = tokens * (a.q.chunks + a.k.chunks);
   };
-  items(4 * NV);
-  const bool deep = a.n_items >= 4096;
+  items(kNormRounds * NV);
+  // one round a warp where two would leave schedulers without a warp (152 SMs x 32 warps)
+  const bool deep = a.n_items >= 4864;
   if (!deep) items(NV);
-  const unsigned grid = (unsigned)((a.n_items + 7) / 8);
+  const unsigned grid = (unsigned)ceil_div(a.n_items, kNormThreads / 32);
   if (deep)
-    qk_norm_rope_kernel<D, FULL, 4><<<grid, 256, 0, st>>>(a);
+    qk_norm_rope_kernel<D, SL, kNormRounds><<<grid, kNormThreads, 0, st>>>(a);
   else
-    qk_norm_rope_kernel<D, FULL, 1><<<grid, 256, 0, st>>>(a);
+    qk_norm_rope_kernel<D, SL, 1><<<grid, kNormThreads, 0, st>>>(a);
 }
 
 bool side_strides_ok(const fade_heads_t* h) {
@@ -242,10 +247,10 @@ extern "C" fade_status_t fade_qk_norm_rope(const fade_config_t* c, const float* 
   a.rh = rope ? rotary_width(c) / 2 : c->head_dim / 2;
   a.n_tokens = n_tokens;
   cudaStream_t s = as_stream(stream);
-  const bool full = a.rh == c->head_dim / 2;
+  const bool wide = a.rh % 8 == 0;
   if (c->head_dim == 64)
-    full ? launch<64, true>(a, tokens, s) : launch<64, false>(a, tokens, s);
+    wide ? launch<64, 8>(a, tokens, s) : launch<64, 4>(a, tokens, s);
   else
-    full ? launch<128, true>(a, tokens, s) : launch<128, false>(a, tokens, s);
+    wide ? launch<128, 8>(a, tokens, s) : launch<128, 4>(a, tokens, s);
   return launch_status("fade_qk_norm_rope");
 }
