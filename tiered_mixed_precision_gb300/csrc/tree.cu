@@ -78,71 +78,198 @@ __global__ void __launch_bounds__(FADE_TREE_MAX_NODES)
 }
 
 // ----------------------------------------------------------------- commit
-// The path's attention mass: one warp per token the unit holds or commits, lane l owning channels
-// l, l + 32, .. of its key (read once); per path node the G dot products, p = exp(s - lse) summed
-// over the heads and folded into the running score in path order. Path token j (score 0) takes
-// the nodes j, j + 1, .. of the path.
+// The path's attention mass. Mathematics: with the path's nodes 0 .. n-1 and their G query rows as
+// columns c (node i = c / G), token j's score becomes decay^k score + sum_c w_c exp(s_jc - lse_c),
+// k the nodes that see it (all n; n - j for the j-th path token, which starts at 0), w_c = 1 and
+// decay = 1 (H2O) or w_c = (1 - delta) delta^(n-1-i) and decay = delta (EMA): the accumulation node by
+// node, written as one sum.
+//
+// Products on mma.sync: 16 tokens are the rows, 8 columns the columns of an instruction. Few columns
+// and every key read once make this a stream over the codes, not a contraction for tcgen05; and it
+// keeps the keys exact: codes are exact fp16 integers (halved), each 32-channel group is summed on
+// its own and meets its scale in fp32. Thread (row g = lane / 4, t = lane % 4) holds channels 8t ..
+// 8t+7 of every group of rows g and g + 8, as the pairs (8t+i, 8t+i+4) its code word unpacks into; the
+// columns are laid out in shared memory in the same order.
+constexpr int kScoreCols = 64;      // columns staged at a time
+constexpr int kScoreTiles = 2;      // 16-token tiles a warp
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t sub_h2(uint32_t x, uint32_t y) {
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Channels 8t .. 8t+7 of a group as the pairs (i, i + 4), i = 0 .. 3: half the codes of a middle row,
+// or the values of an fp16 row.
+template <int KB>
+__device__ __forceinline__ void code_pairs(const uint8_t* group, int t, uint32_t (&p)[4]) {
+  if constexpr (KB == 4) {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(group) + t), h = w >> 8;
+    p[0] = sub_h2((w & 0x000f000fu) ^ 0x60086008u, 0x60086008u);
+    p[1] = sub_h2((w & 0x00f000f0u) ^ 0x50805080u, 0x50805080u);
+    p[2] = sub_h2((h & 0x000f000fu) ^ 0x60086008u, 0x60086008u);
+    p[3] = sub_h2((h & 0x00f000f0u) ^ 0x50805080u, 0x50805080u);
+  } else {
+    const uint32_t v = __ldg(reinterpret_cast<const uint16_t*>(group) + t);
+    const uint32_t w = v | (v >> 8) << 16;   // crumbs 0..3 in the low half, 4..7 in the high one
+    p[0] = sub_h2((w & 0x00030003u) ^ 0x60026002u, 0x60026002u);
+    p[1] = sub_h2((w & 0x000c000cu) ^ 0x58085808u, 0x58085808u);
+    p[2] = sub_h2((w & 0x00300030u) ^ 0x50205020u, 0x50205020u);
+    p[3] = sub_h2((w & 0x00c000c0u) ^ 0x48804880u, 0x48804880u);
+  }
+}
+__device__ __forceinline__ void value_pairs(uint4 x, uint32_t (&p)[4]) {
+  p[0] = prmt(x.x, x.z, 0x5410);
+  p[1] = prmt(x.x, x.z, 0x7632);
+  p[2] = prmt(x.y, x.w, 0x5410);
+  p[3] = prmt(x.y, x.w, 0x7632);
+}
+
 template <int D, int KB>
 __global__ void __launch_bounds__(256) tree_scores_kernel(TreeArgs a, RowLens lens, int policy,
-                                                          float decay,
+                                                          float delta,
                                                           const float* __restrict__ lse,
                                                           const int32_t* __restrict__ path,
                                                           float* __restrict__ path_sc) {
+  constexpr int GR = D / 32;
+  constexpr float kLog2e = 1.4426950408889634f;
+  __shared__ uint4 sq[kScoreCols][GR][4];   // column's pairs of group, t
+  __shared__ float sw[kScoreCols], sl[kScoreCols];
   const int h = blockIdx.y, b = blockIdx.z, unit = b * a.H + h;
   const int n_path = lens.v[b];
-  if (n_path == 0) return;
+  if (n_path == 0) return;   // uniform per CTA, as is the next
   const int32_t* m = a.meta + unit * FADE_META_FIELDS;
   const int n_sink = m[FADE_META_N_SINK], n_mid = m[FADE_META_N_MID];
   const int n_rec = m[FADE_META_N_RECENT], head = m[FADE_META_HEAD], cur = m[FADE_META_CUR];
-  const int held = n_sink + n_mid + n_rec;
-  const int lane = threadIdx.x & 31;
-  const float scale = rsqrtf((float)D);
-  for (int j = blockIdx.x * 8 + (threadIdx.x >> 5); j < held + n_path; j += gridDim.x * 8) {
-    float k[D / 32];
-    float* sc;
-    int first = 0;
-    if (j >= n_sink && j < n_sink + n_mid) {
-      const size_t r = (size_t)unit * a.C + (j - n_sink);
-      const uint8_t* codes = a.mk[cur] + r * (D * KB / 8);
-      const uint16_t* scl = a.mks[cur] + r * (D / kGroup);
+  const int held = n_sink + n_mid + n_rec, total = held + n_path;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int tok0 = (blockIdx.x * 8 + warp) * (16 * kScoreTiles);
+  if (blockIdx.x * 8 * 16 * kScoreTiles >= total) return;
+  const float decay = policy == FADE_EVICT_H2O ? 1.f : delta;
+  const float gain = policy == FADE_EVICT_H2O ? 1.f : 1.f - delta;
+  float sum[kScoreTiles][2] = {};
+  const int cols = n_path * a.G;
+  for (int c0 = 0; c0 < cols; c0 += kScoreCols) {
+    if (c0) __syncthreads();
+    for (int i = threadIdx.x; i < kScoreCols * GR * 4; i += 256) {
+      const int c = i / (GR * 4), gr = (i / 4) % GR, col = c0 + c;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (col < cols) {
+        const int node = tree_node(a, path, b, col >> a.log_g);
+        const size_t q = (((size_t)b * a.T + node) * a.Hq + h * a.G + (col & (a.G - 1)));
+        uint32_t p[4];
+        value_pairs(__ldg(reinterpret_cast<const uint4*>(a.q + q * D + 32 * gr + 8 * (i & 3))), p);
+        x = make_uint4(p[0], p[1], p[2], p[3]);
+        if (gr == 0 && (i & 3) == 0) {
+          float w = gain;
+          for (int e = col >> a.log_g; e < n_path - 1; ++e) w *= decay;
+          sw[c] = w;
+          sl[c] = lse[q] * kLog2e;
+        }
+      } else if (gr == 0 && (i & 3) == 0) {
+        sw[c] = 0.f;
+        sl[c] = INFINITY;   // a probability of 0
+      }
+      sq[c][gr][i & 3] = x;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int tile = 0; tile < kScoreTiles; ++tile) {
+      const int j0 = tok0 + 16 * tile;
+      if (j0 >= total) break;   // uniform over the warp
+      // rows g and g + 8 of the tile: their pairs, and twice their scales
+      uint32_t k[2][GR][4];
+      float sc[2][GR];
+      int first[2];   // the first node that sees the token
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e)
-        k[e] = (float)unpack_code<KB>(codes, 32 * e + lane) * h2f(scl[e]);
-      sc = a.mid_sc[cur] + r;
-    } else {
-      const uint16_t* x;
+      for (int r = 0; r < 2; ++r) {
+        const int j = min(j0 + g + 8 * r, total - 1);
+        first[r] = 0;
+        if (j >= n_sink && j < n_sink + n_mid) {
+          const size_t row = (size_t)unit * a.C + (j - n_sink);
+#pragma unroll
+          for (int e = 0; e < GR; ++e) {
+            code_pairs<KB>(a.mk[cur] + (row * GR + e) * (4 * KB), t, k[r][e]);
+            sc[r][e] = 2.f * h2f(__ldg(a.mks[cur] + row * GR + e));
+          }
+        } else {
+          const uint16_t* x;
+          if (j < n_sink) {
+            x = a.sink_k + ((size_t)unit * a.S + j) * D;
+          } else if (j < held) {
+            x = a.rec_k + ((size_t)unit * a.W + (head + (j - n_sink - n_mid)) % a.W) * D;
+          } else {
+            first[r] = j - held;
+            x = a.tk.x + b * a.tk.row_stride + tree_node(a, path, b, first[r]) * a.tk.token_stride +
+                h * a.tk.head_stride;
+          }
+#pragma unroll
+          for (int e = 0; e < GR; ++e) {
+            value_pairs(*reinterpret_cast<const uint4*>(x + 32 * e + 8 * t), k[r][e]);
+            sc[r][e] = 1.f;
+          }
+        }
+      }
+      const int n = min(kScoreCols, cols - c0);
+#pragma unroll 1
+      for (int nb = 0; nb < n; nb += 8) {
+        float s[4] = {};
+#pragma unroll
+        for (int e = 0; e < GR; ++e) {
+          const uint4 q = sq[nb + g][e][t];   // column g of the eight: the B operand's column
+          float d[4] = {};
+          const uint32_t a0[4] = {k[0][e][0], k[1][e][0], k[0][e][1], k[1][e][1]};
+          const uint32_t a1[4] = {k[0][e][2], k[1][e][2], k[0][e][3], k[1][e][3]};
+          mma_16816(d, a0, q.x, q.y);
+          mma_16816(d, a1, q.z, q.w);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) s[v] = fmaf(d[v], sc[v >> 1][e], s[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {   // row g + 8 (v / 2), column 2t + v % 2
+          const int c = nb + 2 * t + (v & 1);
+          const float w = ((c0 + c) >> a.log_g) >= first[v >> 1] ? sw[c] : 0.f;
+          const float p = exp2f(fmaf(s[v], kLog2e * rsqrtf((float)D), -sl[c]));
+          if (w != 0.f) {
+            if (tile == 0) sum[0][v >> 1] = fmaf(w, p, sum[0][v >> 1]);
+            else sum[1][v >> 1] = fmaf(w, p, sum[1][v >> 1]);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int tile = 0; tile < kScoreTiles; ++tile) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float v = sum[tile][r];
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      v += __shfl_xor_sync(0xffffffffu, v, 2);
+      const int j = tok0 + 16 * tile + g + 8 * r;
+      if (t != 0 || j >= total) continue;
+      float* at;
+      float old = 0.f, keep = 1.f;
       if (j < n_sink) {
-        x = a.sink_k + ((size_t)unit * a.S + j) * D;
-        sc = a.sink_sc + (size_t)unit * a.S + j;
+        at = a.sink_sc + (size_t)unit * a.S + j;
+      } else if (j < n_sink + n_mid) {
+        at = a.mid_sc[cur] + (size_t)unit * a.C + (j - n_sink);
       } else if (j < held) {
-        const int slot = (head + (j - n_sink - n_mid)) % a.W;
-        x = a.rec_k + ((size_t)unit * a.W + slot) * D;
-        sc = a.rec_sc + (size_t)unit * a.W + slot;
+        at = a.rec_sc + (size_t)unit * a.W + (head + (j - n_sink - n_mid)) % a.W;
       } else {
-        first = j - held;
-        x = a.tk.x + b * a.tk.row_stride + tree_node(a, path, b, first) * a.tk.token_stride +
-            h * a.tk.head_stride;
-        sc = path_sc + (size_t)unit * a.T + first;
+        at = path_sc + (size_t)unit * a.T + (j - held);
       }
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) k[e] = h2f(x[32 * e + lane]);
-    }
-    float score = j < held ? *sc : 0.f;
-    for (int i = first; i < n_path; ++i) {
-      const int node = tree_node(a, path, b, i);
-      const size_t q0 = ((size_t)b * a.T + node) * a.Hq + h * a.G;
-      float mass = 0.f;
-      for (int g = 0; g < a.G; ++g) {
-        const uint16_t* q = a.q + (q0 + g) * D;
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) s = fmaf(h2f(q[32 * e + lane]), k[e], s);
-        s = warp_sum(s);
-        mass += __expf(fmaf(s, scale, -lse[q0 + g]));
+      if (j < held) {
+        old = *at;
+        for (int e = 0; e < n_path; ++e) keep *= decay;
       }
-      score = policy == FADE_EVICT_H2O ? score + mass : decay * score + (1.f - decay) * mass;
+      *at = fmaf(old, keep, v);
     }
-    if (lane == 0) *sc = score;
   }
 }
 
@@ -228,8 +355,9 @@ template <int D, int KB>
 fade_status_t launch_scores(const fade_config_t* c, const TreeArgs& a, const RowLens& lens,
                             int max_tokens, const float* lse, const int32_t* path, float* path_sc,
                             cudaStream_t st) {
-  tree_scores_kernel<D, KB><<<dim3(ceil_div(max_tokens, 32), c->num_kv_heads, c->batch), 256, 0,
-                              st>>>(a, lens, c->policy, c->ema_decay, lse, path, path_sc);
+  tree_scores_kernel<D, KB>
+      <<<dim3(ceil_div(max_tokens, 8 * 16 * kScoreTiles), c->num_kv_heads, c->batch), 256, 0, st>>>(
+          a, lens, c->policy, c->ema_decay, lse, path, path_sc);
   return launch_status("fade_tree_commit scores");
 }
 
