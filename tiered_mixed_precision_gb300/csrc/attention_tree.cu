@@ -1184,8 +1184,8 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
   if (g == begin || cta_start(N, P, blockIdx.x) > begin) return;
   const int c1 = cta_of(N, P, end - 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int row = blockIdx.y * 16 + warp; row < blockIdx.y * 16 + 16; row += 8) {
-    const int rr = qb * ROWS + row;
+  {
+    const int row = blockIdx.y * 8 + warp, rr = qb * ROWS + row;
     if (rr >= rt.n * a.G) return;
     float M = -INFINITY, L = 0.f, o[D / 32];
 #pragma unroll
@@ -1206,17 +1206,17 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) o[i] *= fo;
       const int n = min(32, c1 - base + 1);
-#pragma unroll 4
+#pragma unroll 8
       for (int j = 0; j < n; ++j) {
         const float wj = __shfl_sync(0xffffffffu, w, j);
         const int sj = __shfl_sync(0xffffffffu, slot, j);
-        if (wj == 0.f) continue;   // nothing seen, or no tiles: what lies there does not matter
         const float* part = p.part + (size_t)sj * ROWS * (D + 2) + 2 * ROWS + (size_t)row * D;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
           const float2 x = *reinterpret_cast<const float2*>(part + 64 * i + 2 * lane);
-          o[2 * i] = fmaf(x.x, wj, o[2 * i]);
-          o[2 * i + 1] = fmaf(x.y, wj, o[2 * i + 1]);
+          // (weight 0: nothing seen, or no tiles; what lies there does not matter)
+          o[2 * i] = wj == 0.f ? o[2 * i] : fmaf(x.x, wj, o[2 * i]);
+          o[2 * i + 1] = wj == 0.f ? o[2 * i + 1] : fmaf(x.y, wj, o[2 * i + 1]);
         }
       }
       M = Mn;
@@ -1282,7 +1282,7 @@ fade_status_t launch(const fade_config_t* c, const AttnTreeArgs& p, cudaStream_t
   if (s) return s;
   if (P == 1) return FADE_OK;
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(P - 1, 4 * R);
+  lc.gridDim = dim3(P - 1, 8 * R);
   lc.blockDim = dim3(256);
   lc.stream = st;
   cudaLaunchAttribute at[1];

@@ -90,8 +90,7 @@ __global__ void __launch_bounds__(FADE_TREE_MAX_NODES)
 // its own and meets its scale in fp32. Thread (row g = lane / 4, t = lane % 4) holds channels 8t ..
 // 8t+7 of every group of rows g and g + 8, as the pairs (8t+i, 8t+i+4) its code word unpacks into; the
 // columns are laid out in shared memory in the same order.
-constexpr int kScoreCols = 64;      // columns staged at a time
-constexpr int kScoreTiles = 2;      // 16-token tiles a warp
+constexpr int kScoreCols = 64;   // columns staged at a time: longer paths take more passes
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {
@@ -105,19 +104,23 @@ __device__ __forceinline__ uint32_t sub_h2(uint32_t x, uint32_t y) {
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Channels 8t .. 8t+7 of a group as the pairs (i, i + 4), i = 0 .. 3: half the codes of a middle row,
-// or the values of an fp16 row.
+// Channels 8t .. 8t+7 of a group as the pairs (i, i + 4), i = 0 .. 3: half the codes of a middle row's
+// word, or the values of an fp16 row.
 template <int KB>
-__device__ __forceinline__ void code_pairs(const uint8_t* group, int t, uint32_t (&p)[4]) {
+__device__ __forceinline__ uint32_t code_word(const uint8_t* group, int t) {
+  if constexpr (KB == 4) return __ldg(reinterpret_cast<const uint32_t*>(group) + t);
+  return __ldg(reinterpret_cast<const uint16_t*>(group) + t);
+}
+template <int KB>
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&p)[4]) {
   if constexpr (KB == 4) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(group) + t), h = w >> 8;
+    const uint32_t h = w >> 8;
     p[0] = sub_h2((w & 0x000f000fu) ^ 0x60086008u, 0x60086008u);
     p[1] = sub_h2((w & 0x00f000f0u) ^ 0x50805080u, 0x50805080u);
     p[2] = sub_h2((h & 0x000f000fu) ^ 0x60086008u, 0x60086008u);
     p[3] = sub_h2((h & 0x00f000f0u) ^ 0x50805080u, 0x50805080u);
   } else {
-    const uint32_t v = __ldg(reinterpret_cast<const uint16_t*>(group) + t);
-    const uint32_t w = v | (v >> 8) << 16;   // crumbs 0..3 in the low half, 4..7 in the high one
+    w |= (w >> 8) << 16;   // crumbs 0..3 in the low half, 4..7 in the high one
     p[0] = sub_h2((w & 0x00030003u) ^ 0x60026002u, 0x60026002u);
     p[1] = sub_h2((w & 0x000c000cu) ^ 0x58085808u, 0x58085808u);
     p[2] = sub_h2((w & 0x00300030u) ^ 0x50205020u, 0x50205020u);
@@ -149,15 +152,40 @@ __global__ void __launch_bounds__(256) tree_scores_kernel(TreeArgs a, RowLens le
   const int n_rec = m[FADE_META_N_RECENT], head = m[FADE_META_HEAD], cur = m[FADE_META_CUR];
   const int held = n_sink + n_mid + n_rec, total = held + n_path;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int tok0 = (blockIdx.x * 8 + warp) * (16 * kScoreTiles);
-  if (blockIdx.x * 8 * 16 * kScoreTiles >= total) return;
+  // the CTA's tiles of 16 tokens, taken by its warps in turn
+  const int tiles = (total + 15) / 16;
+  const int tile0 = (int)((long long)tiles * blockIdx.x / gridDim.x);
+  const int tile1 = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x);
+  if (tile0 == tile1) return;
   const float decay = policy == FADE_EVICT_H2O ? 1.f : delta;
   const float gain = policy == FADE_EVICT_H2O ? 1.f : 1.f - delta;
-  float sum[kScoreTiles][2] = {};
   const int cols = n_path * a.G;
+  float keep = 1.f;
+  for (int e = 0; e < n_path; ++e) keep *= decay;
+  const uint8_t* codes = a.mk[cur] + (size_t)unit * a.C * GR * (4 * KB);
+  const uint16_t* scales = a.mks[cur] + (size_t)unit * a.C * GR;
+  // the words and scales of rows g and g + 8 of a tile, read as if they were middle tokens (the
+  // nearest one where they are not: those rows are read again from their tier)
+  uint32_t w[2][GR];
+  uint2 sc2[2];
+  auto fetch = [&](int tile) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int i = min(max(16 * tile + g + 8 * r - n_sink, 0), max(n_mid - 1, 0));
+      const size_t row = (size_t)i * GR;
+#pragma unroll
+      for (int e = 0; e < GR; ++e) w[r][e] = code_word<KB>(codes + (row + e) * (4 * KB), t);
+      if constexpr (GR == 4)
+        sc2[r] = __ldg(reinterpret_cast<const uint2*>(scales + row));
+      else
+        sc2[r] = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(scales + row)), 0u);
+    }
+  };
   for (int c0 = 0; c0 < cols; c0 += kScoreCols) {
+    const int n = min(kScoreCols, cols - c0);
+    if (tile0 + warp < tile1) fetch(tile0 + warp);
     if (c0) __syncthreads();
-    for (int i = threadIdx.x; i < kScoreCols * GR * 4; i += 256) {
+    for (int i = threadIdx.x; i < (n + 7) / 8 * 8 * GR * 4; i += 256) {
       const int c = i / (GR * 4), gr = (i / 4) % GR, col = c0 + c;
       uint4 x = make_uint4(0u, 0u, 0u, 0u);
       if (col < cols) {
@@ -167,47 +195,51 @@ __global__ void __launch_bounds__(256) tree_scores_kernel(TreeArgs a, RowLens le
         value_pairs(__ldg(reinterpret_cast<const uint4*>(a.q + q * D + 32 * gr + 8 * (i & 3))), p);
         x = make_uint4(p[0], p[1], p[2], p[3]);
         if (gr == 0 && (i & 3) == 0) {
-          float w = gain;
-          for (int e = col >> a.log_g; e < n_path - 1; ++e) w *= decay;
-          sw[c] = w;
+          float wc = gain;
+          for (int e = col >> a.log_g; e < n_path - 1; ++e) wc *= decay;
+          sw[c] = wc;
           sl[c] = lse[q] * kLog2e;
         }
       } else if (gr == 0 && (i & 3) == 0) {
-        sw[c] = 0.f;
-        sl[c] = INFINITY;   // a probability of 0
+        sw[c] = 0.f;   // left out of the sum
+        sl[c] = 0.f;
       }
       sq[c][gr][i & 3] = x;
     }
     __syncthreads();
 #pragma unroll 1
-    for (int tile = 0; tile < kScoreTiles; ++tile) {
-      const int j0 = tok0 + 16 * tile;
-      if (j0 >= total) break;   // uniform over the warp
-      // rows g and g + 8 of the tile: their pairs, and twice their scales
+    for (int tile = tile0 + warp; tile < tile1; tile += 8) {
+      // rows g and g + 8 of the tile: their pairs and scales (twice, the codes are halved), the
+      // score's place and the first node that sees the token
       uint32_t k[2][GR][4];
-      float sc[2][GR];
-      int first[2];   // the first node that sees the token
+      float sc[2][GR], *at[2];
+      int first[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int j = min(j0 + g + 8 * r, total - 1);
+        const int j = min(16 * tile + g + 8 * r, total - 1);
         first[r] = 0;
         if (j >= n_sink && j < n_sink + n_mid) {
-          const size_t row = (size_t)unit * a.C + (j - n_sink);
+          at[r] = a.mid_sc[cur] + (size_t)unit * a.C + (j - n_sink);
+          const uint32_t sw2[2] = {sc2[r].x, sc2[r].y};
 #pragma unroll
           for (int e = 0; e < GR; ++e) {
-            code_pairs<KB>(a.mk[cur] + (row * GR + e) * (4 * KB), t, k[r][e]);
-            sc[r][e] = 2.f * h2f(__ldg(a.mks[cur] + row * GR + e));
+            code_pairs<KB>(w[r][e], k[r][e]);
+            sc[r][e] = 2.f * h2f((uint16_t)(sw2[e >> 1] >> (16 * (e & 1))));
           }
         } else {
           const uint16_t* x;
           if (j < n_sink) {
             x = a.sink_k + ((size_t)unit * a.S + j) * D;
+            at[r] = a.sink_sc + (size_t)unit * a.S + j;
           } else if (j < held) {
-            x = a.rec_k + ((size_t)unit * a.W + (head + (j - n_sink - n_mid)) % a.W) * D;
+            const size_t slot = (size_t)unit * a.W + (head + (j - n_sink - n_mid)) % a.W;
+            x = a.rec_k + slot * D;
+            at[r] = a.rec_sc + slot;
           } else {
             first[r] = j - held;
             x = a.tk.x + b * a.tk.row_stride + tree_node(a, path, b, first[r]) * a.tk.token_stride +
                 h * a.tk.head_stride;
+            at[r] = path_sc + (size_t)unit * a.T + first[r];
           }
 #pragma unroll
           for (int e = 0; e < GR; ++e) {
@@ -216,7 +248,8 @@ __global__ void __launch_bounds__(256) tree_scores_kernel(TreeArgs a, RowLens le
           }
         }
       }
-      const int n = min(kScoreCols, cols - c0);
+      if (tile + 8 < tile1) fetch(tile + 8);
+      float sum[2] = {0.f, 0.f};
 #pragma unroll 1
       for (int nb = 0; nb < n; nb += 8) {
         float s[4] = {};
@@ -234,41 +267,21 @@ __global__ void __launch_bounds__(256) tree_scores_kernel(TreeArgs a, RowLens le
 #pragma unroll
         for (int v = 0; v < 4; ++v) {   // row g + 8 (v / 2), column 2t + v % 2
           const int c = nb + 2 * t + (v & 1);
-          const float w = ((c0 + c) >> a.log_g) >= first[v >> 1] ? sw[c] : 0.f;
           const float p = exp2f(fmaf(s[v], kLog2e * rsqrtf((float)D), -sl[c]));
-          if (w != 0.f) {
-            if (tile == 0) sum[0][v >> 1] = fmaf(w, p, sum[0][v >> 1]);
-            else sum[1][v >> 1] = fmaf(w, p, sum[1][v >> 1]);
-          }
+          if (sw[c] != 0.f && ((c0 + c) >> a.log_g) >= first[v >> 1])
+            sum[v >> 1] = fmaf(sw[c], p, sum[v >> 1]);
         }
       }
-    }
-  }
 #pragma unroll
-  for (int tile = 0; tile < kScoreTiles; ++tile) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float v = sum[tile][r];
-      v += __shfl_xor_sync(0xffffffffu, v, 1);
-      v += __shfl_xor_sync(0xffffffffu, v, 2);
-      const int j = tok0 + 16 * tile + g + 8 * r;
-      if (t != 0 || j >= total) continue;
-      float* at;
-      float old = 0.f, keep = 1.f;
-      if (j < n_sink) {
-        at = a.sink_sc + (size_t)unit * a.S + j;
-      } else if (j < n_sink + n_mid) {
-        at = a.mid_sc[cur] + (size_t)unit * a.C + (j - n_sink);
-      } else if (j < held) {
-        at = a.rec_sc + (size_t)unit * a.W + (head + (j - n_sink - n_mid)) % a.W;
-      } else {
-        at = path_sc + (size_t)unit * a.T + (j - held);
+      for (int r = 0; r < 2; ++r) {
+        float v = sum[r];
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        const int j = 16 * tile + g + 8 * r;
+        if (t != 0 || j >= total) continue;
+        // the first pass decays the score (a path token starts at 0), later ones add to it
+        *at[r] = c0 == 0 ? (j < held ? fmaf(*at[r], keep, v) : v) : *at[r] + v;
       }
-      if (j < held) {
-        old = *at;
-        for (int e = 0; e < n_path; ++e) keep *= decay;
-      }
-      *at = fmaf(old, keep, v);
     }
   }
 }
@@ -355,8 +368,11 @@ template <int D, int KB>
 fade_status_t launch_scores(const fade_config_t* c, const TreeArgs& a, const RowLens& lens,
                             int max_tokens, const float* lse, const int32_t* path, float* path_sc,
                             cudaStream_t st) {
+  // two CTAs an SM (152 SMs), each with at least one tile a warp
+  const int units = c->num_kv_heads * c->batch;
+  const int most = ceil_div(max_tokens, 8 * 16), fill = ceil_div(2 * 152, units);
   tree_scores_kernel<D, KB>
-      <<<dim3(ceil_div(max_tokens, 8 * 16 * kScoreTiles), c->num_kv_heads, c->batch), 256, 0, st>>>(
+      <<<dim3(fill < most ? fill : most, c->num_kv_heads, c->batch), 256, 0, st>>>(
           a, lens, c->policy, c->ema_decay, lse, path, path_sc);
   return launch_status("fade_tree_commit scores");
 }
