@@ -107,11 +107,6 @@ __device__ __forceinline__ uint32_t sub_h2(uint32_t x, uint32_t y) {
 // Channels 8t .. 8t+7 of a group as the pairs (i, i + 4), i = 0 .. 3: half the codes of a middle row's
 // word, or the values of an fp16 row.
 template <int KB>
-__device__ __forceinline__ uint32_t code_word(const uint8_t* group, int t) {
-  if constexpr (KB == 4) return __ldg(reinterpret_cast<const uint32_t*>(group) + t);
-  return __ldg(reinterpret_cast<const uint16_t*>(group) + t);
-}
-template <int KB>
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&p)[4]) {
   if constexpr (KB == 4) {
     const uint32_t h = w >> 8;
@@ -134,26 +129,45 @@ __device__ __forceinline__ void value_pairs(uint4 x, uint32_t (&p)[4]) {
   p[3] = prmt(x.y, x.w, 0x7632);
 }
 
+// A warp's tiles come through a ring of kScoreStages in shared memory of its own (cp.async), since a
+// tile is little work beside the latency of its 1 KB of codes. A row's 16-byte chunks are stored
+// xor-ed with the row, so that the 32 words a warp reads lie in 32 banks.
+constexpr int kScoreStages = 3;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <int D, int KB>
 __global__ void __launch_bounds__(256) tree_scores_kernel(TreeArgs a, RowLens lens, int policy,
                                                           float delta,
                                                           const float* __restrict__ lse,
                                                           const int32_t* __restrict__ path,
                                                           float* __restrict__ path_sc) {
-  constexpr int GR = D / 32;
+  constexpr int GR = D / 32, ROW = D * KB / 8, CH = ROW / 16;   // groups, bytes and chunks of a row
   constexpr float kLog2e = 1.4426950408889634f;
+  struct Stage {
+    uint8_t codes[16][ROW];
+    uint16_t scales[16][GR];
+    float scores[16];
+  };
   __shared__ uint4 sq[kScoreCols][GR][4];   // column's pairs of group, t
   __shared__ float sw[kScoreCols], sl[kScoreCols];
+  extern __shared__ __align__(16) uint8_t ring_raw[];
   const int h = blockIdx.y, b = blockIdx.z, unit = b * a.H + h;
   const int n_path = lens.v[b];
   if (n_path == 0) return;   // uniform per CTA, as is the next
   const int32_t* m = a.meta + unit * FADE_META_FIELDS;
   const int n_sink = m[FADE_META_N_SINK], n_mid = m[FADE_META_N_MID];
   const int n_rec = m[FADE_META_N_RECENT], head = m[FADE_META_HEAD], cur = m[FADE_META_CUR];
-  const int held = n_sink + n_mid + n_rec, total = held + n_path;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  // the CTA's tiles of 16 tokens, taken by its warps in turn
-  const int tiles = (total + 15) / 16;
+  Stage* ring = reinterpret_cast<Stage*>(ring_raw) + warp * kScoreStages;
+  // tiles of 16 middle tokens, then of 16 FP16 tokens (sinks, ring, path), cut evenly over the CTAs
+  // of the unit and taken by a CTA's warps in turn
+  const int n16 = n_sink + n_rec + n_path, mid_tiles = (n_mid + 15) / 16;
+  const int tiles = mid_tiles + (n16 + 15) / 16;
   const int tile0 = (int)((long long)tiles * blockIdx.x / gridDim.x);
   const int tile1 = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x);
   if (tile0 == tile1) return;
@@ -162,28 +176,31 @@ __global__ void __launch_bounds__(256) tree_scores_kernel(TreeArgs a, RowLens le
   const int cols = n_path * a.G;
   float keep = 1.f;
   for (int e = 0; e < n_path; ++e) keep *= decay;
-  const uint8_t* codes = a.mk[cur] + (size_t)unit * a.C * GR * (4 * KB);
+  const uint8_t* codes = a.mk[cur] + (size_t)unit * a.C * ROW;
   const uint16_t* scales = a.mks[cur] + (size_t)unit * a.C * GR;
-  // the words and scales of rows g and g + 8 of a tile, read as if they were middle tokens (the
-  // nearest one where they are not: those rows are read again from their tier)
-  uint32_t w[2][GR];
-  uint2 sc2[2];
+  float* scores = a.mid_sc[cur] + (size_t)unit * a.C;
+  // a middle tile into its stage (rows past the tier lie within the unit's stride, a multiple of 64)
   auto fetch = [&](int tile) {
+    if (tile < min(tile1, mid_tiles)) {
+      Stage& st = ring[((tile - tile0) >> 3) % kScoreStages];
+      const size_t row = (size_t)16 * tile;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = min(max(16 * tile + g + 8 * r - n_sink, 0), max(n_mid - 1, 0));
-      const size_t row = (size_t)i * GR;
+      for (int i = lane; i < 16 * CH; i += 32) {
+        const int rr = i / CH, c = i % CH;
+        cp_async16(smem_u32(&st.codes[rr][16 * (c ^ ((rr >> 1) & (CH - 1)))]),
+                   codes + (row + rr) * ROW + 16 * c);
+      }
+      constexpr int SW = 16 * GR / 2;   // words of the tile's scales
 #pragma unroll
-      for (int e = 0; e < GR; ++e) w[r][e] = code_word<KB>(codes + (row + e) * (4 * KB), t);
-      if constexpr (GR == 4)
-        sc2[r] = __ldg(reinterpret_cast<const uint2*>(scales + row));
-      else
-        sc2[r] = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(scales + row)), 0u);
+      for (int i = lane; i < SW; i += 32)
+        cp_async4(smem_u32(&st.scales[0][0]) + 4 * i, scales + row * GR + 2 * i);
+      if (lane < 16) cp_async4(smem_u32(&st.scores[lane]), scores + row + lane);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   for (int c0 = 0; c0 < cols; c0 += kScoreCols) {
     const int n = min(kScoreCols, cols - c0);
-    if (tile0 + warp < tile1) fetch(tile0 + warp);
+    for (int i = 0; i < kScoreStages - 1; ++i) fetch(tile0 + warp + 8 * i);
     if (c0) __syncthreads();
     for (int i = threadIdx.x; i < (n + 7) / 8 * 8 * GR * 4; i += 256) {
       const int c = i / (GR * 4), gr = (i / 4) % GR, col = c0 + c;
@@ -209,38 +226,51 @@ __global__ void __launch_bounds__(256) tree_scores_kernel(TreeArgs a, RowLens le
     __syncthreads();
 #pragma unroll 1
     for (int tile = tile0 + warp; tile < tile1; tile += 8) {
+      fetch(tile + 8 * (kScoreStages - 1));
+      asm volatile("cp.async.wait_group %0;" ::"n"(kScoreStages - 1) : "memory");
+      __syncwarp();
+      const bool mid = tile < mid_tiles;
+      const Stage& st = ring[((tile - tile0) >> 3) % kScoreStages];
       // rows g and g + 8 of the tile: their pairs and scales (twice, the codes are halved), the
-      // score's place and the first node that sees the token
+      // score and its place, the first node that sees the token
       uint32_t k[2][GR][4];
-      float sc[2][GR], *at[2];
+      float sc[2][GR], old[2], *at[2];
       int first[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int j = min(16 * tile + g + 8 * r, total - 1);
+        const int row = g + 8 * r;
         first[r] = 0;
-        if (j >= n_sink && j < n_sink + n_mid) {
-          at[r] = a.mid_sc[cur] + (size_t)unit * a.C + (j - n_sink);
-          const uint32_t sw2[2] = {sc2[r].x, sc2[r].y};
+        if (mid) {
+          at[r] = 16 * tile + row < n_mid ? scores + 16 * tile + row : nullptr;
+          old[r] = st.scores[row];
 #pragma unroll
           for (int e = 0; e < GR; ++e) {
-            code_pairs<KB>(w[r][e], k[r][e]);
-            sc[r][e] = 2.f * h2f((uint16_t)(sw2[e >> 1] >> (16 * (e & 1))));
+            const int byte = e * (4 * KB) + t * KB, c = byte / 16;
+            const uint8_t* w = &st.codes[row][16 * (c ^ ((row >> 1) & (CH - 1))) + byte % 16];
+            code_pairs<KB>(KB == 4 ? *reinterpret_cast<const uint32_t*>(w)
+                                   : *reinterpret_cast<const uint16_t*>(w),
+                           k[r][e]);
+            sc[r][e] = 2.f * h2f(st.scales[row][e]);
           }
         } else {
+          const int i = 16 * (tile - mid_tiles) + row, j = min(i, n16 - 1);
           const uint16_t* x;
           if (j < n_sink) {
             x = a.sink_k + ((size_t)unit * a.S + j) * D;
             at[r] = a.sink_sc + (size_t)unit * a.S + j;
-          } else if (j < held) {
-            const size_t slot = (size_t)unit * a.W + (head + (j - n_sink - n_mid)) % a.W;
+          } else if (j < n_sink + n_rec) {
+            const size_t slot = (size_t)unit * a.W + (head + (j - n_sink)) % a.W;
             x = a.rec_k + slot * D;
             at[r] = a.rec_sc + slot;
           } else {
-            first[r] = j - held;
+            first[r] = j - n_sink - n_rec;
             x = a.tk.x + b * a.tk.row_stride + tree_node(a, path, b, first[r]) * a.tk.token_stride +
                 h * a.tk.head_stride;
             at[r] = path_sc + (size_t)unit * a.T + first[r];
           }
+          // a path token starts at 0
+          old[r] = c0 == 0 && j >= n_sink + n_rec ? 0.f : *at[r];
+          if (i != j) at[r] = nullptr;
 #pragma unroll
           for (int e = 0; e < GR; ++e) {
             value_pairs(*reinterpret_cast<const uint4*>(x + 32 * e + 8 * t), k[r][e]);
@@ -248,7 +278,6 @@ __global__ void __launch_bounds__(256) tree_scores_kernel(TreeArgs a, RowLens le
           }
         }
       }
-      if (tile + 8 < tile1) fetch(tile + 8);
       float sum[2] = {0.f, 0.f};
 #pragma unroll 1
       for (int nb = 0; nb < n; nb += 8) {
@@ -277,12 +306,12 @@ __global__ void __launch_bounds__(256) tree_scores_kernel(TreeArgs a, RowLens le
         float v = sum[r];
         v += __shfl_xor_sync(0xffffffffu, v, 1);
         v += __shfl_xor_sync(0xffffffffu, v, 2);
-        const int j = 16 * tile + g + 8 * r;
-        if (t != 0 || j >= total) continue;
-        // the first pass decays the score (a path token starts at 0), later ones add to it
-        *at[r] = c0 == 0 ? (j < held ? fmaf(*at[r], keep, v) : v) : *at[r] + v;
+        // the first pass decays the score, later ones add to it
+        if (t == 0 && at[r]) *at[r] = c0 == 0 ? fmaf(old[r], keep, v) : old[r] + v;
       }
+      __syncwarp();   // the stage is read: the next round fills it
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 }
 
@@ -371,8 +400,10 @@ fade_status_t launch_scores(const fade_config_t* c, const TreeArgs& a, const Row
   // two CTAs an SM (152 SMs), each with at least one tile a warp
   const int units = c->num_kv_heads * c->batch;
   const int most = ceil_div(max_tokens, 8 * 16), fill = ceil_div(2 * 152, units);
+  constexpr int kRing = 8 * kScoreStages * 16 * (D * KB / 8 + D / 32 * 2 + 4);
+  static_assert(kRing + kScoreCols * (D / 32 * 64 + 8) <= 48 * 1024, "the default shared memory");
   tree_scores_kernel<D, KB>
-      <<<dim3(fill < most ? fill : most, c->num_kv_heads, c->batch), 256, 0, st>>>(
+      <<<dim3(fill < most ? fill : most, c->num_kv_heads, c->batch), 256, kRing, st>>>(
           a, lens, c->policy, c->ema_decay, lse, path, path_sc);
   return launch_status("fade_tree_commit scores");
 }
