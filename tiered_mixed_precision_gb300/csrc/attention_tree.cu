@@ -705,12 +705,10 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
           if (use > 0) side_wait(kFree + 8 * st, use - 1);
           if (t + 1 == f16 && t + 1 < t_end) c.load_all();
 #pragma unroll 1
-          for (int i = 0; i < NI; i += 2) {
-            uint4 x[4], y[4];
+          for (int i = 0; i < NI; ++i) {
+            uint4 x[4];
             f16_load(s, t * kTok + tok + APART * i, false, x);
-            f16_load(s, t * kTok + tok + APART * (i + 1), false, y);
             store_f16<KO>(kTile(st) + at16 + i * ROWB, x);
-            store_f16<KO>(kTile(st) + at16 + (i + 1) * ROWB, y);
           }
           fence_proxy_async_smem();
           arrive(kFull + 8 * st);
@@ -778,17 +776,14 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
           if (use > 0) side_wait(vFree + 8 * st, use - 1);
           if (t + 1 == f16 && t + 1 < t_end) c.load_all();
 #pragma unroll 1
-          for (int i = 0; i < NI; i += 2) {
-            uint4 x[4], y[4];
+          for (int i = 0; i < NI; ++i) {
+            uint4 x[4];
             f16_load(s, t * kTok + tok + APART * i, true, x);
-            f16_load(s, t * kTok + tok + APART * (i + 1), true, y);
             // a node's infinities and NaN would reach the rows that do not see it (0 * inf): they
             // are left out of the product and put into the rows that see it at the end
-            const int node = t * kTok + tok + APART * i - n16, next = node + APART;
+            const int node = t * kTok + tok + APART * i - n16;
             if (node >= 0 && clear_nonfinite(x)) atomicOr(bad + (node >> 5), 1u << (node & 31));
-            if (next >= 0 && clear_nonfinite(y)) atomicOr(bad + (next >> 5), 1u << (next & 31));
             store_f16<VO>(vTile(st) + at16 + i * ROWB, x);
-            store_f16<VO>(vTile(st) + at16 + (i + 1) * ROWB, y);
           }
           fence_proxy_async_smem();
           arrive(vFull + 8 * st);
@@ -1120,20 +1115,6 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
             const int e = (i >> 1) & 1;
             o[i] = (w[e][0] == 0.f ? 0.f : o[i] * w[e][0]) + (w[e][1] == 0.f ? 0.f : o1[i] * w[e][1]);
           }
-#pragma unroll 1
-          for (unsigned long long left = bad; left; left &= left - 1) {
-            const int node = __ffsll((long long)left) - 1;
-            const uint16_t* v = a.tv.x + s.b * a.tv.row_stride + node * a.tv.token_stride +
-                                s.h * a.tv.head_stride;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = row0 + 8 * ((i >> 1) & 1);
-              if (r >= rows || !((p.mask[(size_t)s.b * a.T + ((s.r0 + r) >> a.log_g)] >> node) & 1))
-                continue;
-              const float y = h2f(v[channel_of<VO>(c0 + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1))]);
-              if (!isfinite(y)) o[i] += y;
-            }
-          }
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const int e = (i >> 1) & 1, col = c0 + 8 * (i >> 2) + 2 * (lane & 3);
@@ -1144,6 +1125,30 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
             } else {
               *reinterpret_cast<float2*>(part + 2 * ROWS + (size_t)(row0 + 8 * e) * D + col) =
                   make_float2(o[i], o[i + 1]);
+            }
+          }
+        }
+        // what was left out of the product: infinities and NaN of the nodes' values, into the rows
+        // that see them (this thread's own elements; rare, so the code is kept small)
+#pragma unroll 1
+        for (unsigned long long left = bad; left; left &= left - 1) {
+          const int node = __ffsll((long long)left) - 1;
+          const uint16_t* v = a.tv.x + s.b * a.tv.row_stride + node * a.tv.token_stride +
+                              s.h * a.tv.head_stride;
+#pragma unroll 1
+          for (int i = 0; i < D / 4; ++i) {   // D / 8 channels of two rows
+            const int e = i & 1, r = row0 + 8 * e;
+            const int col = stream * (D / 2) + 8 * (i >> 2) + 2 * (lane & 3) + ((i >> 1) & 1);
+            if (r >= rows || !((p.mask[(size_t)s.b * a.T + ((s.r0 + r) >> a.log_g)] >> node) & 1))
+              continue;
+            const int ch = channel_of<VO>(col);
+            const float y = h2f(v[ch]);
+            if (isfinite(y)) continue;
+            if (whole) {
+              uint16_t* at16 = p.out + (e ? vec[1] : vec[0]) * D + ch;
+              *at16 = f2h(h2f(*at16) + y);
+            } else {
+              part[2 * ROWS + (size_t)r * D + col] += y;
             }
           }
         }
