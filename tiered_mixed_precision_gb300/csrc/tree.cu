@@ -81,15 +81,21 @@ __global__ void __launch_bounds__(FADE_TREE_MAX_NODES)
 // The path's attention mass. Mathematics: with the path's nodes 0 .. n-1 and their G query rows as
 // columns c (node i = c / G), token j's score becomes decay^k score + sum_c w_c exp(s_jc - lse_c),
 // k the nodes that see it (all n; n - j for the j-th path token, which starts at 0), w_c = 1 and
-// decay = 1 (H2O) or w_c = (1 - delta) delta^(n-1-i) and decay = delta (EMA): the accumulation node by
-// node, written as one sum.
+// decay = 1 (H2O) or w_c = (1 - delta) delta^(n-1-i) and decay = delta (EMA): the accumulation node
+// by node, written as one sum.
 //
-// Products on mma.sync: 16 tokens are the rows, 8 columns the columns of an instruction. Few columns
-// and every key read once make this a stream over the codes, not a contraction for tcgen05; and it
-// keeps the keys exact: codes are exact fp16 integers (halved), each 32-channel group is summed on
-// its own and meets its scale in fp32. Thread (row g = lane / 4, t = lane % 4) holds channels 8t ..
-// 8t+7 of every group of rows g and g + 8, as the pairs (8t+i, 8t+i+4) its code word unpacks into; the
-// columns are laid out in shared memory in the same order.
+// Products on mma.sync: 16 tokens are the rows, 8 columns the columns of an instruction. Few
+// columns and every key read once make this a stream over the codes, not a contraction for tcgen05;
+// and it keeps the keys exact: codes are exact fp16 integers (halved), each 32-channel group is
+// summed on its own and meets its scale (with log2 e / sqrt d) in fp32. A column's weight goes into
+// its exponent: w exp(s - lse) = 2^(s' - (lse' - log2 w)). Thread (row g = lane / 4, t = lane % 4)
+// holds channels 8t .. 8t+7 of every group of rows g and g + 8, as the pairs (8t+i, 8t+i+4) its
+// code word unpacks into; the columns are laid out in shared memory in the same order.
+//
+// Measured at 4 rows of 16384 middle tokens, 8 KV heads of d = 128, INT4 keys, paths of 1 to 6
+// nodes of 4 queries: 28 us for 43 MB (the copy rate's 6 us). Instruction issue bounds it,
+// unpacking first and the products next; equal stretches of cost rather than of tiles took 10 us
+// off (paths of different lengths, and a second wave of CTAs), weights in the exponents 5.
 constexpr int kScoreCols = 64;   // columns staged at a time: longer paths take more passes
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -99,6 +105,11 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ uint32_t sub_h2(uint32_t x, uint32_t y) {
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
@@ -140,178 +151,229 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// What a CTA takes: row b's tiles cost kTileCost + 1 a block of eight columns each (a pass over the
+// tile's codes, then two products a group a block), the costs of all rows and heads form one line,
+// and every CTA takes an equal stretch of it. Paths differ in length, so equal tiles would not be
+// equal work.
+constexpr int kTileCost = 2;
+struct ScoreRow {
+  int n_sink, n_mid, n_rec;
+  int mid_tiles, tiles, cost;
+};
+__device__ __forceinline__ ScoreRow score_row(const TreeArgs& a, int b, int n_path) {
+  const int32_t* m = a.meta + (size_t)b * a.H * FADE_META_FIELDS;   // a row's heads agree
+  ScoreRow r;
+  r.n_sink = m[FADE_META_N_SINK];
+  r.n_mid = m[FADE_META_N_MID];
+  r.n_rec = m[FADE_META_N_RECENT];
+  r.mid_tiles = (r.n_mid + 15) / 16;
+  r.tiles = n_path ? r.mid_tiles + (r.n_sink + r.n_rec + n_path + 15) / 16 : 0;
+  const int cols = n_path * a.G;
+  r.cost = (cols + kScoreCols - 1) / kScoreCols * kTileCost + (cols + 7) / 8;
+  return r;
+}
+
 template <int D, int KB>
-__global__ void __launch_bounds__(256) tree_scores_kernel(TreeArgs a, RowLens lens, int policy,
+__global__ void __launch_bounds__(256, 2) tree_scores_kernel(TreeArgs a, RowLens lens, int policy,
                                                           float delta,
                                                           const float* __restrict__ lse,
                                                           const int32_t* __restrict__ path,
                                                           float* __restrict__ path_sc) {
   constexpr int GR = D / 32, ROW = D * KB / 8, CH = ROW / 16;   // groups, bytes and chunks of a row
   constexpr float kLog2e = 1.4426950408889634f;
+  constexpr float kScale = kLog2e * (D == 64 ? 0.125f : 0.08838834764831845f);   // log2 e / sqrt D
   struct Stage {
     uint8_t codes[16][ROW];
     uint16_t scales[16][GR];
     float scores[16];
   };
   __shared__ uint4 sq[kScoreCols][GR][4];   // column's pairs of group, t
-  __shared__ float sw[kScoreCols], sl[kScoreCols];
+  __shared__ float sl[kScoreCols];          // lse of the column less its weight's logarithm, base 2
   extern __shared__ __align__(16) uint8_t ring_raw[];
-  const int h = blockIdx.y, b = blockIdx.z, unit = b * a.H + h;
-  const int n_path = lens.v[b];
-  if (n_path == 0) return;   // uniform per CTA, as is the next
-  const int32_t* m = a.meta + unit * FADE_META_FIELDS;
-  const int n_sink = m[FADE_META_N_SINK], n_mid = m[FADE_META_N_MID];
-  const int n_rec = m[FADE_META_N_RECENT], head = m[FADE_META_HEAD], cur = m[FADE_META_CUR];
+  __shared__ long long pre[FADE_MAX_BATCH + 1];   // costs of the rows before
+  __shared__ long long wsum[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   Stage* ring = reinterpret_cast<Stage*>(ring_raw) + warp * kScoreStages;
-  // tiles of 16 middle tokens, then of 16 FP16 tokens (sinks, ring, path), cut evenly over the CTAs
-  // of the unit and taken by a CTA's warps in turn
-  const int n16 = n_sink + n_rec + n_path, mid_tiles = (n_mid + 15) / 16;
-  const int tiles = mid_tiles + (n16 + 15) / 16;
-  const int tile0 = (int)((long long)tiles * blockIdx.x / gridDim.x);
-  const int tile1 = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x);
-  if (tile0 == tile1) return;
+  {
+    const int b = threadIdx.x;   // B <= 256
+    long long v = 0;
+    if (b < a.B && lens.v[b]) {
+      const ScoreRow r = score_row(a, b, lens.v[b]);
+      v = (long long)a.H * r.tiles * r.cost;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) wsum[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) v += wsum[w];
+    pre[b + 1] = v;
+    if (b == 0) pre[0] = 0;
+    __syncthreads();
+  }
+  const long long x0 = pre[a.B] * blockIdx.x / gridDim.x;
+  const long long x1 = pre[a.B] * (blockIdx.x + 1) / gridDim.x;
   const float decay = policy == FADE_EVICT_H2O ? 1.f : delta;
   const float gain = policy == FADE_EVICT_H2O ? 1.f : 1.f - delta;
-  const int cols = n_path * a.G;
-  float keep = 1.f;
-  for (int e = 0; e < n_path; ++e) keep *= decay;
-  const uint8_t* codes = a.mk[cur] + (size_t)unit * a.C * ROW;
-  const uint16_t* scales = a.mks[cur] + (size_t)unit * a.C * GR;
-  float* scores = a.mid_sc[cur] + (size_t)unit * a.C;
-  // a middle tile into its stage (rows past the tier lie within the unit's stride, a multiple of 64)
-  auto fetch = [&](int tile) {
-    if (tile < min(tile1, mid_tiles)) {
-      Stage& st = ring[((tile - tile0) >> 3) % kScoreStages];
-      const size_t row = (size_t)16 * tile;
+  for (int b = 0; b < a.B; ++b) {
+    if (pre[b + 1] <= x0 || pre[b] == pre[b + 1]) continue;
+    if (pre[b] >= x1) break;
+    const int n_path = lens.v[b], cols = n_path * a.G;
+    const ScoreRow sr = score_row(a, b, n_path);
+    // the row's tiles of 16 middle tokens, then of 16 FP16 tokens (sinks, ring, path), head by head;
+    // a CTA's warps take its tiles of a head in turn
+    const int mid_tiles = sr.mid_tiles, n_mid = sr.n_mid;
+    const int n_sink = sr.n_sink, n_rec = sr.n_rec, n16 = n_sink + n_rec + n_path;
+    const int first_tile = (int)((max(x0 - pre[b], 0ll) + sr.cost - 1) / sr.cost);
+    const int end_tile = (int)((min(x1, pre[b + 1]) - pre[b] + sr.cost - 1) / sr.cost);
+    float keep = 1.f;
+    for (int e = 0; e < n_path; ++e) keep *= decay;
+    for (int at_tile = first_tile; at_tile < end_tile;) {
+      const int h = at_tile / sr.tiles, unit = b * a.H + h;
+      const int tile0 = at_tile - h * sr.tiles, tile1 = min(sr.tiles, end_tile - h * sr.tiles);
+      at_tile = h * sr.tiles + tile1;
+      const int head = a.meta[unit * FADE_META_FIELDS + FADE_META_HEAD];
+      const int cur = a.meta[unit * FADE_META_FIELDS + FADE_META_CUR];
+      const uint8_t* codes = a.mk[cur] + (size_t)unit * a.C * ROW;
+      const uint16_t* scales = a.mks[cur] + (size_t)unit * a.C * GR;
+      float* scores = a.mid_sc[cur] + (size_t)unit * a.C;
+      // a middle tile into its stage (rows past the tier lie within the unit's stride, a multiple
+      // of 64)
+      auto fetch = [&](int tile) {
+        if (tile < min(tile1, mid_tiles)) {
+          Stage& st = ring[((tile - tile0) >> 3) % kScoreStages];
+          const size_t row = (size_t)16 * tile;
 #pragma unroll
-      for (int i = lane; i < 16 * CH; i += 32) {
-        const int rr = i / CH, c = i % CH;
-        cp_async16(smem_u32(&st.codes[rr][16 * (c ^ ((rr >> 1) & (CH - 1)))]),
-                   codes + (row + rr) * ROW + 16 * c);
-      }
-      constexpr int SW = 16 * GR / 2;   // words of the tile's scales
+          for (int i = lane; i < 16 * CH; i += 32) {
+            const int rr = i / CH, c = i % CH;
+            cp_async16(smem_u32(&st.codes[rr][16 * (c ^ ((rr >> 1) & (CH - 1)))]),
+                       codes + (row + rr) * ROW + 16 * c);
+          }
+          constexpr int SW = 16 * GR / 2;   // words of the tile's scales
 #pragma unroll
-      for (int i = lane; i < SW; i += 32)
-        cp_async4(smem_u32(&st.scales[0][0]) + 4 * i, scales + row * GR + 2 * i);
-      if (lane < 16) cp_async4(smem_u32(&st.scores[lane]), scores + row + lane);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  for (int c0 = 0; c0 < cols; c0 += kScoreCols) {
-    const int n = min(kScoreCols, cols - c0);
-    for (int i = 0; i < kScoreStages - 1; ++i) fetch(tile0 + warp + 8 * i);
-    if (c0) __syncthreads();
-    for (int i = threadIdx.x; i < (n + 7) / 8 * 8 * GR * 4; i += 256) {
-      const int c = i / (GR * 4), gr = (i / 4) % GR, col = c0 + c;
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (col < cols) {
-        const int node = tree_node(a, path, b, col >> a.log_g);
-        const size_t q = (((size_t)b * a.T + node) * a.Hq + h * a.G + (col & (a.G - 1)));
-        uint32_t p[4];
-        value_pairs(__ldg(reinterpret_cast<const uint4*>(a.q + q * D + 32 * gr + 8 * (i & 3))), p);
-        x = make_uint4(p[0], p[1], p[2], p[3]);
-        if (gr == 0 && (i & 3) == 0) {
-          float wc = gain;
-          for (int e = col >> a.log_g; e < n_path - 1; ++e) wc *= decay;
-          sw[c] = wc;
-          sl[c] = lse[q] * kLog2e;
+          for (int i = lane; i < SW; i += 32)
+            cp_async4(smem_u32(&st.scales[0][0]) + 4 * i, scales + row * GR + 2 * i);
+          if (lane < 16) cp_async4(smem_u32(&st.scores[lane]), scores + row + lane);
         }
-      } else if (gr == 0 && (i & 3) == 0) {
-        sw[c] = 0.f;   // left out of the sum
-        sl[c] = 0.f;
-      }
-      sq[c][gr][i & 3] = x;
-    }
-    __syncthreads();
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      for (int c0 = 0; c0 < cols; c0 += kScoreCols) {
+        const int n = min(kScoreCols, cols - c0);
+        for (int i = 0; i < kScoreStages - 1; ++i) fetch(tile0 + warp + 8 * i);
+        __syncthreads();   // the columns before are read
+        for (int i = threadIdx.x; i < (n + 7) / 8 * 8 * GR * 4; i += 256) {
+          const int c = i / (GR * 4), gr = (i / 4) % GR, col = c0 + c;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (col < cols) {
+            const int node = tree_node(a, path, b, col >> a.log_g);
+            const size_t q = (((size_t)b * a.T + node) * a.Hq + h * a.G + (col & (a.G - 1)));
+            uint32_t p[4];
+            value_pairs(
+                __ldg(reinterpret_cast<const uint4*>(a.q + q * D + 32 * gr + 8 * (i & 3))), p);
+            x = make_uint4(p[0], p[1], p[2], p[3]);
+            if (gr == 0 && (i & 3) == 0) {
+              float wc = gain;
+              for (int e = col >> a.log_g; e < n_path - 1; ++e) wc *= decay;
+              sl[c] = fmaf(lse[q], kLog2e, -log2f(wc));
+            }
+          } else if (gr == 0 && (i & 3) == 0) {
+            sl[c] = INFINITY;   // adds nothing to the sum
+          }
+          sq[c][gr][i & 3] = x;
+        }
+        __syncthreads();
 #pragma unroll 1
-    for (int tile = tile0 + warp; tile < tile1; tile += 8) {
-      fetch(tile + 8 * (kScoreStages - 1));
-      asm volatile("cp.async.wait_group %0;" ::"n"(kScoreStages - 1) : "memory");
-      __syncwarp();
-      const bool mid = tile < mid_tiles;
-      const Stage& st = ring[((tile - tile0) >> 3) % kScoreStages];
-      // rows g and g + 8 of the tile: their pairs and scales (twice, the codes are halved), the
-      // score and its place, the first node that sees the token
-      uint32_t k[2][GR][4];
-      float sc[2][GR], old[2], *at[2];
-      int first[2];
+        for (int tile = tile0 + warp; tile < tile1; tile += 8) {
+          fetch(tile + 8 * (kScoreStages - 1));
+          asm volatile("cp.async.wait_group %0;" ::"n"(kScoreStages - 1) : "memory");
+          __syncwarp();
+          const bool mid = tile < mid_tiles;
+          const Stage& st = ring[((tile - tile0) >> 3) % kScoreStages];
+          // rows g and g + 8 of the tile: their pairs and scales (twice, the codes are halved), the
+          // score and its place, the first column (less c0 and 2t) whose node sees the token
+          uint32_t k[2][GR][4];
+          float sc[2][GR], old[2], *at[2];
+          int first[2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = g + 8 * r;
-        first[r] = 0;
-        if (mid) {
-          at[r] = 16 * tile + row < n_mid ? scores + 16 * tile + row : nullptr;
-          old[r] = st.scores[row];
+          for (int r = 0; r < 2; ++r) {
+            const int row = g + 8 * r;
+            first[r] = 0;
+            if (mid) {
+              at[r] = 16 * tile + row < n_mid ? scores + 16 * tile + row : nullptr;
+              old[r] = st.scores[row];
 #pragma unroll
-          for (int e = 0; e < GR; ++e) {
-            const int byte = e * (4 * KB) + t * KB, c = byte / 16;
-            const uint8_t* w = &st.codes[row][16 * (c ^ ((row >> 1) & (CH - 1))) + byte % 16];
-            code_pairs<KB>(KB == 4 ? *reinterpret_cast<const uint32_t*>(w)
-                                   : *reinterpret_cast<const uint16_t*>(w),
-                           k[r][e]);
-            sc[r][e] = 2.f * h2f(st.scales[row][e]);
-          }
-        } else {
-          const int i = 16 * (tile - mid_tiles) + row, j = min(i, n16 - 1);
-          const uint16_t* x;
-          if (j < n_sink) {
-            x = a.sink_k + ((size_t)unit * a.S + j) * D;
-            at[r] = a.sink_sc + (size_t)unit * a.S + j;
-          } else if (j < n_sink + n_rec) {
-            const size_t slot = (size_t)unit * a.W + (head + (j - n_sink)) % a.W;
-            x = a.rec_k + slot * D;
-            at[r] = a.rec_sc + slot;
-          } else {
-            first[r] = j - n_sink - n_rec;
-            x = a.tk.x + b * a.tk.row_stride + tree_node(a, path, b, first[r]) * a.tk.token_stride +
-                h * a.tk.head_stride;
-            at[r] = path_sc + (size_t)unit * a.T + first[r];
-          }
-          // a path token starts at 0
-          old[r] = c0 == 0 && j >= n_sink + n_rec ? 0.f : *at[r];
-          if (i != j) at[r] = nullptr;
+              for (int e = 0; e < GR; ++e) {
+                const int byte = e * (4 * KB) + t * KB, c = byte / 16;
+                const uint8_t* w = &st.codes[row][16 * (c ^ ((row >> 1) & (CH - 1))) + byte % 16];
+                code_pairs<KB>(KB == 4 ? *reinterpret_cast<const uint32_t*>(w)
+                                       : *reinterpret_cast<const uint16_t*>(w),
+                               k[r][e]);
+                sc[r][e] = 2.f * kScale * h2f(st.scales[row][e]);
+              }
+            } else {
+              const int i = 16 * (tile - mid_tiles) + row, j = min(i, n16 - 1);
+              const uint16_t* x;
+              if (j < n_sink) {
+                x = a.sink_k + ((size_t)unit * a.S + j) * D;
+                at[r] = a.sink_sc + (size_t)unit * a.S + j;
+              } else if (j < n_sink + n_rec) {
+                const size_t slot = (size_t)unit * a.W + (head + (j - n_sink)) % a.W;
+                x = a.rec_k + slot * D;
+                at[r] = a.rec_sc + slot;
+              } else {
+                const int i_path = j - n_sink - n_rec;
+                first[r] = (i_path << a.log_g) - c0 - 2 * t;
+                x = a.tk.x + b * a.tk.row_stride + h * a.tk.head_stride +
+                    tree_node(a, path, b, i_path) * a.tk.token_stride;
+                at[r] = path_sc + (size_t)unit * a.T + i_path;
+              }
+              // a path token starts at 0
+              old[r] = c0 == 0 && j >= n_sink + n_rec ? 0.f : *at[r];
+              if (i != j) at[r] = nullptr;
 #pragma unroll
-          for (int e = 0; e < GR; ++e) {
-            value_pairs(*reinterpret_cast<const uint4*>(x + 32 * e + 8 * t), k[r][e]);
-            sc[r][e] = 1.f;
+              for (int e = 0; e < GR; ++e) {
+                value_pairs(*reinterpret_cast<const uint4*>(x + 32 * e + 8 * t), k[r][e]);
+                sc[r][e] = kScale;
+              }
+            }
           }
-        }
-      }
-      float sum[2] = {0.f, 0.f};
+          float sum[2] = {0.f, 0.f};
 #pragma unroll 1
-      for (int nb = 0; nb < n; nb += 8) {
-        float s[4] = {};
+          for (int nb = 0; nb < n; nb += 8) {
+            float s[4] = {};
 #pragma unroll
-        for (int e = 0; e < GR; ++e) {
-          const uint4 q = sq[nb + g][e][t];   // column g of the eight: the B operand's column
-          float d[4] = {};
-          const uint32_t a0[4] = {k[0][e][0], k[1][e][0], k[0][e][1], k[1][e][1]};
-          const uint32_t a1[4] = {k[0][e][2], k[1][e][2], k[0][e][3], k[1][e][3]};
-          mma_16816(d, a0, q.x, q.y);
-          mma_16816(d, a1, q.z, q.w);
+            for (int e = 0; e < GR; ++e) {
+              const uint4 q = sq[nb + g][e][t];   // column g of the eight: the B operand's column
+              float d[4] = {};
+              const uint32_t a0[4] = {k[0][e][0], k[1][e][0], k[0][e][1], k[1][e][1]};
+              const uint32_t a1[4] = {k[0][e][2], k[1][e][2], k[0][e][3], k[1][e][3]};
+              mma_16816(d, a0, q.x, q.y);
+              mma_16816(d, a1, q.z, q.w);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) s[v] = fmaf(d[v], sc[v >> 1][e], s[v]);
+              for (int v = 0; v < 4; ++v) s[v] = fmaf(d[v], sc[v >> 1][e], s[v]);
+            }
+            const float2 off = *reinterpret_cast<const float2*>(&sl[nb + 2 * t]);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {   // row g + 8 (v / 2), column 2t + v % 2
+              const float p = exp2_approx(s[v] - (v & 1 ? off.y : off.x));
+              if (nb + (v & 1) >= first[v >> 1]) sum[v >> 1] += p;
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float v = sum[r];
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            // the first pass decays the score, later ones add to it
+            if (t == 0 && at[r]) *at[r] = c0 == 0 ? fmaf(old[r], keep, v) : old[r] + v;
+          }
+          __syncwarp();   // the stage is read: the next round fills it
         }
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {   // row g + 8 (v / 2), column 2t + v % 2
-          const int c = nb + 2 * t + (v & 1);
-          const float p = exp2f(fmaf(s[v], kLog2e * rsqrtf((float)D), -sl[c]));
-          if (sw[c] != 0.f && ((c0 + c) >> a.log_g) >= first[v >> 1])
-            sum[v >> 1] = fmaf(sw[c], p, sum[v >> 1]);
-        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float v = sum[r];
-        v += __shfl_xor_sync(0xffffffffu, v, 1);
-        v += __shfl_xor_sync(0xffffffffu, v, 2);
-        // the first pass decays the score, later ones add to it
-        if (t == 0 && at[r]) *at[r] = c0 == 0 ? fmaf(old[r], keep, v) : old[r] + v;
-      }
-      __syncwarp();   // the stage is read: the next round fills it
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 }
 
@@ -395,15 +457,15 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(TreeArgs a, RowLens le
 
 template <int D, int KB>
 fade_status_t launch_scores(const fade_config_t* c, const TreeArgs& a, const RowLens& lens,
-                            int max_tokens, const float* lse, const int32_t* path, float* path_sc,
+                            long long tiles, const float* lse, const int32_t* path, float* path_sc,
                             cudaStream_t st) {
-  // two CTAs an SM (152 SMs), each with at least one tile a warp
-  const int units = c->num_kv_heads * c->batch;
-  const int most = ceil_div(max_tokens, 8 * 16), fill = ceil_div(2 * 152, units);
+  // two CTAs an SM (152 SMs; three measured the same), each with at least one tile a warp
+  const long long most = (tiles + 7) / 8, fill = 2 * 152;
   constexpr int kRing = 8 * kScoreStages * 16 * (D * KB / 8 + D / 32 * 2 + 4);
-  static_assert(kRing + kScoreCols * (D / 32 * 64 + 8) <= 48 * 1024, "the default shared memory");
+  static_assert(kRing + kScoreCols * (D / 32 * 64 + 4) + 8 * (FADE_MAX_BATCH + 9) <= 48 * 1024,
+                "the default shared memory");
   tree_scores_kernel<D, KB>
-      <<<dim3(fill < most ? fill : most, c->num_kv_heads, c->batch), 256, kRing, st>>>(
+      <<<(unsigned)(fill < most ? fill : most), 256, kRing, st>>>(
           a, lens, c->policy, c->ema_decay, lse, path, path_sc);
   return launch_status("fade_tree_commit scores");
 }
@@ -502,7 +564,8 @@ extern "C" fade_status_t fade_tree_commit(const fade_config_t* c, fade_layer_t* 
   if (scored && ws_bytes < need)
     return set_error(FADE_ERR_CAPACITY, "tree workspace %zu bytes, %zu needed", ws_bytes, need);
   RowLens lens{}, to_sink{}, dem{};
-  int any = 0, max_tokens = 0;
+  int any = 0;
+  long long tiles = 0;   // of 16 tokens, one more than every row's at most
   for (int b = 0; b < c->batch; ++b) {
     const int n = h_n_path[b];
     if (n < 0 || n > T)
@@ -521,8 +584,9 @@ extern "C" fade_status_t fade_tree_commit(const fade_config_t* c, fade_layer_t* 
     if (n == 0) dem.v[b] = 0;
     lens.v[b] = n;
     any |= n;
-    const int total = L->h_n_sink[b] + L->h_n_mid[b] + L->h_n_recent[b] + n;
-    if (n && total > max_tokens) max_tokens = total;
+    if (n)
+      tiles += (long long)c->num_kv_heads *
+               ((L->h_n_sink[b] + (long long)L->h_n_mid[b] + L->h_n_recent[b] + n) / 16 + 2);
   }
   if (!any) return FADE_OK;
   const TreeArgs a = make_tree_args(c, L, T, q_rot, tree_k, tree_v);
@@ -530,10 +594,10 @@ extern "C" fade_status_t fade_tree_commit(const fade_config_t* c, fade_layer_t* 
   float* path_sc = scored ? static_cast<float*>(ws) : nullptr;
   const int d = c->head_dim, kb = c->middle_k_bits, vb = c->middle_v_bits;
   if (scored) {
-    st = d == 64 ? (kb == 4 ? launch_scores<64, 4>(c, a, lens, max_tokens, lse, path, path_sc, s)
-                            : launch_scores<64, 2>(c, a, lens, max_tokens, lse, path, path_sc, s))
-                 : (kb == 4 ? launch_scores<128, 4>(c, a, lens, max_tokens, lse, path, path_sc, s)
-                            : launch_scores<128, 2>(c, a, lens, max_tokens, lse, path, path_sc, s));
+    st = d == 64 ? (kb == 4 ? launch_scores<64, 4>(c, a, lens, tiles, lse, path, path_sc, s)
+                            : launch_scores<64, 2>(c, a, lens, tiles, lse, path, path_sc, s))
+                 : (kb == 4 ? launch_scores<128, 4>(c, a, lens, tiles, lse, path, path_sc, s)
+                            : launch_scores<128, 2>(c, a, lens, tiles, lse, path, path_sc, s));
     if (st) return st;
   }
   if (d == 64)
