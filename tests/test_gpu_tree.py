@@ -1,12 +1,16 @@
 """Drafted-token operators on the GPU against plain 64-bit implementations.
 
 Tolerances count roundings. u = 2^-11 is half a step of fp16 relative to the value, 2^-24 of fp32.
-Attention: a dequantised middle key rounds to fp16 once, which moves a logit by at most
-delta = u * scale * sum_c |q_c k_c|; the softmax then moves every probability by a factor within
-e^(+-2 delta); probabilities and dequantised values round to fp16 once each (u each), the output
-once (u |out|); a probability's rounding is off by half a subnormal step, 2^-25, at least, where
-the largest one is held as 2^6 or more: 2^-31 of the largest, sum |v| times over the sum of e; fp32 sums over d channels and N tokens add (N + d) 2^-24, the fast exponential and
-logarithm 2^-20.
+Attention: a middle key is fp16 plus the remainder of its rounding (at most u |k|), which meets the
+query rounded to E5M2 (off by |q| / 8, or half a subnormal step, 2^-17), so a logit moves by at most
+delta = u * scale * sum_c |k_c| (|q_c| / 8 + 2^-17); the softmax then moves every probability by a
+factor within e^(+-2 delta); probabilities and dequantised values round to fp16 once each (u each),
+the output once (u |out|); a probability's rounding is off by half a subnormal step, 2^-25, at
+least, where the largest one is held as 2^6 or more: 2^-31 of the largest, sum |v| times over the
+sum of e; fp32 sums over d channels and N tokens add (N + d) 2^-24, the fast exponential and
+logarithm 2^-20; the scaled logit's own fp32 rounding 2^-23 of the largest.
+Scores: the codes enter the products exactly; sums over d channels, the group's scale, the offset
+and the exponential round in fp32.
 """
 
 import numpy as np
@@ -258,11 +262,12 @@ class Cache:
                                    self.ws)
         return self.out.double().cpu().numpy(), self.lse.double().cpu().numpy()
 
-    def check(self, see, n_nodes=None):
+    def check(self, see, n_nodes=None, rows=None):
+        """Every node of every row, or of the rows given."""
         out, lse = self.attend(see, n_nodes)
         c = self.cfg
         G = c.num_q_heads // c.num_kv_heads
-        for b in range(c.batch):
+        for b in range(c.batch) if rows is None else rows:
             n = see.shape[1] if n_nodes is None else int(n_nodes[b])
             assert (out[b, n:] == 7).all() and (lse[b, n:] == 7).all()
             for h in range(c.num_kv_heads):
@@ -289,7 +294,8 @@ def compare(o, l, q, k, v, where):
     e = np.exp(s - m)
     p = e / e.sum()
     ref, ref_l = p @ v, m + np.log(e.sum())
-    delta = U * scale * (np.abs(k) @ np.abs(q)).max()
+    delta = U * scale * (np.abs(k) @ (np.abs(q) / 8 + 2.0 ** -17)).max() \
+        + 2.0 ** -23 * np.abs(s).max()
     sums = (len(k) + d) * 2.0 ** -24 + 2.0 ** -20
     tol = (np.expm1(2 * delta) + 2 * U + sums) * (p @ np.abs(v)) * (1 + U) + U * np.abs(ref) \
         + 2.0 ** -25 + 2.0 ** -31 / e.sum() * np.abs(v).sum(0)
@@ -334,6 +340,100 @@ def test_attention(F, B, hq, h, d, lens, T, kind, opt, ragged):
         c.dq = dev(c.q)
         c.load_tree()
     c.check(see, n if ragged else None)
+
+
+@pytest.mark.parametrize("B,hq,h,d,T,lens,opt", [
+    (40, 8, 8, 128, 16, (60, 400), {}),                        # a few blocks of query rows a CTA
+    (256, 8, 4, 64, 5, (0, 75), dict(kb=2)),                   # many one-tile blocks a CTA
+    (12, 64, 8, 64, 64, (100, 300), dict(codec="pq")),         # four blocks of rows a unit
+    (64, 16, 8, 128, 13, (64, 330), dict(codec="pq")),
+])
+def test_many_short_blocks(F, B, hq, h, d, T, lens, opt):
+    """CTAs that take many blocks of query rows one after another, ragged rows among them some
+    without nodes."""
+    rng = np.random.default_rng(B)
+    held = rng.integers(lens[0], lens[1] + 1, B).tolist()
+    c = Cache(F, rng, B, hq, h, d, held, **opt)
+    c.draft(rng, T)
+    n = rng.integers(0, T + 1, B).astype(np.int32)
+    n[0], n[B - 1] = 0, T
+    see = np.stack([plain_layout(p, T)[0] for p in random_parents(rng, B, T)])
+    c.check(see, n, sorted({0, 1, B // 3, B // 2, B - 2, B - 1}))
+    first = c.out.clone(), c.lse.clone()
+    for _ in range(3):
+        c.attend(see, n)
+        assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
+
+
+def test_more_blocks_than_one_cta_each_can_list(F):
+    """24576 blocks of query rows: the grid grows past one CTA a multiprocessor."""
+    rng = np.random.default_rng(8)
+    B, hq, h, d, T = 256, 256, 32, 64, 33
+    c = Cache(F, rng, B, hq, h, d, [9] * B, W=8)
+    c.draft(rng, 1)
+    g = torch.Generator("cuda").manual_seed(3)
+    q, k, v = (torch.randn(s, generator=g, device="cuda", dtype=torch.float16)
+               for s in ((B, T, hq, d), (B, T, h, d), (B, T, h, d)))
+    out, lse = torch.full_like(q, 7.0), torch.full((B, T, hq), 7.0, device="cuda")
+    ws = torch.empty(F.fade_tree_ws_bytes(c.cfg, T), dtype=torch.uint8, device="cuda")
+    see = plain_layout(random_parents(rng, 1, T)[0], T)[0]
+    F.fade_tree_attention(c.L, q, k, v, dev(np.tile(mask_words(see[None]), (B, 1))), None, out,
+                          lse, ws)
+    F.fade_check_status(c.L)
+    host = lambda t: t.double().cpu().numpy()
+    for b in [0, 255, *rng.integers(0, B, 10)]:
+        for u in rng.integers(0, h, 2):
+            K, V = c.unit(b, u)[3:5]
+            tk, tv = host(k[b, :, u]), host(v[b, :, u])
+            for i in {0, 32, int(rng.integers(T))}:
+                a = u * 8 + int(rng.integers(8))
+                js = np.nonzero(see[i])[0]
+                compare(host(out[b, i, a]), float(lse[b, i, a]), host(q[b, i, a]),
+                        np.concatenate([K, tk[js]]), np.concatenate([V, tv[js]]), (b, u, i, a))
+
+
+def test_offsets_past_32_bits(F):
+    """A capacity whose codes lie past 4 GiB: attention and commit of the last rows."""
+    rng = np.random.default_rng(32)
+    B, hq, h, d, T = 64, 8, 8, 128, 6
+    c = Cache(F, rng, B, hq, h, d, [300] * B, extra=131072 - 232, policy="h2o", budget=131071)
+    assert c.L.mid_k_codes[0].numel() >= 1 << 32
+    c.draft(rng, T)
+    par = np.tile(np.arange(T, dtype=np.int32) - 1, (B, 1))
+    see = np.stack([plain_layout(p, T)[0] for p in par])
+    c.check(see, None, [0, B - 1])
+    before = c.unit(B - 1, h - 1)
+    lse = c.lse.double().cpu().numpy()
+    path = np.tile(np.arange(T, dtype=np.int32), (B, 1))
+    F.fade_tree_commit(c.L, c.dq, c.lse, c.dk, c.dv, dev(path), [T] * B, c.ws)
+    F.fade_check_status(c.L)
+    now = c.unit(B - 1, h - 1)
+    assert now[:3] == (4, 238, 64)
+    want, tol = scores_reference(c, B - 1, h - 1, 1, before[3], before[5], path[B - 1], lse, "h2o")
+    assert (np.abs(now[5] - want) <= tol).all()
+    assert np.array_equal(now[3][:236], before[3][:236])   # what was in the tiers stays
+
+
+def test_nodes_keys_and_values_of_any_stride(F):
+    """Expanded (stride 0), reversed-layout and padded keys and values: the bits of contiguous
+    ones."""
+    rng = np.random.default_rng(6)
+    B, hq, h, d, T = 3, 8, 4, 64, 9
+    c = Cache(F, rng, B, hq, h, d, [200, 90, 3], policy="h2o")
+    c.draft(rng, T, fused=False)
+    see = np.stack([plain_layout(p, T)[0] for p in random_parents(rng, B, T)])
+    for k, v in ((c.dk[:1].expand(B, T, h, d), c.dv[:, :1].expand(B, T, h, d)),
+                 (c.dk[:, :, :1].expand(B, T, h, d), c.dv.permute(2, 1, 0, 3).contiguous()
+                  .permute(2, 1, 0, 3)),
+                 (torch.nn.functional.pad(c.dk, (0, 8))[..., :d],
+                  torch.nn.functional.pad(c.dv, (16, 8))[..., 16:16 + d])):
+        c.dk, c.dv = k.contiguous(), v.contiguous()
+        c.attend(see)
+        want = c.out.clone(), c.lse.clone()
+        c.dk, c.dv = k, v
+        c.attend(see)
+        assert torch.equal(c.out, want[0]) and torch.equal(c.lse, want[1])
+        c.dk, c.dv = dev(c.tk), dev(c.tv)
 
 
 def test_attention_of_an_empty_cache_with_nodes_that_see_nothing(F):
@@ -484,8 +584,8 @@ def test_commit(F, B, hq, h, d, lens, W, S, T, n_path, opt, policy):
 
 
 def scores_reference(c, b, h, G, K, old, path, lse, policy):
-    """Scores in path order, and a bound: every probability moves by its logit's roundings (the key
-    to fp16 once, fp32 sums) and lse's; each update rounds to fp32 three times."""
+    """Scores in path order, and a bound: every probability moves by its logit's roundings (fp32
+    sums) and lse's; each update rounds to fp32 three times."""
     d = K.shape[1]
     k = np.concatenate([K, c.tk[b, path, h].astype(np.float64)])
     s = np.concatenate([old, np.zeros(len(path))])
@@ -496,7 +596,7 @@ def scores_reference(c, b, h, G, K, old, path, lse, policy):
         q = c.q[b, node, h * G:(h + 1) * G].astype(np.float64)
         z = q @ k[:live].T / np.sqrt(d)
         p = np.exp(z - lse[b, node, h * G:(h + 1) * G][:, None])
-        delta = (U + (d + 4) * 2.0 ** -24) / np.sqrt(d) * (np.abs(q) @ np.abs(k[:live]).T)
+        delta = (d + 4) * 2.0 ** -24 / np.sqrt(d) * (np.abs(q) @ np.abs(k[:live]).T)
         err = (p * (np.expm1(delta) + 2.0 ** -19 + 2.0 ** -23 * np.abs(z))).sum(0)
         if policy == "h2o":
             s[:live] += p.sum(0)
@@ -509,6 +609,41 @@ def scores_reference(c, b, h, G, K, old, path, lse, policy):
         tol[:live] += 4 * 2.0 ** -24 * np.abs(s[:live])
         delta_max = max(delta_max, delta.max())
     return s, tol + 2.0 ** -30
+
+
+@pytest.mark.parametrize("policy", ["h2o", "ema"])
+@pytest.mark.parametrize("B,hq,h,d,hi,kb", [(70, 8, 2, 64, 300, 4), (200, 4, 4, 128, 90, 2),
+                                            (5, 16, 2, 128, 4000, 4)])
+def test_scores_of_ragged_rows(F, B, hq, h, d, hi, kb, policy):
+    """Rows of different lengths and paths (some empty): scores by the 64-bit accumulation, and
+    the same bits from a second cache."""
+    T = 12
+    make = lambda: Cache(F, np.random.default_rng(B), B, hq, h, d,
+                         np.random.default_rng(B + 1).integers(0, hi, B).tolist(), W=16,
+                         policy=policy, kb=kb)
+    c, twin = make(), make()
+    rng = np.random.default_rng(4)
+    c.draft(rng, T)
+    see = np.tile(np.tril(np.ones((T, T), bool)), (B, 1, 1))
+    _, lse = c.attend(see)
+    path = np.tile(np.arange(T, dtype=np.int32), (B, 1))
+    n_path = rng.integers(0, T + 1, B)
+    n_path[B // 2] = 0
+    some = sorted({0, 1, B // 2, B - 1, *rng.integers(0, B, 4)})
+    before = {b: [c.unit(b, u) for u in range(h)] for b in some}
+    for x in (c, twin):
+        F.fade_tree_commit(x.L, c.dq, c.lse, c.dk, c.dv, dev(path), n_path, c.ws)
+        F.fade_check_status(x.L)
+    for b in some:
+        for u in range(h):
+            got, old = c.unit(b, u)[5], before[b][u]
+            if n_path[b] == 0:
+                assert np.array_equal(got, old[5])
+                continue
+            want, tol = scores_reference(c, b, u, hq // h, old[3], old[5], path[b, :n_path[b]],
+                                         lse, policy)
+            assert (np.abs(got - want) <= tol).all(), (b, u)
+            assert np.array_equal(got, twin.unit(b, u)[5])
 
 
 def test_commit_of_a_bad_path_is_recorded(F):
