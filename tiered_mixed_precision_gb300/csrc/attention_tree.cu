@@ -56,8 +56,7 @@ struct Shape {
   static constexpr int STAGES = FIXED + 2 * STAGE <= 226 * 1024 ? 2 : 1;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
   static constexpr int SOFT = 256;                            // softmax threads
-  static constexpr int KT = 128, VT = 128;                    // threads that unpack K, and V
-  static constexpr int UNPACK = KT + VT;
+  static constexpr int UNPACK = 256;                          // threads that unpack K and V
   static constexpr int THREADS = SOFT + UNPACK + 128;         // and four warps: two issue, one prefetches
   static constexpr int TMEM = 512;                            // columns: S (and P) 2 x 128, O 2 x D
 };
@@ -571,9 +570,10 @@ __device__ __forceinline__ void tile_to_l2(const AttnTreeArgs& p, const Segment&
   }
 }
 
-// One CTA per SM, roles that meet at mbarriers. Some warps unpack K and as many V, each into a ring
-// of STAGES (the next tile's codes on their way into the registers); one warp issues S = Q K^T, one O += P V,
-// one asks for coming tiles in L2; 8 warps do the softmax, 16 query rows at a time (a thread: two
+// One CTA per SM, roles that meet at mbarriers. Eight warps unpack a tile's K, then its V, into rings
+// of STAGES (the next tile's codes on their way into the registers; as four warps for K and four for V
+// the K side was the slower one, 188 us against 184 at the throughput workload, 568 against 525 on
+// long rows); one warp issues S = Q K^T, one O += P V, one asks for coming tiles in L2; 8 warps do the softmax, 16 query rows at a time (a thread: two
 // rows, spread over four lanes). A tile's chain (S, softmax, P V) is long and mostly waiting, so even and
 // odd tiles run as two streams, each with its softmax warps, its S (over which P is written), its
 // references and its own O; the segment's end joins them. R: 16-row halves of each 32-lane quarter
@@ -628,8 +628,8 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
     *sDone = 0;
     *sDead = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(kFull + 8 * i, Sh::KT / 32);
-      mbar_init(vFull + 8 * i, Sh::VT / 32);
+      mbar_init(kFull + 8 * i, Sh::UNPACK / 32);
+      mbar_init(vFull + 8 * i, Sh::UNPACK / 32);
       mbar_init(kFree + 8 * i, 1);
       mbar_init(vFree + 8 * i, 1);
       mbar_init(sFull + 8 * i, 1);
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
       mbar_init(oFull + 8 * i, 1);
     }
     mbar_init(oRead, Sh::SOFT / 32);
-    mbar_init(qFull, Sh::VT / 32);
+    mbar_init(qFull, Sh::UNPACK / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if constexpr (Sh::PQ) {
@@ -654,7 +654,10 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
     __syncwarp();
     asm volatile("bar.sync %0, 64;" ::"r"(4 + pair) : "memory");
   };
-  auto wait = [&](uint32_t bar, int phase) { wait_phase(bar, phase, bar0 + 140); };
+  auto wait = [&](uint32_t bar, int phase) {
+    wait_phase(bar, phase, bar0 + 140);
+    __syncwarp();
+  };
   auto arrive = [&](uint32_t bar) {   // once per warp
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -662,20 +665,13 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
 
   if (warp >= Sh::SOFT / 32 && warp < (Sh::SOFT + Sh::UNPACK) / 32) {
     // ================================================================ unpacking
-    const bool is_v = warp >= (Sh::SOFT + Sh::KT) / 32;
-    int it = 0, seg = 0, tok, gq;
-    item_of<D>(is_v ? tid - Sh::SOFT - Sh::KT : tid - Sh::SOFT, tok, gq);
+    // every warp its share of a tile's K, then of its V: K asks for more instructions than V, and
+    // half the items a thread are half the code
+    constexpr int NI = kTok * (D / 32) / Sh::UNPACK, APART = kTok / NI, ROWB = APART * 128;
+    const bool first = tid == Sh::SOFT;
+    int it = 0, tok, gq;
+    item_of<D>(tid - Sh::SOFT, tok, gq);
     const uint32_t at16 = group_at(tok, gq), at8 = low_at(tok, gq);
-    // one warp of the side watches the mbarrier, the others block at a named barrier: eight
-    // watching warps would take the softmax's issue slots
-    auto side_wait = [&](uint32_t bar, int phase) {
-      if (warp == Sh::SOFT / 32 || warp == (Sh::SOFT + Sh::KT) / 32) wait(bar, phase);
-      __syncwarp();
-      if (is_v)
-        asm volatile("bar.sync 3, %0;" ::"n"(Sh::VT) : "memory");
-      else
-        asm volatile("bar.sync 2, %0;" ::"n"(Sh::KT) : "memory");
-    };
     // an FP16 token's share of a row (zeros past the nodes)
     auto f16_load = [&](const Segment& s, int j, bool v, uint4 (&x)[4]) {
 #pragma unroll
@@ -687,94 +683,79 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         for (int c = 0; c < 4; ++c) x[c] = src[c];
       }
     };
-    if (!is_v) {   // -------------------------------------------- keys
-      constexpr int NI = kTok * (D / 32) / Sh::KT, APART = kTok / NI, ROWB = APART * 128;
-      const Fields<KB> kf;
+    const Fields<KB> kf;
+    const Fields<Sh::PQ ? 4 : VB> vf;
 #pragma unroll 1
-      for (; seg < n_seg; ++seg) {
-        const Segment& s = sSeg[seg];
-        const int f16 = s.f16, t_end = s.end;
-        int t = s.begin;
-        Codes<D, KB, true, NI> c;
-        c.start(a.mk[s.cur], a.mks[s.cur], (size_t)s.unit * a.C, s.n_mid,
-                max(t - f16, 0) * kTok + tok, gq);
-        if (t >= f16) c.load_all();
+    for (int seg = 0; seg < n_seg; ++seg) {
+      const Segment& s = sSeg[seg];
+      const int f16 = s.f16, t_end = s.end, n_mid = s.n_mid, n16 = s.n_sink + s.n_rec;
+      uint32_t* bad = sBad + 2 * (seg & 7);
+      int t = s.begin;
+      Codes<D, KB, true, NI> ck;
+      Codes<D, Sh::PQ ? 2 : VB, !Sh::PQ, NI> cv;
+      const int t0 = max(t - f16, 0) * kTok + tok;
+      ck.start(a.mk[s.cur], a.mks[s.cur], (size_t)s.unit * a.C, n_mid, t0, gq);
+      cv.start(a.mv[s.cur], a.mvs[s.cur], (size_t)s.unit * a.C, n_mid, t0, gq);
+      if (t >= f16) {
+        ck.load_all();
+        cv.load_all();
+      }
 #pragma unroll 1
-        for (; t < t_end && t < f16; ++t, ++it) {
-          const int st = it % ST, use = it / ST;
-          if (use > 0) side_wait(kFree + 8 * st, use - 1);
-          if (t + 1 == f16 && t + 1 < t_end) c.load_all();
+      for (; t < t_end; ++t, ++it) {
+        const int st = it % ST, use = it / ST;
+        // ---------------------------------------------- keys
+        if (use > 0) wait(kFree + 8 * st, use - 1);
+        const uint32_t k = kTile(st) + at16, v = vTile(st) + at16;
+        if (t < f16) {
+          if (t + 1 == f16 && t + 1 < t_end) {
+            ck.load_all();
+            cv.load_all();
+          }
 #pragma unroll 1
           for (int i = 0; i < NI; ++i) {
             uint4 x[4];
             f16_load(s, t * kTok + tok + APART * i, false, x);
-            store_f16<KO>(kTile(st) + at16 + i * ROWB, x);
+            store_f16<KO>(k + i * ROWB, x);
           }
-          fence_proxy_async_smem();
-          arrive(kFull + 8 * st);
-        }
-#pragma unroll 1
-        for (; t < t_end; ++t, ++it) {
-          const int st = it % ST, use = it / ST;
-          if (use > 0) side_wait(kFree + 8 * st, use - 1);
-          const uint32_t k = kTile(st) + at16, l = kLow(st) + at8;
+        } else {
+          const uint32_t l = kLow(st) + at8;
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
-            store_codes<KB, Sh::LOW>(k + i * ROWB, l + i * ROWB, kf, c.w[i], c.sc[i]);
-            if (t + 1 < t_end) c.load(i);
+            store_codes<KB, Sh::LOW>(k + i * ROWB, l + i * ROWB, kf, ck.w[i], ck.sc[i]);
+            if (t + 1 < t_end) ck.load(i);
           }
-          fence_proxy_async_smem();
-          arrive(kFull + 8 * st);
-          if (tid == Sh::SOFT) *sDone = it + 1;
-          c.next_tile();
+          ck.next_tile();
         }
-      }
-    } else {   // ------------------------------------------------ values, and Q
-      constexpr int NI = kTok * (D / 32) / Sh::VT, APART = kTok / NI, ROWB = APART * 128;
-      const Fields<Sh::PQ ? 4 : VB> vf;
+        fence_proxy_async_smem();
+        arrive(kFull + 8 * st);
+        if (first) *sDone = it + 1;
+        // ---------------------------------------------- a segment's Q
+        // matrix row 32 q + i holds query row 16 q + i (R = 1, i < 16) or 32 q + i; stored once the
+        // last product that reads the old one is done
+        if (t == s.begin) {
+          if (first) bad[0] = bad[1] = 0;
+          if (it > 0) wait(kFree + 8 * ((it - 1) % ST), (it - 1) / ST);
 #pragma unroll 1
-      for (; seg < n_seg; ++seg) {
-        const Segment& s = sSeg[seg];
-        const int f16 = s.f16, t_end = s.end, n_mid = s.n_mid, n16 = s.n_sink + s.n_rec;
-        uint32_t* bad = sBad + 2 * (seg & 7);
-        int t = s.begin;
-        Codes<D, Sh::PQ ? 2 : VB, !Sh::PQ, NI> c;
-        c.start(a.mv[s.cur], a.mvs[s.cur], (size_t)s.unit * a.C, n_mid,
-                max(t - f16, 0) * kTok + tok, gq);
-        if (t >= f16) c.load_all();
-        if (tid == Sh::SOFT + Sh::KT) bad[0] = bad[1] = 0;
-        // Q: matrix row 32 q + i holds query row 16 q + i (R = 1, i < 16) or 32 q + i; stored once
-        // the last product that reads the old one is done
-#pragma unroll 1
-        for (int i = 0; i < NI; i += 2) {
-          uint4 x[2][4] = {};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int row = tok + APART * (i + j), in = row & 31, qr = (row >> 5) * (16 * R) + in;
+          for (int i = 0; i < NI; ++i) {
+            uint4 x[4] = {};
+            const int row = tok + APART * i, in = row & 31, qr = (row >> 5) * (16 * R) + in;
             if (in < 16 * R && qr < s.rows) {
               const int node = (s.r0 + qr) >> a.log_g, gh = (s.r0 + qr) & (a.G - 1);
               const uint4* src = reinterpret_cast<const uint4*>(
                   a.q + (((size_t)s.b * a.T + node) * a.Hq + s.h * a.G + gh) * D + 32 * gq);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[j][e] = __ldg(src + e);
+              for (int e = 0; e < 4; ++e) x[e] = __ldg(src + e);
             }
+            store_f16<KO>(sQ + at16 + i * ROWB, x);
+            if constexpr (Sh::LOW) store_low(sQL + at8 + i * ROWB, x);
           }
-          if (i == 0 && it > 0) wait(kFree + 8 * ((it - 1) % ST), (it - 1) / ST);
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            store_f16<KO>(sQ + at16 + (i + j) * ROWB, x[j]);
-            if constexpr (Sh::LOW) store_low(sQL + at8 + (i + j) * ROWB, x[j]);
-          }
+          fence_proxy_async_smem();
+          arrive(qFull);
+          asm volatile("bar.sync 2, %0;" ::"n"(Sh::UNPACK) : "memory");   // the nodes' bits are cleared
         }
-        fence_proxy_async_smem();
-        arrive(qFull);
-        asm volatile("bar.sync 3, %0;" ::"n"(Sh::VT) : "memory");   // the nodes' bits are cleared
-#pragma unroll 1
-        for (; t < t_end && t < f16; ++t, ++it) {
-          const int st = it % ST, use = it / ST;
-          if (use > 0) side_wait(vFree + 8 * st, use - 1);
-          if (t + 1 == f16 && t + 1 < t_end) c.load_all();
+        // ---------------------------------------------- values
+        if (use > 0) wait(vFree + 8 * st, use - 1);
+        if (t < f16) {
 #pragma unroll 1
           for (int i = 0; i < NI; ++i) {
             uint4 x[4];
@@ -783,19 +764,13 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
             // are left out of the product and put into the rows that see it at the end
             const int node = t * kTok + tok + APART * i - n16;
             if (node >= 0 && clear_nonfinite(x)) atomicOr(bad + (node >> 5), 1u << (node & 31));
-            store_f16<VO>(vTile(st) + at16 + i * ROWB, x);
+            store_f16<VO>(v + i * ROWB, x);
           }
-          fence_proxy_async_smem();
-          arrive(vFull + 8 * st);
-        }
-#pragma unroll 1
-        for (; t < t_end; ++t, ++it) {
-          const int st = it % ST, use = it / ST;
-          if (use > 0) side_wait(vFree + 8 * st, use - 1);
+        } else {
           const int left = n_mid - (t - f16) * kTok - tok;   // tokens from this row on
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
-            const uint32_t v = vTile(st) + at16 + i * ROWB;
+            const uint32_t vi = v + i * ROWB;
             const bool in = left > APART * i;
             if constexpr (Sh::PQ) {
               // lane-dependent order of the eight sub-spaces: the 32 lanes of a warp read 32
@@ -804,20 +779,20 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const int ss = (e + tok) & 7;
-                const uint32_t w = (ss & 4) ? c.w[i][1] : c.w[i][0];
+                const uint32_t w = (ss & 4) ? cv.w[i][1] : cv.w[i][0];
                 const int code = (w >> (8 * (ss & 3))) & 255;
                 const uint2 x = in ? sCB[code * (D / 4) + 8 * gq + ss] : make_uint2(0u, 0u);
-                st_shared8((v ^ (16 * (ss >> 1))) + 8 * (ss & 1), x.x, x.y);
+                st_shared8((vi ^ (16 * (ss >> 1))) + 8 * (ss & 1), x.x, x.y);
               }
             } else {
-              store_codes<VB, false>(v, 0, vf, c.w[i], in ? c.sc[i] : (uint16_t)0);
+              store_codes<VB, false>(vi, 0, vf, cv.w[i], in ? cv.sc[i] : (uint16_t)0);
             }
-            if (t + 1 < t_end) c.load(i);
+            if (t + 1 < t_end) cv.load(i);
           }
-          fence_proxy_async_smem();
-          arrive(vFull + 8 * st);
-          c.next_tile();
+          cv.next_tile();
         }
+        fence_proxy_async_smem();
+        arrive(vFull + 8 * st);
       }
     }
   } else if (warp >= (Sh::SOFT + Sh::UNPACK) / 32) {
@@ -844,7 +819,6 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
           if (it >= 2) wait(oFull + 8 * (it & 1), (it >> 1) - 1);   // the buffer's P has been read
           if (i == 0) wait(qFull, seg);
           wait(kFull + 8 * st, it / ST);
-          __syncwarp();
           fence_after();
           if (issuer) {
             const uint32_t d = tm + 128 * (it & 1);
@@ -937,7 +911,6 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
       for (int t = t0; t < t_end; t += 2) {
         // S of the tile; the stream's last O += P V is then complete, too
         wait(sFull + 8 * stream, (it0 + t - t_begin) >> 1);
-        __syncwarp();
         fence_after();
         const bool f16 = t < f16_tiles;
 #pragma unroll 1
@@ -1046,7 +1019,6 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
       // the stream's last O (S of its last tile said that the one before is complete)
       const int last = it0 + t_end - t_begin - 1;
       if (t0 < t_end) wait(oFull + 8 * stream, (last - ((last ^ stream) & 1)) >> 1);
-      __syncwarp();
       fence_after();
 
       // ---------------------------------------------- the segment's result: both streams joined
