@@ -296,8 +296,8 @@ struct Fields {
 // upper bytes of their fp16 form, in the same order.
 template <int BITS, bool LOW>
 __device__ __forceinline__ void store_codes(uint32_t at, uint32_t low, const Fields<BITS>& f,
-                                            const uint32_t* x, uint16_t scale) {
-  const __half2 s = __half2half2(__ushort_as_half(scale));
+                                            const uint32_t* x, uint32_t scale) {
+  const __half2 s = __half2half2(__ushort_as_half((unsigned short)scale));
   if constexpr (BITS == 4) {
     uint32_t lo[8];
 #pragma unroll
@@ -395,9 +395,9 @@ __device__ __forceinline__ void ld_words(const uint8_t* p, uint32_t* w) {
   else
     asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
 }
-__device__ __forceinline__ uint16_t ld_half(const uint16_t* p) {
-  uint16_t x;
-  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(x) : "l"(p));
+__device__ __forceinline__ uint32_t ld_half(const uint16_t* p) {
+  uint32_t x;   // a whole register: packing it would wait for the load
+  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=r"(x) : "l"(p));
   return x;
 }
 
@@ -407,7 +407,7 @@ template <int D, int W, bool SCALED, int ITEMS>
 struct Codes {
   static constexpr int G = D / 32, APART = kTok / ITEMS;
   uint32_t w[ITEMS][W];
-  uint16_t sc[ITEMS];
+  uint32_t sc[ITEMS];
   const uint8_t* codes;
   const uint16_t* scales;
   int last;   // tokens from the thread's first row of the tile to come to the tier's last
@@ -437,15 +437,24 @@ struct Codes {
   }
 };
 
-// The key or value row of FP16 token j of a unit (sinks, then the ring oldest first, then nodes).
-__device__ __forceinline__ const uint16_t* f16_row(const TreeArgs& a, int D, int b, int h, int unit,
-                                                   int n_sink, int n_rec, int head, int j, bool v) {
-  if (j < n_sink) return (v ? a.sink_v : a.sink_k) + ((size_t)unit * a.S + j) * D;
+// The key and value rows of FP16 token j of a unit (sinks, then the ring oldest first, then nodes).
+struct Rows16 {
+  const uint16_t *k, *v;
+};
+__device__ __forceinline__ Rows16 f16_rows(const TreeArgs& a, int D, int b, int h, int unit,
+                                           int n_sink, int n_rec, int head, int j) {
+  if (j < n_sink) {
+    const size_t at = ((size_t)unit * a.S + j) * D;
+    return {a.sink_k + at, a.sink_v + at};
+  }
   j -= n_sink;
-  if (j < n_rec) return (v ? a.rec_v : a.rec_k) + ((size_t)unit * a.W + (head + j) % a.W) * D;
+  if (j < n_rec) {
+    const size_t at = ((size_t)unit * a.W + (head + j) % a.W) * D;
+    return {a.rec_k + at, a.rec_v + at};
+  }
   j -= n_rec;
-  const fade_heads_t& t = v ? a.tv : a.tk;
-  return t.x + b * t.row_stride + j * t.token_stride + h * t.head_stride;
+  return {a.tk.x + b * a.tk.row_stride + j * a.tk.token_stride + h * a.tk.head_stride,
+          a.tv.x + b * a.tv.row_stride + j * a.tv.token_stride + h * a.tv.head_stride};
 }
 
 // Waits for the phase-th completion of an mbarrier, for kWaitCycles at most: a wait that gives up sets
@@ -493,13 +502,14 @@ __device__ __forceinline__ int list_segments(const AttnTreeArgs& p, const int* p
     int b = row_of(pre, a.B, g_first);
     RowTiles rt = row_tiles<ROWS>(a, p.n_nodes, b);
     int blk = (g_first - pre[b]) / rt.tiles;
-    while (b < a.B && blk + k >= a.H * rt.blocks) {   // on to the row that holds it
+    while (blk + k >= a.H * rt.blocks) {   // on to the row that holds it, if the CTA gets there
       k -= a.H * rt.blocks - blk;
       blk = 0;
-      if (++b < a.B) rt = row_tiles<ROWS>(a, p.n_nodes, b);
+      if (pre[++b] >= g_end) break;
+      rt = row_tiles<ROWS>(a, p.n_nodes, b);
     }
     blk += k;
-    const int g0 = b < a.B ? pre[b] + blk * rt.tiles : g_end;
+    const int g0 = pre[b] < g_end ? pre[b] + blk * rt.tiles : g_end;
     if (g0 < g_end) {
       Segment s;
       s.b = b;
@@ -544,14 +554,15 @@ __device__ __forceinline__ void tile_to_l2(const AttnTreeArgs& p, const Segment&
   if (t < s.f16) {
     const int end = min((t + 1) * kTok, s.n_sink + s.n_rec + s.n);
 #pragma unroll 1
-    for (int j = t * kTok + lane; j < end; j += 32)
-#pragma unroll 1
-      for (int v = 0; v < 2; ++v) {
-        const uint16_t* x =
-            f16_row(a, D, s.b, s.h, s.unit, s.n_sink, s.n_rec, s.head, j, v != 0);
-        line(x);
-        if (D == 128) line(x + 64);
+    for (int j = t * kTok + lane; j < end; j += 32) {
+      const Rows16 x = f16_rows(a, D, s.b, s.h, s.unit, s.n_sink, s.n_rec, s.head, j);
+      line(x.k);
+      line(x.v);
+      if (D == 128) {
+        line(x.k + 64);
+        line(x.v + 64);
       }
+    }
   } else {
     // contiguous runs of codes and scales, a 128-byte line a lane; the stride of a unit is a multiple
     // of 64 rows, so a run may pass the tier's end but not the buffer's
@@ -672,16 +683,17 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
     int it = 0, tok, gq;
     item_of<D>(tid - Sh::SOFT, tok, gq);
     const uint32_t at16 = group_at(tok, gq), at8 = low_at(tok, gq);
-    // an FP16 token's share of a row (zeros past the nodes)
-    auto f16_load = [&](const Segment& s, int j, bool v, uint4 (&x)[4]) {
+    // a thread's 32 channels of a row (zeros without one)
+    auto load_row = [&](const uint16_t* row, uint4 (&x)[4]) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (j < s.n_sink + s.n_rec + s.n) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            f16_row(a, D, s.b, s.h, s.unit, s.n_sink, s.n_rec, s.head, j, v) + 32 * gq);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[c] = src[c];
-      }
+      for (int c = 0; c < 4; ++c)
+        x[c] = row ? *reinterpret_cast<const uint4*>(row + 32 * gq + 8 * c)
+                   : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto f16_row = [&](const Segment& s, int j) {
+      return j < s.n_sink + s.n_rec + s.n
+                 ? f16_rows(a, D, s.b, s.h, s.unit, s.n_sink, s.n_rec, s.head, j)
+                 : Rows16{nullptr, nullptr};
     };
     const Fields<KB> kf;
     const Fields<Sh::PQ ? 4 : VB> vf;
@@ -707,15 +719,14 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         if (use > 0) wait(kFree + 8 * st, use - 1);
         const uint32_t k = kTile(st) + at16, v = vTile(st) + at16;
         if (t < f16) {
+          uint4 x[NI][4];
+#pragma unroll
+          for (int i = 0; i < NI; ++i) load_row(f16_row(s, t * kTok + tok + APART * i).k, x[i]);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) store_f16<KO>(k + i * ROWB, x[i]);
           if (t + 1 == f16 && t + 1 < t_end) {
             ck.load_all();
             cv.load_all();
-          }
-#pragma unroll 1
-          for (int i = 0; i < NI; ++i) {
-            uint4 x[4];
-            f16_load(s, t * kTok + tok + APART * i, false, x);
-            store_f16<KO>(k + i * ROWB, x);
           }
         } else {
           const uint32_t l = kLow(st) + at8;
@@ -733,21 +744,22 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         // matrix row 32 q + i holds query row 16 q + i (R = 1, i < 16) or 32 q + i; stored once the
         // last product that reads the old one is done
         if (t == s.begin) {
+          uint4 xq[NI][4];
           if (first) bad[0] = bad[1] = 0;
-          if (it > 0) wait(kFree + 8 * ((it - 1) % ST), (it - 1) / ST);
-#pragma unroll 1
-          for (int i = 0; i < NI; ++i) {
-            uint4 x[4] = {};
-            const int row = tok + APART * i, in = row & 31, qr = (row >> 5) * (16 * R) + in;
-            if (in < 16 * R && qr < s.rows) {
-              const int node = (s.r0 + qr) >> a.log_g, gh = (s.r0 + qr) & (a.G - 1);
-              const uint4* src = reinterpret_cast<const uint4*>(
-                  a.q + (((size_t)s.b * a.T + node) * a.Hq + s.h * a.G + gh) * D + 32 * gq);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = __ldg(src + e);
-            }
-            store_f16<KO>(sQ + at16 + i * ROWB, x);
-            if constexpr (Sh::LOW) store_low(sQL + at8 + i * ROWB, x);
+          for (int i = 0; i < NI; ++i) {
+            const int row = tok + APART * i, in = row & 31, qr = (row >> 5) * (16 * R) + in;
+            const int node = (s.r0 + qr) >> a.log_g, gh = (s.r0 + qr) & (a.G - 1);
+            load_row(in < 16 * R && qr < s.rows
+                         ? a.q + (((size_t)s.b * a.T + node) * a.Hq + s.h * a.G + gh) * D
+                         : nullptr,
+                     xq[i]);
+          }
+          if (it > 0) wait(kFree + 8 * ((it - 1) % ST), (it - 1) / ST);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            store_f16<KO>(sQ + at16 + i * ROWB, xq[i]);
+            if constexpr (Sh::LOW) store_low(sQL + at8 + i * ROWB, xq[i]);
           }
           fence_proxy_async_smem();
           arrive(qFull);
@@ -759,7 +771,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
 #pragma unroll 1
           for (int i = 0; i < NI; ++i) {
             uint4 x[4];
-            f16_load(s, t * kTok + tok + APART * i, true, x);
+            load_row(f16_row(s, t * kTok + tok + APART * i).v, x);
             // a node's infinities and NaN would reach the rows that do not see it (0 * inf): they
             // are left out of the product and put into the rows that see it at the end
             const int node = t * kTok + tok + APART * i - n16;
@@ -785,7 +797,7 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
                 st_shared8((vi ^ (16 * (ss >> 1))) + 8 * (ss & 1), x.x, x.y);
               }
             } else {
-              store_codes<VB, false>(vi, 0, vf, cv.w[i], in ? cv.sc[i] : (uint16_t)0);
+              store_codes<VB, false>(vi, 0, vf, cv.w[i], in ? cv.sc[i] : 0u);
             }
             if (t + 1 < t_end) cv.load(i);
           }
