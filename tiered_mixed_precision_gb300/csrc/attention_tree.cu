@@ -61,12 +61,19 @@ struct Shape {
   static constexpr int TMEM = 512;                            // columns: S (and P) 2 x 128, O 2 x D
 };
 
+// What a CTA leaves for the joining kernel: its tiles, and the block of query rows that begins in it
+// and ends in CTA `last` (-1: none; a block within one CTA is finished there).
+struct Joint {
+  int tiles, last, slot, b, h, r0, rows, pad;
+};
+
 struct AttnTreeArgs {
   TreeArgs a;
   const uint64_t* mask;
   const int32_t* n_nodes;
   uint16_t* out;
   float* lse;
+  Joint* joint;  // per CTA
   float* part;   // per CTA two partials: [rows][2] (m, L), then [rows][D] O
 };
 
@@ -581,15 +588,24 @@ __device__ __forceinline__ void tile_to_l2(const AttnTreeArgs& p, const Segment&
   }
 }
 
-// One CTA per SM, roles that meet at mbarriers. Eight warps unpack a tile's K, then its V, into rings
-// of STAGES (the next tile's codes on their way into the registers; as four warps for K and four for V
-// the K side was the slower one, 188 us against 184 at the throughput workload, 568 against 525 on
-// long rows); one warp issues S = Q K^T, one O += P V, one asks for coming tiles in L2; 8 warps do the softmax, 16 query rows at a time (a thread: two
-// rows, spread over four lanes). A tile's chain (S, softmax, P V) is long and mostly waiting, so even and
-// odd tiles run as two streams, each with its softmax warps, its S (over which P is written), its
-// references and its own O; the segment's end joins them. R: 16-row halves of each 32-lane quarter
-// of tensor memory in use: up to 64 query rows take lanes 0..15 of every quarter (R = 1), which
-// gives each scheduler of the SM a share of the softmax; otherwise 128 (R = 2).
+// One CTA per SM, roles that meet at mbarriers. Eight warps unpack a tile's K, then its V, into
+// rings of STAGES, the next tile's codes on their way into the registers; one warp issues
+// S = Q K^T, one O += P V, one asks for coming tiles in L2; 8 warps do the softmax, 16 query rows at
+// a time (a thread: two rows, spread over four lanes). A tile's chain (S, softmax, P V) is long and
+// mostly waiting, so even and odd tiles run as two streams, each with its softmax warps, its S (over
+// which P is written), its references and its own O; the segment's end joins them. R: 16-row halves
+// of each 32-lane quarter of tensor memory in use: up to 64 query rows take lanes 0..15 of every
+// quarter (R = 1), which gives each scheduler of the SM a share of the softmax; otherwise 128 (R = 2).
+//
+// What bounds it: the unpacking warps, which wait for 6 % of the time (a tile costs them some 800
+// instructions a scheduler, and every segment the latencies of its FP16 tile and its Q).
+// Four warps for K and four for V left the K side as the slower one: 188 and 568 us where all
+// eight on both take 184 and 524 (the two workloads below). Without softmax and products the kernel
+// still takes 157 and 385, without the unpacking arithmetic, stores and loads as well 105 and 221.
+// Measured, unpacking and joining included: 64 rows of 4096 middle tokens, 8 KV heads of d = 128,
+// INT4 K and INT2 V, 16 nodes of 4 query heads: 173 us (271 MB, 61 GFLOP, of which the copy rate
+// asks 41 us). 4 rows of 65 to 131 thousand tokens, 64 nodes: 514 us (409 GFLOP: 211 us at the rate
+// of a large matrix product).
 template <int D, int KB, int VB, int R>
 __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
     tree_attention_kernel(const __grid_constant__ AttnTreeArgs p) {
@@ -626,8 +642,18 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
   const int N = sPre[a.B];
   const int g_first = cta_start(N, gridDim.x, blockIdx.x);
   const int g_end = cta_start(N, gridDim.x, blockIdx.x + 1);
-  if (g_first >= g_end) return;   // uniform over the CTA; nothing allocated yet
+  if (g_first >= g_end) {   // uniform over the CTA; nothing allocated yet
+    if (tid == 0) p.joint[blockIdx.x] = Joint{0, -1};
+    return;
+  }
   const int n_seg = list_segments<ROWS>(p, sPre, g_first, g_end, sSeg);
+  if (tid == Sh::THREADS - 32) {
+    const Segment& s = sSeg[n_seg - 1];
+    Joint j{g_end - g_first, -1, n_seg == 1 ? 0 : 1, s.b, s.h, s.r0, s.rows, 0};
+    if (s.begin == 0 && s.end < s.tiles)
+      j.last = cta_of(N, gridDim.x, g_end - s.end + s.tiles - 1);
+    p.joint[blockIdx.x] = j;
+  }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(sTm)),
@@ -1151,52 +1177,44 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
 }
 
 // Joins the partials of a block of query rows that several CTAs shared, in the order of their
-// tiles. CTA x takes the block in which the tiles of CTA x end and those of x + 1 begin, if x is
-// the first to share it: one warp a row, lane l its channels (in V's order) 2l + 64 i and the next.
+// tiles. CTA x takes the block that begins in CTA x of the attention kernel and ends in a later one
+// (what that CTA left says which; without it, the schedule's divisions and searches took longer than
+// the sums): one warp a row, lane l its channels (in V's order) 2l + 64 i and the next. At one request
+// (2 blocks of 33 partials) the attention call took 30.6 us with the schedule derived here and the
+// last partials loaded one by one, 24 us now.
 template <int D, int VB, int R>
-__global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ AttnTreeArgs p,
-                                                           int P) {
+__global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ AttnTreeArgs p) {
   constexpr int ROWS = 64 * R, VO = order_of(VB);
-  __shared__ int pre[257];
   const TreeArgs& a = p.a;
-  tile_prefix<ROWS>(a, p.n_nodes, pre);
-  const int N = pre[a.B];
-  const int g = cta_start(N, P, blockIdx.x + 1);
   // a programmatic dependent of the attention kernel: its partials are complete from here on (and
   // no CTA ends before it, so that what follows on the stream finds it done)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (g >= N) return;
-  const int b = row_of(pre, a.B, g);
-  const RowTiles rt = row_tiles<ROWS>(a, p.n_nodes, b);
-  const int blk = (g - pre[b]) / rt.tiles, h = blk / rt.blocks, qb = blk % rt.blocks;
-  const int begin = pre[b] + blk * rt.tiles, end = begin + rt.tiles;
-  if (g == begin || cta_start(N, P, blockIdx.x) > begin) return;
-  const int c1 = cta_of(N, P, end - 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  {
-    const int row = blockIdx.y * 8 + warp, rr = qb * ROWS + row;
-    if (rr >= rt.n * a.G) return;
-    float M = -INFINITY, L = 0.f, o[D / 32];
+  const int x0 = blockIdx.x;
+  const Joint jt = p.joint[x0];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * 8 + warp;
+  if (row >= jt.rows || jt.last < 0) return;
+  float M = -INFINITY, L = 0.f, o[D / 32];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-    // up to 32 partials at a time: lane l reads the (m, L) of the l-th and weighs it, then every
-    // lane adds its channels of all of them, the loads independent of each other
-    for (int base = blockIdx.x; base <= c1; base += 32) {
-      const int c = base + lane;
-      const int g0 = c <= c1 ? cta_start(N, P, c) : 0;
-      const bool in = c <= c1 && g0 < cta_start(N, P, c + 1);   // a CTA with tiles
-      const int slot = 2 * c + (g0 >= begin ? 0 : 1);
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (in) ml = *reinterpret_cast<const float2*>(p.part + (size_t)slot * ROWS * (D + 2) + 2 * row);
-      const float Mn = fmaxf(M, warp_max(ml.x));
-      const float fo = M == -INFINITY ? 0.f : ex2(M - Mn);
-      const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - Mn);
-      L = fmaf(L, fo, warp_sum(ml.y * w));
+  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+  // up to 32 partials at a time: lane l reads the (m, L) of the l-th and weighs it, then every lane
+  // adds its channels, the loads of eight partials at a time independent of each other (lanes past
+  // the last partial repeat its slot with weight 0)
+  for (int base = x0; base <= jt.last; base += 32) {
+    const int c = min(base + lane, jt.last);
+    const int slot = 2 * c + (c == x0 ? jt.slot : 0);
+    float2 ml = *reinterpret_cast<const float2*>(p.part + (size_t)slot * ROWS * (D + 2) + 2 * row);
+    if (base + lane > jt.last || p.joint[c].tiles == 0) ml = make_float2(-INFINITY, 0.f);
+    const float Mn = fmaxf(M, warp_max(ml.x));
+    const float fo = M == -INFINITY ? 0.f : ex2(M - Mn);
+    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - Mn);
+    L = fmaf(L, fo, warp_sum(ml.y * w));
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] *= fo;
-      const int n = min(32, c1 - base + 1);
-#pragma unroll 8
-      for (int j = 0; j < n; ++j) {
+    for (int i = 0; i < D / 32; ++i) o[i] *= fo;
+    const int n = min(32, jt.last - base + 1);
+#pragma unroll 1
+    for (int j0 = 0; j0 < n; j0 += 8) {
+#pragma unroll
+      for (int j = j0; j < j0 + 8; ++j) {
         const float wj = __shfl_sync(0xffffffffu, w, j);
         const int sj = __shfl_sync(0xffffffffu, slot, j);
         const float* part = p.part + (size_t)sj * ROWS * (D + 2) + 2 * ROWS + (size_t)row * D;
@@ -1208,17 +1226,18 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
           o[2 * i + 1] = wj == 0.f ? o[2 * i + 1] : fmaf(x.y, wj, o[2 * i + 1]);
         }
       }
-      M = Mn;
     }
-    const size_t vec =
-        ((size_t)b * a.T + (rr >> a.log_g)) * a.Hq + h * a.G + (rr & (a.G - 1));
-    const float inv = M == -INFINITY ? 0.f : 1.f / L;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      p.out[vec * D + channel_of<VO>(64 * (i >> 1) + 2 * lane + (i & 1))] = f2h(o[i] * inv);
-    if (lane == 0)
-      p.lse[vec] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    M = Mn;
   }
+  const int rr = jt.r0 + row;
+  const size_t vec =
+      ((size_t)jt.b * a.T + (rr >> a.log_g)) * a.Hq + jt.h * a.G + (rr & (a.G - 1));
+  const float inv = M == -INFINITY ? 0.f : 1.f / L;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+    p.out[vec * D + channel_of<VO>(64 * (i >> 1) + 2 * lane + (i & 1))] = f2h(o[i] * inv);
+  if (lane == 0)
+    p.lse[vec] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // SMs of the current device (cached: the query is not free); 0 on an error.
@@ -1279,7 +1298,7 @@ fade_status_t launch(const fade_config_t* c, const AttnTreeArgs& p, cudaStream_t
   at[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
   lc.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&lc, tree_combine_kernel<D, VB, R>, p, P);
+  const cudaError_t e = cudaLaunchKernelEx(&lc, tree_combine_kernel<D, VB, R>, p);
   if (e != cudaSuccess)
     return set_error(FADE_ERR_CUDA, "fade_tree_attention combine: %s", cudaGetErrorString(e));
   return launch_status("fade_tree_attention combine");
@@ -1296,7 +1315,7 @@ size_t tree_attention_ws(const fade_config_t* c, int T) {
   const int rows = rows_of(c, T);
   const long long blocks = (long long)c->batch * c->num_kv_heads *
                            ceil_div((long long)T * (c->num_q_heads / c->num_kv_heads), rows);
-  return (size_t)tree_ctas(blocks, kMaxSM) * 2 * rows * (c->head_dim + 2) * 4;
+  return (size_t)tree_ctas(blocks, kMaxSM) * (sizeof(Joint) + 2 * rows * (c->head_dim + 2) * 4);
 }
 
 }  // namespace fade
@@ -1330,7 +1349,11 @@ extern "C" fade_status_t fade_tree_attention(const fade_config_t* c, const fade_
   p.n_nodes = n_nodes;
   p.out = out;
   p.lse = lse;
-  p.part = static_cast<float*>(ws);
+  // the workspace: a Joint a CTA, then the partials
+  const long long blocks =
+      (long long)c->batch * c->num_kv_heads * ceil_div((long long)T * p.a.G, rows_of(c, T));
+  p.joint = static_cast<Joint*>(ws);
+  p.part = reinterpret_cast<float*>(p.joint + tree_ctas(blocks, kMaxSM));
   cudaStream_t s = as_stream(stream);
   const int kb = c->middle_k_bits, vb = c->v_codec == FADE_V_PQ ? kPQ : c->middle_v_bits;
 #define FADE_TREE_CASE(D_, KB_, VB_)               \
