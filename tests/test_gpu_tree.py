@@ -507,6 +507,44 @@ def test_attention_runs_the_same_twice_and_beside_another_stream(F):
     assert torch.equal(out2, first[0]) and torch.equal(lse2, first[1])
 
 
+def test_rows_without_nodes_leave_everything_as_it_was(F):
+    rng = np.random.default_rng(21)
+    c = Cache(F, rng, 3, 8, 2, 64, [500, 0, 90])
+    c.draft(rng, 5)
+    see = np.tile(np.tril(np.ones((5, 5), bool)), (3, 1, 1))
+    for n in ([0, 0, 0], [5, 0, 2], [0, 5, 0]):
+        c.out.fill_(7), c.lse.fill_(7)
+        c.check(see, np.array(n, np.int32))
+
+
+def test_two_captured_calls_replayed_in_any_order(F):
+    """Two layers' calls captured into graphs of their own, each with its workspace, replayed at
+    once and in either order: the bits of eager calls."""
+    rng = np.random.default_rng(22)
+    calls, see = [], np.tril(np.ones((2, 9, 9), bool))
+    for lens in ([700, 90], [33, 2000]):
+        c = Cache(F, rng, 2, 8, 2, 128, lens)
+        c.draft(rng, 9)
+        c.check(see)
+        calls.append((c, c.out.clone(), c.lse.clone(), torch.cuda.CUDAGraph()))
+    mask = dev(mask_words(see))
+    for c, _, _, g in calls:
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            F.fade_tree_attention(c.L, c.dq, c.dk, c.dv, mask, None, c.out, c.lse, c.ws)
+    side = torch.cuda.Stream()
+    for order in ((0, 1), (1, 0), (0, 1)):
+        for c, *_ in calls:
+            c.out.fill_(7), c.lse.fill_(7), c.ws.fill_(255)
+        side.wait_stream(torch.cuda.current_stream())
+        calls[order[0]][3].replay()
+        with torch.cuda.stream(side):
+            calls[order[1]][3].replay()
+        torch.cuda.synchronize()
+        for c, out, lse, _ in calls:
+            assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+
+
 # --------------------------------------------------------------------------- commit
 def state(c):
     """Every unit's held bytes in cache order (codes as they are)."""

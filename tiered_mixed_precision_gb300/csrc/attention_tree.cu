@@ -1270,7 +1270,8 @@ fade_status_t launch(const fade_config_t* c, const AttnTreeArgs& p, cudaStream_t
   using Sh = Shape<D, KB, VB, R>;
   int device = 0;
   const int sms = sm_count(&device);
-  if (sms == 0) return launch_status("fade_tree_attention device query");
+  if (sms == 0)
+    return set_error(FADE_ERR_CUDA, "fade_tree_attention: no device, or one past the 64th");
   // no more CTAs than the configuration can have tiles (not the present counts: see the header)
   const long long blocks = ceil_div((long long)p.a.T * p.a.G, 64 * R);
   const long long most = (long long)p.a.B * p.a.H * blocks *
