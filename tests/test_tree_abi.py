@@ -165,6 +165,9 @@ def test_norm_refusals(T):
         f(cfg, tab, 32, q, k, w[:32], w, 1e-6, pos, q, k, stream=_S())
     with pytest.raises(ValueError):
         f(cfg, tab, 32, q, k, w, w, 1e-6, pos.long(), q, k, stream=_S())
+    for bad in (tab[:-1], tab.double(), torch.zeros(64 * 64)[::2]):   # short, wrong type, strided
+        with pytest.raises(ValueError):
+            f(cfg, bad, 32, q, k, w, w, 1e-6, pos, q, k, stream=_S())
     # no tokens: nothing to do
     f(cfg, tab, 32, q[:, :0], k[:, :0], w, w, 1e-6, pos[:, :0].contiguous(), q[:, :0], k[:, :0],
       stream=_S())
@@ -183,3 +186,14 @@ def test_model_refusals(T):
     with pytest.raises(T.FadeError):
         fc.tree_begin(torch.zeros((2, 65), dtype=torch.int32))
     assert np.all(fc.layers[0].h_n_sink == 0)
+
+
+def test_a_strided_workspace_is_refused(T):
+    L = _layer(T)
+    a = _args(L)
+    a["ws"] = torch.zeros(1 << 21, dtype=torch.uint8)[::2]
+    with pytest.raises(ValueError):
+        _attend(T, L, a)
+    with pytest.raises(ValueError):
+        T.fade_tree_commit(L, a["q_rot"], a["lse"], a["tree_k"], a["tree_v"],
+                           torch.zeros((2, 5), dtype=torch.int32), [1, 1], a["ws"], stream=_S())

@@ -583,6 +583,11 @@ def fade_qk_norm_rope(cfg: Config, table, max_pos, q, k, q_weight, k_weight, eps
     _tensor(dev, "q_weight", q_weight, "float16", (d,))
     _tensor(dev, "k_weight", k_weight, "float16", (d,))
     _tensor(dev, "pos", pos, "int32", (n, t))
+    if table is not None and cfg.rope_kind != "none":
+        _tensor(dev, "table", table, "float32", table.shape)
+        if table.numel() < max_pos * d:
+            raise ValueError(f"the table holds {table.numel()} values, {max_pos} positions of "
+                             f"{d} channels need {max_pos * d}")
     _check(lib().fade_qk_norm_rope(ctypes.byref(cfg.c()), _ptr(table), max_pos, _heads(q),
                                    _heads(q_rot), _ptr(q_weight), _heads(k), _heads(k_rot),
                                    _ptr(k_weight), eps, _ptr(pos), n, t, _stream(stream)))
@@ -606,6 +611,8 @@ def _tree_tensors(dev, layer, q_rot, tree_k, tree_v, ws):
     for name, t in (("the layer", layer.meta), ("ws", ws)):
         if dev is not None and t is not None and t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
     return T
 
 
