@@ -392,6 +392,73 @@ def test_more_blocks_than_one_cta_each_can_list(F):
                         np.concatenate([K, tk[js]]), np.concatenate([V, tv[js]]), (b, u, i, a))
 
 
+@pytest.mark.parametrize("hq,h,T,long,pattern", [
+    (32, 8, 16, 16384, "L" * 32 + "s" * 32),                 # the short rows behind the long ones
+    (16, 2, 64, 131000, ("L" + "s" * 40) * 2 + "L"),         # 512 query rows a unit, long between short
+    (8, 8, 5, 30000, "s" * 50 + "L" + "s" * 77 + "LL"),
+])
+def test_short_rows_beside_long_ones(F, hq, h, T, long, pattern):
+    """CTAs take equal tiles, so beside long rows some take hundreds of one-tile blocks: every block
+    of the short rows is written, and by the 64-bit form."""
+    rng = np.random.default_rng(len(pattern))
+    B, d = len(pattern), 64
+    c = Cache(F, rng, B, hq, h, d, [60] * B, extra=long)
+    rows = [b for b in range(B) if pattern[b] == "L"]
+    fill_middle(c, rows, long)
+    c.draft(rng, T)
+    n = rng.integers(max(1, T // 2), T + 1, B).astype(np.int32)
+    see = np.stack([plain_layout(p, T)[0] for p in random_parents(rng, B, T)])
+    out, lse = c.attend(see, n)
+    for b in range(B):   # every block is written
+        assert not (out[b, :n[b]] == 7).all(-1).any() and not (lse[b, :n[b]] == 7).any(), b
+    some = [b for b in range(B) if pattern[b] == "s"]
+    c.check(see, n, some if T * hq * len(some) <= 1 << 14 else some[::6])
+    first = c.out.clone(), c.lse.clone()
+    # the long rows, against the same rows by themselves
+    few = Cache(F, rng, len(rows), hq, h, d, [60] * len(rows), extra=long)
+    for name in ("sink_k", "sink_v", "recent_k", "recent_v", "meta"):
+        getattr(few.L, name).copy_(getattr(c.L, name)[rows])
+    cur = int(c.L.meta[0, 0, 4])
+    for name in ("mid_k_codes", "mid_v_codes", "mid_k_scales", "mid_v_scales"):
+        getattr(few.L, name)[cur].copy_(getattr(c.L, name)[cur][rows])
+    few.draft(rng, T)
+    few.dq, few.dk, few.dv = c.dq[rows], c.dk[rows].contiguous(), c.dv[rows].contiguous()
+    want, want_lse = few.attend(see[rows], n[rows])
+    for i, b in enumerate(rows):
+        # other cuts of the tiles, so other references: every probability rounds anew (U, and |v| of
+        # the middle tokens is below 1), as does the output; sums of 32 terms a thread and tile, of 1024
+        # tiles, of 152 partials and their exponentials round in fp32
+        w, wl = want[i, :n[b]], want_lse[i, :n[b]]
+        assert np.abs(out[b, :n[b]] - w).max() <= 3 * U * (1 + np.abs(w).max())
+        assert np.abs(lse[b, :n[b]] - wl).max() <= 2 * (1300 * 2.0 ** -24 + 2.0 ** -20)
+    c.attend(see, n)
+    assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
+    c.out.fill_(7), c.lse.fill_(7)
+    one = np.zeros(B, np.int32)
+    one[rows[0]] = 1
+    c.check(see, one, rows[:1])
+
+
+def fill_middle(c, rows, n_mid):
+    """Random codes and scales in the middle tiers of rows, n_mid tokens each."""
+    L, cfg = c.L, c.cfg
+    g = torch.Generator("cuda").manual_seed(n_mid)
+    cur = int(L.meta[0, 0, 4])
+    for b in rows:
+        for codes, scales, bits in ((L.mid_k_codes, L.mid_k_scales, cfg.middle_k_bits),
+                                    (L.mid_v_codes, L.mid_v_scales, cfg.middle_v_bits)):
+            x, q = codes[cur][b, :, :n_mid], 2 ** (bits - 1) - 1
+            w = torch.zeros(x.shape, dtype=torch.int32, device="cuda")
+            for i in range(8 // bits):
+                code = torch.randint(-q, q + 1, x.shape, generator=g, device="cuda", dtype=torch.int32)
+                w |= (code & ((1 << bits) - 1)) << (bits * i)
+            x.copy_(w)
+            s = scales[cur][b, :, :n_mid]
+            s.copy_(torch.rand(s.shape, generator=g, device="cuda") / q)
+        L.meta[b, :, c.F.META["n_mid"]] = n_mid
+        L.h_n_mid[b] = n_mid
+
+
 def test_offsets_past_32_bits(F):
     """A capacity whose codes lie past 4 GiB: attention and commit of the last rows."""
     rng = np.random.default_rng(32)

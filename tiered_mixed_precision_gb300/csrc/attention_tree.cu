@@ -21,11 +21,11 @@
 #include <math.h>
 
 #include "tree.cuh"
+#include "tree_schedule.h"
 
 namespace fade {
 namespace {
 
-constexpr int kTok = 128;            // tokens of a tile
 constexpr int kRefBelow = 6;         // log2 a new reference lies below the maximum it follows
 constexpr int kRefSlack = 14;        // log2 a row's logits may pass its reference by
 constexpr int kAhead = 4;            // tiles that L2 is asked for ahead of their use
@@ -78,35 +78,19 @@ struct AttnTreeArgs {
 };
 
 // ---------------------------------------------------------------- schedule
-// Tiles are numbered row by row, KV head by KV head, block of query rows by block, FP16 tiles
-// before middle tiles; CTA c of P takes tiles [N c / P, N (c + 1) / P). Everything is derived on
-// the device from the counts, so a captured launch follows the cache.
-struct RowTiles {
-  int n;        // nodes
-  int blocks;   // blocks of query rows
-  int f16;      // FP16 tiles
-  int tiles;    // tiles of one block
-};
 template <int ROWS>
 __device__ __forceinline__ RowTiles row_tiles(const TreeArgs& a, const int32_t* n_nodes, int b) {
-  RowTiles r;
-  r.n = n_nodes ? min(max(n_nodes[b], 0), a.T) : a.T;
   const int32_t* m = a.meta + (size_t)b * a.H * FADE_META_FIELDS;
-  r.blocks = (r.n * a.G + ROWS - 1) / ROWS;
-  r.f16 = (m[FADE_META_N_SINK] + m[FADE_META_N_RECENT] + r.n + kTok - 1) / kTok;
-  r.tiles = r.f16 + (m[FADE_META_N_MID] + kTok - 1) / kTok;
-  return r;
+  return make_row_tiles(n_nodes ? min(max(n_nodes[b], 0), a.T) : a.T, a.G, ROWS,
+                        m[FADE_META_N_SINK] + m[FADE_META_N_RECENT], m[FADE_META_N_MID]);
 }
-// Inclusive prefix of the rows' tiles into pre[1 .. B] (pre[0] = 0), by the whole CTA (256 threads at least).
-template <int ROWS>
-__device__ __forceinline__ void tile_prefix(const TreeArgs& a, const int32_t* n_nodes, int* pre) {
+// Inclusive prefix over the rows of f(row) into pre[1 .. B] (pre[0] = 0), by the whole CTA (256 threads
+// at least).
+template <class F>
+__device__ __forceinline__ void row_prefix(int B, int* pre, const F& f) {
   __shared__ int wsum[8];
   const int b = threadIdx.x, lane = b & 31, warp = b >> 5;
-  int v = 0;
-  if (b < a.B) {   // B <= 256
-    const RowTiles r = row_tiles<ROWS>(a, n_nodes, b);
-    v = a.H * r.blocks * r.tiles;
-  }
+  int v = b < B ? f(b) : 0;   // B <= 256
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int t = __shfl_up_sync(0xffffffffu, v, o);
@@ -121,19 +105,20 @@ __device__ __forceinline__ void tile_prefix(const TreeArgs& a, const int32_t* n_
   }
   __syncthreads();
 }
-__device__ __forceinline__ int row_of(const int* pre, int B, int g) {   // pre[b] <= g < pre[b+1]
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid + 1] > g) hi = mid; else lo = mid + 1;
-  }
-  return lo;
+// The CTA's first tile, the one after its last, and the charge, where shares are long (out of line:
+// inline it took a small launch 19 to 21 us; so did the other, 173 to 176 at 64 rows of 4096 tokens).
+template <int ROWS>
+__device__ __noinline__ int3 long_share(const AttnTreeArgs* p, const int* pre, int* pre_blocks) {
+  const TreeArgs& a = p->a;
+  row_prefix(a.B, pre_blocks, [&](int b) { return a.H * row_tiles<ROWS>(a, p->n_nodes, b).blocks; });
+  const int P = gridDim.x, c = blockIdx.x;
+  const Rows r{pre, pre_blocks, a.B, tree_charge(pre[a.B], pre_blocks[a.B], P)};
+  return make_int3(cta_start(r, P, c), cta_start(r, P, c + 1), r.charge);
 }
-__device__ __forceinline__ int cta_start(int N, int P, int c) {
-  return (int)((long long)N * c / P);
-}
-__device__ __forceinline__ int cta_of(int N, int P, int g) {
-  return (int)((((long long)g + 1) * P - 1) / N);
+
+// The CTA that takes the last tile of a block of row b that begins at tile g0, likewise.
+__device__ __noinline__ int long_last(const Rows* r, int b, int g0, int tiles) {
+  return cta_of(*r, gridDim.x, b, g0, tiles, tiles - 1);
 }
 
 // ---------------------------------------------------------------- tensor memory and products
@@ -495,35 +480,24 @@ struct Segment {
   int begin, end;                            // its tiles in this segment
   int n_sink, n_mid, n_rec, head, cur;
 };
-constexpr int kMaxSeg = 128;   // segments of a CTA at most (the grid is sized for it)
 template <int ROWS>
-__device__ __forceinline__ int list_segments(const AttnTreeArgs& p, const int* pre, int g_first,
+__device__ __forceinline__ int list_segments(const AttnTreeArgs& p, const Rows& rows, int g_first,
                                              int g_end, Segment* list) {
   const TreeArgs& a = p.a;
   __shared__ int count;
   if (threadIdx.x == 0) count = 0;
   __syncthreads();
   if (threadIdx.x < kMaxSeg) {
-    // the k-th block from the one that holds g_first
-    int k = threadIdx.x;
-    int b = row_of(pre, a.B, g_first);
-    RowTiles rt = row_tiles<ROWS>(a, p.n_nodes, b);
-    int blk = (g_first - pre[b]) / rt.tiles;
-    while (blk + k >= a.H * rt.blocks) {   // on to the row that holds it, if the CTA gets there
-      k -= a.H * rt.blocks - blk;
-      blk = 0;
-      if (pre[++b] >= g_end) break;
-      rt = row_tiles<ROWS>(a, p.n_nodes, b);
-    }
-    blk += k;
-    const int g0 = pre[b] < g_end ? pre[b] + blk * rt.tiles : g_end;
-    if (g0 < g_end) {
+    const Place at = block_from([&](int b) { return row_tiles<ROWS>(a, p.n_nodes, b); }, rows, a.H,
+                                g_first, threadIdx.x, g_end);
+    const RowTiles& rt = at.rt;
+    if (at.g0 < g_end) {
       Segment s;
-      s.b = b;
-      s.begin = max(g_first - g0, 0);
-      s.end = min(rt.tiles, g_end - g0);
-      s.h = blk / rt.blocks;
-      s.r0 = (blk % rt.blocks) * ROWS;
+      s.b = at.b;
+      s.begin = max(g_first - at.g0, 0);
+      s.end = min(rt.tiles, g_end - at.g0);
+      s.h = at.blk / rt.blocks;
+      s.r0 = (at.blk % rt.blocks) * ROWS;
       s.rows = min(ROWS, rt.n * a.G - s.r0);
       s.n = rt.n;
       s.f16 = rt.f16;
@@ -623,7 +597,8 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
   volatile int* sDone = reinterpret_cast<volatile int*>(small + 136);   // tiles unpacked
   volatile int* sDead = reinterpret_cast<volatile int*>(small + 140);   // a wait gave up
   uint32_t* sBad = reinterpret_cast<uint32_t*>(small + 160);   // [8 segments][2] see below
-  int* sPre = reinterpret_cast<int*>(small + 256);             // [257]
+  int* sPre = reinterpret_cast<int*>(small + 256);             // [257] rows' first tiles
+  int* sBlocks = reinterpret_cast<int*>(small + 2556);         // [257] and blocks
   float* sMax = reinterpret_cast<float*>(small + 1536);        // [softmax warps][2][16 rows]
   Segment* sSeg = reinterpret_cast<Segment*>(small + 3584);    // [kMaxSeg]
   auto kTile = [&](int st) { return stages + st * Sh::STAGE; };
@@ -638,20 +613,27 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
 
   // the combine kernel may be scheduled as this one drains
   asm volatile("griddepcontrol.launch_dependents;");
-  tile_prefix<ROWS>(a, p.n_nodes, sPre);
+  row_prefix(a.B, sPre, [&](int b) {
+    const RowTiles r = row_tiles<ROWS>(a, p.n_nodes, b);
+    return a.H * r.blocks * r.tiles;
+  });
   const int N = sPre[a.B];
-  const int g_first = cta_start(N, gridDim.x, blockIdx.x);
-  const int g_end = cta_start(N, gridDim.x, blockIdx.x + 1);
+  int3 share = make_int3(equal_start(N, gridDim.x, blockIdx.x),
+                         equal_start(N, gridDim.x, blockIdx.x + 1), 0);
+  if (N > tree_hold(gridDim.x)) share = long_share<ROWS>(&p, sPre, sBlocks);
+  const int g_first = share.x, g_end = share.y;
+  const Rows all{sPre, sBlocks, a.B, share.z};
   if (g_first >= g_end) {   // uniform over the CTA; nothing allocated yet
     if (tid == 0) p.joint[blockIdx.x] = Joint{0, -1};
     return;
   }
-  const int n_seg = list_segments<ROWS>(p, sPre, g_first, g_end, sSeg);
+  const int n_seg = list_segments<ROWS>(p, all, g_first, g_end, sSeg);
   if (tid == Sh::THREADS - 32) {
     const Segment& s = sSeg[n_seg - 1];
     Joint j{g_end - g_first, -1, n_seg == 1 ? 0 : 1, s.b, s.h, s.r0, s.rows, 0};
     if (s.begin == 0 && s.end < s.tiles)
-      j.last = cta_of(N, gridDim.x, g_end - s.end + s.tiles - 1);
+      j.last = all.charge ? long_last(&all, s.b, g_end - s.end, s.tiles)
+                          : equal_cta_of(N, gridDim.x, g_end - s.end + s.tiles - 1);
     p.joint[blockIdx.x] = j;
   }
   if (warp == 0) {
@@ -1254,13 +1236,6 @@ int sm_count(int* device) {
   return known[d];
 }
 
-// One CTA per SM, more where a CTA's list of segments (one more than its blocks of query rows) would
-// not hold them.
-int tree_ctas(long long blocks, int sms) {
-  const long long least = (blocks + kMaxSeg - 3) / (kMaxSeg - 2);
-  return (int)(least > sms ? least : sms);
-}
-
 int rows_of(const fade_config_t* c, int T) {   // query rows of a block: 64 where they are enough
   return T * (c->num_q_heads / c->num_kv_heads) <= 64 ? 64 : 128;
 }
@@ -1277,7 +1252,7 @@ fade_status_t launch(const fade_config_t* c, const AttnTreeArgs& p, cudaStream_t
   const long long most = (long long)p.a.B * p.a.H * blocks *
                          (ceil_div(p.a.C, kTok) + ceil_div(p.a.S + p.a.W + p.a.T, kTok));
   const long long all = (long long)p.a.B * p.a.H * blocks;
-  const int P = tree_ctas(all, most < sms ? (int)most : sms);
+  const int P = tree_ctas(all, most < sms ? (int)most : sms);   // one an SM
   auto kern = tree_attention_kernel<D, KB, VB, R>;
   static bool opted[64];   // per device: the kernel has its shared memory
   if (!opted[device]) {
