@@ -766,6 +766,39 @@ def test_commit_of_a_bad_path_is_recorded(F):
     assert np.array_equal(ring[1], c.tk[0, 0, 0].astype(np.float64))
 
 
+@pytest.mark.parametrize("policy", ["h2o", "ema"])
+def test_a_replayed_commit_past_the_capacity_leaves_the_row(F, policy):
+    """A captured commit replayed until one row's middle tier is full: from then on the row keeps all it
+    holds, its scores among it, the refusal is recorded, and the other row goes on."""
+    rng = np.random.default_rng(14)
+    c = Cache(F, rng, 2, 8, 2, 64, [200, 150], policy=policy, extra=60)
+    T, n_path = 4, [3, 3]
+    c.draft(rng, T)
+    see = np.tile(np.tril(np.ones((T, T), bool)), (2, 1, 1))
+    c.attend(see)
+    path = torch.arange(T, dtype=torch.int32, device="cuda").repeat(2, 1)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        F.fade_tree_commit(c.L, c.dq, c.lse, c.dk, c.dv, path, n_path, c.ws)
+    slots = c.L.mid_k_codes[0].shape[2]
+    fits = (slots - 132) // 3
+    for _ in range(fits):
+        g.replay()
+    F.fade_check_status(c.L)
+    assert c.unit(0, 0)[1] == 132 + 3 * fits
+    held = lambda b: [x for h in range(2) for x in (*state(c)[b * 2 + h], c.unit(b, h)[5])]
+    before, other = held(0), c.unit(1, 0)
+    g.replay()
+    for got, want in zip(held(0), before):
+        assert np.array_equal(got.view(np.uint8), want.view(np.uint8))
+    assert c.unit(1, 0)[1] == other[1] + 3
+    assert not np.array_equal(c.unit(1, 0)[5][:other[1]], other[5][:other[1]])
+    with pytest.raises(F.FadeError) as e:
+        F.fade_check_status(c.L)
+    assert e.value.status == 6
+
+
 # --------------------------------------------------------------------------- together
 @pytest.mark.parametrize("policy,codec,norm", [("none", "int", True), ("position", "int", False),
                                                ("h2o", "int", True), ("ema", "pq", False)])

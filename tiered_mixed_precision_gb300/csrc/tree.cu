@@ -151,6 +151,26 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// The tokens of a path of n_path that become sinks, and those that the ring then demotes.
+struct PathPlan {
+  int to_sink, dem;
+};
+__device__ __forceinline__ PathPlan path_plan(const TreeArgs& a, const int32_t* m, int n_path) {
+  PathPlan p;
+  p.to_sink = min(max(a.S - m[FADE_META_N_SINK], 0), n_path);
+  p.dem = max(0, m[FADE_META_N_RECENT] + n_path - p.to_sink - a.W);
+  return p;
+}
+// Whether the commit takes a unit's path: its counts index the tiers and the middle tier holds the
+// demotions (a captured commit may be replayed past what the host checked). Both kernels ask, so that a
+// unit that is refused keeps its scores, too.
+__device__ __forceinline__ bool takes_path(const TreeArgs& a, const int32_t* m, int n_path) {
+  const int n_sink = m[FADE_META_N_SINK], n_mid = m[FADE_META_N_MID];
+  const int n_rec = m[FADE_META_N_RECENT], head = m[FADE_META_HEAD], cur = m[FADE_META_CUR];
+  return n_sink >= 0 && n_sink <= a.S && n_rec >= 0 && n_rec <= a.W && head >= 0 && head < a.W &&
+         (cur & ~1) == 0 && n_mid >= 0 && n_mid <= a.C - path_plan(a, m, n_path).dem;
+}
+
 // What a CTA takes: row b's tiles cost kTileCost + 1 a block of eight columns each (a pass over the
 // tile's codes, then two products a group a block), the costs of all rows and heads form one line,
 // and every CTA takes an equal stretch of it. Paths differ in length, so equal tiles would not be
@@ -167,7 +187,8 @@ __device__ __forceinline__ ScoreRow score_row(const TreeArgs& a, int b, int n_pa
   r.n_mid = m[FADE_META_N_MID];
   r.n_rec = m[FADE_META_N_RECENT];
   r.mid_tiles = (r.n_mid + 15) / 16;
-  r.tiles = n_path ? r.mid_tiles + (r.n_sink + r.n_rec + n_path + 15) / 16 : 0;
+  r.tiles = n_path && takes_path(a, m, n_path)
+                ? r.mid_tiles + (r.n_sink + r.n_rec + n_path + 15) / 16 : 0;
   const int cols = n_path * a.G;
   r.cost = (cols + kScoreCols - 1) / kScoreCols * kTileCost + (cols + 7) / 8;
   return r;
@@ -234,6 +255,7 @@ __global__ void __launch_bounds__(256, 2) tree_scores_kernel(TreeArgs a, RowLens
       const int h = at_tile / sr.tiles, unit = b * a.H + h;
       const int tile0 = at_tile - h * sr.tiles, tile1 = min(sr.tiles, end_tile - h * sr.tiles);
       at_tile = h * sr.tiles + tile1;
+      if (!takes_path(a, a.meta + (size_t)unit * FADE_META_FIELDS, n_path)) continue;   // uniform
       const int head = a.meta[unit * FADE_META_FIELDS + FADE_META_HEAD];
       const int cur = a.meta[unit * FADE_META_FIELDS + FADE_META_CUR];
       const uint8_t* codes = a.mk[cur] + (size_t)unit * a.C * ROW;
@@ -391,10 +413,8 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(TreeArgs a, RowLens le
   int32_t* m = a.meta + unit * FADE_META_FIELDS;
   const int n_sink = m[FADE_META_N_SINK], n_mid = m[FADE_META_N_MID];
   const int n_rec = m[FADE_META_N_RECENT], head = m[FADE_META_HEAD], cur = m[FADE_META_CUR];
-  const int to_sink = min(max(a.S - n_sink, 0), n_path);
-  const int dem = max(0, n_rec + n_path - to_sink - a.W);
-  if (n_sink < 0 || head < 0 || head >= a.W || n_rec < 0 || n_rec > a.W || n_mid < 0 ||
-      n_mid + dem > a.C) {
+  const auto [to_sink, dem] = path_plan(a, m, n_path);
+  if (!takes_path(a, m, n_path)) {
     if (threadIdx.x == 0) record_status(a.status, kCheckTreeSlot);
     return;
   }
