@@ -197,3 +197,46 @@ def test_a_strided_workspace_is_refused(T):
     with pytest.raises(ValueError):
         T.fade_tree_commit(L, a["q_rot"], a["lse"], a["tree_k"], a["tree_v"],
                            torch.zeros((2, 5), dtype=torch.int32), [1, 1], a["ws"], stream=_S())
+
+
+def test_pointers_off_their_type_are_refused(T):
+    """What a kernel would read or write in words that do not start on a multiple of their size."""
+    import ctypes
+
+    from tiered_mixed_precision_gb300 import fade as F
+
+    L = _layer(T)
+    a = _args(L)
+    c, lib, n = L.cfg, T.lib(), 5
+    cfg, layer = ctypes.byref(c.c()), ctypes.byref(L.c)
+    room = torch.zeros(1 << 16, dtype=torch.uint8)
+    at = (room.data_ptr() + 15) // 16 * 16
+    q, out = a["q_rot"].data_ptr(), torch.zeros_like(a["q_rot"])
+    k, v, ws, size = F._heads(a["tree_k"]), F._heads(a["tree_v"]), a["ws"].data_ptr(), 1 << 20
+    lens = np.ones(2, np.int32)
+
+    def attend(mask=at, n_nodes=at, lse=at):
+        return lib.fade_tree_attention(cfg, layer, n, q, k, v, mask, n_nodes, out.data_ptr(), lse,
+                                       ws, size, None)
+
+    def commit(path=at, lse=at):
+        return lib.fade_tree_commit(cfg, layer, n, q, lse, k, v, path, lens.ctypes.data, ws, size,
+                                    None)
+
+    def layout(**kw):
+        p = {**dict(parents=at, n_nodes=at, base=at, mask=at, pos=at), **kw}
+        return lib.fade_tree_layout(cfg, n, p["parents"], p["n_nodes"], p["base"], p["mask"],
+                                    p["pos"], None)
+
+    for call in (lambda: attend(mask=at + 4), lambda: attend(lse=at + 2),
+                 lambda: attend(n_nodes=at + 2), lambda: commit(path=at + 2),
+                 lambda: commit(lse=at + 2), lambda: layout(mask=at + 4),
+                 *(lambda x=x: layout(**{x: at + 2}) for x in ("parents", "n_nodes", "base", "pos")),
+                 lambda: lib.fade_qk_norm_rope(cfg, at, 8, k, k, None, None, None, None,
+                                               ctypes.c_float(1.0), at + 2, 2, n, None)):
+        assert call() == 1
+        assert "aligned" in F.fade_last_error()
+    scores = L.c.recent_scores
+    L.c.recent_scores = scores + 2
+    assert commit() == 1 and "scores" in F.fade_last_error()
+    L.c.recent_scores = scores

@@ -1316,6 +1316,9 @@ extern "C" fade_status_t fade_tree_attention(const fade_config_t* c, const fade_
   if ((reinterpret_cast<uintptr_t>(q_rot) | reinterpret_cast<uintptr_t>(out) |
        reinterpret_cast<uintptr_t>(ws)) & 15)
     return set_error(FADE_ERR_INVALID_ARGUMENT, "q_rot, out and ws must be 16-byte aligned");
+  if (!aligned(mask, 8) || !aligned(lse, 4) || !aligned(n_nodes, 4))
+    return set_error(FADE_ERR_INVALID_ARGUMENT,
+                     "mask must be 8-byte aligned, lse and n_nodes 4-byte");
   if (ws_bytes < tree_attention_ws(c, T))
     return set_error(FADE_ERR_CAPACITY, "tree workspace %zu bytes, %zu needed", ws_bytes,
                      tree_attention_ws(c, T));

@@ -214,6 +214,8 @@ extern "C" fade_status_t fade_qk_norm_rope(const fade_config_t* c, const float* 
   if (rope && !pos && n_tokens > max_pos)
     return set_error(FADE_ERR_CAPACITY, "positions up to %d exceed the table (%d)", n_tokens - 1,
                      max_pos);
+  if (reinterpret_cast<uintptr_t>(pos) & 3)
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "pos must be 4-byte aligned");
   const uint16_t* w[2] = {q_in ? q_weight : nullptr, k_in ? k_weight : nullptr};
   if ((w[0] || w[1]) && !(eps > 0.f && isfinite(eps)))
     return set_error(FADE_ERR_INVALID_ARGUMENT, "eps must be positive and finite");

@@ -40,6 +40,10 @@ fade_status_t validate_tree_layer(const fade_config_t* c, const fade_layer_t* L)
     any |= reinterpret_cast<uintptr_t>(p);
   if (any & 15)
     return set_error(FADE_ERR_INVALID_ARGUMENT, "the layer's K and V buffers must be 16-byte aligned");
+  if (!aligned(L->sink_scores, 4) || !aligned(L->mid_scores[0], 4) || !aligned(L->mid_scores[1], 4) ||
+      !aligned(L->recent_scores, 4) || !aligned(L->meta, 4) || !aligned(L->status, 4))
+    return set_error(FADE_ERR_INVALID_ARGUMENT,
+                     "the layer's scores, meta and status must be 4-byte aligned");
   return FADE_OK;
 }
 
@@ -548,6 +552,10 @@ extern "C" fade_status_t fade_tree_layout(const fade_config_t* c, int32_t T,
   if (st) return st;
   if (!parents || !base_pos || !mask || !pos)
     return set_error(FADE_ERR_INVALID_ARGUMENT, "NULL parents, base_pos, mask or pos");
+  if (!aligned(mask, 8) || !aligned(parents, 4) || !aligned(n_nodes, 4) || !aligned(base_pos, 4) ||
+      !aligned(pos, 4))
+    return set_error(FADE_ERR_INVALID_ARGUMENT,
+                     "mask must be 8-byte aligned, parents, n_nodes, base_pos and pos 4-byte");
   tree_layout_kernel<<<c->batch, FADE_TREE_MAX_NODES, 0, as_stream(stream)>>>(
       T, parents, n_nodes, base_pos, mask, pos);
   return launch_status("fade_tree_layout");
@@ -575,11 +583,14 @@ extern "C" fade_status_t fade_tree_commit(const fade_config_t* c, fade_layer_t* 
   if (st) return st;
   if (!path || !h_n_path)
     return set_error(FADE_ERR_INVALID_ARGUMENT, "NULL path or path lengths");
+  if (!aligned(path, 4)) return set_error(FADE_ERR_INVALID_ARGUMENT, "path must be 4-byte aligned");
   const bool scored = c->policy == FADE_EVICT_H2O || c->policy == FADE_EVICT_EMA;
   if (scored && (!q_rot || !lse || !ws))
     return set_error(FADE_ERR_INVALID_ARGUMENT, "H2O and EMA need q_rot, lse and a workspace");
   if (scored && ((reinterpret_cast<uintptr_t>(q_rot) | reinterpret_cast<uintptr_t>(ws)) & 15))
     return set_error(FADE_ERR_INVALID_ARGUMENT, "q_rot and the workspace must be 16-byte aligned");
+  if (scored && !aligned(lse, 4))
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "lse must be 4-byte aligned");
   const size_t need = (size_t)c->batch * c->num_kv_heads * T * 4;
   if (scored && ws_bytes < need)
     return set_error(FADE_ERR_CAPACITY, "tree workspace %zu bytes, %zu needed", ws_bytes, need);

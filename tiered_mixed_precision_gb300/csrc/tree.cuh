@@ -23,6 +23,10 @@ __device__ __forceinline__ int tree_node(const TreeArgs& a, const int32_t* path,
   return n >= 0 && n < a.T ? n : 0;
 }
 
+// Whether a pointer (NULL included) starts on a multiple of `bytes`.
+inline bool aligned(const void* p, size_t bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0;
+}
 fade_status_t validate_tree(const fade_config_t* c, int32_t T);
 // validate_layer, and the 16-byte alignment that vector loads of the tiers need.
 fade_status_t validate_tree_layer(const fade_config_t* c, const fade_layer_t* L);
