@@ -910,3 +910,12 @@ def test_a_captured_tree_step_follows_the_cache(F):
         torch.cuda.synchronize()
         assert torch.equal(out2, c.out) and torch.equal(lse2, c.lse)
     c.check(see)
+
+
+def test_the_codes_that_a_commit_records_are_named(F):
+    c = Cache(F, np.random.default_rng(0), 1, 4, 1, 64, [20])
+    for code, name in ((20, "path node"), (21, "middle slot or ring head")):
+        c.L.status[0] = code
+        with pytest.raises(F.FadeError) as e:
+            F.fade_check_status(c.L)
+        assert e.value.status == 6 and f"{code} tree commit's {name}" in str(e.value)

@@ -42,8 +42,9 @@ extern "C" fade_status_t fade_check_status(const fade_layer_t* L, void* stream) 
   if (w[0] >= kDevCheckBase)
     return set_error(FADE_ERR_DEVICE_CHECK,
                      "a device-side check failed (code %d: 16 demote slot, 17 append slot, "
-                     "18 compaction row, 19 attention tile); results since the last reset are "
-                     "invalid", w[0]);
+                     "18 compaction row, 19 attention tile, 20 tree commit's path node, 21 tree "
+                     "commit's middle slot or ring head); results since the last reset are invalid",
+                     w[0]);
   if (w[0] != 0)
     return set_error(FADE_ERR_TIMEOUT,
                      "a kernel gave up a bounded wait (code %d: 1 consumer stage, 2 producer "
