@@ -535,6 +535,32 @@ def test_what_a_node_does_not_see_does_not_reach_it(F, d, codec):
     assert np.isnan(o[0, 8:]).all()
 
 
+@pytest.mark.parametrize("lens", [[300], [6000], [0]])
+def test_a_query_that_is_not_a_number_gives_none(F, lens):
+    """NaN in a query row: NaN and a NaN lse in that row, not the zeros of a row that sees nothing; the
+    other rows' bits stay. NaN in a cached key: in every row."""
+    rng = np.random.default_rng(17)
+    c = Cache(F, rng, 1, 8, 2, 64, lens)
+    T = 6
+    c.draft(rng, T)
+    see = np.tril(np.ones((1, T, T), bool))
+    c.check(see)
+    clean, clean_lse = c.out.clone(), c.lse.clone()
+    c.dq[0, 2, 5, 9], c.dq[0, 4, 1] = float("nan"), float("nan")
+    c.attend(see)
+    assert torch.isnan(c.out[0, 2, 5]).all() and torch.isnan(c.lse[0, 2, 5])
+    assert torch.isnan(c.out[0, 4, 1]).all() and torch.isnan(c.lse[0, 4, 1])
+    rest = torch.ones(1, T, 8, dtype=torch.bool, device="cuda")
+    rest[0, 2, 5] = rest[0, 4, 1] = False
+    assert torch.equal(c.out[rest], clean[rest]) and torch.equal(c.lse[rest], clean_lse[rest])
+    c.dq = dev(c.q)
+    if lens[0]:
+        c.L.sink_k[0, 1, 0, 3] = float("nan")
+        c.attend(see)
+        assert torch.equal(c.out[:, :, :4], clean[:, :, :4])
+        assert torch.isnan(c.out[:, :, 4:]).all() and torch.isnan(c.lse[:, :, 4:]).all()
+
+
 def test_large_logits_and_extreme_scales(F):
     """Logits hundreds apart (the running maximum moves by whole exponents), keys near fp16's
     largest value and values among its smallest."""

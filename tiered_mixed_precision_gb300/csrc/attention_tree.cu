@@ -1072,8 +1072,9 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
         for (int e = 0; e < 2; ++e) {
           const float m1 = other16[(lane >> 2) + 8 * e], l1 = other16[(lane >> 2) + 8 * e + 16];
           const float M = fmaxf(mref[e], m1);
-          const float w0 = mref[e] == -INFINITY ? 0.f : ex2(mref[e] - M);
-          const float w1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+          // (a row without a maximum has seen nothing, sum 0, or NaN alone, sum NaN)
+          const float w0 = mref[e] == -INFINITY ? lsum[e] : ex2(mref[e] - M);
+          const float w1 = m1 == -INFINITY ? l1 : ex2(m1 - M);
           // the same order of the sum in both warps
           const float L = stream ? fmaf(l1, w1, lsum[e] * w0) : fmaf(lsum[e], w0, l1 * w1);
           w[e][0] = stream ? w1 : w0;
@@ -1081,11 +1082,11 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
           const int r = row0 + 8 * e, rr = s.r0 + min(r, rows - 1);
           vec[e] =
               ((size_t)s.b * a.T + (rr >> a.log_g)) * a.Hq + s.h * a.G + (rr & (a.G - 1));
-          inv[e] = M == -INFINITY ? 0.f : 1.f / L;
+          inv[e] = M == -INFINITY ? L : 1.f / L;
           if (stream == 0 && (lane & 3) == 0 && r < rows) {
             if (whole)
               p.lse[vec[e]] =
-                  M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+                  M == -INFINITY ? L - INFINITY : (M + log2f(L)) * 0.6931471805599453f;
             else
               *reinterpret_cast<float2*>(part + 2 * r) = make_float2(M, L);
           }
@@ -1188,7 +1189,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
     if (base + lane > jt.last || p.joint[c].tiles == 0) ml = make_float2(-INFINITY, 0.f);
     const float Mn = fmaxf(M, warp_max(ml.x));
     const float fo = M == -INFINITY ? 0.f : ex2(M - Mn);
-    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - Mn);
+    const float w = ml.x == -INFINITY ? ml.y : ex2(ml.x - Mn);   // (0, or NaN)
     L = fmaf(L, fo, warp_sum(ml.y * w));
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) o[i] *= fo;
@@ -1214,12 +1215,12 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
   const int rr = jt.r0 + row;
   const size_t vec =
       ((size_t)jt.b * a.T + (rr >> a.log_g)) * a.Hq + jt.h * a.G + (rr & (a.G - 1));
-  const float inv = M == -INFINITY ? 0.f : 1.f / L;
+  const float inv = M == -INFINITY ? L : 1.f / L;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
     p.out[vec * D + channel_of<VO>(64 * (i >> 1) + 2 * lane + (i & 1))] = f2h(o[i] * inv);
   if (lane == 0)
-    p.lse[vec] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    p.lse[vec] = M == -INFINITY ? L - INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // SMs of the current device (cached: the query is not free); 0 on an error.
