@@ -793,6 +793,33 @@ def test_commit_of_a_bad_path_is_recorded(F):
 
 
 @pytest.mark.parametrize("policy", ["h2o", "ema"])
+def test_a_key_of_minus_infinity_gets_no_mass(F, policy):
+    """A cached key whose logits are -inf: probability 0, whatever the number of query rows."""
+    rng = np.random.default_rng(15)
+    c = Cache(F, rng, 1, 4, 2, 64, [150], policy=policy)
+    T, a = 5, 3
+    c.draft(rng, T)
+    c.q[..., 3] = np.abs(c.q[..., 3]) + np.float16(0.25)
+    c.dq = dev(c.q)
+    c.L.sink_k[0, :, 2, 3] = -float("inf")
+    see = np.tril(np.ones((1, T, T), bool))
+    _, lse = c.attend(see)
+    before = [c.unit(0, u) for u in range(2)]
+    path = np.arange(T, dtype=np.int32)[None]
+    F.fade_tree_commit(c.L, c.dq, c.lse, c.dk, c.dv, dev(path), [a], c.ws)
+    F.fade_check_status(c.L)
+    for u in range(2):
+        _, _, _, K, _, old = before[u]
+        got = c.unit(0, u)[5]
+        keep = 1.0 if policy == "h2o" else np.float64(np.float32(0.9)) ** a
+        assert abs(got[2] - keep * old[2]) <= 4 * 2.0 ** -24 * old[2]
+        K[2] = 0.0   # the rest as in any commit
+        want, tol = scores_reference(c, 0, u, 2, K, old, path[0, :a], lse, policy)
+        rest = np.arange(len(want)) != 2
+        assert (np.abs(got - want) <= tol)[rest].all()
+
+
+@pytest.mark.parametrize("policy", ["h2o", "ema"])
 def test_a_replayed_commit_past_the_capacity_leaves_the_row(F, policy):
     """A captured commit replayed until one row's middle tier is full: from then on the row keeps all it
     holds, its scores among it, the refusal is recorded, and the other row goes on."""

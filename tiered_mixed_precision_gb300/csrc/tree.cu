@@ -290,24 +290,20 @@ __global__ void __launch_bounds__(256, 2) tree_scores_kernel(TreeArgs a, RowLens
         for (int i = 0; i < kScoreStages - 1; ++i) fetch(tile0 + warp + 8 * i);
         __syncthreads();   // the columns before are read
         for (int i = threadIdx.x; i < (n + 7) / 8 * 8 * GR * 4; i += 256) {
-          const int c = i / (GR * 4), gr = (i / 4) % GR, col = c0 + c;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (col < cols) {
-            const int node = tree_node(a, path, b, col >> a.log_g);
-            const size_t q = (((size_t)b * a.T + node) * a.Hq + h * a.G + (col & (a.G - 1)));
-            uint32_t p[4];
-            value_pairs(
-                __ldg(reinterpret_cast<const uint4*>(a.q + q * D + 32 * gr + 8 * (i & 3))), p);
-            x = make_uint4(p[0], p[1], p[2], p[3]);
-            if (gr == 0 && (i & 3) == 0) {
-              float wc = gain;
-              for (int e = col >> a.log_g; e < n_path - 1; ++e) wc *= decay;
-              sl[c] = fmaf(lse[q], kLog2e, -log2f(wc));
-            }
-          } else if (gr == 0 && (i & 3) == 0) {
-            sl[c] = INFINITY;   // adds nothing to the sum
+          // (columns past the last repeat it with an offset of inf, which adds nothing to the sum;
+          // zeros would add NaN where they meet an infinite key)
+          const int c = i / (GR * 4), gr = (i / 4) % GR, col = min(c0 + c, cols - 1);
+          const int node = tree_node(a, path, b, col >> a.log_g);
+          const size_t q = (((size_t)b * a.T + node) * a.Hq + h * a.G + (col & (a.G - 1)));
+          uint32_t p[4];
+          value_pairs(
+              __ldg(reinterpret_cast<const uint4*>(a.q + q * D + 32 * gr + 8 * (i & 3))), p);
+          sq[c][gr][i & 3] = make_uint4(p[0], p[1], p[2], p[3]);
+          if (gr == 0 && (i & 3) == 0) {
+            float wc = gain;
+            for (int e = col >> a.log_g; e < n_path - 1; ++e) wc *= decay;
+            sl[c] = c0 + c < cols ? fmaf(lse[q], kLog2e, -log2f(wc)) : INFINITY;
           }
-          sq[c][gr][i & 3] = x;
         }
         __syncthreads();
 #pragma unroll 1
