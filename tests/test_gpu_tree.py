@@ -972,3 +972,92 @@ def test_the_codes_that_a_commit_records_are_named(F):
         with pytest.raises(F.FadeError) as e:
             F.fade_check_status(c.L)
         assert e.value.status == 6 and f"{code} tree commit's {name}" in str(e.value)
+
+
+# --------------------------------------------------------------------------- norms that change
+def twins(F, rng, policy, budget, layers=2):
+    """Two caches of the same contents and a function that draws a step's q, k and v."""
+    from tiered_mixed_precision_gb300.model import FadeCache
+
+    B, hq, h, d, P = 2, 8, 2, 64, 200
+    cfg = F.Config(batch=B, num_q_heads=hq, num_kv_heads=h, head_dim=d, n_sink=4, recent_window=16,
+                   int4_budget=budget, mid_capacity=400, policy=policy)
+    draw = lambda *s: dev(rng.standard_normal(s).astype(np.float16))
+    prompt = [(draw(B, h, P, d), draw(B, h, P, d)) for _ in range(layers)]
+    caches = []
+    for _ in range(2):
+        caches.append(FadeCache(cfg, layers, P, 800))
+        for layer, (k, v) in enumerate(prompt):
+            caches[-1].prefill(layer, k.clone(), v.clone())
+    step = lambda n=1: (draw(n, layers, B, hq, d), draw(n, layers, B, h, d), draw(n, layers, B, h, d))
+    weights = lambda: [dev((1 + 0.5 * rng.standard_normal(d)).astype(np.float16)) for _ in range(2)]
+    return (*caches, step, weights)
+
+
+def test_growing_steps_follow_a_changed_norm(F):
+    """growing_step after set_qk_norm sets, changes (weights, eps) or clears the norm: the bits of an
+    eager step."""
+    rng = np.random.default_rng(19)
+    grow, eager, step, weights = twins(F, rng, "none", -1)
+    bufs = [t[0].clone() for t in step()]
+    out, want = torch.empty_like(bufs[0]), torch.empty_like(bufs[0])
+    w = weights()
+    for norm in (None, (*w, 1e-6), (*weights(), 1e-6), (*w, 0.5), (w[0], None, 1e-6), (None, None, 1.0)):
+        for c in (grow, eager):
+            if norm:
+                c.set_qk_norm(*norm)
+        for _ in range(2):
+            x = [t[0] for t in step()]
+            for b, t in zip(bufs, x):
+                b.copy_(t)
+            grow.growing_step(*bufs, out)
+            eager.step_all(*x, want)
+            assert torch.equal(out, want), norm
+    assert grow.growing_captures <= 8   # one a norm, and for rows that reach a new tile
+
+
+def test_host_fed_steps_follow_a_changed_norm(F):
+    rng = np.random.default_rng(20)
+    fed, eager, step, weights = twins(F, rng, "position", 90)
+    want = torch.empty_like(step()[0][0])
+    for _ in range(3):   # to the steady state
+        x = [t[0] for t in step()]
+        for c in (fed, eager):
+            c.step_all(*x, want)
+    for norm in (None, (*weights(), 1e-6), (*weights(), 1e-5), (None, None, 1.0)):
+        for c in (fed, eager):
+            if norm:
+                c.set_qk_norm(*norm)
+        x = step(3)
+        host = [t.cpu().pin_memory() for t in x]
+        out = torch.zeros(x[0].shape, dtype=torch.float16).pin_memory()
+        fed.run_from_host(*host, out)
+        torch.cuda.current_stream().synchronize()
+        for s in range(3):
+            eager.step_all(x[0][s], x[1][s], x[2][s], want)
+            assert torch.equal(out[s], want.cpu()), norm
+
+
+def test_a_captured_step_keeps_its_norm_weights(F):
+    """set_qk_norm after a capture: the graph's weights stay allocated and its replays read them."""
+    import gc
+    import weakref
+
+    rng = np.random.default_rng(23)
+    grow, eager, step, weights = twins(F, rng, "none", -1)
+    w = weights()
+    kept = [t.clone() for t in w]
+    grow.set_qk_norm(*w)
+    eager.set_qk_norm(*kept)
+    bufs = [t[0].clone() for t in step()]
+    out, want = torch.empty_like(bufs[0]), torch.empty_like(bufs[0])
+    g = grow.capture_growing_step(*bufs, out)
+    refs = [weakref.ref(t) for t in w]
+    del w
+    grow.set_qk_norm(None, None)
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    junk = [torch.full((64,), float("nan"), dtype=torch.float16, device="cuda") for _ in range(64)]
+    grow.replay_growing(g)
+    eager.step_all(*bufs, want)
+    assert torch.equal(out, want) and len(junk) == 64

@@ -87,8 +87,10 @@ class FadeCache:
         self.launches = 0       # kernels enqueued by step_layer calls
         self._pos_ring, self._pos_ring_ev, self._pos_ring_i = None, None, 0
         self._growing = None        # (key, graph) of growing_step
+        self._host_pipe = None      # graphs and buffers of run_from_host
         self.growing_captures = 0   # captures made by growing_step
         self.qk_norm = [None] * num_layers   # per layer (q weight, k weight, eps): set_qk_norm
+        self._captured_norms = {}   # those that captured steps read, kept for their replays
         self._tree_bufs = {}        # per tree size: the buffers of a DraftTree
 
     # ------------------------------------------------------------------ session persistence
@@ -172,8 +174,9 @@ class FadeCache:
     def set_qk_norm(self, q_weight, k_weight, eps: float = 1e-6, layer=None):
         """Models that norm each head of q and k before the rotation: fp16 [d] weights (None: that
         side is not normed) for one layer, or every layer. Prefill, decode steps and drafted trees
-        of the layer then norm and rotate in one pass (``fade_qk_norm_rope``). Captured steps keep
-        the weights they were captured with."""
+        of the layer then norm and rotate in one pass (``fade_qk_norm_rope``). A step that the caller
+        captured (``capture_step``, ``capture_growing_step``) keeps the weights it was captured with;
+        ``growing_step`` and ``run_from_host``, which capture by themselves, capture again."""
         for w in (q_weight, k_weight):
             if w is not None and (w.dtype != torch.float16 or tuple(w.shape) != (
                     self.cfg.head_dim,) or not w.is_contiguous()):
@@ -181,10 +184,14 @@ class FadeCache:
         for i in (range(len(self.layers)) if layer is None else [layer]):
             self.qk_norm[i] = (None if q_weight is None and k_weight is None
                                else (q_weight, k_weight, eps))
+        self._growing = self._host_pipe = None
 
     def _norm_rope(self, layer: int, q, k, pos, q_rot, k_rot):
         """q [B][n][Hq][d], k [B][n][H][d] normed (if the layer norms) and rotated to pos."""
-        qw, kw, eps = self.qk_norm[layer] or (None, None, 1.0)
+        norm = self.qk_norm[layer]
+        qw, kw, eps = norm or (None, None, 1.0)
+        if norm and self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+            self._captured_norms[id(norm)] = norm
         F.fade_qk_norm_rope(self.cfg, self.table, self.max_pos, q, k, qw, kw, eps, pos, q_rot,
                             k_rot)
 
@@ -423,7 +430,7 @@ class FadeCache:
         """Capture the two step graphs ``run_from_host`` alternates between (steady state
         only, see ``capture_step``): each reads its own q/k/v buffers and writes its own output
         buffer, so one step's inputs can be copied in while the other graph runs."""
-        if getattr(self, "_host_pipe", None) is not None:
+        if self._host_pipe is not None:
             return
         c, L, dev = self.cfg, len(self.layers), self.device
         shp_q = (L, c.batch, c.num_q_heads, c.head_dim)
