@@ -974,6 +974,87 @@ def test_the_codes_that_a_commit_records_are_named(F):
         assert e.value.status == 6 and f"{code} tree commit's {name}" in str(e.value)
 
 
+def test_tree_buffers_do_not_pile_up(F):
+    """Trees of every size, each attended to: at most two sizes' buffers are held. Trees of two sizes can
+    be held at once, each with buffers of its own."""
+    rng = np.random.default_rng(25)
+    c, _, _, _ = twins(F, rng, "none", -1)
+    B, hq, h, d = 2, 8, 2, 64
+
+    def attend(T):
+        par = torch.arange(T, dtype=torch.int32, device="cuda").sub(1).repeat(B, 1)
+        tree = c.tree_begin(par)
+        x = torch.randn((B, T, hq + 2 * h, d), device="cuda").half()
+        out = torch.empty((B, T, hq, d), dtype=torch.float16, device="cuda")
+        for layer in range(2):
+            c.tree_attend(layer, tree, x[:, :, :hq], x[:, :, hq:hq + h], x[:, :, hq + h:], out)
+        return tree
+
+    size = lambda t: sum(x.untyped_storage().nbytes()
+                         for x in (t.mask, t.pos, t.q_rot, t.k_rot, t.lse, t.ws))
+    attend(64)
+    torch.cuda.synchronize()
+    start = torch.cuda.memory_allocated()
+    largest = size(c.tree_begin(torch.zeros((B, 64), dtype=torch.int32, device="cuda")))
+    for T in range(1, 64):
+        attend(T)
+    assert torch.cuda.memory_allocated() <= start + largest
+    small, wide = attend(9), attend(30)
+    assert small.q_rot.data_ptr() != wide.q_rot.data_ptr()
+    lse = small.lse.clone()
+    again = attend(30)
+    assert again.q_rot.data_ptr() == wide.q_rot.data_ptr()   # as many nodes: the same buffers
+    path = torch.arange(9, dtype=torch.int32, device="cuda").repeat(B, 1)
+    before = F.fade_tier_counts(c.layers[0]).sum(1)
+    c.tree_commit(small, path, [9, 4])
+    assert torch.equal(small.lse, lse)
+    assert (F.fade_tier_counts(c.layers[0]).sum(1) - before).tolist() == [9, 4]
+
+
+def test_tree_buffers_of_captured_and_side_stream_calls_outlive_their_tree(F):
+    """A captured tree_attend whose tree is dropped: the next tree of as many nodes has its buffers, and a
+    replay writes there. Calls on another stream: the buffers are not given away while they run."""
+    rng = np.random.default_rng(26)
+    c, _, _, _ = twins(F, rng, "none", -1)
+    B, hq, h, d, T = 2, 8, 2, 64, 12
+    par = torch.arange(T, dtype=torch.int32, device="cuda").sub(1).repeat(B, 1)
+    x = torch.randn((B, T, hq + 2 * h, d), device="cuda").half()
+    out, want = (torch.empty((B, T, hq, d), dtype=torch.float16, device="cuda") for _ in range(2))
+    run = lambda tree, o: c.tree_attend(0, tree, x[:, :, :hq], x[:, :, hq:hq + h],
+                                        x[:, :, hq + h:], o)
+    tree = c.tree_begin(par)
+    run(tree, want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(tree, out)
+    at = tree.q_rot.data_ptr()
+    del tree
+    for n in (3, 40, 7):   # other sizes, and memory of other uses
+        c.tree_begin(par[:, :n].contiguous() if n < T else torch.full((B, n), -1, dtype=torch.int32,
+                                                                      device="cuda"))
+        torch.full((1 << 20,), 0xff, dtype=torch.uint8, device="cuda")
+    tree = c.tree_begin(par)
+    assert tree.q_rot.data_ptr() == at
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    side = torch.cuda.Stream()
+    for _ in range(4):
+        tree = c.tree_begin(par[:, :9].contiguous())
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20000000)
+            c.tree_attend(0, tree, x[:, :9, :hq], x[:, :9, hq:hq + h], x[:, :9, hq + h:],
+                          out.view(-1)[:B * 9 * hq * d].view(B, 9, hq, d))
+        got = tree.q_rot.untyped_storage().data_ptr()
+        del tree
+        c.tree_begin(par[:, :5].contiguous())   # the nine nodes' buffers are let go
+        other = torch.empty(2 * B * 9 * hq * d, dtype=torch.float16, device="cuda")
+        assert other.data_ptr() != got
+        side.synchronize()
+
+
 # --------------------------------------------------------------------------- norms that change
 def twins(F, rng, policy, budget, layers=2):
     """Two caches of the same contents and a function that draws a step's q, k and v."""

@@ -9,6 +9,7 @@ CUDA library on the caller's stream; this module only allocates buffers and pass
 from __future__ import annotations
 
 import ctypes
+import weakref
 from dataclasses import dataclass
 
 import numpy as np
@@ -39,6 +40,20 @@ def _record_event(ev):
         raise RuntimeError(f"cudaEventRecordWithFlags failed ({rc})")
 
 
+class TreeBuffers:
+    """The device buffers of a tree size, every layer's."""
+
+    def __init__(self, cfg: F.Config, layers: int, T: int, device):
+        e = lambda dt, *s: torch.empty(s, dtype=dt, device=device)
+        B, Hq, H, d = cfg.batch, cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim
+        self.tensors = dict(
+            mask=e(torch.int64, B, T), pos=e(torch.int32, B, T),
+            q_rot=e(torch.float16, layers, B, T, Hq, d),
+            k_rot=e(torch.float16, layers, B, T, H, d), lse=e(torch.float32, layers, B, T, Hq),
+            ws=e(torch.uint8, F.fade_tree_ws_bytes(cfg, T)))
+        self.stream = torch.cuda.current_stream(device) if device.type == "cuda" else None
+
+
 @dataclass
 class DraftTree:
     """A step's drafted tree (``FadeCache.tree_begin``): masks and positions for every layer, and
@@ -51,6 +66,7 @@ class DraftTree:
     lse: torch.Tensor              # f32 [L][B][T][Hq]
     ws: torch.Tensor
     v: list                        # per layer: the values its attention read
+    buffers: TreeBuffers | None = None   # what mask .. ws lie in
 
 
 class FadeCache:
@@ -91,7 +107,10 @@ class FadeCache:
         self.growing_captures = 0   # captures made by growing_step
         self.qk_norm = [None] * num_layers   # per layer (q weight, k weight, eps): set_qk_norm
         self._captured_norms = {}   # those that captured steps read, kept for their replays
-        self._tree_bufs = {}        # per tree size: the buffers of a DraftTree
+        # per tree size: the buffers of its trees, as long as one of them is held; those of the last
+        # tree, and those that captured steps use, are held here
+        self._tree_bufs = weakref.WeakValueDictionary()
+        self._last_tree, self._captured_trees = None, {}
 
     # ------------------------------------------------------------------ session persistence
     # Page "FADE：面向LLM推理的注意力感知分层KV缓存压缩技术", §会话持久化: the compressed cache is
@@ -381,34 +400,45 @@ class FadeCache:
         [B][T], n_nodes: device i32 [B] or None): every layer's maintenance is done, and the
         tree's masks and positions are built. Then ``tree_attend`` every layer and
         ``tree_commit`` the accepted paths (or begin again, which leaves the cache as it is). A
-        cache that evicts needs mid_capacity >= int4_budget + T. The tree's buffers are reused by
-        the next tree of as many nodes."""
+        cache that evicts needs mid_capacity >= int4_budget + T. Trees of as many nodes share their
+        buffers: the next one reuses them. They live as long as such a tree does, or, once used in a
+        captured step, as the cache; the last tree's until the next."""
         c, L = self.cfg, len(self.layers)
         if parents.dim() != 2 or parents.shape[0] != c.batch:
             raise ValueError(f"parents must be [{c.batch}][nodes]")
         T = parents.shape[1]
-        ws_bytes = F.fade_tree_ws_bytes(c, T)
         b = self._tree_bufs.get(T)
         if b is None:
-            e = lambda dt, *s: torch.empty(s, dtype=dt, device=self.device)
-            b = self._tree_bufs[T] = dict(
-                mask=e(torch.int64, c.batch, T), pos=e(torch.int32, c.batch, T),
-                q_rot=e(torch.float16, L, c.batch, T, c.num_q_heads, c.head_dim),
-                k_rot=e(torch.float16, L, c.batch, T, c.num_kv_heads, c.head_dim),
-                lse=e(torch.float32, L, c.batch, T, c.num_q_heads),
-                ws=e(torch.uint8, ws_bytes))
+            b = self._tree_bufs[T] = TreeBuffers(c, L, T, self.device)
+        self._last_tree = b
+        self._hold(b)
         # from pageable memory: the copy has left the host array when the call returns
         self.pos.copy_(torch.from_numpy(self.next_positions()))
         self.maintain_all()
-        F.fade_tree_layout(c, parents, n_nodes, self.pos, b["mask"], b["pos"])
+        F.fade_tree_layout(c, parents, n_nodes, self.pos, b.tensors["mask"], b.tensors["pos"])
         self.launches += 1
-        return DraftTree(n_nodes=n_nodes, v=[None] * L, **b)
+        return DraftTree(n_nodes=n_nodes, v=[None] * L, buffers=b, **b.tensors)
+
+    def _hold(self, b: TreeBuffers | None):
+        """What a tree's buffers need before a call on the current stream uses them, so that they can be
+        freed when nothing holds them: a captured step holds them itself, another stream than their
+        own is made known to the allocator."""
+        if b is None or b.stream is None:
+            return
+        if torch.cuda.is_current_stream_capturing():
+            self._captured_trees[id(b)] = b
+            return
+        here = torch.cuda.current_stream(self.device)
+        if here != b.stream:
+            for t in b.tensors.values():
+                t.record_stream(here)
 
     def tree_attend(self, layer: int, tree: DraftTree, q_raw: torch.Tensor, k_raw: torch.Tensor,
                     v: torch.Tensor, out: torch.Tensor):
         """One layer's attention of the tree: q_raw [B][T][Hq][d], k_raw and v [B][T][H][d] (fp16,
         any strides over the first three dimensions; v is read again by the commit); out fp16
         [B][T][Hq][d], left as it is past a row's nodes."""
+        self._hold(tree.buffers)
         self._norm_rope(layer, q_raw, k_raw, tree.pos, tree.q_rot[layer], tree.k_rot[layer])
         F.fade_tree_attention(self.layers[layer], tree.q_rot[layer], tree.k_rot[layer], v,
                               tree.mask, tree.n_nodes, out, tree.lse[layer], tree.ws)
@@ -420,6 +450,7 @@ class FadeCache:
         every layer, each of which has attended to the tree."""
         if any(v is None for v in tree.v):
             raise ValueError("tree_attend every layer before the commit")
+        self._hold(tree.buffers)
         for i, L in enumerate(self.layers):
             F.fade_tree_commit(L, tree.q_rot[i], tree.lse[i], tree.k_rot[i], tree.v[i], path,
                                n_path, tree.ws)
