@@ -491,9 +491,11 @@ size_t fade_tree_ws_bytes(const fade_config_t* cfg, int32_t T);
  * is left as it was, in out and lse, and what its q, k, v and mask hold does not matter. What a
  * node does not attend to does not reach its output, whatever it holds (infinities and NaN
  * included). The cache may be empty.
- * Middle keys keep all bits of code * scale (an INT4 one as fp16 plus the remainder of that
- * rounding, which meets the query rounded to 3 significant bits: a logit is off by 2^-14 of its
- * terms at most); dequantised INT4 values round to fp16 (2^-11 relative). Products accumulate in
+ * Middle keys of scales of 2^-5 and more keep all bits of code * scale (an INT4 one as fp16 plus
+ * the remainder of that rounding, which meets the query rounded to 3 significant bits: a logit is
+ * off by 2^-14 of its terms at most); an INT4 key of a smaller scale is off by 2^-15, and by 2^-11
+ * of itself (2^-24 at least), at most. Dequantised values round to fp16: 2^-11 relative for INT4,
+ * 2^-24 at least. Products accumulate in
  * fp32, the softmax is fp32 and its probabilities are rounded to fp16 before they meet V.
  * Every count is read on the device and the launch does not depend on the counts: a captured call
  * stays valid while the cache grows or is evicted from. ws: DEVICE, 16-byte aligned,

@@ -580,6 +580,56 @@ def test_large_logits_and_extreme_scales(F):
     c.check(see)
 
 
+def key_error(K, s):
+    """How far a middle INT4 key of scale s may be from code * scale: nothing from 2^-5 on (fp16 and an
+    E5M2 remainder hold its 14 bits), else what lies under E5M2's last bit, 2^-16 of a halved key and
+    never more than the remainder itself, and half of fp16's last bit for a halved key, 2^-25."""
+    return np.zeros_like(K) if s >= 2.0 ** -5 else np.minimum(U * np.abs(K), 2.0 ** -15) + 2.0 ** -24
+
+
+@pytest.mark.parametrize("d,kb", [(64, 4), (128, 4), (64, 2)])
+@pytest.mark.parametrize("exp", [-20, -14, -13, -10, -7, -5, -2, 4, 13])
+def test_keys_of_every_scale(F, d, kb, exp):
+    """Middle keys whose fp16 roundings all fall to the same side, queries that make logits of about 40 of
+    them. From scales of 2^-5 on the log-sum moves by 2^-14 of a logit's terms at most (a rounding to
+    fp16 alone would move it six times as far); below, by the keys' error as well."""
+    rng = np.random.default_rng(exp + 100)
+    c = Cache(F, rng, 1, 4, 1, d, [300], kb=kb)
+    L, T = c.L, 5
+    cur = int(L.meta[0, 0, 4])
+    # 5 x 1026 units: half an ulp of fp16 past an even number; subnormal scales are whole 2^-24
+    s = 1026 * 2.0 ** (exp - 10) if exp >= -14 else 33 * 2.0 ** -24
+    code = 5 if kb == 4 else 1
+    L.mid_k_codes[cur].fill_(0x55)        # INT4 5, INT2 1
+    L.mid_k_scales[cur].fill_(s)
+    if kb == 4:   # a few keys of other codes
+        L.mid_k_codes[cur][:, :, ::7] = torch.tensor(0x33, dtype=torch.uint8, device="cuda")
+    L.sink_k.zero_(), L.recent_k.zero_()
+    c.draft(rng, T)
+    q = 40 / (code * s * np.sqrt(d)) * rng.uniform(0.75, 1.25, c.q.shape)
+    c.q = np.minimum(q, 60000).astype(np.float16)
+    c.tk[:] = 0
+    c.dq = dev(c.q)
+    c.load_tree()
+    see = np.tril(np.ones((1, T, T), bool))
+    _, lse = c.attend(see)
+    _, _, _, K, V, _ = c.unit(0, 0)
+    for i in range(T):
+        for g in range(4):
+            qq = c.q[0, i, g].astype(np.float64)
+            z = np.concatenate([K, np.zeros((i + 1, d))]) @ qq / np.sqrt(d)
+            want = z.max() + np.log(np.exp(z - z.max()).sum())
+            terms = (np.abs(K) @ qq).max() / np.sqrt(d)
+            # the remainder against E5M2 queries (1/8, a subnormal's half step 2^-17), the keys' own
+            # error; fp32: products, the logarithm, the sum
+            off = U * np.abs(K) @ (qq / 8 + 2.0 ** -17)
+            off = off + (key_error(K, s) @ qq if kb == 4 else 2.0 ** -24 * qq.sum() * (s < 2.0 ** -13))
+            tol = off.max() / np.sqrt(d) + 2.0 ** -22 * terms + (len(z) + d) * 2.0 ** -24 + 2.0 ** -20
+            assert abs(lse[0, i, g] - want) <= tol, (i, g, lse[0, i, g], want, tol)
+    if s >= 2.0 ** -5:
+        c.check(see)
+
+
 def test_attention_runs_the_same_twice_and_beside_another_stream(F):
     rng = np.random.default_rng(3)
     c = Cache(F, rng, 2, 8, 2, 128, [1500, 700])

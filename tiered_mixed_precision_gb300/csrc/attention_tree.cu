@@ -14,10 +14,16 @@
 // codes are unpacked once per tile into shared memory (fp16, the 128-byte swizzle), S and O live in
 // tensor memory, P goes back to tensor memory as the A operand of the second product.
 //
-// Roundings to fewer than 32 bits: P and dequantised INT4 values to fp16 (2^-11 relative). INT4
-// keys keep all their bits: code * scale has at most 14, its fp16 rounding leaves a remainder of at
-// most 3, which E5M2 holds exactly; the remainder meets an E5M2 copy of the query in a second
-// product (at the doubled 8-bit rate), so a logit is off by about 2^-15 of its terms, not 2^-12.
+// Roundings to fewer than 32 bits: P and dequantised values to fp16 (2^-11 relative for INT4; values are
+// held halved, so 2^-24 at least). INT4 keys: code * scale has at most 14 bits, its fp16 rounding leaves
+// a remainder of at most 3, kept in E5M2; the remainder meets an E5M2 copy of the query in a second
+// product (at the doubled 8-bit rate), so a logit is off by 2^-14 of its terms at most, not 2^-11. That
+// holds for scales of 2^-5 and more. E5M2 ends at 2^-16, so below them a halved remainder, a multiple of
+// its scale's last bit over two, loses what lies under 2^-16: a key is off by 2^-15 at most, and never by
+// more than the 2^-11 of itself that fp16 alone would leave (2^-24 at least). Remainders scaled by 2^12
+// (and the sum by 2^-12, which the product does for nothing) would keep every bit down to scales of
+// 2^-13, but the multiplication is one more on the pipe that bounds the unpacking: 171 to 181 us at 64
+// rows of 4096 tokens, 515 to 541 at the long ones.
 #include <math.h>
 
 #include "tree.cuh"
