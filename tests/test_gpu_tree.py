@@ -1169,6 +1169,49 @@ def test_host_fed_steps_follow_a_changed_norm(F):
             assert torch.equal(out[s], want.cpu()), norm
 
 
+def test_host_fed_steps_after_a_drafted_tree(F):
+    """A committed path leaves evictions to the next step: the captured steady-state steps are refused
+    until a step has made them, and then go on with the bits of eager ones."""
+    rng = np.random.default_rng(27)
+    fed, eager, step, _ = twins(F, rng, "position", 90)
+    B, hq, h, d, T = 2, 8, 2, 64, 6
+    want = torch.empty_like(step()[0][0])
+
+    def both(x):
+        for c in (fed, eager):
+            c.step_all(*(t[0] for t in x), want)
+
+    def host_fed():
+        x = step(2)
+        out = torch.zeros(x[0].shape, dtype=torch.float16).pin_memory()
+        fed.run_from_host(*(t.cpu().pin_memory() for t in x), out)
+        torch.cuda.current_stream().synchronize()
+        for s in range(2):
+            eager.step_all(x[0][s], x[1][s], x[2][s], want)
+            assert torch.equal(out[s], want.cpu())
+
+    for _ in range(3):   # to the steady state
+        both(step())
+    host_fed()
+    par = torch.arange(T, dtype=torch.int32, device="cuda").sub(1).repeat(B, 1)
+    x = torch.randn((B, T, hq + 2 * h, d), device="cuda").half()
+    out = torch.empty((B, T, hq, d), dtype=torch.float16, device="cuda")
+    for c in (fed, eager):
+        tree = c.tree_begin(par)
+        for layer in range(2):
+            c.tree_attend(layer, tree, x[:, :, :hq], x[:, :, hq:hq + h], x[:, :, hq + h:], out)
+        c.tree_commit(tree, par + 1, [4, 1])
+    q, k, v = (t.cpu().pin_memory() for t in step(1))
+    before = [[a.copy() for a in m] for m in fed.mirror()]
+    with pytest.raises(RuntimeError):
+        fed.run_from_host(q, k, v, torch.zeros(q.shape, dtype=torch.float16).pin_memory())
+    assert all((a == b).all() for m, n in zip(fed.mirror(), before) for a, b in zip(m, n))
+    both(step())
+    host_fed()
+    for layer in range(2):
+        assert (F.fade_tier_counts(fed.layers[layer]) == F.fade_tier_counts(eager.layers[layer])).all()
+
+
 def test_a_captured_step_keeps_its_norm_weights(F):
     """set_qk_norm after a capture: the graph's weights stay allocated and its replays read them."""
     import gc

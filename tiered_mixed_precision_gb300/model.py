@@ -477,6 +477,7 @@ class FadeCache:
         ev = lambda: [torch.cuda.Event(), torch.cuda.Event()]
         self._host_pipe = {"graphs": graphs, "bufs": bufs, "copy": torch.cuda.Stream(device=dev),
                            "in_ready": ev(), "done": ev(), "out_copied": ev(),
+                           "mirror": self.mirror(),
                            "out_used": [False, False]}
 
     def run_from_host(self, qh, kh, vh, oh, side=None):
@@ -485,9 +486,14 @@ class FadeCache:
         on a copy stream while step s runs (the two captured graphs of
         ``prepare_host_pipeline`` take the steps in turn), and step s's outputs are copied back
         while step s+1 runs. Enqueued on the current stream, which waits for the last output
-        copy: synchronise it (or record an event on it) to know the outputs have arrived."""
+        copy: synchronise it (or record an event on it) to know the outputs have arrived.
+        RuntimeError if the tier counts are no longer those of the captured steady state (a drafted
+        tree's commit leaves evictions to the next step: take that one by ``step_all``)."""
         self.prepare_host_pipeline(side)
         P = self._host_pipe
+        for now, then in zip(self.mirror(), P["mirror"]):
+            if any((x != y).any() for x, y in zip(now, then)):
+                raise RuntimeError("run_from_host needs a steady-state cache (tier counts changed)")
         main, cs = torch.cuda.current_stream(), P["copy"]
         K = qh.shape[0]
         if K == 0:
