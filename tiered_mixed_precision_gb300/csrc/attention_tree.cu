@@ -604,8 +604,8 @@ __global__ void __launch_bounds__((Shape<D, KB, VB, R>::THREADS), 1)
   volatile int* sDead = reinterpret_cast<volatile int*>(small + 140);   // a wait gave up
   uint32_t* sBad = reinterpret_cast<uint32_t*>(small + 160);   // [8 segments][2] see below
   int* sPre = reinterpret_cast<int*>(small + 256);             // [257] rows' first tiles
-  int* sBlocks = reinterpret_cast<int*>(small + 2556);         // [257] and blocks
-  float* sMax = reinterpret_cast<float*>(small + 1536);        // [softmax warps][2][16 rows]
+  float* sMax = reinterpret_cast<float*>(small + 1296);        // [softmax warps][2][16 rows]
+  int* sBlocks = reinterpret_cast<int*>(small + 2320);         // [257] rows' blocks before
   Segment* sSeg = reinterpret_cast<Segment*>(small + 3584);    // [kMaxSeg]
   auto kTile = [&](int st) { return stages + st * Sh::STAGE; };
   auto vTile = [&](int st) { return stages + st * Sh::STAGE + Sh::TILE; };
