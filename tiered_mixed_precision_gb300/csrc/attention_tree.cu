@@ -577,8 +577,10 @@ __device__ __forceinline__ void tile_to_l2(const AttnTreeArgs& p, const Segment&
 // of each 32-lane quarter of tensor memory in use: up to 64 query rows take lanes 0..15 of every
 // quarter (R = 1), which gives each scheduler of the SM a share of the softmax; otherwise 128 (R = 2).
 //
-// What bounds it: the unpacking warps, which wait for 6 % of the time (a tile costs them some 800
-// instructions a scheduler, and every segment the latencies of its FP16 tile and its Q).
+// What bounds it: the unpacking warps, which wait for others 8 to 11 % of the time (the softmax warps
+// 43 to 65 %); a tile costs them some 800 instructions a scheduler, and every segment the latencies of
+// its FP16 tile and its Q. More than 64 query rows a unit are several blocks, each of which unpacks the
+// unit's tiles anew: twice at 256 rows (the long rows below), four times at 512.
 // Four warps for K and four for V left the K side as the slower one: 188 and 568 us where all
 // eight on both take 184 and 524 (the two workloads below). Without softmax and products the kernel
 // still takes 157 and 385, without the unpacking arithmetic, stores and loads as well 105 and 221.

@@ -83,7 +83,9 @@ __device__ __forceinline__ void store_slots(uint16_t* y, int l, int rh, const fl
 // counts is bytes in flight: every load of a warp is issued before the first is waited for, 64
 // registers keep 32 warps an SM. 4 x 8191 tokens of 32 + 8 heads of 128 (684 MB): 150 us, 4.56 TB/s,
 // 0.68 of the copy rate; one round a warp 166 us, four (2 CTAs' registers) 210 us, CTAs of 256
-// threads 155 us, 8-byte loads (4 slots a lane) 185 us.
+// threads 155 us, 8-byte loads (4 slots a lane) 185 us. Rotary widths that are no multiple of 16 (SL = 4,
+// 4-byte words): 194 us at 44 of the 128 channels. Every load goes to a register here, so registers
+// limit the bytes in flight; staging tokens in shared memory was not tried.
 constexpr int kNormThreads = 128, kNormRounds = 2;
 template <int D, int SL, int U>
 __global__ void __launch_bounds__(kNormThreads, 8) qk_norm_rope_kernel(const __grid_constant__ NormArgs a) {
