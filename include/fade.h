@@ -518,8 +518,9 @@ fade_status_t fade_tree_attention(const fade_config_t* cfg, const fade_layer_t* 
  * A row with h_n_path 0 is left unchanged. Pending evictions are made by the next
  * fade_evict_rerope: mid_capacity has to hold them (budget + T is always enough when every step
  * starts with its maintenance); FADE_ERR_CAPACITY, nothing enqueued, if a row's middle tier would
- * overflow. Rows sharing their tier decisions need equal path lengths. A path node outside [0, T)
- * is recorded in the layer's status and read as node 0.
+ * overflow; a row that would overflow when a captured commit is replayed is recorded in the layer's
+ * status and left unchanged, its scores included. Rows sharing their tier decisions need equal path
+ * lengths. A path node outside [0, T) is recorded in the layer's status and read as node 0.
  * q_rot, lse: as in fade_tree_attention, and ws (16-byte aligned, fade_tree_ws_bytes(cfg, T)):
  * needed by H2O and EMA, otherwise ignored (may be NULL). h_n_path is read at the call: a
  * captured commit replays the same lengths. */
