@@ -8,8 +8,11 @@
 // of a block) in shared memory, kMaxSeg at most. With equal tiles alone it could have any number of them:
 // beside long rows a CTA's share is hundreds of tiles, and blocks of short rows have one each. Blocks
 // wholly inside a share cost charge + 1 at least, so a share of (kMaxSeg - 2) (charge + 1) holds; that
-// is N + charge K <= (kMaxSeg - 2) P (charge + 1) for N tiles in K blocks. The charge is the least one,
-// 0 while a share is kMaxSeg - 2 tiles or less.
+// is N + charge K <= (kMaxSeg - 2) P (charge + 1) for N tiles in K blocks. While a share is kMaxSeg - 2
+// tiles or less, nothing is charged; else what the list needs, and kStartTiles at least, about what a
+// segment's start costs (its Q, its FP16 rows, its epilogue, beside 1.3 us a tile): 64 rows, half of
+// 16384 and half of 60 tokens, take 669 us with the least charge the list needs, 358 with 3, 304 with 4,
+// 312 with 5, and 292 without the short rows.
 #pragma once
 
 #ifdef __CUDACC__
@@ -22,6 +25,7 @@ namespace fade {
 
 constexpr int kTok = 128;      // tokens of a tile
 constexpr int kMaxSeg = 128;   // segments of a CTA at most
+constexpr int kStartTiles = 4;   // the least charge
 
 struct RowTiles {
   int n;        // nodes
@@ -39,8 +43,8 @@ FADE_SCHED RowTiles make_row_tiles(int n, int G, int rows, int held16, int n_mid
   r.tiles = r.f16 + (n_mid + kTok - 1) / kTok;
   return r;
 }
-// CTAs for at most K blocks where `wanted` would be taken: K is half of what they may list, so that the
-// charge stays below a 60th of a CTA's tiles.
+// CTAs for at most K blocks where `wanted` would be taken: K is half of what they may list, so that what
+// the list needs stays below a 60th of a CTA's tiles.
 FADE_SCHED int tree_ctas(long long K, int wanted) {
   const long long least = (K + kMaxSeg / 2 - 1) / (kMaxSeg / 2);
   return (int)(least > wanted ? least : wanted);
@@ -49,7 +53,9 @@ FADE_SCHED int tree_ctas(long long K, int wanted) {
 FADE_SCHED int tree_hold(int P) { return (kMaxSeg - 2) * P; }
 FADE_SCHED int tree_charge(int N, int K, int P) {
   const int hold = tree_hold(P);
-  return N <= hold ? 0 : (N - hold - 1) / (hold - K) + 1;
+  if (N <= hold) return 0;
+  const int least = (N - hold - 1) / (hold - K) + 1;
+  return least > kStartTiles ? least : kStartTiles;
 }
 // Prefix sums of the rows: tiles and blocks of the rows before row b; `charge` makes them costs.
 struct Rows {
