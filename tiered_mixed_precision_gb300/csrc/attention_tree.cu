@@ -579,7 +579,7 @@ __device__ __forceinline__ void tile_to_l2(const AttnTreeArgs& p, const Segment&
 //
 // What bounds it: the unpacking warps, which wait for others 8 to 11 % of the time (the softmax warps
 // 43 to 65 %); a tile costs them some 800 instructions a scheduler, and every segment the latencies of
-// its FP16 tile and its Q. More than 64 query rows a unit are several blocks, each of which unpacks the
+// its FP16 tile and its Q. More than 128 query rows a unit are several blocks, each of which unpacks the
 // unit's tiles anew: twice at 256 rows (the long rows below), four times at 512.
 // Four warps for K and four for V left the K side as the slower one: 188 and 568 us where all
 // eight on both take 184 and 524 (the two workloads below). Without softmax and products the kernel

@@ -44,13 +44,14 @@ class TreeBuffers:
     """The device buffers of a tree size, every layer's."""
 
     def __init__(self, cfg: F.Config, layers: int, T: int, device):
+        ws_bytes = F.fade_tree_ws_bytes(cfg, T)   # (refuses a T outside the limits)
         e = lambda dt, *s: torch.empty(s, dtype=dt, device=device)
         B, Hq, H, d = cfg.batch, cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim
         self.tensors = dict(
             mask=e(torch.int64, B, T), pos=e(torch.int32, B, T),
             q_rot=e(torch.float16, layers, B, T, Hq, d),
             k_rot=e(torch.float16, layers, B, T, H, d), lse=e(torch.float32, layers, B, T, Hq),
-            ws=e(torch.uint8, F.fade_tree_ws_bytes(cfg, T)))
+            ws=e(torch.uint8, ws_bytes))
         self.stream = torch.cuda.current_stream(device) if device.type == "cuda" else None
 
 
