@@ -530,6 +530,48 @@ fade_status_t fade_tree_commit(const fade_config_t* cfg, fade_layer_t* layer, in
                                const int32_t* path, const int32_t* h_n_path, void* ws,
                                size_t ws_bytes, void* stream);
 
+/* ---- Prompts: the attention of many tokens over FP16 keys and values, and its column sums, from which
+ * the scores of a prompt start. Queries are the last q_len of a row's kv_len tokens (a whole prompt:
+ * q_len = kv_len; a chunk of a prompt, or one token: fewer); query i is at position
+ * kv_len - q_len + i. It sees token j <= its position if window is 0 or j > position - window or
+ * j < n_sink: with n_sink and a window as the cache's sinks and its other tokens under position
+ * eviction, what a token-by-token decode would see. h_q_len, h_kv_len: HOST i32 [B], read at the call
+ * (a captured call replays the same lengths); NULL: n_q, n_kv in every row; 0 <= q_len <= n_q,
+ * q_len <= kv_len <= n_kv. q: fp16 [B][n_q][Hq][d], k and v: fp16 [B][n_kv][H][d], any strides that
+ * fade_heads_t allows and none below 0 (tokens, and the heads of q, may not share a vector). Tokens and
+ * queries past a row's lengths are not looked at, whatever they hold. */
+#define FADE_PROMPT_MAX_TOKENS (1 << 24)
+
+/* Workspace bytes (16-byte aligned) of fade_prompt_attention and fade_prompt_mass for up to n_q queries
+ * and n_kv tokens a row; 0 on invalid arguments (fade_last_error says why). */
+size_t fade_prompt_ws_bytes(const fade_config_t* cfg, int32_t n_q, int32_t n_kv);
+
+/* Attention with scale 1/sqrt(d), q and k rotated. out: fp16 [B][n_q][Hq][d], its vectors apart from
+ * each other and from the inputs; lse: f32 [B][n_q][Hq] (NULL: not wanted), the log of the sum of
+ * exp(s) over what the query sees. Past q_len both are left as they were. What a query does not see
+ * does not reach its output, whatever it holds (infinities and NaN included). Products accumulate in
+ * fp32, the softmax is fp32 and its probabilities are rounded to fp16 before they meet V. status:
+ * DEVICE i32 [FADE_STATUS_WORDS] (a layer's; NULL: none), as fade_check_status reads it. Calls that may
+ * overlap need workspaces of their own. */
+fade_status_t fade_prompt_attention(const fade_config_t* cfg, const fade_heads_t* q,
+                                    const fade_heads_t* k, const fade_heads_t* v, int32_t n_q,
+                                    int32_t n_kv, const int32_t* h_q_len, const int32_t* h_kv_len,
+                                    int32_t n_sink, int32_t window, const fade_heads_t* out,
+                                    float* lse, int32_t* status, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* Column sums of that attention (KVLong §1.3.1 H2O), from its log-sum-exp: mass: f32 [B][H][n_kv],
+ * mass[b][h][j] = sum over the query heads of KV head h and over the queries that see token j of
+ * exp(s - lse); 0 past a row's kv_len. accumulate != 0: added to what mass holds (a prompt in chunks).
+ * fp32 arithmetic in one fixed order: the result is identical on every run. With n_sink 0 and window 0
+ * what fade_prefill_mass computes, on the tensor cores and without its first pass. lse: as
+ * fade_prompt_attention left it. */
+fade_status_t fade_prompt_mass(const fade_config_t* cfg, const fade_heads_t* q,
+                               const fade_heads_t* k, int32_t n_q, int32_t n_kv,
+                               const int32_t* h_q_len, const int32_t* h_kv_len, int32_t n_sink,
+                               int32_t window, const float* lse, int32_t accumulate, float* mass,
+                               int32_t* status, void* ws, size_t ws_bytes, void* stream);
+
 /* Host: cache position of row `row`'s next token = held tokens after the next step's
  * demotion and eviction (KVLong §1.2.2: positions inside the cache). -1 on bad arguments. */
 int32_t fade_next_position(const fade_config_t* cfg, const fade_layer_t* layer, int32_t row);

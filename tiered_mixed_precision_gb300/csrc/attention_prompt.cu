@@ -1,0 +1,810 @@
+// Causal attention of a prompt, of a chunk of it, or of single tokens, over FP16 keys and values: every
+// earlier token, or a sliding window and the first tokens ("sinks") that stay visible.
+// Page "FADE：面向LLM推理的注意力感知分层KV缓存压缩技术", §第一层 (sink and recent tokens) and §核心机制:
+// a position-evicted cache of S sinks and w other tokens shows a query what this attention does with
+// n_sink = S and window = w.
+//
+// Mathematics: the query rows of a unit (row b, KV head h) are its tokens' G heads, r = token * G + g.
+// Over tiles of 128 tokens, S = Q K^T, P = 2^(c S - m) with c = log2(e)/sqrt(d) and a running reference
+// m per row, O += P V, L += rowsum P; out = O / L, lse = (m + log2 L) ln 2. The reference is put 6 below
+// a maximum and moves only when a tile's maximum passes it by more than 14 (P stays below 2^15; fp16
+// loses only what is 2^-31 of the largest P), which spares most rescalings of O.
+//
+// Roundings to fewer than 32 bits: P to fp16 before it meets V, the output. Products of fp16 operands
+// are exact in fp32, sums are fp32.
+#include <math.h>
+
+#include <algorithm>
+
+#include "prompt.cuh"
+#include "tensor_core.cuh"
+#include "tensor_map.cuh"
+
+namespace fade {
+namespace {
+
+constexpr int kRefBelow = 6;     // log2 a new reference lies below the maximum it follows
+constexpr int kRefSlack = 14;    // log2 a row's logits may pass its reference by
+constexpr int kTile = 128;       // tokens of a tile, and query rows of one
+constexpr int kBlk = kTile * 128;   // bytes of a [128][64] fp16 block
+constexpr int kBadBufs = 8, kBadTiles = 8;   // see the checking warps
+
+template <int D>
+struct Shape {
+  static constexpr int TILE = D / 64 * kBlk;            // bytes of a Q, K or V tile
+  static constexpr int STAGES = D == 128 ? 5 : 10;      // ring of K and V tiles
+  static constexpr int SMALL = 2048;
+  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + SMALL;
+  static constexpr int THREADS = 384;   // 8 softmax warps, load, products, 2 that check values
+  static constexpr int TMEM = 512;      // columns: S (and P) 2 x 128, O 2 x D
+};
+
+struct Args {
+  CUtensorMap q, k, v;
+  PromptShape s;
+  PromptRows rows;
+  const uint16_t* vx;            // values by address, for the rows that hold infinities or NaN
+  int64_t v_row, v_tok, v_head;
+  uint16_t* out;
+  int64_t o_row, o_tok, o_head;
+  float* lse;                    // NULL: not asked for
+  float* part;                   // per (block, split) [part_rows][2] (m, L), then [part_rows][D] O
+  int32_t* status;
+  int blocks, splits;            // blocks of two query tiles of the longest row; splits of a block
+  int part_rows;
+};
+
+// One piece of work: the tiles [begin, end) of a block of two query tiles of a unit.
+struct Item {
+  int b, h, tok0, active;   // first query token, query tiles with queries
+  int off;                  // position of query token 0
+  int p0, p1;               // positions of the block's first and last query
+  int sinks, lo;            // tiles: 0 .. sinks - 1, then lo, lo + 1, ..
+  int begin, n, split, all; // of the block's `all` tiles, n from the begin-th on
+  __device__ __forceinline__ int tile(int j) const {
+    const int t = begin + j;
+    return t < sinks ? t : lo + t - sinks;
+  }
+};
+__device__ __forceinline__ Item item_at(const Args& a, int index) {
+  const PromptShape& s = a.s;
+  const int units = s.B * s.H;
+  Item it;
+  it.split = index % a.splits;
+  index /= a.splits;
+  const int u = index % units, rank = index / units;
+  it.b = a.rows.order[u / s.H];
+  it.h = u % s.H;
+  const int q_len = a.rows.q_len[it.b], kv_len = a.rows.kv_len[it.b];
+  const int per = kTile >> s.log_g, blocks = (q_len + 2 * per - 1) / (2 * per);
+  it.n = 0;
+  it.all = 0;
+  if (rank >= blocks) return it;
+  it.tok0 = (blocks - 1 - rank) * 2 * per;
+  it.active = q_len - it.tok0 > per ? 2 : 1;
+  it.off = kv_len - q_len;
+  it.p0 = it.off + it.tok0;
+  it.p1 = it.off + min(it.tok0 + 2 * per, q_len) - 1;
+  const int first = s.sight.window ? max(it.p0 - s.sight.window + 1, 0) : 0;
+  it.lo = first / kTile;
+  it.sinks = min((s.sight.sink + kTile - 1) / kTile, it.lo);
+  it.all = it.sinks + it.p1 / kTile - it.lo + 1;
+  it.begin = (int)((long long)it.all * it.split / a.splits);
+  it.n = (int)((long long)it.all * (it.split + 1) / a.splits) - it.begin;
+  return it;
+}
+// Whether a query of the block may not see all of tile kt. At most seven tiles of a block: the last
+// tiles' positions and the window's first ones span at most 255 tokens each, and one tile holds the
+// end of the sinks.
+__device__ __forceinline__ bool is_masked(const Sight& s, const Item& it, int kt) {
+  const int t0 = kt * kTile, t1 = t0 + kTile - 1;
+  return t1 > it.p0 || (s.window && t0 < it.p1 - s.window + 1 && t1 >= s.sink);
+}
+__device__ __forceinline__ bool sees(const Sight& s, int pos, int j) {
+  return j <= pos && (!s.window || j > pos - s.window || j < s.sink);
+}
+// The k-th item of CTA c of P: forth and back, so that the order by length evens out.
+__device__ __forceinline__ int item_index(int k) {
+  const int P = gridDim.x, c = blockIdx.x;
+  return k * P + ((k & 1) ? P - 1 - c : c);
+}
+
+// 32 lanes (a query row each) x 32 columns.
+__device__ __forceinline__ void tm_ld_row(uint32_t addr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_ld_row16(uint32_t addr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st_row16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
+// One persistent CTA per SM; an item is two tiles of 128 query rows of a unit, which share every K and
+// V tile. Roles meet at mbarriers: one warp loads (bulk tensor copies into a ring of K and V tiles), one
+// issues the products, four softmax warps a query tile (a thread a row) turn S into P in place. While
+// one tile's softmax runs the other's products do: PV and the next S of a tile are issued together.
+//
+// A value that is infinite or NaN would reach queries that do not see its token (0 * inf), so two warps
+// look through the V tiles that some query of the block sees only in part, clear such values and mark
+// their tokens; at the end they are added for the rows that see them. Marks are kept per item, for as
+// many items as the ring can run ahead of the softmax.
+template <int D>
+__global__ void __launch_bounds__(Shape<D>::THREADS, 1)
+    prompt_attention_kernel(const __grid_constant__ Args a) {
+  using Sh = Shape<D>;
+  constexpr int NS = Sh::STAGES;
+  constexpr float kLog2e = 1.4426950408889634f;
+  extern __shared__ char raw[];
+  char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sQ = smem_u32(base), ring = sQ + 2 * Sh::TILE;
+  char* small = base + (2 + NS) * Sh::TILE;
+  uint32_t* sBad = reinterpret_cast<uint32_t*>(small);   // [kBadBufs][kBadTiles][4]
+  const uint32_t bars = smem_u32(small + kBadBufs * kBadTiles * 16);
+  const uint32_t qFull = bars, qFree = bars + 8, sFull = bars + 16, pFull = bars + 32,
+                 oFull = bars + 48, full = bars + 64, empty = full + 8 * NS, loaded = empty + 8 * NS,
+                 after = loaded + 8 * NS;
+  static_assert(kBadBufs * kBadTiles * 16 + 64 + 24 * NS + 16 <= Sh::SMALL, "small arrays");
+  const uint32_t dead = after;
+  volatile int* sDead = reinterpret_cast<volatile int*>(small + (after - smem_u32(small)));
+  uint32_t* sTm = const_cast<uint32_t*>(reinterpret_cast<volatile uint32_t*>(sDead) + 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const PromptShape& s = a.s;
+  const int items = a.blocks * a.splits * s.B * s.H;
+
+  // (only the joining kernel may start early: nothing after a call without it expects to)
+  if (a.splits > 1) asm volatile("griddepcontrol.launch_dependents;");
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(sTm)),
+                 "r"(Sh::TMEM)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    *sDead = 0;
+    mbar_init(qFull, 1);
+    mbar_init(qFree, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sFull + 8 * i, 1);
+      mbar_init(pFull + 8 * i, 4);
+      mbar_init(oFull + 8 * i, 1);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+      mbar_init(loaded + 8 * i, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = *sTm;
+  auto wait = [&](uint32_t bar, int phase) {
+    wait_phase(bar, phase, dead);
+    __syncwarp();
+  };
+
+  if (warp == 8) {
+    // ================================================================ loads
+    const bool issuer = elect_one();
+    const int per = kTile >> s.log_g;
+    int seq = 0, count = 0;   // tiles, items
+#pragma unroll 1
+    for (int k = 0; k * gridDim.x < items; ++k) {
+      const int index = item_index(k);
+      if (index >= items) continue;
+      const Item it = item_at(a, index);
+      if (it.n == 0) continue;
+      if (count > 0) wait(qFree, count - 1);
+      if (issuer) {
+        mbar_expect_tx(qFull, it.active * Sh::TILE);
+#pragma unroll 1
+        for (int t = 0; t < it.active; ++t)
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            load_box(sQ + t * Sh::TILE + c * kBlk, &a.q, 64 * c, it.h * s.G, it.tok0 + t * per,
+                     it.b * s.q_row, qFull);
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int j = 0; j < it.n; ++j) {
+        const int kt = it.tile(j);
+        const bool masked = is_masked(s.sight, it, kt);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++seq) {
+          const int st = seq % NS, use = seq / NS;
+          if (use > 0) wait(empty + 8 * st, use - 1);
+          if (issuer) {
+            const uint32_t bar = (kv && masked ? loaded : full) + 8 * st;
+            mbar_expect_tx(bar, Sh::TILE);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              load_box(ring + st * Sh::TILE + c * kBlk, kv ? &a.v : &a.k, 64 * c, kt * kTile,
+                       it.h * s.kv_head[kv], it.b * s.kv_row[kv], bar);
+          }
+          __syncwarp();
+        }
+      }
+      ++count;
+    }
+  } else if (warp == 9) {
+    // ================================================================ products
+    const bool issuer = elect_one();
+    const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(ring, 16, 1024);
+    const uint64_t dV = smem_desc(ring, kBlk, 1024);
+    constexpr uint32_t kStage = Sh::TILE >> 4;
+    int seq = 0, count = 0, p_uses[2] = {0, 0};
+    auto issue_s = [&](int t, int st) {   // S_t = Q_t K^T
+      if (issuer) {
+        const uint64_t q = dQ + t * kStage, kk = dK + st * kStage;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t off = ((i >> 2) * kBlk + (i & 3) * 32) >> 4;
+          mma_ss(tm + 128 * t, q + off, kk + off, instr_desc(kTile, false), i > 0);
+        }
+        mma_commit(sFull + 8 * t);
+      }
+    };
+#pragma unroll 1
+    for (int k = 0; k * gridDim.x < items; ++k) {
+      const int index = item_index(k);
+      if (index >= items) continue;
+      const Item it = item_at(a, index);
+      if (it.n == 0) continue;
+      wait(qFull, count);
+      wait(full + 8 * (seq % NS), seq / NS);
+      fence_after();
+#pragma unroll 1
+      for (int t = 0; t < it.active; ++t) issue_s(t, seq % NS);
+      if (issuer) {
+        mma_commit(empty + 8 * (seq % NS));
+        if (it.n == 1) mma_commit(qFree);
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int j = 0; j < it.n; ++j, seq += 2) {
+        const int sv = (seq + 1) % NS, sk = (seq + 2) % NS;
+        const bool next = j + 1 < it.n;
+        if (next) wait(full + 8 * sk, (seq + 2) / NS);
+        wait(full + 8 * sv, (seq + 1) / NS);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t >= it.active) break;
+          wait(pFull + 8 * t, p_uses[t]++);
+          fence_after();
+          if (issuer) {
+            const uint64_t v = dV + sv * kStage;
+#pragma unroll
+            for (int i = 0; i < kTile / 16; ++i)
+              mma_ts(tm + 256 + D * t, tm + 128 * t + 8 * i, v + ((i * 2048) >> 4),
+                     instr_desc(D, true), j > 0 || i > 0);
+            if (!next) mma_commit(oFull + 8 * t);
+          }
+          if (next) issue_s(t, sk);
+          __syncwarp();
+        }
+        if (issuer) {
+          mma_commit(empty + 8 * sv);
+          if (next) mma_commit(empty + 8 * sk);
+          if (j + 2 == it.n) mma_commit(qFree);
+        }
+        __syncwarp();
+      }
+      ++count;
+    }
+  } else if (warp >= 10) {
+    // ================================================================ values that are not finite
+    const int th = tid - 320;
+    uint32_t phases = 0;   // of `loaded`, a bit a stage
+    int seq = 0, count = 0;
+#pragma unroll 1
+    for (int k = 0; k * gridDim.x < items; ++k) {
+      const int index = item_index(k);
+      if (index >= items) continue;
+      const Item it = item_at(a, index);
+      if (it.n == 0) continue;
+      uint32_t* bad = sBad + (count % kBadBufs) * (kBadTiles * 4);
+      if (warp == 10) bad[lane] = 0;
+      asm volatile("bar.sync 1, 64;" ::: "memory");
+      int slot = 0;
+#pragma unroll 1
+      for (int j = 0; j < it.n; ++j, seq += 2) {
+        if (!is_masked(s.sight, it, it.tile(j))) continue;
+        const int st = (seq + 1) % NS;
+        wait(loaded + 8 * st, (phases >> st) & 1);
+        phases ^= 1u << st;
+        char* tile = base + (2 + st) * Sh::TILE;
+#pragma unroll 4
+        for (int i = th; i < Sh::TILE / 16; i += 64) {
+          uint4* at = reinterpret_cast<uint4*>(tile + i * 16);
+          uint4 x = *at;
+          auto inf = [](uint32_t w) { return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u; };
+          if (inf(x.x) | inf(x.y) | inf(x.z) | inf(x.w)) {
+            auto clear = [](uint32_t w) {
+              if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;
+              if ((w & 0x7c000000u) == 0x7c000000u) w &= 0xffffu;
+              return w;
+            };
+            *at = make_uint4(clear(x.x), clear(x.y), clear(x.z), clear(x.w));
+            const int row = (i >> 3) & 127;
+            atomicOr(bad + 4 * slot + (row >> 5), 1u << (row & 31));
+          }
+        }
+        ++slot;
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 1, 64;" ::: "memory");
+        if (th == 0) mbar_arrive(full + 8 * st);
+      }
+      ++count;
+    }
+  } else {
+    // ================================================================ softmax
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tm + 128 * t + lanes, tO = tm + 256 + D * t + lanes;
+    const float c = kLog2e * rsqrtf((float)D);
+    const f2x c2 = f2_pack(c, c);
+    int s_uses = 0, o_uses = 0, count = -1;
+#pragma unroll 1
+    for (int k = 0; k * gridDim.x < items; ++k) {
+      const int index = item_index(k);
+      if (index >= items) continue;
+      const Item it = item_at(a, index);
+      if (it.n > 0) ++count;
+      if (it.all == 0 || t >= it.active) continue;
+      const int per = kTile >> s.log_g, tok = it.tok0 + t * per + (r >> s.log_g);
+      const int q_len = a.rows.q_len[it.b], pos = it.off + tok;
+      // rows of this warp with a query, uniformly
+      const bool live = it.tok0 + t * per + (((warp & 3) * 32) >> s.log_g) < q_len;
+      float ref = -INFINITY, sum = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < it.n; ++j) {
+        wait(sFull + 8 * t, s_uses++);
+        fence_after();
+        if (live) {
+          const int kt = it.tile(j);
+          float x[128];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tm_ld_row(tS + 32 * i, x + 32 * i);
+          tm_wait_ld();
+          if (is_masked(s.sight, it, kt)) {
+            const int hi = pos - kt * kTile;
+            const int lo = s.sight.window ? hi - s.sight.window : -1;   // the last one not seen
+            const int si = s.sight.sink - kt * kTile;
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i > hi || (i <= lo && i >= si)) x[i] = -INFINITY;
+          }
+          float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i < 128; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              m4[e] = i + 4 + e < 128 ? fmaxf(fmaxf(m4[e], x[i + e]), x[i + 4 + e])
+                                      : fmaxf(m4[e], x[i + e]);
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+          const bool up = mx > ref + kRefSlack;   // true from -inf
+          if (__any_sync(0xffffffffu, up)) {
+            const float to = up ? mx - kRefBelow : ref, fac = up ? ex2(ref - to) : 1.f;
+            ref = to;
+            sum *= fac;
+            if (j > 0) {
+#pragma unroll 1
+              for (int q = 0; q < D / 16; ++q) {
+                float o[16];
+                tm_ld_row16(tO + 16 * q, o);
+                tm_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= fac;
+                tm_st_row16(tO + 16 * q, reinterpret_cast<const uint32_t*>(o));
+              }
+            }
+          }
+          const float sub = ref == -INFINITY ? 0.f : -ref;
+          const f2x sub2 = f2_pack(sub, sub);
+          f2x acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const f2x y = f2_fma(f2_pack(x[32 * q + 2 * i], x[32 * q + 2 * i + 1]), c2, sub2);
+              float y0, y1;
+              f2_unpack(y, y0, y1);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              acc[i & 1] = f2_add(acc[i & 1], f2_pack(y0, y1));
+              const __half2 h2 = __floats2half2_rn(y0, y1);
+              pk[i] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            tm_st_row16(tS + 16 * q, pk);
+          }
+          float a0, a1, b0, b1;
+          f2_unpack(acc[0], a0, a1);
+          f2_unpack(acc[1], b0, b1);
+          sum += (a0 + a1) + (b0 + b1);
+          tm_wait_st();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pFull + 8 * t);
+      }
+      if (it.n > 0) {
+        wait(oFull + 8 * t, o_uses++);
+        fence_after();
+      }
+      if (!live) continue;
+
+      // ---------------------------------------------- the item's result
+      const bool mine = tok < q_len, whole = a.splits == 1;
+      const int head = it.h * s.G + (r & (s.G - 1));
+      const uint32_t* bad = sBad + (count % kBadBufs) * (kBadTiles * 4);
+      const bool any_bad = it.n > 0 && __any_sync(0xffffffffu, bad[lane] != 0);
+      const float inv = 1.f / sum;
+      uint16_t* out = a.out + it.b * a.o_row + tok * a.o_tok + head * a.o_head;
+      float* part = a.part + (size_t)index * a.part_rows * (D + 2);
+      if (mine) {
+        if (!whole)
+          *reinterpret_cast<float2*>(part + 2 * (128 * t + r)) = make_float2(ref, sum);
+        else if (a.lse)
+          a.lse[((size_t)it.b * s.n_q + tok) * s.Hq + head] =
+              (ref + log2f(sum)) * 0.6931471805599453f;
+      }
+      if (it.n == 0) continue;
+      part += 2 * a.part_rows + (size_t)(128 * t + r) * D;
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        float o[32];
+        tm_ld_row(tO + 32 * q, o);
+        tm_wait_ld();
+        if (any_bad) {
+          int slot = 0;
+#pragma unroll 1
+          for (int j = 0; j < it.n; ++j) {
+            const int kt = it.tile(j);
+            if (!is_masked(s.sight, it, kt)) continue;
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w)
+#pragma unroll 1
+              for (uint32_t left = bad[4 * slot + w]; left; left &= left - 1) {
+                const int key = kt * kTile + 32 * w + __ffs(left) - 1;
+                if (!sees(s.sight, pos, key)) continue;
+                const uint16_t* v = a.vx + it.b * a.v_row + key * a.v_tok + it.h * a.v_head + 32 * q;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float y = h2f(v[i]);
+                  if (!isfinite(y)) o[i] += y;
+                }
+              }
+            ++slot;
+          }
+        }
+        if (!mine) continue;
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 h2 =
+                  __floats2half2_rn(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
+              w[e] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            *reinterpret_cast<uint4*>(out + 32 * q + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(part + 32 * q + 4 * i) =
+                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      fence_before();
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (tid == 0 && *sDead) record_status(a.status, 1);
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(Sh::TMEM));
+}
+
+// Joins the splits of a block, in their order: a warp a query row, lane l the channels 2l + 64 i and the
+// next.
+template <int D>
+__global__ void __launch_bounds__(256) prompt_combine_kernel(const __grid_constant__ Args a) {
+  const PromptShape& s = a.s;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int index = blockIdx.x * a.splits;
+  const Item it = item_at(a, index);
+  const int per = kTile >> s.log_g, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int tok = it.tok0 + (row >> s.log_g);   // (tile 1 begins at row 128 = per tokens)
+  if (it.all == 0 || tok >= a.rows.q_len[it.b] || row >= 2 * per * s.G) return;
+  float M = -INFINITY, L = 0.f, o[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+  const size_t next = (size_t)a.part_rows * (D + 2);
+  const float* part = a.part + index * next;
+#pragma unroll 1
+  for (int z0 = 0; z0 < a.splits; z0 += 8) {
+    const int n = min(8, a.splits - z0);
+    float2 ml[8];
+    float2 x[8][D / 64];
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      const float* p = part + (z0 + min(z, n - 1)) * next;
+      ml[z] = *reinterpret_cast<const float2*>(p + 2 * row);
+      if (z >= n) ml[z] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        x[z][i] = *reinterpret_cast<const float2*>(p + 2 * a.part_rows + (size_t)row * D + 64 * i + 2 * lane);
+    }
+    float Mn = M;
+#pragma unroll
+    for (int z = 0; z < 8; ++z) Mn = fmaxf(Mn, ml[z].x);
+    const float f = M == -INFINITY ? 0.f : ex2(M - Mn);
+    L *= f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] *= f;
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      // a split without tiles, or whose keys gave no maximum: its sum is 0, or NaN
+      const float w = ml[z].x == -INFINITY ? ml[z].y : ex2(ml[z].x - Mn);
+      if (w == 0.f) continue;
+      L = fmaf(ml[z].y, w, L);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        o[2 * i] = fmaf(x[z][i].x, w, o[2 * i]);
+        o[2 * i + 1] = fmaf(x[z][i].y, w, o[2 * i + 1]);
+      }
+    }
+    M = Mn;
+  }
+  const int head = it.h * s.G + (row & (s.G - 1));
+  uint16_t* out = a.out + it.b * a.o_row + tok * a.o_tok + head * a.o_head;
+  const float inv = 1.f / L;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const __half2 h2 = __floats2half2_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
+    *reinterpret_cast<uint32_t*>(out + 64 * i + 2 * lane) = *reinterpret_cast<const uint32_t*>(&h2);
+  }
+  if (lane == 0 && a.lse)
+    a.lse[((size_t)it.b * s.n_q + tok) * s.Hq + head] = (M + log2f(L)) * 0.6931471805599453f;
+}
+
+constexpr int kMaxSM = 160;      // SMs the workspace is sized for
+constexpr int kMinSplit = 2;     // tiles of a split at least
+
+// Blocks of two query tiles of a unit whose row has n queries.
+int blocks_of(const fade_config_t* c, long long n) {
+  return ceil_div(n * (c->num_q_heads / c->num_kv_heads), 2 * kTile);
+}
+// Splits of a block for a call of up to n_q queries a row: blocks that would leave SMs without work are
+// split along their tokens, to at most an item an SM.
+int most_splits(const fade_config_t* c, int n_q, int sms) {
+  const long long slots = (long long)c->batch * c->num_kv_heads * blocks_of(c, n_q);
+  return slots < sms ? (int)(sms / slots) : 1;
+}
+// Query rows of a split's partial; a multiple of 8, so that its vectors start 16-byte aligned.
+int partial_rows(const fade_config_t* c, int n_q) {
+  const long long rows = (long long)n_q * (c->num_q_heads / c->num_kv_heads);
+  return (int)std::min<long long>((rows + 7) / 8 * 8, 2 * kTile);
+}
+
+template <int D>
+fade_status_t launch(const fade_config_t* c, Args& a, int tiles, cudaStream_t st) {
+  using Sh = Shape<D>;
+  int device = 0;
+  const int sms = prompt_sms(&device);
+  if (sms == 0) return FADE_ERR_CUDA;
+  a.splits = std::min(most_splits(c, a.s.n_q, sms), ceil_div(tiles, kMinSplit));
+  a.part_rows = partial_rows(c, a.s.n_q);
+  auto kern = prompt_attention_kernel<D>;
+  static bool opted[64];   // per device: the kernel has its shared memory
+  if (!opted[device]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM) !=
+        cudaSuccess)
+      return launch_status("fade_prompt_attention shared-memory opt-in");
+    opted[device] = true;
+  }
+  const long long items = (long long)a.blocks * a.splits * a.s.B * a.s.H;
+  if (items > (1 << 30))
+    return set_error(FADE_ERR_UNSUPPORTED, "fade_prompt_attention: more than 2^30 blocks of queries");
+  kern<<<(unsigned)(items < sms ? items : sms), Sh::THREADS, Sh::SMEM, st>>>(a);
+  fade_status_t s = launch_status("fade_prompt_attention");
+  if (s || a.splits == 1) return s;
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3(a.blocks * a.s.B * a.s.H, ceil_div(std::min(a.s.n_q * a.s.G, 2 * kTile), 8));
+  lc.blockDim = dim3(256);
+  lc.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&lc, prompt_combine_kernel<D>, a);
+  if (e != cudaSuccess)
+    return set_error(FADE_ERR_CUDA, "fade_prompt_attention combine: %s", cudaGetErrorString(e));
+  return launch_status("fade_prompt_attention combine");
+}
+
+}  // namespace
+
+size_t prompt_attention_ws(const fade_config_t* c, int32_t n_q) {
+  const long long slots = (long long)c->batch * c->num_kv_heads * blocks_of(c, n_q);
+  const int splits = most_splits(c, n_q, kMaxSM);
+  return splits == 1 ? 0 : (size_t)slots * splits * partial_rows(c, n_q) * (c->head_dim + 2) * 4;
+}
+
+int prompt_sms(int* device) {
+  static int known[64];
+  if (cudaGetDevice(device) != cudaSuccess || *device >= 64) {
+    set_error(FADE_ERR_CUDA, "no device, or one past the 64th");
+    return 0;
+  }
+  const int d = *device;
+  if (known[d] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d) != cudaSuccess) {
+      launch_status("SM count");
+      return 0;
+    }
+    known[d] = n < kMaxSM ? n : kMaxSM;
+  }
+  return known[d];
+}
+
+fade_status_t prompt_shape(const fade_config_t* c, const fade_heads_t* q, const fade_heads_t* k,
+                           const fade_heads_t* v, int32_t n_q, int32_t n_kv, const int32_t* h_q_len,
+                           const int32_t* h_kv_len, int32_t n_sink, int32_t window,
+                           PromptShape* shape, PromptRows* rows) {
+  fade_status_t st = validate_config(c);
+  if (st) return st;
+  if (n_q < 1 || n_kv < 1 || n_q > FADE_PROMPT_MAX_TOKENS || n_kv > FADE_PROMPT_MAX_TOKENS)
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "%d queries or %d tokens outside [1, %d]", n_q, n_kv,
+                     FADE_PROMPT_MAX_TOKENS);
+  if (n_sink < 0 || window < 0)
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "n_sink %d or window %d below 0", n_sink, window);
+  struct {
+    const fade_heads_t* x;
+    const char* name;
+    int tokens, heads;
+  } in[3] = {{q, "q", n_q, c->num_q_heads},
+             {k, "k", n_kv, c->num_kv_heads},
+             {v, "v", n_kv, c->num_kv_heads}};
+  for (int i = 0; i < (v ? 3 : 2); ++i) {
+    if ((st = validate_heads(in[i].x, in[i].name))) return st;
+    const fade_heads_t& x = *in[i].x;
+    if (x.row_stride < 0 || x.token_stride < 0 || x.head_stride < 0)
+      return set_error(FADE_ERR_UNSUPPORTED, "%s: negative strides", in[i].name);
+    if ((x.token_stride == 0 && in[i].tokens > 1) ||
+        (i == 0 && x.head_stride == 0 && in[i].heads > 1))
+      return set_error(FADE_ERR_UNSUPPORTED, "%s: the same vector for every token%s", in[i].name,
+                       i == 0 ? " or head" : "");
+  }
+  PromptShape& s = *shape;
+  s.B = c->batch;
+  s.H = c->num_kv_heads;
+  s.Hq = c->num_q_heads;
+  s.G = s.Hq / s.H;
+  s.log_g = 0;
+  while ((1 << s.log_g) < s.G) ++s.log_g;   // G is 1, 2, 4 or 8
+  s.n_q = n_q;
+  s.n_kv = n_kv;
+  s.sight.window = window < n_kv ? window : 0;   // (a window of all tokens hides none)
+  s.sight.sink = s.sight.window ? std::min(n_sink, n_kv) : 0;
+  s.q_row = q->row_stride != 0;
+  s.kv_row[0] = k->row_stride != 0;
+  s.kv_head[0] = k->head_stride != 0;
+  s.kv_row[1] = v && v->row_stride != 0;
+  s.kv_head[1] = v && v->head_stride != 0;
+  for (int b = 0; b < s.B; ++b) {
+    const int ql = h_q_len ? h_q_len[b] : n_q, kl = h_kv_len ? h_kv_len[b] : n_kv;
+    if (ql < 0 || ql > n_q || kl < 0 || kl > n_kv || ql > kl)
+      return set_error(FADE_ERR_INVALID_ARGUMENT,
+                       "row %d: %d queries outside [0, %d], %d tokens outside [0, %d], or fewer tokens "
+                       "than queries",
+                       b, ql, n_q, kl, n_kv);
+    rows->q_len[b] = ql;
+    rows->kv_len[b] = kl;
+    rows->order[b] = (uint8_t)b;
+  }
+  std::stable_sort(rows->order, rows->order + s.B,
+                   [&](uint8_t x, uint8_t y) { return rows->kv_len[x] > rows->kv_len[y]; });
+  return FADE_OK;
+}
+
+}  // namespace fade
+
+using namespace fade;
+
+extern "C" size_t fade_prompt_ws_bytes(const fade_config_t* c, int32_t n_q, int32_t n_kv) {
+  clear_error();
+  if (validate_config(c)) return 0;
+  if (n_q < 1 || n_kv < 1 || n_q > FADE_PROMPT_MAX_TOKENS || n_kv > FADE_PROMPT_MAX_TOKENS) {
+    set_error(FADE_ERR_INVALID_ARGUMENT, "%d queries or %d tokens outside [1, %d]", n_q, n_kv,
+              FADE_PROMPT_MAX_TOKENS);
+    return 0;
+  }
+  return std::max<size_t>(std::max(prompt_attention_ws(c, n_q), prompt_mass_ws(c, n_q, n_kv)), 16);
+}
+
+extern "C" fade_status_t fade_prompt_attention(const fade_config_t* c, const fade_heads_t* q,
+                                               const fade_heads_t* k, const fade_heads_t* v,
+                                               int32_t n_q, int32_t n_kv, const int32_t* h_q_len,
+                                               const int32_t* h_kv_len, int32_t n_sink,
+                                               int32_t window, const fade_heads_t* out, float* lse,
+                                               int32_t* status, void* ws, size_t ws_bytes,
+                                               void* stream) {
+  clear_error();
+  FADE_RANGE("fade_prompt_attention");
+  if (!v || !v->x) return set_error(FADE_ERR_INVALID_ARGUMENT, "NULL v");
+  Args a{};
+  fade_status_t st = prompt_shape(c, q, k, v, n_q, n_kv, h_q_len, h_kv_len, n_sink, window, &a.s,
+                                  &a.rows);
+  if (!st) st = validate_heads(out, "out");
+  if (st) return st;
+  if (!ws || !aligned(ws, 16))
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "workspace is NULL or not 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(status, 4))
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "lse and status must be 4-byte aligned");
+  if (ws_bytes < prompt_attention_ws(c, n_q))
+    return set_error(FADE_ERR_CAPACITY, "prompt workspace %zu bytes, %zu needed", ws_bytes,
+                     prompt_attention_ws(c, n_q));
+  int tiles = 0;   // of a block, at most
+  for (int b = 0; b < a.s.B; ++b) {
+    const int n = blocks_of(c, a.rows.q_len[b]);
+    a.blocks = std::max(a.blocks, n);
+    if (n == 0) continue;
+    const int seen = a.s.sight.window
+                         ? a.s.sight.window + 2 * kTile / a.s.G + a.s.sight.sink + 2 * kTile
+                         : a.rows.kv_len[b];
+    tiles = std::max(tiles, ceil_div(std::min(seen, a.rows.kv_len[b]), kTile));
+  }
+  if (a.blocks == 0) return FADE_OK;
+  const int d = c->head_dim, per = kTile / a.s.G;
+  st = encode_heads(&a.q, "q", *q, d, a.s.Hq, n_q, a.s.B, a.s.G, per, true);
+  if (!st) st = encode_heads(&a.k, "k", *k, d, a.s.H, n_kv, a.s.B, 1, kTile, false);
+  if (!st) st = encode_heads(&a.v, "v", *v, d, a.s.H, n_kv, a.s.B, 1, kTile, false);
+  if (st) return st;
+  a.vx = v->x;
+  a.v_row = v->row_stride;
+  a.v_tok = v->token_stride;
+  a.v_head = v->head_stride;
+  a.out = out->x;
+  a.o_row = out->row_stride;
+  a.o_tok = out->token_stride;
+  a.o_head = out->head_stride;
+  a.lse = lse;
+  a.part = static_cast<float*>(ws);
+  a.status = status;
+  return d == 64 ? launch<64>(c, a, tiles, as_stream(stream))
+                 : launch<128>(c, a, tiles, as_stream(stream));
+}

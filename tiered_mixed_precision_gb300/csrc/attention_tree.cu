@@ -26,6 +26,7 @@
 // rows of 4096 tokens, 515 to 541 at the long ones.
 #include <math.h>
 
+#include "tensor_core.cuh"
 #include "tree.cuh"
 #include "tree_schedule.h"
 
@@ -128,21 +129,6 @@ __device__ __noinline__ int long_last(const Rows* r, int b, int g0, int tiles) {
 }
 
 // ---------------------------------------------------------------- tensor memory and products
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lbo >> 4) << 16) |
-         ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);   // 128-byte swizzle
-}
-// fp16 operands, fp32 accumulator, M = 128; B's N rows K-major, or (mn) channels contiguous.
-__host__ __device__ constexpr uint32_t instr_desc(int n, bool mn) {
-  return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
-      : "memory");
-}
 // E5M2 operands, fp32 accumulator.
 __host__ __device__ constexpr uint32_t instr_desc_low(int n) {
   return instr_desc(n, false) | (1u << 7) | (1u << 10);
@@ -151,30 +137,6 @@ __device__ __forceinline__ void mma_low(uint32_t d, uint64_t a, uint64_t b, uint
   asm volatile("tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, 1;" ::"r"(d), "l"(a),
                "l"(b), "r"(id)
                : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, int acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(ok));
-  return ok != 0;
-}
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   bar)
-               : "memory");
-}
-__device__ __forceinline__ void fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 // 16 lanes x 32 fp32 columns: v[4i .. 4i+1] row lane/4, columns 8i + 2(lane%4) + {0, 1};
 // v[4i+2 .. 4i+3] the same columns of row lane/4 + 8.
@@ -206,18 +168,6 @@ __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t* r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
-__device__ __forceinline__ void tm_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tm_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // ---------------------------------------------------------------- tiles in shared memory
 // Rows of 64 channels (128 bytes) under the 128-byte swizzle, one [128][64] block per 64 channels.
 // An unpacking thread always writes the same group of 32 channels of the same row: four 16-byte
@@ -453,22 +403,6 @@ __device__ __forceinline__ Rows16 f16_rows(const TreeArgs& a, int D, int b, int 
   j -= n_rec;
   return {a.tk.x + b * a.tk.row_stride + j * a.tk.token_stride + h * a.tk.head_stride,
           a.tv.x + b * a.tv.row_stride + j * a.tv.token_stride + h * a.tv.head_stride};
-}
-
-// Waits for the phase-th completion of an mbarrier, for kWaitCycles at most: a wait that gives up sets
-// the CTA's word `dead`, which ends every other wait at once; the flow stays the same.
-__device__ __forceinline__ void wait_phase(uint32_t bar, int phase, uint32_t dead) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n .reg .s64 t0, t1;\n .reg .u32 d;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n @p bra DONE;\n"
-      " mov.u64 t0, %%clock64;\n"
-      "WAIT:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n @p bra DONE;\n"
-      " ld.volatile.shared.u32 d, [%2];\n setp.ne.u32 q, d, 0;\n @q bra DONE;\n"
-      " mov.u64 t1, %%clock64;\n sub.s64 t1, t1, t0;\n setp.lt.s64 q, t1, %3;\n @q bra WAIT;\n"
-      " st.volatile.shared.u32 [%2], 1;\n"
-      "DONE:\n}\n" ::"r"(bar),
-      "r"((uint32_t)phase & 1), "r"(dead), "n"(kWaitCycles)
-      : "memory");
 }
 
 // The lowest n bits; x moved up by n places (down for a negative n). Any n.

@@ -141,6 +141,12 @@ def lib():
                                             S(HeadsT), c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
             "fade_tree_commit": (c_i32, [S(ConfigT), S(LayerT), c_i32, c_vp, c_vp, S(HeadsT),
                                          S(HeadsT), c_vp, c_vp, c_vp, c_sz, c_vp]),
+            "fade_prompt_ws_bytes": (c_sz, [S(ConfigT), c_i32, c_i32]),
+            "fade_prompt_attention": (c_i32, [S(ConfigT), S(HeadsT), S(HeadsT), S(HeadsT), c_i32,
+                                              c_i32, c_vp, c_vp, c_i32, c_i32, S(HeadsT), c_vp,
+                                              c_vp, c_vp, c_sz, c_vp]),
+            "fade_prompt_mass": (c_i32, [S(ConfigT), S(HeadsT), S(HeadsT), c_i32, c_i32, c_vp, c_vp,
+                                         c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_sz, c_vp]),
             "fade_last_error": (ctypes.c_char_p, []),
         }
         for name, (res, args) in sig.items():
@@ -654,6 +660,73 @@ def fade_tree_commit(layer: TieredLayer, q_rot, lse, tree_k, tree_v, path, n_pat
                                   lens.ctypes.data, _ptr(ws),
                                   0 if ws is None else ws.numel() * ws.element_size(),
                                   _stream(stream)))
+
+
+def fade_prompt_ws_bytes(cfg: Config, n_q: int, n_kv: int) -> int:
+    """Workspace bytes of fade_prompt_attention and fade_prompt_mass for up to n_q queries and n_kv
+    tokens a row."""
+    n = lib().fade_prompt_ws_bytes(ctypes.byref(cfg.c()), n_q, n_kv)
+    if n == 0:
+        raise FadeError(FADE_ERR_INVALID_ARGUMENT, fade_last_error())
+    return n
+
+
+def _prompt_args(cfg, dev, q, k, v, q_len, kv_len, ws, status):
+    """Checks of what the prompt calls share; (n_q, n_kv, host lengths, workspace)."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [rows][tokens][heads][channels]")
+    n_q, n_kv, d = q.shape[1], k.shape[1], cfg.head_dim
+    _tensor(dev, "q", q, "float16", (cfg.batch, n_q, cfg.num_q_heads, d), True)
+    kv = (cfg.batch, n_kv, cfg.num_kv_heads, d)
+    _tensor(dev, "k", k, "float16", kv, True)
+    _tensor(dev, "v", v, "float16", kv, True)
+    lens = []
+    for name, x in (("q_len", q_len), ("kv_len", kv_len)):
+        if x is not None:
+            x = np.ascontiguousarray(x, np.int32)
+            if x.shape != (cfg.batch,):
+                raise ValueError(f"{name} must hold {cfg.batch} lengths")
+        lens.append(x)
+    if status is not None:
+        _tensor(dev, "status", status, "int32", (STATUS_WORDS,))
+    if ws is None:
+        ws = _torch.empty(fade_prompt_ws_bytes(cfg, n_q, n_kv), dtype=_torch.uint8, device=q.device)
+    elif not ws.is_contiguous() or (dev is not None and ws.get_device() != dev):
+        raise ValueError("ws must be contiguous and on the current CUDA device")
+    return n_q, n_kv, lens, ws
+
+
+def fade_prompt_attention(cfg: Config, q, k, v, out, lse=None, q_len=None, kv_len=None, n_sink=0,
+                          window=0, ws=None, status=None, stream=None):
+    """Causal attention of q [B][n_q][Hq][d] over k and v [B][n_kv][H][d] (fp16, any strides over the
+    first three dimensions) into out (like q) and lse (f32 [B][n_q][Hq], optional). A row's queries are
+    the last q_len[b] of its kv_len[b] tokens (host integers; None: all). window > 0: a query sees the
+    last ``window`` tokens and the first ``n_sink``. ws: fade_prompt_ws_bytes (made here when not
+    given); status: a layer's status words."""
+    dev = _device(stream)
+    n_q, n_kv, (ql, kl), ws = _prompt_args(cfg, dev, q, k, v, q_len, kv_len, ws, status)
+    _tensor(dev, "out", out, "float16", q.shape, True)
+    _tensor(dev, "lse", lse, "float32", q.shape[:3])
+    _check(lib().fade_prompt_attention(
+        ctypes.byref(cfg.c()), _heads(q), _heads(k), _heads(v), n_q, n_kv,
+        None if ql is None else ql.ctypes.data, None if kl is None else kl.ctypes.data, n_sink, window,
+        _heads(out), _ptr(lse), _ptr(status), _ptr(ws), ws.numel() * ws.element_size(),
+        _stream(stream)))
+
+
+def fade_prompt_mass(cfg: Config, q, k, lse, mass, q_len=None, kv_len=None, n_sink=0, window=0,
+                     accumulate=False, ws=None, status=None, stream=None):
+    """Column sums of fade_prompt_attention's probabilities, from the lse it left: mass f32
+    [B][H][n_kv] (accumulate: added to)."""
+    dev = _device(stream)
+    n_q, n_kv, (ql, kl), ws = _prompt_args(cfg, dev, q, k, None, q_len, kv_len, ws, status)
+    _tensor(dev, "lse", lse, "float32", q.shape[:3])
+    _tensor(dev, "mass", mass, "float32", (cfg.batch, cfg.num_kv_heads, n_kv))
+    _check(lib().fade_prompt_mass(
+        ctypes.byref(cfg.c()), _heads(q), _heads(k), n_q, n_kv,
+        None if ql is None else ql.ctypes.data, None if kl is None else kl.ctypes.data, n_sink, window,
+        _ptr(lse), int(bool(accumulate)), _ptr(mass), _ptr(status), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def fade_attention_tiled(cfg: Config) -> bool:
