@@ -507,6 +507,46 @@ fade_status_t fade_tree_attention(const fade_config_t* cfg, const fade_layer_t* 
                                   const int32_t* n_nodes, uint16_t* out, float* lse, void* ws,
                                   size_t ws_bytes, void* stream);
 
+/* Logits after the nodes of every row's tree, [B][T][vocab] with the vocabulary contiguous: element
+ * strides from one row and node to the next (any; node_stride is not read where there are no nodes). */
+typedef struct {
+  const void* x;
+  int64_t row_stride, node_stride;
+} fade_logits_t;
+typedef enum { FADE_LOGITS_F16 = 0, FADE_LOGITS_BF16 = 1, FADE_LOGITS_F32 = 2 } fade_logit_type_t;
+#define FADE_MAX_VOCAB (1 << 24)
+
+/* Verify the drafted tokens of every row's tree: the path that is kept (what fade_tree_commit takes) and
+ * the token after it, distributed as the target's own tokens are. parents, n_nodes: as for
+ * fade_tree_layout; tokens: DEVICE i32 [B][T]. target: logits after every node, all of `type`
+ * (fade_logit_type_t); target_root: logits after the last cached token [B][vocab], whose candidates are
+ * the nodes without parent; NULL: node 0 is a token that is already certain and heads every path, and
+ * other nodes without parent are not reached. draft, draft_root: the logits from which the children of
+ * a node were drawn, independently of each other, laid out like the target's; NULL: drafts without
+ * probabilities (the drafter's likeliest tokens, a lookup).
+ * temperature: DEVICE f32 [B] (NULL: 1), dividing target and drafter logits; 0 or less: a greedy row. u: DEVICE f32
+ * [B][T] uniform in [0, 1), u[b][i] decides node i; NULL: every row is greedy, and draft must be NULL.
+ * noise: DEVICE f32 [B][vocab] exponential variates (> 0) for the token after the path; NULL: the
+ * likeliest one.
+ * With p and q the softmax of target and drafter logits after the path's last node, its children are
+ * tried in the order of their indices: the child with token x is kept if u q(x) W < max(p(x) - a q(x),
+ * 0), a = 0 and W = 1 at first; a refused one adds W to a, and W becomes the sum of max(p - a q, 0).
+ * Without draft: kept if u W < p(x); a refused one's p(x) is set to 0 and leaves W. When no child is
+ * kept, next is the token with the largest max(p - a q, 0) / noise (p itself if nothing of it is left).
+ * Greedy: a child is kept if its token has the largest logit, which is next otherwise. Ties go to the
+ * lowest token. Logits of -inf or NaN have no probability, +inf reads as the largest number; tokens
+ * outside [0, vocab) are refused.
+ * Writes path: i32 [B][T] (0 past its length), n_path: i32 [B], next: i32 [B] (-1 where there is nothing
+ * to draw from: no logit above -inf, or no node and no target_root). fp32 arithmetic in one fixed order.
+ * Reads only the logits after kept nodes. 1 <= vocab <= FADE_MAX_VOCAB. */
+fade_status_t fade_tree_verify(const fade_config_t* cfg, int32_t T, int32_t vocab, int32_t type,
+                               const int32_t* parents, const int32_t* n_nodes,
+                               const int32_t* tokens, const fade_logits_t* target,
+                               const fade_logits_t* target_root, const fade_logits_t* draft,
+                               const fade_logits_t* draft_root, const float* temperature,
+                               const float* u, const float* noise, int32_t* path, int32_t* n_path,
+                               int32_t* next, void* stream);
+
 /* Commit an accepted path: row b's nodes path[b][0 .. h_n_path[b] - 1] (DEVICE i32 [B][T], each
  * the parent of the next and the first a root; h_n_path: HOST i32 [B], each in [0, T]) become the
  * row's newest tokens, as that many decode steps without eviction would make them: each is

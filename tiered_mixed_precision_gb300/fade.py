@@ -78,6 +78,10 @@ class HeadsT(ctypes.Structure):
                 ("head_stride", c_i64)]
 
 
+class LogitsT(ctypes.Structure):
+    _fields_ = [("x", c_vp), ("row_stride", c_i64), ("node_stride", c_i64)]
+
+
 class LayoutT(ctypes.Structure):
     _fields_ = [(n, c_sz) for n in (
         "sink_k", "sink_v", "recent_k", "recent_v", "mid_k_codes", "mid_k_scales",
@@ -141,6 +145,9 @@ def lib():
                                             S(HeadsT), c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
             "fade_tree_commit": (c_i32, [S(ConfigT), S(LayerT), c_i32, c_vp, c_vp, S(HeadsT),
                                          S(HeadsT), c_vp, c_vp, c_vp, c_sz, c_vp]),
+            "fade_tree_verify": (c_i32, [S(ConfigT), c_i32, c_i32, c_i32, c_vp, c_vp, c_vp,
+                                         S(LogitsT), S(LogitsT), S(LogitsT), S(LogitsT), c_vp, c_vp,
+                                         c_vp, c_vp, c_vp, c_vp, c_vp]),
             "fade_prompt_ws_bytes": (c_sz, [S(ConfigT), c_i32, c_i32]),
             "fade_prompt_attention": (c_i32, [S(ConfigT), S(HeadsT), S(HeadsT), S(HeadsT), c_i32,
                                               c_i32, c_vp, c_vp, c_i32, c_i32, S(HeadsT), c_vp,
@@ -660,6 +667,48 @@ def fade_tree_commit(layer: TieredLayer, q_rot, lse, tree_k, tree_v, path, n_pat
                                   lens.ctypes.data, _ptr(ws),
                                   0 if ws is None else ws.numel() * ws.element_size(),
                                   _stream(stream)))
+
+
+LOGIT_TYPES = {"float16": 0, "bfloat16": 1, "float32": 2}   # fade_logit_type_t
+
+
+def _logits(dev, name, t, dtype, shape):
+    """A [B][T][vocab] (or [B][vocab]) tensor of logits as a fade_logits_t."""
+    if t is None:
+        return None
+    _tensor(dev, name, t, dtype, shape, True)
+    return ctypes.byref(LogitsT(t.data_ptr(), t.stride(0), t.stride(1) if t.dim() == 3 else 0))
+
+
+def fade_tree_verify(cfg: Config, parents, n_nodes, tokens, target, target_root, draft, draft_root,
+                     temperature, u, noise, path, n_path, next_token, stream=None):
+    """Which drafted tokens are kept: parents, tokens i32 [B][T], n_nodes i32 [B] or None; target
+    [B][T][vocab] logits after every node, target_root [B][vocab] after the last cached token (None:
+    node 0 is certain); draft, draft_root: the drafter's, of the same type (None: drafts without
+    probabilities). temperature f32 [B] or None, u f32 [B][T] (None: greedy), noise f32 [B][vocab] or
+    None -> path i32 [B][T], n_path i32 [B], next_token i32 [B]."""
+    if target.dim() != 3 or parents.dim() != 2:
+        raise ValueError("target must be [rows][nodes][vocabulary], parents [rows][nodes]")
+    B, T = cfg.batch, parents.shape[1]
+    V = target.shape[2]
+    dev = _device(stream)
+    dtype = str(target.dtype).removeprefix("torch.")
+    if dtype not in LOGIT_TYPES:
+        raise ValueError(f"logits must be float16, bfloat16 or float32, not {dtype}")
+    for name, t, dt, shape in (("parents", parents, "int32", (B, T)), ("n_nodes", n_nodes, "int32", (B,)),
+                               ("tokens", tokens, "int32", (B, T)),
+                               ("temperature", temperature, "float32", (B,)),
+                               ("u", u, "float32", (B, T)), ("noise", noise, "float32", (B, V)),
+                               ("path", path, "int32", (B, T)), ("n_path", n_path, "int32", (B,)),
+                               ("next_token", next_token, "int32", (B,))):
+        _tensor(dev, name, t, dt, shape)
+    _check(lib().fade_tree_verify(
+        ctypes.byref(cfg.c()), T, V, LOGIT_TYPES[dtype], _ptr(parents), _ptr(n_nodes), _ptr(tokens),
+        _logits(dev, "target", target, dtype, (B, T, V)),
+        _logits(dev, "target_root", target_root, dtype, (B, V)),
+        _logits(dev, "draft", draft, dtype, (B, T, V)),
+        _logits(dev, "draft_root", draft_root, dtype, (B, V)), _ptr(temperature), _ptr(u), _ptr(noise),
+        _ptr(path), _ptr(n_path), _ptr(next_token), _stream(stream)))
 
 
 def fade_prompt_ws_bytes(cfg: Config, n_q: int, n_kv: int) -> int:
