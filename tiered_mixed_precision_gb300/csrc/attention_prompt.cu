@@ -25,18 +25,21 @@ namespace {
 
 constexpr int kRefBelow = 6;     // log2 a new reference lies below the maximum it follows
 constexpr int kRefSlack = 14;    // log2 a row's logits may pass its reference by
-constexpr int kTile = 128;       // tokens of a tile, and query rows of one
+constexpr int kTile = kPromptTile;
 constexpr int kBlk = kTile * 128;   // bytes of a [128][64] fp16 block
-constexpr int kBadBufs = 8, kBadTiles = 8;   // see the checking warps
+constexpr int kBadBufs = 8, kBadTiles = 8;   // see the checking warp
 
 template <int D>
 struct Shape {
   static constexpr int TILE = D / 64 * kBlk;            // bytes of a Q, K or V tile
+  static constexpr int QBUFS = D == 128 ? 1 : 2;        // of each query tile
   static constexpr int STAGES = D == 128 ? 5 : 10;      // ring of K and V tiles
   static constexpr int SMALL = 2048;
-  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + SMALL;
-  static constexpr int THREADS = 384;   // 8 softmax warps, load, products, 2 that check values
-  static constexpr int TMEM = 512;      // columns: S (and P) 2 x 128, O 2 x D
+  static constexpr int SMEM = 1024 + (2 * QBUFS + STAGES) * TILE + SMALL;
+  static constexpr int THREADS = 384;   // 8 softmax warps, load, products of either tile, checks
+  // Tensor memory, 512 columns: S 2 x 128, O 2 x D. P is written over S where nothing is left (d =
+  // 128); otherwise it has columns of its own, and the next S need not wait for P V.
+  static constexpr bool OVER = D == 128;
 };
 
 struct Args {
@@ -48,65 +51,25 @@ struct Args {
   uint16_t* out;
   int64_t o_row, o_tok, o_head;
   float* lse;                    // NULL: not asked for
-  float* part;                   // per (block, split) [part_rows][2] (m, L), then [part_rows][D] O
+  float* part;                   // per CTA two partials: [part_rows][2] (m, L), then [part_rows][D] O
   int32_t* status;
-  int blocks, splits;            // blocks of two query tiles of the longest row; splits of a block
   int part_rows;
+  PromptSchedule sched;
 };
 
-// One piece of work: the tiles [begin, end) of a block of two query tiles of a unit.
-struct Item {
-  int b, h, tok0, active;   // first query token, query tiles with queries
-  int off;                  // position of query token 0
-  int p0, p1;               // positions of the block's first and last query
-  int sinks, lo;            // tiles: 0 .. sinks - 1, then lo, lo + 1, ..
-  int begin, n, split, all; // of the block's `all` tiles, n from the begin-th on
-  __device__ __forceinline__ int tile(int j) const {
-    const int t = begin + j;
-    return t < sinks ? t : lo + t - sinks;
-  }
-};
-__device__ __forceinline__ Item item_at(const Args& a, int index) {
-  const PromptShape& s = a.s;
-  const int units = s.B * s.H;
-  Item it;
-  it.split = index % a.splits;
-  index /= a.splits;
-  const int u = index % units, rank = index / units;
-  it.b = a.rows.order[u / s.H];
-  it.h = u % s.H;
-  const int q_len = a.rows.q_len[it.b], kv_len = a.rows.kv_len[it.b];
-  const int per = kTile >> s.log_g, blocks = (q_len + 2 * per - 1) / (2 * per);
-  it.n = 0;
-  it.all = 0;
-  if (rank >= blocks) return it;
-  it.tok0 = (blocks - 1 - rank) * 2 * per;
-  it.active = q_len - it.tok0 > per ? 2 : 1;
-  it.off = kv_len - q_len;
-  it.p0 = it.off + it.tok0;
-  it.p1 = it.off + min(it.tok0 + 2 * per, q_len) - 1;
-  const int first = s.sight.window ? max(it.p0 - s.sight.window + 1, 0) : 0;
-  it.lo = first / kTile;
-  it.sinks = min((s.sight.sink + kTile - 1) / kTile, it.lo);
-  it.all = it.sinks + it.p1 / kTile - it.lo + 1;
-  it.begin = (int)((long long)it.all * it.split / a.splits);
-  it.n = (int)((long long)it.all * (it.split + 1) / a.splits) - it.begin;
-  return it;
-}
 // Whether a query of the block may not see all of tile kt. At most seven tiles of a block: the last
 // tiles' positions and the window's first ones span at most 255 tokens each, and one tile holds the
 // end of the sinks.
-__device__ __forceinline__ bool is_masked(const Sight& s, const Item& it, int kt) {
+__device__ __forceinline__ bool is_masked(const Sight& s, const PromptItem& it, int kt) {
   const int t0 = kt * kTile, t1 = t0 + kTile - 1;
   return t1 > it.p0 || (s.window && t0 < it.p1 - s.window + 1 && t1 >= s.sink);
 }
 __device__ __forceinline__ bool sees(const Sight& s, int pos, int j) {
   return j <= pos && (!s.window || j > pos - s.window || j < s.sink);
 }
-// The k-th item of CTA c of P: forth and back, so that the order by length evens out.
-__device__ __forceinline__ int item_index(int k) {
-  const int P = gridDim.x, c = blockIdx.x;
-  return k * P + ((k & 1) ? P - 1 - c : c);
+// The lowest n bits; any n.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1;
 }
 
 // 32 lanes (a query row each) x 32 columns.
@@ -146,61 +109,69 @@ __device__ __forceinline__ void tm_st_row16(uint32_t addr, const uint32_t* r) {
 
 // One persistent CTA per SM; an item is two tiles of 128 query rows of a unit, which share every K and
 // V tile. Roles meet at mbarriers: one warp loads (bulk tensor copies into a ring of K and V tiles), one
-// issues the products, four softmax warps a query tile (a thread a row) turn S into P in place. While
-// one tile's softmax runs the other's products do: PV and the next S of a tile are issued together.
+// for either query tile issues its products, four softmax warps a query tile (a thread a row) turn S
+// into P. The two query tiles run free of each other but for the ring, and an item's first S is issued
+// behind the last P V of the one before, while that one's result is written out.
 //
-// A value that is infinite or NaN would reach queries that do not see its token (0 * inf), so two warps
-// look through the V tiles that some query of the block sees only in part, clear such values and mark
-// their tokens; at the end they are added for the rows that see them. Marks are kept per item, for as
-// many items as the ring can run ahead of the softmax.
+// A value that is infinite or NaN would reach queries that do not see its token (0 * inf), so a warp
+// looks through the V tiles that some query of the block sees only in part, clears such values and
+// marks their tokens; at the end they are added for the rows that see them. Marks are kept per item, in
+// kBadBufs buffers; the warp writes to a buffer only once every softmax warp is past its last user.
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
     prompt_attention_kernel(const __grid_constant__ Args a) {
   using Sh = Shape<D>;
-  constexpr int NS = Sh::STAGES;
+  constexpr int NS = Sh::STAGES, QB = Sh::QBUFS;
   constexpr float kLog2e = 1.4426950408889634f;
   extern __shared__ char raw[];
   char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  const uint32_t sQ = smem_u32(base), ring = sQ + 2 * Sh::TILE;
-  char* small = base + (2 + NS) * Sh::TILE;
+  char* tiles = base + 2 * QB * Sh::TILE;
+  const uint32_t sQ = smem_u32(base), ring = smem_u32(tiles);
+  char* small = tiles + NS * Sh::TILE;
   uint32_t* sBad = reinterpret_cast<uint32_t*>(small);   // [kBadBufs][kBadTiles][4]
-  const uint32_t bars = smem_u32(small + kBadBufs * kBadTiles * 16);
-  const uint32_t qFull = bars, qFree = bars + 8, sFull = bars + 16, pFull = bars + 32,
-                 oFull = bars + 48, full = bars + 64, empty = full + 8 * NS, loaded = empty + 8 * NS,
-                 after = loaded + 8 * NS;
-  static_assert(kBadBufs * kBadTiles * 16 + 64 + 24 * NS + 16 <= Sh::SMALL, "small arrays");
-  const uint32_t dead = after;
-  volatile int* sDead = reinterpret_cast<volatile int*>(small + (after - smem_u32(small)));
-  uint32_t* sTm = const_cast<uint32_t*>(reinterpret_cast<volatile uint32_t*>(sDead) + 1);
+  constexpr int kBad = kBadBufs * kBadTiles * 16;
+  volatile int* sDone = reinterpret_cast<volatile int*>(small + kBad);   // [8] items behind each warp
+  volatile int* sDead = sDone + 8;
+  uint32_t* sTm = reinterpret_cast<uint32_t*>(small + kBad + 36);
+  const uint32_t dead = smem_u32(small) + kBad + 32, bars = dead + 32;
+  // [2] each, of the query tiles (Q: [QB][2])
+  const uint32_t qFull = bars, qFree = qFull + 16 * QB, sFull = qFree + 16 * QB, sRead = sFull + 16,
+                 pFull = sRead + 16, oDone = pFull + 16;
+  const uint32_t full = oDone + 16, empty = full + 8 * NS, loaded = empty + 8 * NS;
+  static_assert(kBad + 64 + 32 * QB + 64 + 24 * NS <= Sh::SMALL, "small arrays");
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const PromptShape& s = a.s;
-  const int items = a.blocks * a.splits * s.B * s.H;
 
-  // (only the joining kernel may start early: nothing after a call without it expects to)
-  if (a.splits > 1) asm volatile("griddepcontrol.launch_dependents;");
+  // (only the joining kernel may start early: nothing else after this call expects to)
+  if (a.sched.join[0].last) asm volatile("griddepcontrol.launch_dependents;");
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(sTm)),
-                 "r"(Sh::TMEM)
+                 "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid == 0) {
     *sDead = 0;
-    mbar_init(qFull, 1);
-    mbar_init(qFree, 1);
+    for (int i = 0; i < 2 * QB; ++i) {
+      mbar_init(qFull + 8 * i, 1);
+      mbar_init(qFree + 8 * i, 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sFull + 8 * i, 1);
+      mbar_init(sRead + 8 * i, 4);
       mbar_init(pFull + 8 * i, 4);
-      mbar_init(oFull + 8 * i, 1);
+      mbar_init(oDone + 8 * i, 1);
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 1);
+      mbar_init(empty + 8 * i, 2);   // the products of either query tile
       mbar_init(loaded + 8 * i, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (tid < kBad / 4) sBad[tid] = 0;
+  if (tid < 8) sDone[tid] = 0;
   fence_before();
   __syncthreads();
   fence_after();
@@ -209,29 +180,17 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
     wait_phase(bar, phase, dead);
     __syncwarp();
   };
+  PromptWalk walk;
+  PromptItem it;
+  auto next = [&](PromptItem& x) { return walk.next(s, a.rows, a.sched, gridDim.x, blockIdx.x, x); };
 
   if (warp == 8) {
     // ================================================================ loads
     const bool issuer = elect_one();
     const int per = kTile >> s.log_g;
-    int seq = 0, count = 0;   // tiles, items
+    int seq = 0, q_uses[2] = {0, 0};
 #pragma unroll 1
-    for (int k = 0; k * gridDim.x < items; ++k) {
-      const int index = item_index(k);
-      if (index >= items) continue;
-      const Item it = item_at(a, index);
-      if (it.n == 0) continue;
-      if (count > 0) wait(qFree, count - 1);
-      if (issuer) {
-        mbar_expect_tx(qFull, it.active * Sh::TILE);
-#pragma unroll 1
-        for (int t = 0; t < it.active; ++t)
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            load_box(sQ + t * Sh::TILE + c * kBlk, &a.q, 64 * c, it.h * s.G, it.tok0 + t * per,
-                     it.b * s.q_row, qFull);
-      }
-      __syncwarp();
+    while (next(it)) {
 #pragma unroll 1
       for (int j = 0; j < it.n; ++j) {
         const int kt = it.tile(j);
@@ -250,88 +209,110 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
           }
           __syncwarp();
         }
-      }
-      ++count;
-    }
-  } else if (warp == 9) {
-    // ================================================================ products
-    const bool issuer = elect_one();
-    const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(ring, 16, 1024);
-    const uint64_t dV = smem_desc(ring, kBlk, 1024);
-    constexpr uint32_t kStage = Sh::TILE >> 4;
-    int seq = 0, count = 0, p_uses[2] = {0, 0};
-    auto issue_s = [&](int t, int st) {   // S_t = Q_t K^T
-      if (issuer) {
-        const uint64_t q = dQ + t * kStage, kk = dK + st * kStage;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = ((i >> 2) * kBlk + (i & 3) * 32) >> 4;
-          mma_ss(tm + 128 * t, q + off, kk + off, instr_desc(kTile, false), i > 0);
-        }
-        mma_commit(sFull + 8 * t);
-      }
-    };
-#pragma unroll 1
-    for (int k = 0; k * gridDim.x < items; ++k) {
-      const int index = item_index(k);
-      if (index >= items) continue;
-      const Item it = item_at(a, index);
-      if (it.n == 0) continue;
-      wait(qFull, count);
-      wait(full + 8 * (seq % NS), seq / NS);
-      fence_after();
-#pragma unroll 1
-      for (int t = 0; t < it.active; ++t) issue_s(t, seq % NS);
-      if (issuer) {
-        mma_commit(empty + 8 * (seq % NS));
-        if (it.n == 1) mma_commit(qFree);
-      }
-      __syncwarp();
-#pragma unroll 1
-      for (int j = 0; j < it.n; ++j, seq += 2) {
-        const int sv = (seq + 1) % NS, sk = (seq + 2) % NS;
-        const bool next = j + 1 < it.n;
-        if (next) wait(full + 8 * sk, (seq + 2) / NS);
-        wait(full + 8 * sv, (seq + 1) / NS);
+        if (j > 0) continue;
+        // Q after the item's first tiles, whose copies need not wait for the last item
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (t >= it.active) break;
-          wait(pFull + 8 * t, p_uses[t]++);
-          fence_after();
+          const int buf = 2 * (q_uses[t] % QB) + t, use = q_uses[t] / QB;
+          ++q_uses[t];
+          if (use > 0) wait(qFree + 8 * buf, use - 1);
           if (issuer) {
-            const uint64_t v = dV + sv * kStage;
+            mbar_expect_tx(qFull + 8 * buf, Sh::TILE);
 #pragma unroll
-            for (int i = 0; i < kTile / 16; ++i)
-              mma_ts(tm + 256 + D * t, tm + 128 * t + 8 * i, v + ((i * 2048) >> 4),
-                     instr_desc(D, true), j > 0 || i > 0);
-            if (!next) mma_commit(oFull + 8 * t);
+            for (int c = 0; c < D / 64; ++c)
+              load_box(sQ + buf * Sh::TILE + c * kBlk, &a.q, 64 * c, it.h * s.G, it.tok0 + t * per,
+                       it.b * s.q_row, qFull + 8 * buf);
           }
-          if (next) issue_s(t, sk);
           __syncwarp();
         }
+      }
+    }
+  } else if (warp == 9 || warp == 10) {
+    // ================================================================ products of query tile t
+    const bool issuer = elect_one();
+    const int t = warp - 9;
+    const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(ring, 16, 1024);
+    const uint64_t dV = smem_desc(ring, kBlk, 1024);
+    const uint32_t tS = tm + 128 * t, tO = tm + 256 + D * t, tP = Sh::OVER ? tS : tm + 384 + 64 * t;
+    constexpr uint32_t kStage = Sh::TILE >> 4;
+    int seq = 0, q_uses = 0, n_s = 0, n_p = 0;   // S issued, P taken
+#pragma unroll 1
+    while (next(it)) {
+      if (t >= it.active) {   // (full first: a stage's next use has then begun)
+#pragma unroll 1
+        for (int j = 0; j < 2 * it.n; ++j, ++seq) {
+          wait(full + 8 * (seq % NS), seq / NS);
+          if (issuer) mbar_arrive(empty + 8 * (seq % NS));
+          __syncwarp();
+        }
+        continue;
+      }
+      const int buf = 2 * (q_uses % QB) + t;
+      wait(qFull + 8 * buf, q_uses / QB);
+      ++q_uses;
+      auto issue_s = [&](int at, bool last) {   // S = Q K^T of the tile whose K is at ring place `at`
+        wait(full + 8 * (at % NS), at / NS);
+        if (!Sh::OVER && n_s > 0) wait(sRead + 8 * t, n_s - 1);
+        ++n_s;
+        fence_after();
         if (issuer) {
-          mma_commit(empty + 8 * sv);
-          if (next) mma_commit(empty + 8 * sk);
-          if (j + 2 == it.n) mma_commit(qFree);
+          const uint64_t q = dQ + buf * kStage, kk = dK + (at % NS) * kStage;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = ((i >> 2) * kBlk + (i & 3) * 32) >> 4;
+            mma_ss(tS, q + off, kk + off, instr_desc(kTile, false), i > 0);
+          }
+          mma_commit(sFull + 8 * t);
+          mma_commit(empty + 8 * (at % NS));
+          if (last) mma_commit(qFree + 8 * buf);
         }
         __syncwarp();
+      };
+      issue_s(seq, it.n == 1);
+#pragma unroll 1
+      for (int j = 0; j < it.n; ++j, seq += 2) {
+        const int sv = (seq + 1) % NS;
+        const bool more = j + 1 < it.n;
+        if (!Sh::OVER && more) issue_s(seq + 2, j + 2 == it.n);
+        wait(full + 8 * sv, (seq + 1) / NS);
+        wait(pFull + 8 * t, n_p++);
+        fence_after();
+        if (issuer) {
+          const uint64_t v = dV + sv * kStage;
+#pragma unroll
+          for (int i = 0; i < kTile / 16; ++i)
+            mma_ts(tO, tP + 8 * i, v + ((i * 2048) >> 4), instr_desc(D, true), j > 0 || i > 0);
+          mma_commit(oDone + 8 * t);
+          mma_commit(empty + 8 * sv);
+        }
+        __syncwarp();
+        if (Sh::OVER && more) issue_s(seq + 2, j + 2 == it.n);
       }
-      ++count;
     }
-  } else if (warp >= 10) {
+  } else if (warp == 11) {
     // ================================================================ values that are not finite
-    const int th = tid - 320;
-    uint32_t phases = 0;   // of `loaded`, a bit a stage
+    uint32_t phases = 0, dirty = 0;   // of `loaded`, a bit a stage; buffers that hold marks
     int seq = 0, count = 0;
 #pragma unroll 1
-    for (int k = 0; k * gridDim.x < items; ++k) {
-      const int index = item_index(k);
-      if (index >= items) continue;
-      const Item it = item_at(a, index);
-      if (it.n == 0) continue;
-      uint32_t* bad = sBad + (count % kBadBufs) * (kBadTiles * 4);
-      if (warp == 10) bad[lane] = 0;
-      asm volatile("bar.sync 1, 64;" ::: "memory");
+    for (; next(it); ++count) {
+      const int buf = count % kBadBufs;
+      uint32_t* bad = sBad + buf * (kBadTiles * 4);
+      bool ready = false;
+      auto own = [&]() {   // the buffer's last user is done with it (a bounded wait)
+        if (!ready && count >= kBadBufs) {
+          const long long t0 = clock64();
+          while (!*sDead && __any_sync(0xffffffffu, sDone[lane & 7] <= count - kBadBufs))
+            if (clock64() - t0 > kWaitCycles) *sDead = 1;
+        }
+        ready = true;
+      };
+      if ((dirty >> buf) & 1) {
+        own();
+        bad[lane] = 0;
+        dirty &= ~(1u << buf);
+        __syncwarp();
+      }
       int slot = 0;
 #pragma unroll 1
       for (int j = 0; j < it.n; ++j, seq += 2) {
@@ -339,67 +320,101 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
         const int st = (seq + 1) % NS;
         wait(loaded + 8 * st, (phases >> st) & 1);
         phases ^= 1u << st;
-        char* tile = base + (2 + st) * Sh::TILE;
-#pragma unroll 4
-        for (int i = th; i < Sh::TILE / 16; i += 64) {
-          uint4* at = reinterpret_cast<uint4*>(tile + i * 16);
-          uint4 x = *at;
-          auto inf = [](uint32_t w) { return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u; };
-          if (inf(x.x) | inf(x.y) | inf(x.z) | inf(x.w)) {
-            auto clear = [](uint32_t w) {
-              if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;
-              if ((w & 0x7c000000u) == 0x7c000000u) w &= 0xffffu;
-              return w;
-            };
-            *at = make_uint4(clear(x.x), clear(x.y), clear(x.z), clear(x.w));
-            const int row = (i >> 3) & 127;
-            atomicOr(bad + 4 * slot + (row >> 5), 1u << (row & 31));
+        uint4* tile = reinterpret_cast<uint4*>(tiles + st * Sh::TILE);
+#pragma unroll 1
+        for (int i0 = lane; i0 < Sh::TILE / 16; i0 += 8 * 32) {
+          uint32_t inf[8];
+          uint4 x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = tile[i0 + 32 * e];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            auto f = [](uint32_t w) { return (w & 0x7c007c00u) + 0x04000400u; };
+            inf[e] = (f(x[e].x) | f(x[e].y) | f(x[e].z) | f(x[e].w)) & 0x80008000u;
+          }
+          if (!__any_sync(0xffffffffu, inf[0] | inf[1] | inf[2] | inf[3] | inf[4] | inf[5] | inf[6] |
+                                           inf[7]))
+            continue;
+          own();
+          dirty |= 1u << buf;
+#pragma unroll 1
+          for (int e = 0; e < 8; ++e) {
+            const int i = i0 + 32 * e, row = (i >> 3) & 127;
+            uint32_t w[4] = {tile[i].x, tile[i].y, tile[i].z, tile[i].w};
+            bool any = false;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t lo = (w[q] & 0x7c00u) == 0x7c00u ? 0xffffu : 0u;
+              const uint32_t hi = (w[q] & 0x7c000000u) == 0x7c000000u ? 0xffff0000u : 0u;
+              any |= (lo | hi) != 0;
+              w[q] &= ~(lo | hi);
+            }
+            if (any) {
+              tile[i] = make_uint4(w[0], w[1], w[2], w[3]);
+              atomicOr(bad + 4 * slot + (row >> 5), 1u << (row & 31));
+            }
           }
         }
         ++slot;
         fence_proxy_async_smem();
-        asm volatile("bar.sync 1, 64;" ::: "memory");
-        if (th == 0) mbar_arrive(full + 8 * st);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + 8 * st);
       }
-      ++count;
     }
   } else {
     // ================================================================ softmax
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tm + 128 * t + lanes, tO = tm + 256 + D * t + lanes;
+    const uint32_t tP = Sh::OVER ? tS : tm + 384 + 64 * t + lanes;
     const float c = kLog2e * rsqrtf((float)D);
     const f2x c2 = f2_pack(c, c);
-    int s_uses = 0, o_uses = 0, count = -1;
+    auto arrive = [&](uint32_t bar) {
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    int n_s = 0, count = 0;   // S waited for, items
 #pragma unroll 1
-    for (int k = 0; k * gridDim.x < items; ++k) {
-      const int index = item_index(k);
-      if (index >= items) continue;
-      const Item it = item_at(a, index);
-      if (it.n > 0) ++count;
-      if (it.all == 0 || t >= it.active) continue;
+    for (; next(it); ++count) {
+      __syncwarp();
+      if (lane == 0) sDone[warp] = count;
+      if (t >= it.active) continue;
       const int per = kTile >> s.log_g, tok = it.tok0 + t * per + (r >> s.log_g);
       const int q_len = a.rows.q_len[it.b], pos = it.off + tok;
       // rows of this warp with a query, uniformly
       const bool live = it.tok0 + t * per + (((warp & 3) * 32) >> s.log_g) < q_len;
       float ref = -INFINITY, sum = 0.f;
+      bool masks = false;
 #pragma unroll 1
       for (int j = 0; j < it.n; ++j) {
-        wait(sFull + 8 * t, s_uses++);
+        const int kt = it.tile(j);
+        const bool masked = is_masked(s.sight, it, kt);
+        masks |= masked;
+        wait(sFull + 8 * t, n_s++);
         fence_after();
+        float x[128];
         if (live) {
-          const int kt = it.tile(j);
-          float x[128];
 #pragma unroll
           for (int i = 0; i < 4; ++i) tm_ld_row(tS + 32 * i, x + 32 * i);
           tm_wait_ld();
-          if (is_masked(s.sight, it, kt)) {
+        }
+        if (!Sh::OVER) arrive(sRead + 8 * t);
+        float fac = 1.f;
+        bool up = false;
+        if (live) {
+          if (masked) {
             const int hi = pos - kt * kTile;
             const int lo = s.sight.window ? hi - s.sight.window : -1;   // the last one not seen
             const int si = s.sight.sink - kt * kTile;
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i > hi || (i <= lo && i >= si)) x[i] = -INFINITY;
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t see = low_bits(hi + 1 - 32 * q) &
+                                   (~low_bits(lo + 1 - 32 * q) | low_bits(si - 32 * q));
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(see & (1u << i))) x[32 * q + i] = -INFINITY;
+            }
           }
           float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -409,23 +424,30 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
               m4[e] = i + 4 + e < 128 ? fmaxf(fmaxf(m4[e], x[i + e]), x[i + 4 + e])
                                       : fmaxf(m4[e], x[i + e]);
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
-          const bool up = mx > ref + kRefSlack;   // true from -inf
-          if (__any_sync(0xffffffffu, up)) {
-            const float to = up ? mx - kRefBelow : ref, fac = up ? ex2(ref - to) : 1.f;
-            ref = to;
+          up = mx > ref + kRefSlack;   // true from -inf
+          if (up) {
+            fac = ex2(ref - (mx - kRefBelow));
+            ref = mx - kRefBelow;
             sum *= fac;
-            if (j > 0) {
+          }
+        }
+        // the last P V is done: O may be scaled, P's columns written
+        if (j > 0) {
+          wait(oDone + 8 * t, n_s - 2);
+          fence_after();
+          if (__any_sync(0xffffffffu, up)) {
 #pragma unroll 1
-              for (int q = 0; q < D / 16; ++q) {
-                float o[16];
-                tm_ld_row16(tO + 16 * q, o);
-                tm_wait_ld();
+            for (int q = 0; q < D / 16; ++q) {
+              float o[16];
+              tm_ld_row16(tO + 16 * q, o);
+              tm_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] *= fac;
-                tm_st_row16(tO + 16 * q, reinterpret_cast<const uint32_t*>(o));
-              }
+              for (int i = 0; i < 16; ++i) o[i] *= fac;
+              tm_st_row16(tO + 16 * q, reinterpret_cast<const uint32_t*>(o));
             }
           }
+        }
+        if (live) {
           const float sub = ref == -INFINITY ? 0.f : -ref;
           const f2x sub2 = f2_pack(sub, sub);
           f2x acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
@@ -443,7 +465,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
               const __half2 h2 = __floats2half2_rn(y0, y1);
               pk[i] = *reinterpret_cast<const uint32_t*>(&h2);
             }
-            tm_st_row16(tS + 16 * q, pk);
+            tm_st_row16(tP + 16 * q, pk);
           }
           float a0, a1, b0, b1;
           f2_unpack(acc[0], a0, a1);
@@ -451,24 +473,21 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
           sum += (a0 + a1) + (b0 + b1);
           tm_wait_st();
         }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pFull + 8 * t);
+        arrive(pFull + 8 * t);
       }
-      if (it.n > 0) {
-        wait(oFull + 8 * t, o_uses++);
-        fence_after();
-      }
+      wait(oDone + 8 * t, n_s - 1);
+      fence_after();
       if (!live) continue;
 
       // ---------------------------------------------- the item's result
-      const bool mine = tok < q_len, whole = a.splits == 1;
+      const bool mine = tok < q_len, whole = it.n == it.all;
       const int head = it.h * s.G + (r & (s.G - 1));
       const uint32_t* bad = sBad + (count % kBadBufs) * (kBadTiles * 4);
-      const bool any_bad = it.n > 0 && __any_sync(0xffffffffu, bad[lane] != 0);
+      const bool any_bad =
+          masks && __any_sync(0xffffffffu, reinterpret_cast<const volatile uint32_t*>(bad)[lane] != 0);
       const float inv = 1.f / sum;
       uint16_t* out = a.out + it.b * a.o_row + tok * a.o_tok + head * a.o_head;
-      float* part = a.part + (size_t)index * a.part_rows * (D + 2);
+      float* part = a.part + ((size_t)blockIdx.x * 2 + (it.begin == 0 ? 1 : 0)) * a.part_rows * (D + 2);
       if (mine) {
         if (!whole)
           *reinterpret_cast<float2*>(part + 2 * (128 * t + r)) = make_float2(ref, sum);
@@ -476,7 +495,6 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
           a.lse[((size_t)it.b * s.n_q + tok) * s.Hq + head] =
               (ref + log2f(sum)) * 0.6931471805599453f;
       }
-      if (it.n == 0) continue;
       part += 2 * a.part_rows + (size_t)(128 * t + r) * D;
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
@@ -527,44 +545,48 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
       }
       fence_before();
     }
+    __syncwarp();
+    if (lane == 0) sDone[warp] = 1 << 30;
   }
   fence_before();
   __syncthreads();
   if (tid == 0 && *sDead) record_status(a.status, 1);
   if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(Sh::TMEM));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
 }
 
-// Joins the splits of a block, in their order: a warp a query row, lane l the channels 2l + 64 i and the
-// next.
+// Joins the partials of an item that several CTAs shared, in the order of its tiles: a warp a query
+// row, lane l the channels 2l + 64 i and the next.
 template <int D>
 __global__ void __launch_bounds__(256) prompt_combine_kernel(const __grid_constant__ Args a) {
   const PromptShape& s = a.s;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int index = blockIdx.x * a.splits;
-  const Item it = item_at(a, index);
-  const int per = kTile >> s.log_g, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int tok = it.tok0 + (row >> s.log_g);   // (tile 1 begins at row 128 = per tokens)
-  if (it.all == 0 || tok >= a.rows.q_len[it.b] || row >= 2 * per * s.G) return;
+  const auto& jn = a.sched.join[blockIdx.x];
+  const PromptItem it = prompt_item(s, a.rows, jn.item);
+  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int tok = it.tok0 + (row >> s.log_g);   // (query tile 1 begins at row 128)
+  if (tok >= a.rows.q_len[it.b]) return;
   float M = -INFINITY, L = 0.f, o[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-  const size_t next = (size_t)a.part_rows * (D + 2);
-  const float* part = a.part + index * next;
+  const size_t slot = (size_t)a.part_rows * (D + 2);
 #pragma unroll 1
-  for (int z0 = 0; z0 < a.splits; z0 += 8) {
-    const int n = min(8, a.splits - z0);
+  for (int c0 = jn.first; c0 <= jn.last; c0 += 8) {
     float2 ml[8];
     float2 x[8][D / 64];
 #pragma unroll
     for (int z = 0; z < 8; ++z) {
-      const float* p = part + (z0 + min(z, n - 1)) * next;
-      ml[z] = *reinterpret_cast<const float2*>(p + 2 * row);
-      if (z >= n) ml[z] = make_float2(-INFINITY, 0.f);
+      const int c = min(c0 + z, (int)jn.last);
+      // (a CTA between them may have no share)
+      const bool has = c0 + z <= jn.last && (a.sched.start[c].item != a.sched.start[c + 1].item ||
+                                             a.sched.start[c].tile != a.sched.start[c + 1].tile);
+      const float* p = a.part + (2 * c + (c == jn.first ? 1 : 0)) * slot;
+      ml[z] = has ? *reinterpret_cast<const float2*>(p + 2 * row) : make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int i = 0; i < D / 64; ++i)
-        x[z][i] = *reinterpret_cast<const float2*>(p + 2 * a.part_rows + (size_t)row * D + 64 * i + 2 * lane);
+        x[z][i] = has ? *reinterpret_cast<const float2*>(p + 2 * a.part_rows + (size_t)row * D +
+                                                         64 * i + 2 * lane)
+                      : make_float2(0.f, 0.f);
     }
     float Mn = M;
 #pragma unroll
@@ -575,7 +597,7 @@ __global__ void __launch_bounds__(256) prompt_combine_kernel(const __grid_consta
     for (int i = 0; i < D / 32; ++i) o[i] *= f;
 #pragma unroll
     for (int z = 0; z < 8; ++z) {
-      // a split without tiles, or whose keys gave no maximum: its sum is 0, or NaN
+      // without a maximum nothing was seen, sum 0, or NaN alone, sum NaN
       const float w = ml[z].x == -INFINITY ? ml[z].y : ex2(ml[z].x - Mn);
       if (w == 0.f) continue;
       L = fmaf(ml[z].y, w, L);
@@ -599,33 +621,25 @@ __global__ void __launch_bounds__(256) prompt_combine_kernel(const __grid_consta
     a.lse[((size_t)it.b * s.n_q + tok) * s.Hq + head] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
-constexpr int kMaxSM = 160;      // SMs the workspace is sized for
-constexpr int kMinSplit = 2;     // tiles of a split at least
-
 // Blocks of two query tiles of a unit whose row has n queries.
 int blocks_of(const fade_config_t* c, long long n) {
   return ceil_div(n * (c->num_q_heads / c->num_kv_heads), 2 * kTile);
 }
-// Splits of a block for a call of up to n_q queries a row: blocks that would leave SMs without work are
-// split along their tokens, to at most an item an SM.
-int most_splits(const fade_config_t* c, int n_q, int sms) {
-  const long long slots = (long long)c->batch * c->num_kv_heads * blocks_of(c, n_q);
-  return slots < sms ? (int)(sms / slots) : 1;
-}
-// Query rows of a split's partial; a multiple of 8, so that its vectors start 16-byte aligned.
+// Query rows of a partial; a multiple of 8, so that its vectors start 16-byte aligned.
 int partial_rows(const fade_config_t* c, int n_q) {
   const long long rows = (long long)n_q * (c->num_q_heads / c->num_kv_heads);
   return (int)std::min<long long>((rows + 7) / 8 * 8, 2 * kTile);
 }
 
 template <int D>
-fade_status_t launch(const fade_config_t* c, Args& a, int tiles, cudaStream_t st) {
+fade_status_t launch(const fade_config_t* c, Args& a, int blocks, cudaStream_t st) {
   using Sh = Shape<D>;
   int device = 0;
   const int sms = prompt_sms(&device);
   if (sms == 0) return FADE_ERR_CUDA;
-  a.splits = std::min(most_splits(c, a.s.n_q, sms), ceil_div(tiles, kMinSplit));
   a.part_rows = partial_rows(c, a.s.n_q);
+  int P = 0;
+  const int joins = prompt_schedule(a.s, a.rows, blocks, sms, a.sched, &P);
   auto kern = prompt_attention_kernel<D>;
   static bool opted[64];   // per device: the kernel has its shared memory
   if (!opted[device]) {
@@ -634,14 +648,11 @@ fade_status_t launch(const fade_config_t* c, Args& a, int tiles, cudaStream_t st
       return launch_status("fade_prompt_attention shared-memory opt-in");
     opted[device] = true;
   }
-  const long long items = (long long)a.blocks * a.splits * a.s.B * a.s.H;
-  if (items > (1 << 30))
-    return set_error(FADE_ERR_UNSUPPORTED, "fade_prompt_attention: more than 2^30 blocks of queries");
-  kern<<<(unsigned)(items < sms ? items : sms), Sh::THREADS, Sh::SMEM, st>>>(a);
+  kern<<<P, Sh::THREADS, Sh::SMEM, st>>>(a);
   fade_status_t s = launch_status("fade_prompt_attention");
-  if (s || a.splits == 1) return s;
+  if (s || joins == 0) return s;
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(a.blocks * a.s.B * a.s.H, ceil_div(std::min(a.s.n_q * a.s.G, 2 * kTile), 8));
+  lc.gridDim = dim3(joins, a.part_rows / 8);
   lc.blockDim = dim3(256);
   lc.stream = st;
   cudaLaunchAttribute at[1];
@@ -658,9 +669,7 @@ fade_status_t launch(const fade_config_t* c, Args& a, int tiles, cudaStream_t st
 }  // namespace
 
 size_t prompt_attention_ws(const fade_config_t* c, int32_t n_q) {
-  const long long slots = (long long)c->batch * c->num_kv_heads * blocks_of(c, n_q);
-  const int splits = most_splits(c, n_q, kMaxSM);
-  return splits == 1 ? 0 : (size_t)slots * splits * partial_rows(c, n_q) * (c->head_dim + 2) * 4;
+  return (size_t)2 * kPromptSMs * partial_rows(c, n_q) * (c->head_dim + 2) * 4;
 }
 
 int prompt_sms(int* device) {
@@ -676,7 +685,7 @@ int prompt_sms(int* device) {
       launch_status("SM count");
       return 0;
     }
-    known[d] = n < kMaxSM ? n : kMaxSM;
+    known[d] = n < kPromptSMs ? n : kPromptSMs;
   }
   return known[d];
 }
@@ -778,17 +787,11 @@ extern "C" fade_status_t fade_prompt_attention(const fade_config_t* c, const fad
   if (ws_bytes < prompt_attention_ws(c, n_q))
     return set_error(FADE_ERR_CAPACITY, "prompt workspace %zu bytes, %zu needed", ws_bytes,
                      prompt_attention_ws(c, n_q));
-  int tiles = 0;   // of a block, at most
-  for (int b = 0; b < a.s.B; ++b) {
-    const int n = blocks_of(c, a.rows.q_len[b]);
-    a.blocks = std::max(a.blocks, n);
-    if (n == 0) continue;
-    const int seen = a.s.sight.window
-                         ? a.s.sight.window + 2 * kTile / a.s.G + a.s.sight.sink + 2 * kTile
-                         : a.rows.kv_len[b];
-    tiles = std::max(tiles, ceil_div(std::min(seen, a.rows.kv_len[b]), kTile));
-  }
-  if (a.blocks == 0) return FADE_OK;
+  int blocks = 0;
+  for (int b = 0; b < a.s.B; ++b) blocks = std::max(blocks, blocks_of(c, a.rows.q_len[b]));
+  if (blocks == 0) return FADE_OK;
+  if ((long long)blocks * a.s.B * a.s.H > (1 << 30))
+    return set_error(FADE_ERR_UNSUPPORTED, "fade_prompt_attention: more than 2^30 blocks of queries");
   const int d = c->head_dim, per = kTile / a.s.G;
   st = encode_heads(&a.q, "q", *q, d, a.s.Hq, n_q, a.s.B, a.s.G, per, true);
   if (!st) st = encode_heads(&a.k, "k", *k, d, a.s.H, n_kv, a.s.B, 1, kTile, false);
@@ -805,6 +808,6 @@ extern "C" fade_status_t fade_prompt_attention(const fade_config_t* c, const fad
   a.lse = lse;
   a.part = static_cast<float*>(ws);
   a.status = status;
-  return d == 64 ? launch<64>(c, a, tiles, as_stream(stream))
-                 : launch<128>(c, a, tiles, as_stream(stream));
+  return d == 64 ? launch<64>(c, a, blocks, as_stream(stream))
+                 : launch<128>(c, a, blocks, as_stream(stream));
 }

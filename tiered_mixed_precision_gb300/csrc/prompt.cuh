@@ -2,27 +2,10 @@
 // host checks.
 #pragma once
 
+#include "prompt_schedule.h"
 #include "tree.cuh"
 
 namespace fade {
-
-// The rows of a call. Queries are the last q_len of a row's kv_len tokens.
-struct PromptRows {
-  int32_t q_len[FADE_MAX_BATCH], kv_len[FADE_MAX_BATCH];
-  uint8_t order[FADE_MAX_BATCH];   // rows, the most tokens first
-};
-
-// What queries see: token j of position i's past if window is 0, j > i - window or j < sink.
-struct Sight {
-  int sink, window;   // window 0: sink 0, too
-};
-
-struct PromptShape {
-  int B, H, G, log_g, Hq, n_q, n_kv;
-  Sight sight;
-  // 0 where a stride is 0 (a broadcast dimension): the tensor map's extent is 1 there
-  int q_row, kv_row[2], kv_head[2];
-};
 
 // Checks what the prompt calls share and fills rows and shape. v: NULL where the call has none.
 fade_status_t prompt_shape(const fade_config_t* c, const fade_heads_t* q, const fade_heads_t* k,

@@ -15,10 +15,12 @@
 // 312 with 5, and 292 without the short rows.
 #pragma once
 
+#ifndef FADE_SCHED
 #ifdef __CUDACC__
 #define FADE_SCHED __host__ __device__ __forceinline__
 #else
 #define FADE_SCHED inline
+#endif
 #endif
 
 namespace fade {
