@@ -97,6 +97,37 @@ __device__ __forceinline__ void tm_ld_row16(uint32_t addr, float* v) {
       : "r"(addr)
       : "memory");
 }
+// 16 lanes x 32 columns: v[4i .. 4i+1] row lane/4, columns 8i + 2(lane%4) + {0, 1}; v[4i+2 .. 4i+3] the
+// same columns of row lane/4 + 8.
+__device__ __forceinline__ void tm_ld_quads(uint32_t addr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+// Words w[i] of lane k of a quad become words w[k] of lane i.
+__device__ __forceinline__ void transpose_quad(uint32_t (&w)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int b = 1; b < 4; b <<= 1) {
+    const bool high = lane & b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & b) continue;
+      const uint32_t give = high ? w[i] : w[i | b];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, give, b);
+      if (high)
+        w[i] = got;
+      else
+        w[i | b] = got;
+    }
+  }
+}
 __device__ __forceinline__ void tm_st_row16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -374,16 +405,23 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
+    const int turn = 1 + 2 * (warp & 3) + t, others = 1 + 2 * (warp & 3) + (t ^ 1);
+    if (t == 1) asm volatile("bar.arrive %0, 64;" ::"r"(others) : "memory");
     int n_s = 0, count = 0;   // S waited for, items
+    bool some = next(it);
 #pragma unroll 1
-    for (; next(it); ++count) {
+    for (; some; ++count) {
       __syncwarp();
       if (lane == 0) sDone[warp] = count;
-      if (t >= it.active) continue;
+      if (t >= it.active) {
+        some = next(it);
+        continue;
+      }
       const int per = kTile >> s.log_g, tok = it.tok0 + t * per + (r >> s.log_g);
       const int q_len = a.rows.q_len[it.b], pos = it.off + tok;
       // rows of this warp with a query, uniformly
       const bool live = it.tok0 + t * per + (((warp & 3) * 32) >> s.log_g) < q_len;
+      const bool turns = it.active == 2 && it.tok0 + (((warp & 3) * 32 + 128) >> s.log_g) < q_len;
       float ref = -INFINITY, sum = 0.f;
       bool masks = false;
 #pragma unroll 1
@@ -447,6 +485,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
             }
           }
         }
+        if (turns) asm volatile("bar.sync %0, 64;" ::"r"(turn) : "memory");
         if (live) {
           const float sub = ref == -INFINITY ? 0.f : -ref;
           const f2x sub2 = f2_pack(sub, sub);
@@ -467,6 +506,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
             }
             tm_st_row16(tP + 16 * q, pk);
           }
+          if (turns) asm volatile("bar.arrive %0, 64;" ::"r"(others) : "memory");
           float a0, a1, b0, b1;
           f2_unpack(acc[0], a0, a1);
           f2_unpack(acc[1], b0, b1);
@@ -475,78 +515,108 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
         }
         arrive(pFull + 8 * t);
       }
+      // the next item is worked out while the last P V runs
+      const PromptItem now = it;
+      some = next(it);
       wait(oDone + 8 * t, n_s - 1);
       fence_after();
       if (!live) continue;
 
       // ---------------------------------------------- the item's result
-      const bool mine = tok < q_len, whole = it.n == it.all;
-      const int head = it.h * s.G + (r & (s.G - 1));
+      // Read so that a quad of lanes holds consecutive channels of a row, and written 64 bytes a row:
+      // with a thread a row, every 16-byte store met 32 lines (64 single-channel tiles of d = 128 took
+      // 5 us to write, 1 us now).
+      const bool whole = now.n == now.all;
       const uint32_t* bad = sBad + (count % kBadBufs) * (kBadTiles * 4);
       const bool any_bad =
           masks && __any_sync(0xffffffffu, reinterpret_cast<const volatile uint32_t*>(bad)[lane] != 0);
-      const float inv = 1.f / sum;
-      uint16_t* out = a.out + it.b * a.o_row + tok * a.o_tok + head * a.o_head;
-      float* part = a.part + ((size_t)blockIdx.x * 2 + (it.begin == 0 ? 1 : 0)) * a.part_rows * (D + 2);
-      if (mine) {
+      float* part = a.part + ((size_t)blockIdx.x * 2 + (now.begin == 0 ? 1 : 0)) * a.part_rows * (D + 2);
+      if (tok < q_len) {
         if (!whole)
           *reinterpret_cast<float2*>(part + 2 * (128 * t + r)) = make_float2(ref, sum);
         else if (a.lse)
-          a.lse[((size_t)it.b * s.n_q + tok) * s.Hq + head] =
+          a.lse[((size_t)now.b * s.n_q + tok) * s.Hq + now.h * s.G + (r & (s.G - 1))] =
               (ref + log2f(sum)) * 0.6931471805599453f;
       }
-      part += 2 * a.part_rows + (size_t)(128 * t + r) * D;
+      const float inv = 1.f / sum;
+      part += 2 * a.part_rows;
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        float o[32];
-        tm_ld_row(tO + 32 * q, o);
-        tm_wait_ld();
-        if (any_bad) {
-          int slot = 0;
-#pragma unroll 1
-          for (int j = 0; j < it.n; ++j) {
-            const int kt = it.tile(j);
-            if (!is_masked(s.sight, it, kt)) continue;
-#pragma unroll 1
-            for (int w = 0; w < 4; ++w)
-#pragma unroll 1
-              for (uint32_t left = bad[4 * slot + w]; left; left &= left - 1) {
-                const int key = kt * kTile + 32 * w + __ffs(left) - 1;
-                if (!sees(s.sight, pos, key)) continue;
-                const uint16_t* v = a.vx + it.b * a.v_row + key * a.v_tok + it.h * a.v_head + 32 * q;
+      for (int f = 0; f < 2; ++f) {   // 16 rows at a time, two of them in a thread
+        int64_t at[2];
+        int row[2], tk[2];
+        float scale[2];
+        bool mine[2];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float y = h2f(v[i]);
-                  if (!isfinite(y)) o[i] += y;
-                }
-              }
-            ++slot;
-          }
+        for (int e = 0; e < 2; ++e) {
+          row[e] = (warp & 3) * 32 + 16 * f + 8 * e + (lane >> 2);
+          tk[e] = now.tok0 + t * per + (row[e] >> s.log_g);
+          mine[e] = tk[e] < q_len;
+          scale[e] = __shfl_sync(0xffffffffu, inv, 16 * f + 8 * e + (lane >> 2));
+          at[e] = now.b * a.o_row + tk[e] * a.o_tok + (now.h * s.G + (row[e] & (s.G - 1))) * a.o_head;
         }
-        if (!mine) continue;
-        if (whole) {
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          float o[16];
+          __syncwarp();
+          tm_ld_quads(tO + ((uint32_t)(16 * f) << 16) + 32 * q, o);
+          tm_wait_ld();
+          if (any_bad) {   // what was left out of the products, into the rows that see it
+            int slot = 0;
+#pragma unroll 1
+            for (int j = 0; j < now.n; ++j) {
+              const int kt = now.tile(j);
+              if (!is_masked(s.sight, now, kt)) continue;
+#pragma unroll 1
+              for (int w = 0; w < 4; ++w)
+#pragma unroll 1
+                for (uint32_t left = bad[4 * slot + w]; left; left &= left - 1) {
+                  const int key = kt * kTile + 32 * w + __ffs(left) - 1;
+                  const uint16_t* v = a.vx + now.b * a.v_row + key * a.v_tok + now.h * a.v_head +
+                                      32 * q + 2 * (lane & 3);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+                  for (int e = 0; e < 2; ++e) {
+                    if (!mine[e] || !sees(s.sight, now.off + tk[e], key)) continue;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __half2 h2 =
-                  __floats2half2_rn(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
-              w[e] = *reinterpret_cast<const uint32_t*>(&h2);
+                    for (int i = 0; i < 8; ++i) {
+                      const float y = h2f(v[8 * (i >> 1) + (i & 1)]);
+                      if (!isfinite(y)) o[4 * (i >> 1) + 2 * e + (i & 1)] += y;
+                    }
+                  }
+                }
+              ++slot;
             }
-            *reinterpret_cast<uint4*>(out + 32 * q + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(part + 32 * q + 4 * i) =
-                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int e = 0; e < 2; ++e) {
+            if (whole) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const __half2 h2 = __floats2half2_rn(o[4 * i + 2 * e] * scale[e],
+                                                     o[4 * i + 2 * e + 1] * scale[e]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              __syncwarp();
+              transpose_quad(w);
+              if (mine[e])
+                *reinterpret_cast<uint4*>(a.out + at[e] + 32 * q + 8 * (lane & 3)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            } else if (mine[e]) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float2*>(part + (size_t)(128 * t + row[e]) * D + 32 * q + 8 * i +
+                                           2 * (lane & 3)) =
+                    make_float2(o[4 * i + 2 * e], o[4 * i + 2 * e + 1]);
+            }
+          }
         }
       }
+      __syncwarp();
       fence_before();
     }
     __syncwarp();
     if (lane == 0) sDone[warp] = 1 << 30;
+    if (t == 0) asm volatile("bar.sync %0, 64;" ::"r"(turn) : "memory");   // (the first turn again)
   }
   fence_before();
   __syncthreads();
