@@ -46,12 +46,14 @@ int main() {
     struct Range { int c, begin, n, slot; };
     std::map<std::pair<int, std::pair<int, int>>, std::vector<Range>> got;   // (b, h, tok0)
     double most = 0, total = 0, largest = 0;
+    auto each = [](const PromptItem& it) { return it.active == 2 ? kCostTwo : kCostOne; };
     for (int c = 0; c < P; ++c) {
-      PromptWalk walk;
+      PromptWalk<PromptItem> walk;
       PromptItem it;
       std::set<int> slots;
       double cost = 0;
-      while (walk.next(s, rows, a, P, c, it)) {
+      auto at = [&](int index) { return prompt_item(s, rows, index); };
+      while (walk.next(a, P, c, at, it)) {
         MUST(it.n > 0 && it.begin >= 0 && it.begin + it.n <= it.all);
         MUST(it.b >= 0 && it.b < s.B && it.h >= 0 && it.h < s.H);
         const int slot = it.n == it.all ? -1 : 2 * c + (it.begin == 0 ? 1 : 0);
@@ -68,8 +70,8 @@ int main() {
                                    t1 >= s.sight.sink);
         }
         MUST(masked <= 7);
-        cost += it.n * prompt_tile_cost(it);
-        largest = std::max<double>(largest, prompt_cost(it));
+        cost += it.n * each(it);
+        largest = std::max<double>(largest, kCostStart + it.all * each(it));
       }
       most = std::max(most, cost);
       total += cost;
@@ -124,6 +126,59 @@ int main() {
         }
       }
     MUST(taken == (int)got.size() && shared == joins);
+    // ---- the column sums: every query tile that sees a key of a pair meets it once
+    s.n_kv = 1;
+    for (int b = 0; b < s.B; ++b) s.n_kv = std::max(s.n_kv, rows.kv_len[b]);
+    const int pairs = (s.n_kv + 255) / 256, per = kPromptTile >> s.log_g;
+    static PromptSchedule m;
+    m = PromptSchedule{};
+    int Pm = 0, sharedm = 0;
+    const int joinsm = mass_schedule(s, rows, sms, m, &Pm);
+    MUST(Pm >= 1 && Pm <= sms && joinsm <= Pm && m.whole == 0);
+    std::map<std::pair<int, std::pair<int, int>>, std::vector<Range>> met;   // (b, h, k0)
+    double mostm = 0, totalm = 0;
+    for (int c = 0; c < Pm; ++c) {
+      PromptWalk<MassItem> walk;
+      MassItem it;
+      std::set<int> slots;
+      int tiles = 0;
+      auto at = [&](int index) { return mass_item(s, rows, index); };
+      while (walk.next(m, Pm, c, at, it)) {
+        MUST(it.n > 0 && it.begin >= 0 && it.begin + it.n <= it.all);
+        const int slot = it.n == it.all ? -1 : 2 * c + (it.begin == 0 ? 1 : 0);
+        if (slot >= 0) MUST(slots.insert(slot).second);
+        met[{it.b, {it.h, it.k0}}].push_back({c, it.begin, it.n, slot});
+        tiles += it.n;
+      }
+      mostm = std::max<double>(mostm, tiles);
+      totalm += tiles;
+    }
+    for (int i = 0; i < pairs * s.B * s.H; ++i) {
+      const MassItem it = mass_item(s, rows, i);
+      const int kv = rows.kv_len[it.b], q = rows.q_len[it.b], w = s.sight.window;
+      for (int tok = 0; tok < q; ++tok) {   // a query that sees one of the keys is in a tile
+        const int p = kv - q + tok, hi = std::min(std::min(it.k0 + 255, kv - 1), p);
+        const bool sees = it.k0 <= hi && (!w || hi > p - w || it.k0 < s.sight.sink);
+        if (sees) MUST(tok / per >= it.first && tok / per < it.first + it.all);
+      }
+      MUST(it.all == 0 || it.first + it.all <= (q + per - 1) / per);
+      auto& r = met[{it.b, {it.h, it.k0}}];
+      std::sort(r.begin(), r.end(), [](const Range& x, const Range& y) { return x.begin < y.begin; });
+      int at = 0;
+      for (auto& x : r) {
+        MUST(x.begin == at);
+        at += x.n;
+      }
+      MUST(at == it.all);
+      if (r.size() > 1) {
+        int found = 0;
+        for (int j = 0; j < joinsm; ++j) found += m.join[j].item == i && m.join[j].first == r[0].c &&
+                                                  m.join[j].last == r.back().c;
+        MUST(found == 1);
+        ++sharedm;
+      }
+    }
+    MUST(sharedm == joinsm && mostm <= 1.1 * totalm / Pm + 8);
     printf("%d %d %d %g %g %g\n", P, joins, a.whole, total / P, most, largest);
   }
   return 0;

@@ -211,9 +211,12 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
     wait_phase(bar, phase, dead);
     __syncwarp();
   };
-  PromptWalk walk;
+  PromptWalk<PromptItem> walk;
   PromptItem it;
-  auto next = [&](PromptItem& x) { return walk.next(s, a.rows, a.sched, gridDim.x, blockIdx.x, x); };
+  auto next = [&](PromptItem& x) {
+    return walk.next(a.sched, gridDim.x, blockIdx.x,
+                     [&](int index) { return prompt_item(s, a.rows, index); }, x);
+  };
 
   if (warp == 8) {
     // ================================================================ loads
@@ -832,7 +835,7 @@ extern "C" size_t fade_prompt_ws_bytes(const fade_config_t* c, int32_t n_q, int3
               FADE_PROMPT_MAX_TOKENS);
     return 0;
   }
-  return std::max<size_t>(std::max(prompt_attention_ws(c, n_q), prompt_mass_ws(c, n_q, n_kv)), 16);
+  return std::max(prompt_attention_ws(c, n_q), prompt_mass_ws());
 }
 
 extern "C" fade_status_t fade_prompt_attention(const fade_config_t* c, const fade_heads_t* q,

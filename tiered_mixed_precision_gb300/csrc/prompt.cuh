@@ -15,6 +15,6 @@ fade_status_t prompt_shape(const fade_config_t* c, const fade_heads_t* q, const 
 // SMs of the current device (0: an error, which is set).
 int prompt_sms(int* device);
 size_t prompt_attention_ws(const fade_config_t* c, int32_t n_q);
-size_t prompt_mass_ws(const fade_config_t* c, int32_t n_q, int32_t n_kv);
+size_t prompt_mass_ws();
 
 }  // namespace fade

@@ -7,8 +7,8 @@
 // second sum. Products run transposed, S^T = K Q^T, so that a thread of a softmax warp owns a key and
 // its sum stays in a register.
 //
-// Sums are fp32, tile by tile (128 terms, then a tile's sum a term), in one fixed order: no atomics, the
-// same bits on every run.
+// Sums are fp32: 16 terms a key and lane in a tile, the tiles of a share, four lanes, two warps, the
+// shares of the CTAs that took the key's tiles; each in one fixed order. No atomics: the same bits on every run.
 #include <math.h>
 
 #include <algorithm>
@@ -20,20 +20,17 @@
 namespace fade {
 namespace {
 
-constexpr int kTile = 128;          // keys of a tile, and query rows of one
-constexpr int kBlk = kTile * 128;   // bytes of a [128][64] fp16 block
-constexpr int kPair = 2 * kTile;    // keys of an item
-constexpr int kMaxChunks = 16;      // pieces that a pair's queries are cut into at most
-constexpr int kMinChunk = 8;        // query tiles of a piece at least
-constexpr int kMaxSM = 160;         // SMs the workspace is sized for
+constexpr int kTile = kPromptTile;   // keys of a tile, and query rows of one
+constexpr int kBlk = kTile * 128;    // bytes of a [128][64] fp16 block
+constexpr int kPair = 2 * kTile;     // keys of an item
 
 template <int D>
 struct Shape {
   static constexpr int TILE = D / 64 * kBlk;          // bytes of a K or Q tile
   static constexpr int STAGES = D == 128 ? 4 : 8;     // ring of Q tiles
-  static constexpr int SMALL = 1024 + STAGES * 512;   // barriers, then the rows' -l of every stage
+  static constexpr int SMALL = 3072;
   static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + SMALL;
-  static constexpr int THREADS = 384;   // 8 warps that sum, load, products, 2 that scale lse
+  static constexpr int THREADS = 640;   // 16 warps that sum, load, products, 2 that scale lse
 };
 
 struct Args {
@@ -42,68 +39,31 @@ struct Args {
   PromptRows rows;
   const float* lse;
   float* mass;
-  float* part;      // chunks > 1: [chunk][unit][pairs * kPair]
+  float* part;      // per CTA two partials of kPair sums
   int32_t* status;
-  int pairs, chunks, add;
+  int add;
+  PromptSchedule sched;
 };
 
-// The query tiles [begin, begin + n) that see a pair of key tiles; a chunk of them.
-struct Item {
-  int b, h, u, k0, chunk, chunks, begin, n;
-  int off, q_len;   // position of query token 0; the row's queries
-};
-__device__ __forceinline__ Item item_at(const Args& a, int index) {
-  const PromptShape& s = a.s;
-  const int units = s.B * s.H;
-  Item it;
-  it.chunk = index % a.chunks;
-  index /= a.chunks;
-  const int u = index % units;
-  it.k0 = index / units * kPair;
-  it.b = a.rows.order[u / s.H];
-  it.h = u % s.H;
-  it.u = it.b * s.H + it.h;
-  it.q_len = a.rows.q_len[it.b];
-  const int kv_len = a.rows.kv_len[it.b], per = kTile >> s.log_g;
-  it.off = kv_len - it.q_len;
-  const int first = max(it.k0 - it.off, 0);
-  int last = it.q_len - 1;
-  if (s.sight.window && it.k0 >= s.sight.sink)
-    last = min(last, it.k0 + kPair - 1 + s.sight.window - 1 - it.off);
-  const int all = it.k0 < kv_len && first <= last ? last / per - first / per + 1 : 0;
-  it.chunks = min(a.chunks, max((all + kMinChunk - 1) / kMinChunk, 1));
-  it.begin = 0;
-  it.n = 0;
-  if (it.chunk < it.chunks) {
-    const int from = all * it.chunk / it.chunks;
-    it.begin = first / per + from;
-    it.n = all * (it.chunk + 1) / it.chunks - from;
-  }
-  return it;
-}
-__device__ __forceinline__ int item_index(int k) {   // forth and back over the CTAs
-  const int P = gridDim.x, c = blockIdx.x;
-  return k * P + ((k & 1) ? P - 1 - c : c);
-}
-
-__device__ __forceinline__ void tm_ld_row(uint32_t addr, float* v) {   // 32 lanes x 32 columns
+// 16 lanes x 32 columns: v[4i .. 4i+1] row lane/4, columns 8i + 2(lane%4) + {0, 1}; v[4i+2 .. 4i+3] the
+// same columns of row lane/4 + 8.
+__device__ __forceinline__ void tm_ld_quads(uint32_t addr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[14]), "=r"(r[15])
       : "r"(addr)
       : "memory");
 }
 
 // One persistent CTA per SM; an item is two tiles of 128 keys of a unit, both met by every query tile of
 // the ring. Roles meet at mbarriers: one warp loads (bulk tensor copies), two bring the rows' lse, one
-// issues the products, four warps a key tile (a thread a key) sum; S has two buffers a key tile, so
-// products run ahead of the sums.
+// issues the products, four warps a key tile sum; S has two buffers a key tile, so products run ahead of
+// the sums. A summing thread reads two columns of every eight of four keys: their lse, two words, serve
+// all four (with a thread a key, every lse was read by every thread: 113 us at 8 prompts of 2048).
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
     prompt_mass_kernel(const __grid_constant__ Args a) {
@@ -114,7 +74,8 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
   char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sK = smem_u32(base), ring = sK + 2 * Sh::TILE;
   char* small = base + (2 + NS) * Sh::TILE;
-  float* sL = reinterpret_cast<float*>(small + 1024);   // [NS][128]
+  float* sL = reinterpret_cast<float*>(small + 1024);   // [2 buffers][128]
+  float* sHalf = sL + 2 * kTile;                        // [kPair] sums of the second halves
   const uint32_t bars = smem_u32(small);
   const uint32_t kFull = bars, kFree = bars + 8, sFull = bars + 16, sFree = bars + 48,
                  full = bars + 80, empty = full + 8 * NS, dead = empty + 8 * NS;
@@ -123,9 +84,9 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
   uint32_t* sTm = reinterpret_cast<uint32_t*>(small + (dead - bars) + 4);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const PromptShape& s = a.s;
-  const int items = a.pairs * a.chunks * s.B * s.H, per = kTile >> s.log_g;
+  const int per = kTile >> s.log_g;
 
-  if (a.chunks > 1) asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.launch_dependents;");   // (the joining kernel always follows)
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(sTm)),
@@ -138,12 +99,12 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
     mbar_init(kFull, 1);
     mbar_init(kFree, 1);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(sFull + 8 * i, 1);
-      mbar_init(sFree + 8 * i, 4);
+      mbar_init(sFull + 8 * i, 3);   // the products, two warps of lse
+      mbar_init(sFree + 8 * i, 8);
     }
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full + 8 * i, 3);    // the copy, two warps of lse
-      mbar_init(empty + 8 * i, 9);   // the products, eight warps that read lse
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -155,28 +116,19 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
     wait_phase(bar, phase, dead);
     __syncwarp();
   };
+  PromptWalk<MassItem> walk;
+  MassItem it;
+  auto next = [&]() {
+    return walk.next(a.sched, gridDim.x, blockIdx.x,
+                     [&](int index) { return mass_item(s, a.rows, index); }, it);
+  };
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ================================================================ loads
     const bool issuer = elect_one();
     int seq = 0, count = 0;
 #pragma unroll 1
-    for (int k = 0; k * gridDim.x < items; ++k) {
-      const int index = item_index(k);
-      if (index >= items) continue;
-      const Item it = item_at(a, index);
-      if (it.n == 0) continue;
-      if (count > 0) wait(kFree, count - 1);
-      if (issuer) {
-        mbar_expect_tx(kFull, 2 * Sh::TILE);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            load_box(sK + t * Sh::TILE + c * kBlk, &a.k, 64 * c, it.k0 + t * kTile,
-                     it.h * s.kv_head[0], it.b * s.kv_row[0], kFull);
-      }
-      __syncwarp();
+    while (next()) {
 #pragma unroll 1
       for (int j = 0; j < it.n; ++j, ++seq) {
         const int st = seq % NS, use = seq / NS;
@@ -185,25 +137,33 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
           mbar_expect_tx(full + 8 * st, Sh::TILE);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            load_box(ring + st * Sh::TILE + c * kBlk, &a.q, 64 * c, it.h * s.G, (it.begin + j) * per,
-                     it.b * s.q_row, full + 8 * st);
+            load_box(ring + st * Sh::TILE + c * kBlk, &a.q, 64 * c, it.h * s.G,
+                     (it.first + it.begin + j) * per, it.b * s.q_row, full + 8 * st);
+        }
+        __syncwarp();
+        if (j > 0) continue;
+        if (count > 0) wait(kFree, count - 1);
+        if (issuer) {
+          mbar_expect_tx(kFull, 2 * Sh::TILE);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              load_box(sK + t * Sh::TILE + c * kBlk, &a.k, 64 * c, it.k0 + t * kTile,
+                       it.h * s.kv_head[0], it.b * s.kv_row[0], kFull);
         }
         __syncwarp();
       }
       ++count;
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ================================================================ products
     const bool issuer = elect_one();
     const uint64_t dK = smem_desc(sK, 16, 1024), dQ = smem_desc(ring, 16, 1024);
     constexpr uint32_t kStage = Sh::TILE >> 4;
     int seq = 0, count = 0;
 #pragma unroll 1
-    for (int k = 0; k * gridDim.x < items; ++k) {
-      const int index = item_index(k);
-      if (index >= items) continue;
-      const Item it = item_at(a, index);
-      if (it.n == 0) continue;
+    while (next()) {
       wait(kFull, count);
 #pragma unroll 1
       for (int j = 0; j < it.n; ++j, ++seq) {
@@ -232,110 +192,150 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
       }
       ++count;
     }
-  } else if (warp >= 10) {
+  } else if (warp >= 18) {
     // ================================================================ lse
-    const int r0 = (warp - 10) * 64 + lane;
+    const int r0 = (warp - 18) * 64 + lane;
     int seq = 0;
 #pragma unroll 1
-    for (int k = 0; k * gridDim.x < items; ++k) {
-      const int index = item_index(k);
-      if (index >= items) continue;
-      const Item it = item_at(a, index);
+    while (next()) {
 #pragma unroll 1
       for (int j = 0; j < it.n; ++j, ++seq) {
-        const int st = seq % NS, use = seq / NS;
+        const int buf = seq & 1;
         float l[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = r0 + 32 * e, tok = (it.begin + j) * per + (r >> s.log_g);
+          const int r = r0 + 32 * e, tok = (it.first + it.begin + j) * per + (r >> s.log_g);
           l[e] = tok < it.q_len ? a.lse[((size_t)it.b * s.n_q + tok) * s.Hq + it.h * s.G +
                                         (r & (s.G - 1))]
                                 : 0.f;
         }
-        if (use > 0) wait(empty + 8 * st, use - 1);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) sL[st * kTile + r0 + 32 * e] = -kLog2e * l[e];
+        for (int t = 0; t < 2; ++t)
+          if (seq >= 2) wait(sFree + 16 * t + 8 * buf, (seq >> 1) - 1);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sL[buf * kTile + r0 + 32 * e] = -kLog2e * l[e];
         __syncwarp();
-        if (lane == 0) mbar_arrive(full + 8 * st);
+        if (lane == 0) {
+          mbar_arrive(sFull + 8 * buf);
+          mbar_arrive(sFull + 16 + 8 * buf);
+        }
       }
     }
   } else {
     // ================================================================ sums
-    const int t = warp >> 2, key = t * kTile + (warp & 3) * 32 + lane;
-    const uint32_t tS = tm + 256 * t + ((uint32_t)((warp & 3) * 32) << 16);
+    // two warps a group of 32 keys, each with half of a tile's query rows
+    const int t = warp >> 3, half = (warp >> 2) & 1, col = 2 * (lane & 3);
+    const int key0 = t * kTile + (warp & 3) * 32 + (lane >> 2);   // the thread's keys: + 16 f + 8 e
+    const uint32_t tS = tm + 256 * t + 64 * half + ((uint32_t)((warp & 3) * 32) << 16);
     const float c = kLog2e * rsqrtf((float)D);
     const f2x c2 = f2_pack(c, c);
+    // of the columns 64 half + 8 i + col + {0, 1}, those below n, a bit each
+    auto below = [&](int n) {
+      n -= 64 * half;
+      const int bits = 2 * (n >> 3) + min(max((n & 7) - col, 0), 2);
+      return n <= 0 ? 0u : bits >= 32 ? ~0u : (1u << bits) - 1;
+    };
     int seq = 0;
 #pragma unroll 1
-    for (int k = 0; k * gridDim.x < items; ++k) {
-      const int index = item_index(k);
-      if (index >= items) continue;
-      const Item it = item_at(a, index);
-      if (it.chunk >= it.chunks) continue;
-      const int j = it.k0 + key, k_end = it.k0 + t * kTile + kTile - 1;
-      float total = 0.f;
+    while (next()) {
+      const int k_end = it.k0 + t * kTile + kTile - 1;   // the tile's last key
+      f2x total[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) total[e] = f2_pack(0.f, 0.f);
 #pragma unroll 1
       for (int i = 0; i < it.n; ++i, ++seq) {
-        const int st = seq % NS, buf = seq & 1, tok0 = (it.begin + i) * per;
-        const int p0 = it.off + tok0;
-        // rows that see the key: columns [lo, hi)
-        const int hi_tok = min(s.sight.window && j >= s.sight.sink ? j + s.sight.window - p0 : per,
-                               it.q_len - tok0);
-        const int lo = max(j - p0, 0) << s.log_g, hi = min(max(hi_tok, 0), per) << s.log_g;
-        const bool all = k_end <= p0 && it.q_len - tok0 >= per &&
-                         (!s.sight.window || k_end < s.sight.sink ||
-                          k_end - kTile + 1 + s.sight.window >= p0 + per);   // uniform
+        const int buf = seq & 1, tok0 = (it.first + it.begin + i) * per;
+        const int p0 = it.off + tok0, left = it.q_len - tok0;   // positions from p0, `left` queries
+        const int w = s.sight.window;
+        // whether every query sees every key of the tile, and whether any sees any
+        const bool all = k_end <= p0 && left >= per &&
+                         (!w || k_end < s.sight.sink || k_end - kTile + 1 + w >= p0 + per);
+        const bool none = k_end - kTile + 1 >= p0 + per ||
+                          (w && k_end - kTile + 1 >= s.sight.sink && p0 >= k_end + w);
         wait(sFull + 16 * t + 8 * buf, seq >> 1);
-        wait(full + 8 * st, seq / NS);   // (complete: what was written there is seen from here on)
         fence_after();
-        f2x acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-        const float4* l4 = reinterpret_cast<const float4*>(sL + st * kTile);
-        auto sum_tile = [&](auto some) {
+        if (!none) {
+          float x[2][2][16];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float x[32];
-            tm_ld_row(tS + 128 * buf + 32 * q, x);
-            tm_wait_ld();
+          for (int f = 0; f < 2; ++f)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 l = l4[8 * q + e];
-              float y[4];
-              f2_unpack(f2_fma(f2_pack(x[4 * e], x[4 * e + 1]), c2, f2_pack(l.x, l.y)), y[0], y[1]);
-              f2_unpack(f2_fma(f2_pack(x[4 * e + 2], x[4 * e + 3]), c2, f2_pack(l.z, l.w)), y[2],
-                        y[3]);
+            for (int q = 0; q < 2; ++q)
+              tm_ld_quads(tS + 128 * buf + 32 * q + ((uint32_t)(16 * f) << 16), x[f][q]);
+          const float* l = sL + buf * kTile + 64 * half + col;
+          f2x acc[4];
 #pragma unroll
-              for (int i4 = 0; i4 < 4; ++i4) {
-                y[i4] = ex2(y[i4]);
-                const int col = 32 * q + 4 * e + i4;
-                if (decltype(some)::value && (col < lo || col >= hi)) y[i4] = 0.f;
+          for (int e = 0; e < 4; ++e) acc[e] = f2_pack(0.f, 0.f);
+          tm_wait_ld();
+          auto sum_tile = [&](auto some) {
+            uint32_t see[4];
+            if constexpr (decltype(some)::value) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {   // queries that see the key: columns [lo, hi)
+                const int j = it.k0 + key0 + 8 * e;
+                const int end = min(w && j >= s.sight.sink ? j + w - p0 : per, left);
+                see[e] = below(min(max(end, 0), per) << s.log_g) &
+                         ~below(min(max(j - p0, 0), per) << s.log_g);
               }
-              acc[0] = f2_add(acc[0], f2_pack(y[0], y[1]));
-              acc[1] = f2_add(acc[1], f2_pack(y[2], y[3]));
             }
-          }
-        };
-        if (all)
-          sum_tile(std::false_type());
-        else
-          sum_tile(std::true_type());
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i8 = 0; i8 < 4; ++i8) {
+                const float2 ll = *reinterpret_cast<const float2*>(l + 32 * q + 8 * i8);
+                const f2x l2 = f2_pack(ll.x, ll.y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float* y = &x[e >> 1][q][4 * i8 + 2 * (e & 1)];
+                  float y0, y1;
+                  f2_unpack(f2_fma(f2_pack(y[0], y[1]), c2, l2), y0, y1);
+                  y0 = ex2(y0);
+                  y1 = ex2(y1);
+                  if constexpr (decltype(some)::value) {
+                    const uint32_t bit = 1u << (2 * (4 * q + i8));
+                    if (!(see[e] & bit)) y0 = 0.f;
+                    if (!(see[e] & (bit << 1))) y1 = 0.f;
+                  }
+                  acc[e] = f2_add(acc[e], f2_pack(y0, y1));
+                }
+              }
+          };
+          if (all)
+            sum_tile(std::false_type());
+          else
+            sum_tile(std::true_type());
+#pragma unroll
+          for (int e = 0; e < 4; ++e) total[e] = f2_add(total[e], acc[e]);
+        }
         fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(sFree + 16 * t + 8 * buf);
-          mbar_arrive(empty + 8 * st);
+        if (lane == 0) mbar_arrive(sFree + 16 * t + 8 * buf);
+      }
+      float* out = it.n == it.all
+                       ? a.mass + ((size_t)it.b * s.H + it.h) * s.n_kv
+                       : a.part + ((size_t)blockIdx.x * 2 + (it.begin == 0 ? 1 : 0)) * kPair - it.k0;
+      const int end = it.n == it.all ? a.rows.kv_len[it.b] : it.k0 + kPair;
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float y1;
+        f2_unpack(total[e], y[e], y1);
+        y[e] += y1;
+        y[e] += __shfl_xor_sync(0xffffffffu, y[e], 1);
+        y[e] += __shfl_xor_sync(0xffffffffu, y[e], 2);
+        if (half && (lane & 3) == 0) sHalf[key0 + 8 * e] = y[e];
+      }
+      const int pair = 1 + 4 * t + (warp & 3);   // the two warps' named barrier
+      asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+      if (!half && (lane & 3) == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = it.k0 + key0 + 8 * e;
+          const float z = y[e] + sHalf[key0 + 8 * e];
+          if (j < end) out[j] = it.n == it.all && a.add ? out[j] + z : z;
         }
-        float a0, a1, b0, b1;
-        f2_unpack(acc[0], a0, a1);
-        f2_unpack(acc[1], b0, b1);
-        total += (a0 + a1) + (b0 + b1);
       }
-      if (a.chunks > 1) {
-        a.part[((size_t)it.chunk * s.B * s.H + it.u) * a.pairs * kPair + j] = total;
-      } else if (j < s.n_kv) {
-        float* m = a.mass + (size_t)it.u * s.n_kv + j;
-        if (j >= a.rows.kv_len[it.b]) total = 0.f;   // (n > 0: whatever lies there)
-        *m = a.add ? *m + total : total;
-      }
+      __syncwarp();
+      asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");   // (read: the next item may write)
     }
   }
   fence_before();
@@ -345,29 +345,32 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512));
 }
 
-// The chunks of every pair, added in their order.
-__global__ void __launch_bounds__(kPair) prompt_mass_join_kernel(const __grid_constant__ Args a) {
+// The pairs that several CTAs shared, added in their order (block x < joins), and zeros where no query
+// sees a key: pairs without tiles, keys past a row's length (block joins + pair * units + unit).
+__global__ void __launch_bounds__(kPair) prompt_mass_join_kernel(const __grid_constant__ Args a,
+                                                                 int joins) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PromptShape& s = a.s;
-  const Item it = item_at(a, blockIdx.x * a.chunks);
-  const int j = it.k0 + threadIdx.x;
+  const bool shared = (int)blockIdx.x < joins;
+  const MassItem it =
+      mass_item(s, a.rows, shared ? a.sched.join[blockIdx.x].item : blockIdx.x - joins);
+  const int j = it.k0 + threadIdx.x, kv_len = a.rows.kv_len[it.b];
+  float* m = a.mass + ((size_t)it.b * s.H + it.h) * s.n_kv + j;
   if (j >= s.n_kv) return;
+  if (!shared) {
+    if (!a.add && (it.all == 0 || j >= kv_len)) *m = 0.f;
+    return;
+  }
+  if (j >= kv_len) return;
   float total = 0.f;
-  if (j < a.rows.kv_len[it.b])
-    for (int i = 0; i < it.chunks; ++i)
-      total += a.part[((size_t)i * s.B * s.H + it.u) * a.pairs * kPair + j];
-  float* m = a.mass + (size_t)it.u * s.n_kv + j;
+  const auto& jn = a.sched.join[blockIdx.x];
+  for (int c = jn.first; c <= jn.last; ++c) {
+    if (a.sched.start[c].item == a.sched.start[c + 1].item &&
+        a.sched.start[c].tile == a.sched.start[c + 1].tile)
+      continue;   // no share
+    total += a.part[((size_t)c * 2 + (c == jn.first ? 1 : 0)) * kPair + threadIdx.x];
+  }
   *m = a.add ? *m + total : total;
-}
-
-int pairs_of(int32_t n_kv) { return ceil_div(n_kv, kPair); }
-
-// Pieces of a pair's queries: enough for several items an SM.
-int most_chunks(const fade_config_t* c, int32_t n_q, int32_t n_kv) {
-  const long long items = (long long)c->batch * c->num_kv_heads * pairs_of(n_kv);
-  const int tiles = ceil_div((long long)n_q * (c->num_q_heads / c->num_kv_heads), kTile);
-  return std::min({kMaxChunks, (int)std::min<long long>(ceil_div(8 * kMaxSM, items), kMaxChunks),
-                   ceil_div(tiles, kMinChunk)});
 }
 
 template <int D>
@@ -384,14 +387,13 @@ fade_status_t launch(Args& a, cudaStream_t st) {
       return launch_status("fade_prompt_mass shared-memory opt-in");
     opted[device] = true;
   }
-  const long long items = (long long)a.pairs * a.chunks * a.s.B * a.s.H;
-  if (items > (1 << 30))
-    return set_error(FADE_ERR_UNSUPPORTED, "fade_prompt_mass: more than 2^30 blocks of keys");
-  kern<<<(unsigned)std::min<long long>(items, sms), Sh::THREADS, Sh::SMEM, st>>>(a);
+  int P = 0;
+  const int joins = mass_schedule(a.s, a.rows, sms, a.sched, &P);
+  kern<<<P, Sh::THREADS, Sh::SMEM, st>>>(a);
   fade_status_t s = launch_status("fade_prompt_mass");
-  if (s || a.chunks == 1) return s;
+  if (s) return s;
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3((unsigned)(items / a.chunks));
+  lc.gridDim = dim3(joins + ceil_div(a.s.n_kv, kPair) * a.s.B * a.s.H);
   lc.blockDim = dim3(kPair);
   lc.stream = st;
   cudaLaunchAttribute at[1];
@@ -399,7 +401,7 @@ fade_status_t launch(Args& a, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
   lc.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&lc, prompt_mass_join_kernel, a);
+  const cudaError_t e = cudaLaunchKernelEx(&lc, prompt_mass_join_kernel, a, joins);
   if (e != cudaSuccess)
     return set_error(FADE_ERR_CUDA, "fade_prompt_mass join: %s", cudaGetErrorString(e));
   return launch_status("fade_prompt_mass join");
@@ -407,11 +409,7 @@ fade_status_t launch(Args& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t prompt_mass_ws(const fade_config_t* c, int32_t n_q, int32_t n_kv) {
-  const int chunks = most_chunks(c, n_q, n_kv);
-  return chunks == 1 ? 0
-                     : (size_t)chunks * c->batch * c->num_kv_heads * pairs_of(n_kv) * kPair * 4;
-}
+size_t prompt_mass_ws() { return (size_t)2 * kPromptSMs * kPair * 4; }
 
 }  // namespace fade
 
@@ -434,9 +432,9 @@ extern "C" fade_status_t fade_prompt_mass(const fade_config_t* c, const fade_hea
     return set_error(FADE_ERR_INVALID_ARGUMENT, "workspace is NULL or not 16-byte aligned");
   if (!aligned(lse, 4) || !aligned(mass, 4) || !aligned(status, 4))
     return set_error(FADE_ERR_INVALID_ARGUMENT, "lse, mass and status must be 4-byte aligned");
-  if (ws_bytes < prompt_mass_ws(c, n_q, n_kv))
+  if (ws_bytes < prompt_mass_ws())
     return set_error(FADE_ERR_CAPACITY, "prompt workspace %zu bytes, %zu needed", ws_bytes,
-                     prompt_mass_ws(c, n_q, n_kv));
+                     prompt_mass_ws());
   const int d = c->head_dim;
   st = encode_heads(&a.q, "q", *q, d, a.s.Hq, n_q, a.s.B, a.s.G, kTile / a.s.G, true);
   if (!st) st = encode_heads(&a.k, "k", *k, d, a.s.H, n_kv, a.s.B, 1, kTile, false);
@@ -445,8 +443,8 @@ extern "C" fade_status_t fade_prompt_mass(const fade_config_t* c, const fade_hea
   a.mass = mass;
   a.part = static_cast<float*>(ws);
   a.status = status;
-  a.pairs = pairs_of(n_kv);
-  a.chunks = most_chunks(c, n_q, n_kv);
+  if ((long long)ceil_div(n_kv, kPair) * a.s.B * a.s.H > (1 << 30))
+    return set_error(FADE_ERR_UNSUPPORTED, "fade_prompt_mass: more than 2^30 blocks of keys");
   a.add = accumulate != 0;
   return d == 64 ? launch<64>(a, as_stream(stream)) : launch<128>(a, as_stream(stream));
 }

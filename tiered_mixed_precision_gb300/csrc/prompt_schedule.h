@@ -91,17 +91,48 @@ FADE_SCHED PromptItem prompt_item(const PromptShape& s, const PromptRows& rows, 
   it.h = u - row * s.H;
   return it;
 }
+// Two tiles of 128 keys of a unit, and the query tiles [begin, begin + n) that meet them; `all` of them
+// do, from the first-th on.
+struct MassItem {
+  int b, h, k0;     // first key
+  int off, q_len;   // position of query token 0; the row's queries
+  int first, begin, n, all;
+};
+// Items by pair of key tiles, then row (in their order by length), then head.
+FADE_SCHED MassItem mass_item(const PromptShape& s, const PromptRows& rows, int index) {
+  const int units = s.B * s.H, pair = index / units, u = index - pair * units, row = u / s.H;
+  const int per = kPromptTile >> s.log_g;
+  MassItem it;
+  it.b = rows.order[row];
+  it.h = u - row * s.H;
+  it.k0 = pair * 2 * kPromptTile;
+  it.q_len = rows.q_len[it.b];
+  const int kv_len = rows.kv_len[it.b];
+  it.off = kv_len - it.q_len;
+  const int from = it.k0 > it.off ? it.k0 - it.off : 0;   // queries before their keys see none
+  int to = it.q_len - 1;
+  if (s.sight.window && it.k0 >= s.sight.sink) {
+    const int last = it.k0 + 2 * kPromptTile - 1 + s.sight.window - 1 - it.off;
+    if (last < to) to = last;
+  }
+  it.begin = 0;
+  it.first = from / per;
+  it.n = it.all = it.k0 < kv_len && from <= to ? to / per - it.first + 1 : 0;
+  return it;
+}
+
 // A CTA's items one after another: whole ones, forth and back over the CTAs so that the order by length
-// evens out; then its share of the tail.
+// evens out; then its share of the tail. item_at: the whole item of an index.
+template <class Item>
 struct PromptWalk {
   int k = 0, item = -1, tile = 0;
-  FADE_SCHED bool next(const PromptShape& s, const PromptRows& rows, const PromptSchedule& a, int P,
-                       int c, PromptItem& it) {
+  template <class F>
+  FADE_SCHED bool next(const PromptSchedule& a, int P, int c, const F& item_at, Item& it) {
     while (k * P < a.whole) {
       const int index = k * P + ((k & 1) ? P - 1 - c : c);
       ++k;
       if (index >= a.whole) continue;
-      it = prompt_item(s, rows, index);
+      it = item_at(index);
       if (it.n > 0) return true;
     }
     if (item < 0) {
@@ -110,7 +141,7 @@ struct PromptWalk {
     }
     const int last = a.start[c + 1].item, end = a.start[c + 1].tile;
     while (item < last || (item == last && tile < end)) {
-      it = prompt_item(s, rows, item);
+      it = item_at(item);
       it.begin = tile;
       it.n = (item == last ? end : it.all) - tile;
       ++item;
@@ -121,43 +152,38 @@ struct PromptWalk {
   }
 };
 
-constexpr int kShareTiles = 2;     // tiles of a share of an item at least
-// What an item costs, in quarters of a tile of two query tiles: its tiles, and its start and end.
-constexpr int kCostStart = 8, kCostTwo = 4, kCostOne = 3;
+constexpr int kShareTiles = 2;   // tiles of a share of an item at least
 
-inline int prompt_tile_cost(const PromptItem& it) { return it.active == 2 ? kCostTwo : kCostOne; }
-inline int prompt_cost(const PromptItem& it) {
-  return it.all ? kCostStart + it.all * prompt_tile_cost(it) : 0;
-}
-
-// The schedule: `whole` items first, as many rounds over the CTAs as leave no CTA above the mean; the
-// tail's tiles then fill every CTA up to the mean. Sets the CTAs that have work; returns the number of
-// items that CTAs share.
-inline int prompt_schedule(const PromptShape& s, const PromptRows& rows, int blocks, int sms,
-                           PromptSchedule& a, int* ctas) {
-  const int units = s.B * s.H, items = blocks * units;
-  auto item = [&](int index) {
-    const int b = rows.order[index % units / s.H];
-    return prompt_block(s, b, rows.q_len[b], rows.kv_len[b], index / units);
-  };
+// An item's tiles, and what one costs.
+struct PromptWork {
+  int tiles, each;
+};
+// Deals items 0 .. items - 1 (work: of an index; `group` consecutive ones cost the same) to at most sms
+// CTAs. With a start cost: whole items first, as many rounds over the CTAs as leave no CTA above the
+// mean; the tail's tiles then fill every CTA up to the mean, and so do all items' without one. Sets the
+// CTAs that have work; returns the number of items that CTAs share.
+template <class F>
+int prompt_deal(int items, int group, int sms, int start, const F& work, PromptSchedule& a,
+                int* ctas) {
+  auto cost_of = [&](const PromptWork& w) { return w.tiles ? start + (long long)w.tiles * w.each : 0; };
   long long total = 0, tiles = 0, load[kPromptSMs] = {}, then[kPromptSMs];
-  for (int index = 0; index < items; index += s.H) {   // (the heads of a row cost the same)
-    const PromptItem it = item(index);
-    total += (long long)s.H * prompt_cost(it);
-    tiles += (long long)s.H * it.all;
+  for (int index = 0; index < items; index += group) {
+    const PromptWork w = work(index);
+    total += group * cost_of(w);
+    tiles += (long long)group * w.tiles;
   }
   const int P = *ctas = (int)std::min<long long>(sms, std::max(tiles / kShareTiles, 1LL));
   const double mean = (double)total / P;
-  long long placed = 0, work = 0;   // cost of the whole items; of the tail's tiles alone
+  long long placed = 0, tail = 0, cost = 0;   // cost of the whole items; of the tail's tiles alone
   a.whole = 0;
-  for (int k = 0, row = -1, cost = 0; (long long)k * P < items; ++k) {
+  for (int k = 0, last = -1; start && (long long)k * P < items; ++k) {
     long long most = 0, sum = placed;
     std::copy(load, load + P, then);
     for (int c = 0; c < P && k * P + c < items; ++c) {
       const int index = k * P + c;
-      if (index / s.H != row) {
-        row = index / s.H;
-        cost = prompt_cost(item(index));
+      if (index / group != last) {
+        last = index / group;
+        cost = cost_of(work(index));
       }
       long long& l = then[(k & 1) ? P - 1 - c : c];
       l += cost;
@@ -169,26 +195,30 @@ inline int prompt_schedule(const PromptShape& s, const PromptRows& rows, int blo
     placed = sum;
     a.whole = std::min((k + 1) * P, items);
   }
-  for (int index = a.whole; index < items; ++index) {
-    const PromptItem it = item(index);
-    if (it.all) work += (long long)it.all * prompt_tile_cost(it);
+  for (int index = a.whole, last = -1; index < items; ++index) {
+    if (index / group != last) {
+      last = index / group;
+      const PromptWork w = work(index);
+      cost = (long long)w.tiles * w.each;
+    }
+    tail += cost;
   }
   // the tail: CTA c takes tiles worth mean - load[c], the items' starts spread over their tiles
-  const double price = work ? (double)(total - placed) / work : 1.0;
+  const double price = tail ? (double)(total - placed) / tail : 1.0;
   int at = a.whole, tile = 0, joins = 0, open = -1;
   double owed = 0;   // what the CTAs so far should have taken beyond what they took
-  PromptItem it = at < items ? item(at) : PromptItem{};
+  PromptWork w = at < items ? work(at) : PromptWork{};
   for (int c = 0; c < P; ++c) {
     a.start[c].item = at;
     a.start[c].tile = tile;
     owed += mean - (double)load[c];
     while (at < items) {
-      if (it.all == 0) {
-        if (++at < items) it = item(at);
+      if (w.tiles == 0) {
+        if (++at < items) w = work(at);
         continue;
       }
-      const double each = price * prompt_tile_cost(it);
-      const int left = it.all - tile;
+      const double each = price * w.each;
+      const int left = w.tiles - tile;
       int take = c + 1 == P ? left : (int)std::min<double>(left, owed / each + 0.5);
       if (take + kShareTiles > left) take = left;
       if (take < std::min(kShareTiles, left)) break;
@@ -207,12 +237,31 @@ inline int prompt_schedule(const PromptShape& s, const PromptRows& rows, int blo
         break;
       }
       tile = 0;
-      if (++at < items) it = item(at);
+      if (++at < items) w = work(at);
     }
   }
   a.start[P].item = at;
   a.start[P].tile = tile;
   return joins;
+}
+
+// What an item of the attention costs, in quarters of a tile of two query tiles: its tiles, and its
+// start and end.
+constexpr int kCostStart = 8, kCostTwo = 4, kCostOne = 3;
+
+inline int prompt_schedule(const PromptShape& s, const PromptRows& rows, int blocks, int sms,
+                           PromptSchedule& a, int* ctas) {
+  auto work = [&](int index) {
+    const PromptItem it = prompt_item(s, rows, index);
+    return PromptWork{it.all, it.all == 0 || it.active == 2 ? kCostTwo : kCostOne};
+  };
+  return prompt_deal(blocks * s.B * s.H, s.H, sms, kCostStart, work, a, ctas);
+}
+inline int mass_schedule(const PromptShape& s, const PromptRows& rows, int sms, PromptSchedule& a,
+                         int* ctas) {
+  const int pairs = (s.n_kv + 2 * kPromptTile - 1) / (2 * kPromptTile);
+  auto work = [&](int index) { return PromptWork{mass_item(s, rows, index).all, 1}; };
+  return prompt_deal(pairs * s.B * s.H, s.H, sms, 0, work, a, ctas);
 }
 
 }  // namespace fade
