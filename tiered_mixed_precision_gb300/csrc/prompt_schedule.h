@@ -154,30 +154,36 @@ struct PromptWalk {
 
 constexpr int kShareTiles = 2;   // tiles of a share of an item at least
 
-// An item's tiles, and what one costs.
+// An item's tiles, what one costs, and what the item's start costs.
 struct PromptWork {
-  int tiles, each;
+  int tiles, each, start;
 };
 // Deals items 0 .. items - 1 (work: of an index; `group` consecutive ones cost the same) to at most sms
-// CTAs. With a start cost: whole items first, as many rounds over the CTAs as leave no CTA above the
-// mean; the tail's tiles then fill every CTA up to the mean, and so do all items' without one. Sets the
-// CTAs that have work; returns the number of items that CTAs share.
+// CTAs. rounds: whole items first, as many rounds over the CTAs as leave no CTA above the mean. The
+// others' tiles then fill every CTA up to the mean, an item's start charged to who takes its first tile.
+// Sets the CTAs that have work; returns the number of items that CTAs share.
 template <class F>
-int prompt_deal(int items, int group, int sms, int start, const F& work, PromptSchedule& a,
+int prompt_deal(int items, int group, int sms, bool rounds, const F& work, PromptSchedule& a,
                 int* ctas) {
-  auto cost_of = [&](const PromptWork& w) { return w.tiles ? start + (long long)w.tiles * w.each : 0; };
-  long long total = 0, tiles = 0, load[kPromptSMs] = {}, then[kPromptSMs];
+  long long alone = 0, tiles = 0, load[kPromptSMs] = {}, then[kPromptSMs];
   for (int index = 0; index < items; index += group) {
     const PromptWork w = work(index);
-    total += group * cost_of(w);
+    alone += (long long)group * w.tiles * w.each;
     tiles += (long long)group * w.tiles;
   }
   const int P = *ctas = (int)std::min<long long>(sms, std::max(tiles / kShareTiles, 1LL));
+  // (shares of a few tiles all have their start: only beside long ones does it count)
+  auto start_of = [&](const PromptWork& w) { return (int)std::min<long long>(w.start, alone / P / 4); };
+  auto cost_of = [&](const PromptWork& w) {
+    return w.tiles ? start_of(w) + (long long)w.tiles * w.each : 0;
+  };
+  long long total = 0;
+  for (int index = 0; index < items; index += group) total += group * cost_of(work(index));
   const double mean = (double)total / P;
-  long long placed = 0, tail = 0, cost = 0;   // cost of the whole items; of the tail's tiles alone
+  long long cost = 0;
   a.whole = 0;
-  for (int k = 0, last = -1; start && (long long)k * P < items; ++k) {
-    long long most = 0, sum = placed;
+  for (int k = 0, last = -1; rounds && (long long)k * P < items; ++k) {
+    long long most = 0;
     std::copy(load, load + P, then);
     for (int c = 0; c < P && k * P + c < items; ++c) {
       const int index = k * P + c;
@@ -187,24 +193,13 @@ int prompt_deal(int items, int group, int sms, int start, const F& work, PromptS
       }
       long long& l = then[(k & 1) ? P - 1 - c : c];
       l += cost;
-      sum += cost;
       most = std::max(most, l);
     }
     if ((double)most > mean) break;
     std::copy(then, then + P, load);
-    placed = sum;
     a.whole = std::min((k + 1) * P, items);
   }
-  for (int index = a.whole, last = -1; index < items; ++index) {
-    if (index / group != last) {
-      last = index / group;
-      const PromptWork w = work(index);
-      cost = (long long)w.tiles * w.each;
-    }
-    tail += cost;
-  }
-  // the tail: CTA c takes tiles worth mean - load[c], the items' starts spread over their tiles
-  const double price = tail ? (double)(total - placed) / tail : 1.0;
+  // the tail: CTA c takes tiles worth mean - load[c]
   int at = a.whole, tile = 0, joins = 0, open = -1;
   double owed = 0;   // what the CTAs so far should have taken beyond what they took
   PromptWork w = at < items ? work(at) : PromptWork{};
@@ -217,12 +212,11 @@ int prompt_deal(int items, int group, int sms, int start, const F& work, PromptS
         if (++at < items) w = work(at);
         continue;
       }
-      const double each = price * w.each;
-      const int left = w.tiles - tile;
-      int take = c + 1 == P ? left : (int)std::min<double>(left, owed / each + 0.5);
+      const int left = w.tiles - tile, start = tile == 0 ? start_of(w) : 0;
+      int take = c + 1 == P ? left : (int)std::min<double>(left, (owed - start) / w.each + 0.5);
       if (take + kShareTiles > left) take = left;
       if (take < std::min(kShareTiles, left)) break;
-      owed -= each * take;
+      owed -= start + (double)w.each * take;
       if (take < left || tile > 0) {   // shared with other CTAs
         if (open != at) {
           open = at;
@@ -253,15 +247,20 @@ inline int prompt_schedule(const PromptShape& s, const PromptRows& rows, int blo
                            PromptSchedule& a, int* ctas) {
   auto work = [&](int index) {
     const PromptItem it = prompt_item(s, rows, index);
-    return PromptWork{it.all, it.all == 0 || it.active == 2 ? kCostTwo : kCostOne};
+    return PromptWork{it.all, it.all == 0 || it.active == 2 ? kCostTwo : kCostOne, kCostStart};
   };
-  return prompt_deal(blocks * s.B * s.H, s.H, sms, kCostStart, work, a, ctas);
+  return prompt_deal(blocks * s.B * s.H, s.H, sms, true, work, a, ctas);
 }
 inline int mass_schedule(const PromptShape& s, const PromptRows& rows, int sms, PromptSchedule& a,
                          int* ctas) {
   const int pairs = (s.n_kv + 2 * kPromptTile - 1) / (2 * kPromptTile);
-  auto work = [&](int index) { return PromptWork{mass_item(s, rows, index).all, 1}; };
-  return prompt_deal(pairs * s.B * s.H, s.H, sms, 0, work, a, ctas);
+  // a pair's first 2 G tiles hide some keys from some queries, which costs half as much again; so do
+  // all of a pair with sinks and other tokens (one of its two key tiles, mostly)
+  auto work = [&](int index) {
+    const MassItem it = mass_item(s, rows, index);
+    return PromptWork{it.all, s.sight.window && it.k0 < s.sight.sink ? 10 : 8, 16 + 8 * s.G};
+  };
+  return prompt_deal(pairs * s.B * s.H, s.H, sms, false, work, a, ctas);
 }
 
 }  // namespace fade
