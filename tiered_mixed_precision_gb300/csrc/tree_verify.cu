@@ -11,27 +11,31 @@
 // W_k+1 = W_k - p(x). The final draw is the largest r(i) / E_i with E_i given exponential variates (the
 // first of independent arrivals at rates r), greedy rows take the largest logit.
 //
-// p(i) = 2^((x_i - M) log2(e) / temperature) / S in fp32, M the row's maximum: the largest terms lose
-// nothing in the subtraction. Sums are fp32, in one fixed order.
+// p(i) = 2^(x_i c - M c - log2 S) in fp32 with c = log2(e) / temperature and M the row's maximum; what M c
+// and log2 S lose in rounding is the same for every token. Sums are fp32, in one fixed order. A row with
+// NaN or +inf (its sum says so) is gone over again with those replaced.
 //
 // What bounds it: only nodes on the kept path are looked at, one after another, so a row is a chain of
-// reads of its vocabulary. A cluster of CTAs takes a row, each a share of the vocabulary; sums and maxima
-// are exchanged through distributed shared memory, and every CTA then decides the same from the same
-// numbers.
+// passes over its vocabulary. A cluster of CTAs takes a row, each a share of the vocabulary; sums and
+// maxima are exchanged through distributed shared memory, and every CTA then decides the same from the
+// same numbers. Where all nodes' logits are little to read, their maxima and sums are taken in one pass
+// at the start, which leaves the chain one exchange.
 #include <cuda_bf16.h>
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "prompt.cuh"
 
 namespace fade {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
 constexpr int kCluster = 8;   // CTAs of a row
-constexpr int kUnroll = 4;    // vectors in flight a thread and array
+constexpr int kBatch = 16;    // values exchanged at once
+constexpr int kNodes = FADE_TREE_MAX_NODES + 1;   // the root first
+constexpr long long kAheadBytes = 64ll << 20;   // logits of all rows and nodes that are looked at ahead
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
@@ -41,6 +45,7 @@ struct Args {
   const float *temperature, *u, *noise;
   int32_t *path, *n_path, *next;
   int T, V, greedy;   // greedy: every row
+  int ahead;          // all nodes are looked at in one pass, kBatch of them a time
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -48,18 +53,19 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// A logit: NaN reads as -inf, +inf as the largest number.
-__device__ __forceinline__ float logit(float x) { return x != x ? -INFINITY : fminf(x, 3.402823466e38f); }
-
-template <typename E>
-struct Vec {
-  static constexpr int N = 16 / sizeof(E);
-};
+// A logit as it counts: NaN reads as -inf, +inf as the largest number.
+__device__ __forceinline__ float logit(float x) {
+  return x != x ? -INFINITY : fminf(x, 3.402823466e38f);
+}
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// N consecutive elements from i on; `wide`: x + i is 16-byte aligned.
+// 16 bytes of consecutive elements; `wide`: they start on a 16-byte boundary.
+template <typename E>
+struct Vec {
+  static constexpr int N = 16 / sizeof(E);
+};
 template <typename E>
 union Words {
   uint4 w;
@@ -76,9 +82,13 @@ __device__ __forceinline__ void load(const E* x, int i, bool wide, Words<E>& v) 
   }
 }
 template <typename E>
-__device__ __forceinline__ void logits(const Words<E>& v, float (&y)[Vec<E>::N]) {
+__device__ __forceinline__ void logits(const Words<E>& v, bool careful, float (&y)[Vec<E>::N]) {
 #pragma unroll
-  for (int j = 0; j < Vec<E>::N; ++j) y[j] = logit(to_float(v.e[j]));
+  for (int j = 0; j < Vec<E>::N; ++j) y[j] = to_float(v.e[j]);
+  if (careful) {
+#pragma unroll
+    for (int j = 0; j < Vec<E>::N; ++j) y[j] = logit(y[j]);
+  }
 }
 
 // ---------------------------------------------------------------- cluster
@@ -139,9 +149,10 @@ struct Best {   // the larger value, the lower index where they are equal (y: th
 };
 
 struct Shared {
-  float4 warps[kWarps];
-  float4 ranks[2][kCluster];   // what each CTA of the cluster found, two calls in turn
-  uint64_t kids[FADE_TREE_MAX_NODES + 1];   // children of node i - 1
+  float4 warps[kBatch][kMaxWarps];
+  float4 ranks[2][kBatch][kCluster];   // what each CTA of the cluster found, two calls in turn
+  float4 stats[kNodes];                // of node i - 1
+  uint64_t kids[kNodes];               // children of node i - 1
   // from CTA 0, the same in all: per node its parent, token, uniform number, its target and drafter
   // logits after its parent; then nodes, temperature
   int32_t parent[FADE_TREE_MAX_NODES], token[FADE_TREE_MAX_NODES];
@@ -151,127 +162,373 @@ struct Shared {
   int32_t refused[FADE_TREE_MAX_NODES];
 };
 
-// The value over the whole cluster, in every thread; `turn` alternates between calls.
 template <class Op>
-__device__ __forceinline__ float4 reduce(Shared& sh, float4 v, const Op& op, int& turn) {
+__device__ __forceinline__ float4 warp_reduce(float4 v, const Op& op, int width) {
+  for (int o = width / 2; o; o >>= 1)
+    v = op(v, make_float4(__shfl_xor_sync(~0u, v.x, o), __shfl_xor_sync(~0u, v.y, o),
+                          __shfl_xor_sync(~0u, v.z, o), __shfl_xor_sync(~0u, v.w, o)));
+  return v;
+}
+// A thread's value joined over its warp, kept as the i-th.
+template <class Op>
+__device__ __forceinline__ void keep(Shared& sh, int i, float4 v, const Op& op) {
+  v = warp_reduce(v, op, 32);
+  if ((threadIdx.x & 31) == 0) sh.warps[i][threadIdx.x >> 5] = v;
+}
+// The values 0 .. count - 1 joined over the whole cluster, from then on in sh.ranks (exchanged).
+template <class Op>
+__device__ __forceinline__ void exchange(Shared& sh, int count, const Op& op, int& turn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_rank(), size = cluster_size();
-  auto shuffle = [&](float4 x, int o) {
-    return make_float4(__shfl_xor_sync(~0u, x.x, o), __shfl_xor_sync(~0u, x.y, o),
-                       __shfl_xor_sync(~0u, x.z, o), __shfl_xor_sync(~0u, x.w, o));
-  };
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = op(v, shuffle(v, o));
-  if (lane == 0) sh.warps[warp] = v;
+  const int warps = blockDim.x / 32;   // a power of two: every group of as many lanes has them all
   __syncthreads();
-  if (warp == 0) {
-    v = sh.warps[lane & (kWarps - 1)];
-#pragma unroll
-    for (int o = kWarps / 2; o; o >>= 1) v = op(v, shuffle(v, o));
-    if (lane < size) st_remote4(remote(&sh.ranks[turn][rank], lane), v);
+  for (int i = warp; i < count; i += warps) {
+    const float4 v = warp_reduce(sh.warps[i][lane & (warps - 1)], op, warps);
+    if (lane < size) st_remote4(remote(&sh.ranks[turn][i][rank], lane), v);
   }
   cluster_sync();
-  v = sh.ranks[turn][0];
-  for (uint32_t r = 1; r < size; ++r) v = op(v, sh.ranks[turn][r]);
   turn ^= 1;
+}
+template <class Op>
+__device__ __forceinline__ float4 exchanged(const Shared& sh, int i, const Op& op, int turn) {
+  float4 v = sh.ranks[turn ^ 1][i][0];
+  for (uint32_t r = 1; r < cluster_size(); ++r) v = op(v, sh.ranks[turn ^ 1][i][r]);
+  return v;
+}
+template <class Op>
+__device__ __forceinline__ float4 reduce(Shared& sh, float4 v, const Op& op, int& turn) {
+  keep(sh, 0, v, op);
+  exchange(sh, 1, op, turn);
+  return exchanged(sh, 0, op, turn);
+}
+
+// ---------------------------------------------------------------- passes over the vocabulary
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
   return v;
 }
 
-// The distributions after a node: the vocabulary's logits, and how a thread walks its share.
-template <typename E, bool DRAFT>
+// The logits after a node.
+template <typename E>
 struct Node {
-  static constexpr int N = Vec<E>::N;
   const E *t, *d;
-  int V, head, vecs;   // elements before the first 16-byte boundary of t; whole vectors from there
-  bool wide_t, wide_d;
-  int first, step;     // of this thread's vectors
+  int head, vecs;   // elements before the first 16-byte boundary of t; whole vectors from there
+  bool wide_d;      // d has the same boundaries
+};
 
-  // f(index, target logits, drafter logits) for each vector; g the same for single elements, at the ends
-  template <class F, class G>
-  __device__ __forceinline__ void each(const F& f, const G& g) const {
-    for (int v = first; v < vecs; v += kUnroll * step) {
-      Words<E> wt[kUnroll], wd[kUnroll];
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int at = head + min(v + k * step, vecs - 1) * N;
-        load(t, at, true, wt[k]);
-        if (DRAFT) load(d, at, wide_d, wd[k]);
+constexpr int kSlots = 8;   // 16-byte words of a thread that copies are in flight to
+
+// A row and a thread's share of it.
+template <typename E, bool DRAFT>
+struct Row {
+  static constexpr int N = Vec<E>::N;
+  const Args& a;
+  int b, first, step;             // the row; the thread's vectors
+  uint32_t slot0, slot_bytes;     // its slots
+  __device__ __forceinline__ Node<E> node_at(int node) const {   // (-1: the root)
+    Node<E> x;
+    x.t = reinterpret_cast<const E*>(node < 0 ? a.target_root + b * a.tr_row
+                                              : a.target + b * a.t_row + node * a.t_node);
+    x.d = !DRAFT ? nullptr
+                 : reinterpret_cast<const E*>(node < 0 ? a.draft_root + b * a.dr_row
+                                                       : a.draft + b * a.d_row + node * a.d_node);
+    x.head = min((int)((16 - (reinterpret_cast<uintptr_t>(x.t) & 15)) & 15) / (int)sizeof(E), a.V);
+    x.vecs = (a.V - x.head) / N;
+    x.wide_d = DRAFT && (reinterpret_cast<uintptr_t>(x.d + x.head) & 15) == 0;
+    return x;
+  }
+  // One pass over the logits after node `at`, then those after then(at), .., `most` nodes (-2: no more).
+  // f(index, words of t, d, noise) for a thread's vectors, g(index, t, d, noise) for single elements at
+  // the ends, done(k) after the k-th node. D, NOISE: d and the noise are read, too. Words come by
+  // asynchronous copies into slots of the thread's own, several vectors ahead, across nodes.
+  template <bool D, bool NOISE, class Then, class F, class G, class Done>
+  __device__ __forceinline__ void sweep(int at, int most, const Then& then, const F& f, const G& g,
+                                        const Done& done) const {
+    constexpr int EW = NOISE ? N / 4 : 0;               // words of noise a vector
+    constexpr int P = 1 + (D ? 1 : 0) + EW;             // words of a vector
+    constexpr int S = P == 1 ? 8 : P == 2 ? 4 : 2;      // vectors in flight
+    const float* noise = NOISE && a.noise ? a.noise + (size_t)b * a.V : nullptr;
+    auto wide_e = [&](const Node<E>& x) {
+      return noise && (reinterpret_cast<uintptr_t>(noise + x.head) & 15) == 0;
+    };
+    int ai = at, ki = 0, vi = first;
+    Node<E> ni = node_at(at);
+    uint32_t si = 0, sp = 0;
+    auto issue = [&]() {
+      while (ai != -2 && vi >= ni.vecs) {
+        ai = ++ki < most ? then(ai) : -2;
+        if (ai == -2) break;
+        ni = node_at(ai);
+        vi = first;
       }
+      if (ai != -2) {
+        const int i = ni.head + vi * N;
+        const uint32_t to = slot0 + si * P * slot_bytes;
+        copy16(to, ni.t + i);
+        if (D && ni.wide_d) copy16(to + slot_bytes, ni.d + i);
+        if (NOISE && wide_e(ni)) {
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k)
-        if (v + k * step < vecs) {
-          float x[N], y[N];
-          logits(wt[k], x);
-          if (DRAFT) logits(wd[k], y);
-          f(head + (v + k * step) * N, x, y);
+          for (int k = 0; k < EW; ++k) copy16(to + (P - EW + k) * slot_bytes, noise + i + 4 * k);
         }
+        vi += step;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      si = si + 1 == S ? 0 : si + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < S; ++i) issue();
+#pragma unroll 1
+    for (int k = 0; at != -2; at = ++k < most ? then(at) : -2) {
+      const Node<E> node = node_at(at);
+#pragma unroll 1
+      for (int v = first; v < node.vecs; v += step) {
+        const int i = node.head + v * N;
+        const uint32_t from = slot0 + sp * P * slot_bytes;
+        Words<E> t, d;
+        float e[N];
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        t.w = ld_shared16(from);
+        if (D) {
+          if (node.wide_d)
+            d.w = ld_shared16(from + slot_bytes);
+          else
+            load(node.d, i, false, d);
+        }
+        if (NOISE) {
+          if (wide_e(node)) {
+#pragma unroll
+            for (int q = 0; q < EW; ++q) {
+              const uint4 z = ld_shared16(from + (P - EW + q) * slot_bytes);
+              e[4 * q] = __uint_as_float(z.x), e[4 * q + 1] = __uint_as_float(z.y);
+              e[4 * q + 2] = __uint_as_float(z.z), e[4 * q + 3] = __uint_as_float(z.w);
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < N; ++q) e[q] = noise ? noise[i + q] : 1.f;
+          }
+        }
+        issue();
+        sp = sp + 1 == S ? 0 : sp + 1;
+        f(i, t, d, e);
+      }
+      const int ends = a.V - node.vecs * N;
+      if (first < ends) {
+        const int i = first < node.head ? first : first + node.vecs * N;
+        g(i, logit(to_float(node.t[i])), D ? logit(to_float(node.d[i])) : 0.f,
+          NOISE && noise ? noise[i] : 1.f);
+      }
+      done(k);
     }
-    const int ends = V - vecs * N;
-    if (first < ends) {
-      const int i = first < head ? first : first + vecs * N;
-      g(i, logit(to_float(t[i])), DRAFT ? logit(to_float(d[i])) : 0.f);
+  }
+};
+
+// The distributions after a node. p(i) = 2^(x_i c + pt), a q(i) = 2^(y_i c + qt + la); an empty row's are
+// 2^-inf. Where p and q are the same numbers, p - 1 q is nothing to the last bit. careful: the logits
+// have NaN or infinities, or are too large to multiply first.
+template <typename E, bool DRAFT>
+struct Probs {
+  static constexpr int N = Vec<E>::N;
+  float c, mt, md, lt, ld, pt, qt;
+  float taken, la;   // a, log2 a
+  bool careful;
+  __device__ __forceinline__ float p_of(float x) const {
+    return ex2(careful ? (x - mt) * c + lt : fmaf(x, c, pt));
+  }
+  __device__ __forceinline__ float q_of(float y, float l) const {
+    return ex2(careful ? (y - md) * c + (ld + l) : fmaf(y, c, qt + l));
+  }
+  __device__ __forceinline__ float r_of(float x, float y) const {
+    const float p = p_of(x);
+    return DRAFT && taken > 0.f ? fmaxf(p - q_of(y, la), 0.f) : p;
+  }
+  // r of a vector: the cases are told apart once for all of it
+  template <bool Q>
+  __device__ __forceinline__ void rest(const Words<E>& t, const Words<E>& d, float (&r)[N]) const {
+    float x[N], y[N];
+    logits(t, careful, x);
+    if constexpr (Q) logits(d, careful, y);
+    if (careful) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) r[j] = r_of(x[j], Q ? y[j] : 0.f);
+    } else {
+      const float qa = qt + la;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        r[j] = ex2(fmaf(x[j], c, pt));
+        if constexpr (Q) r[j] = fmaxf(r[j] - ex2(fmaf(y[j], c, qa)), 0.f);
+      }
     }
   }
 };
 
 template <typename E, bool DRAFT>
-__global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kMaxThreads, 1) tree_verify_kernel(const __grid_constant__ Args a) {
   constexpr int N = Vec<E>::N;
   __shared__ Shared sh;
-  const int tid = threadIdx.x;
+  extern __shared__ uint4 slots[];   // [kSlots][threads]
+  const int tid = threadIdx.x, threads = blockDim.x;
   const uint32_t rank = cluster_rank(), size = cluster_size();
   const int b = blockIdx.x / size;
+  const Row<E, DRAFT> row{a, b, (int)(rank * threads + tid), (int)(size * threads),
+                          smem_u32(slots + tid), (uint32_t)threads * 16};
   int turn = 0;
+  // (waited for before the first write to another CTA, which has to have started by then)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
-  auto row_of = [&](int node, const E*& t, const E*& d) {   // logits after a node (-1: the root)
-    t = reinterpret_cast<const E*>(node < 0 ? a.target_root + b * a.tr_row
-                                            : a.target + b * a.t_row + node * a.t_node);
-    d = !DRAFT ? nullptr
-               : reinterpret_cast<const E*>(node < 0 ? a.draft_root + b * a.dr_row
-                                                     : a.draft + b * a.d_row + node * a.d_node);
+  auto stop = [](int) { return -2; };
+  auto nothing = [](int) {};
+
+  // a thread's share of rows' maxima and sums, or of their greatest logits (greedy): kept as the 0th, 1st, ..
+  const Best best_of;
+  const float4 none = make_float4(0.f, __int_as_float(0x7fffffff), 0.f, 0.f);
+  auto look = [&](int at, int most, auto then, bool greedy, float c, bool careful) {
+    const Stats join{c};
+    if (greedy) {
+      float4 best = none;
+      best.x = -INFINITY;
+      row.template sweep<false, false>(
+            at, most, then,
+            [&](int i, const Words<E>& t, const Words<E>&, const float(&)[N]) {
+              float x[N];
+              logits(t, false, x);
+              float top = x[0];
+#pragma unroll
+              for (int j = 1; j < N; ++j) top = fmaxf(top, x[j]);
+              if (top > best.x) {   // (ascending in a thread)
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                  if (logit(x[j]) > best.x)
+                    best = make_float4(logit(x[j]), __int_as_float(i + j), 0.f, 0.f);
+              }
+            },
+            [&](int i, float x, float, float) {
+              if (x > -INFINITY) best = best_of(best, make_float4(x, __int_as_float(i), 0.f, 0.f));
+            },
+            [&](int k) {
+              keep(sh, k, best, best_of);
+              best = none;
+              best.x = -INFINITY;
+            });
+      return;
+    }
+    float4 st = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    auto add = [&](float& m, float& s, const Words<E>& w) {
+      float x[N];
+      logits(w, careful, x);
+      float top = x[0];
+#pragma unroll
+      for (int j = 1; j < N; ++j) top = fmaxf(top, x[j]);
+      if (top > m) {
+        s *= ex2((m - top) * c);   // (0 from -inf)
+        m = top;
+      }
+      if (m == -INFINITY) return;
+      float part[2] = {0.f, 0.f};
+      if (careful) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) part[j & 1] += ex2((x[j] - m) * c);
+      } else {
+        const float mc = m * c;
+#pragma unroll
+        for (int j = 0; j < N; ++j) part[j & 1] += ex2(fmaf(x[j], c, -mc));
+      }
+      s += part[0] + part[1];
+    };
+    row.template sweep<DRAFT, false>(
+          at, most, then,
+          [&](int, const Words<E>& t, const Words<E>& d, const float(&)[N]) {
+            add(st.x, st.y, t);
+            if (DRAFT) add(st.z, st.w, d);
+          },
+          [&](int, float x, float y, float) {
+            st = join(st, make_float4(x, x == -INFINITY ? 0.f : 1.f, DRAFT ? y : -INFINITY,
+                                      DRAFT && y != -INFINITY ? 1.f : 0.f));
+          },
+          [&](int k) {
+            keep(sh, k, st, join);
+            st = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+          });
   };
-  // what CTA 0 reads of the tree is what every CTA decides by
-  if (rank == 0) {
-    if (tid < a.T) {
-      const size_t at = (size_t)b * a.T + tid;
-      int parent = a.parents[at];
-      if (parent < 0 || parent >= tid) parent = -1;
-      const int token = a.tokens[at];
-      float tl = -INFINITY, ql = -INFINITY;
-      if (token >= 0 && token < a.V && (parent >= 0 || a.target_root)) {
-        const E *t, *d;
-        row_of(parent, t, d);
-        tl = logit(to_float(t[token]));
-        if (DRAFT) ql = logit(to_float(d[token]));
-      }
-      const float u = a.greedy ? 0.f : a.u[at];
-      for (uint32_t r = 0; r < size; ++r) {
-        st_remote(remote(&sh.parent[tid], r), parent);
-        st_remote(remote(&sh.token[tid], r), token);
-        st_remote(remote(&sh.u[tid], r), __float_as_uint(u));
-        st_remote(remote(&sh.tl[tid], r), __float_as_uint(tl));
-        st_remote(remote(&sh.ql[tid], r), __float_as_uint(ql));
-      }
-    } else if (tid == kThreads - 1) {
-      const int n = a.n_nodes ? min(max(a.n_nodes[b], 0), a.T) : a.T;
-      const float temp = a.greedy ? 0.f : a.temperature ? a.temperature[b] : 1.f;
-      for (uint32_t r = 0; r < size; ++r) {
-        st_remote(remote(&sh.n, r), n);
-        st_remote(remote(&sh.temperature, r), __float_as_uint(temp));
-      }
+  auto scale_of = [](float temp) { return kLog2e / fminf(fmaxf(temp, 1e-30f), 1e30f); };
+  auto in_line = [&](int at) { return at + 1 < a.T ? at + 1 : -2; };
+  const int most = a.ahead ? kBatch : 1;
+
+  // The first nodes' pass needs nothing of the tree but the temperature; CTA 0 hands out the rest
+  // meanwhile, and what every CTA decides by is what CTA 0 read.
+  int cur = a.target_root ? -1 : 0;
+  const float own_temp = a.greedy ? 0.f : a.temperature ? a.temperature[b] : 1.f;
+  const bool mine = rank == 0 && tid < a.T, last = rank == 0 && tid == threads - 1;
+  int parent = -1, token = -1, nodes = a.T;
+  float tl = -INFINITY, ql = -INFINITY, u = 0.f;
+  if (mine) {
+    const size_t at = (size_t)b * a.T + tid;
+    parent = a.parents[at];
+    if (parent < 0 || parent >= tid) parent = -1;
+    token = a.tokens[at];
+    if (!a.greedy) u = a.u[at];
+    if (token >= 0 && token < a.V && (parent >= 0 || a.target_root)) {
+      const Node<E> x = row.node_at(parent);
+      tl = logit(to_float(x.t[token]));
+      if (DRAFT) ql = logit(to_float(x.d[token]));
+    }
+  } else if (last && a.n_nodes) {
+    nodes = min(max(a.n_nodes[b], 0), a.T);
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  for (uint32_t r = 0; r < size; ++r) {
+    if (mine) {
+      st_remote(remote(&sh.parent[tid], r), parent);
+      st_remote(remote(&sh.token[tid], r), token);
+      st_remote(remote(&sh.u[tid], r), __float_as_uint(u));
+      st_remote(remote(&sh.tl[tid], r), __float_as_uint(tl));
+      st_remote(remote(&sh.ql[tid], r), __float_as_uint(ql));
+    }
+    if (last) {
+      st_remote(remote(&sh.n, r), nodes);
+      st_remote(remote(&sh.temperature, r), __float_as_uint(own_temp));
     }
   }
-  if (tid <= FADE_TREE_MAX_NODES) sh.kids[tid] = 0;
-  cluster_sync();
+  if (tid < kNodes) sh.kids[tid] = 0;
+  uint64_t known = 0;   // nodes whose maxima and sums lie in sh.stats
+  bool known_root = false;
+  // nodes cur, cur + 1, .. looked at, and their values exchanged
+  auto look_on = [&](bool greedy, float c) {
+    const int count = min(most, a.T - cur);
+    const Stats join{c};
+    look(cur, most, in_line, greedy, c, false);
+    if (greedy)
+      exchange(sh, count, best_of, turn);
+    else
+      exchange(sh, count, join, turn);
+    if (tid < count)
+      sh.stats[cur + 1 + tid] =
+          greedy ? exchanged(sh, tid, best_of, turn) : exchanged(sh, tid, join, turn);
+    for (int k = 0; k < count; ++k) {
+      if (cur + k < 0)
+        known_root = true;
+      else
+        known |= 1ull << (cur + k);
+    }
+  };
+  look_on(!(own_temp > 0.f), scale_of(own_temp));
   const int n = sh.n;
+  const bool greedy = !(sh.temperature > 0.f);
+  const float c = scale_of(sh.temperature);
+  const Stats join{c};
   if (tid < n)
     atomicOr(reinterpret_cast<unsigned long long*>(&sh.kids[sh.parent[tid] + 1]), 1ull << tid);
   __syncthreads();
-  const bool greedy = !(sh.temperature > 0.f);
-  const float c = kLog2e / fminf(fmaxf(sh.temperature, 1e-30f), 1e30f);
   const bool lead = rank == 0 && tid == 0;
 
-  int cur = a.target_root ? -1 : 0, kept = 0, next = -1;
+  int kept = 0, next = -1;
   int32_t* path = a.path + (size_t)b * a.T;
   if (!a.target_root && n > 0) {
     if (lead) path[0] = 0;
@@ -279,98 +536,71 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
   }
   const bool any = a.target_root || n > 0;   // (no node and no root: nothing to draw from)
   while (any) {
-    Node<E, DRAFT> node;
-    row_of(cur, node.t, node.d);
-    node.V = a.V;
-    node.head = min((int)((16 - (reinterpret_cast<uintptr_t>(node.t) & 15)) & 15) / (int)sizeof(E), a.V);
-    node.vecs = (a.V - node.head) / N;
-    node.wide_d = DRAFT && (reinterpret_cast<uintptr_t>(node.d + node.head) & 15) == 0;
-    node.first = rank * kThreads + tid;
-    node.step = size * kThreads;
     const uint64_t kids = sh.kids[cur + 1];
     int take = -1;
+    if (!(cur < 0 ? known_root : (known >> cur) & 1)) {
+      look_on(greedy, c);
+      __syncthreads();
+    }
+    float4 st = sh.stats[cur + 1];
 
     if (greedy) {
-      float4 best = make_float4(-INFINITY, __int_as_float(0x7fffffff), 0.f, 0.f);
-      const Best op;
-      auto see = [&](int i, float x) {
-        if (x > best.x) best = make_float4(x, __int_as_float(i), 0.f, 0.f);   // ascending in a thread
-      };
-      node.each(
-          [&](int i, const float(&x)[N], const float(&)[N]) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) see(i + j, x[j]);
-          },
-          [&](int i, float x, float) {
-            best = op(best, make_float4(x, __int_as_float(x == -INFINITY ? 0x7fffffff : i), 0.f, 0.f));
-          });
-      best = reduce(sh, best, op, turn);
-      const int top = best.x == -INFINITY ? -1 : __float_as_int(best.y);
+      const int top = st.x == -INFINITY ? -1 : __float_as_int(st.y);
       for (uint64_t left = kids; left && take < 0; left &= left - 1) {
         const int i = __ffsll((long long)left) - 1;
         if (top >= 0 && sh.token[i] == top) take = i;
       }
       next = top;
     } else {
-      // -------------------------------------------- maxima and sums
-      float4 st = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-      const Stats join{c};
-      auto add = [&](float& m, float& s, const float(&x)[N]) {
-        float top = x[0];
-#pragma unroll
-        for (int j = 1; j < N; ++j) top = fmaxf(top, x[j]);
-        if (top > m) {
-          s *= ex2((m - top) * c);   // (0 from -inf)
-          m = top;
-        }
-        if (m == -INFINITY) return;
-#pragma unroll
-        for (int j = 0; j < N; ++j) s += ex2((x[j] - m) * c);
+      // maxima and sums are numbers (NaN and +inf show in them), and maximum times c is, too
+      auto fine = [&](float m, float s) {
+        return s < INFINITY && (m == -INFINITY || fabsf(m) * c < 1e38f);
       };
-      node.each(
-          [&](int, const float(&x)[N], const float(&y)[N]) {
-            add(st.x, st.y, x);
-            if (DRAFT) add(st.z, st.w, y);
-          },
-          [&](int, float x, float y) {
-            st = join(st, make_float4(x, x == -INFINITY ? 0.f : 1.f, DRAFT ? y : -INFINITY,
-                                      DRAFT && y != -INFINITY ? 1.f : 0.f));
-          });
-      st = reduce(sh, st, join, turn);
-      const float mt = st.x == -INFINITY ? 0.f : st.x, md = st.z == -INFINITY ? 0.f : st.z;
-      const float it = st.y > 0.f ? 1.f / st.y : 0.f, id = st.w > 0.f ? 1.f / st.w : 0.f;
-      // (each product and difference rounded by itself: where p and q are the same numbers, nothing is
-      // left of p - q, not what a fused operation would leave)
-      auto p_of = [&](float x) { return __fmul_rn(ex2((x - mt) * c), it); };
-      auto q_of = [&](float y) { return DRAFT ? __fmul_rn(ex2((y - md) * c), id) : 0.f; };
-      float taken = 0.f, left_mass = 1.f;   // a and W
-      auto r_of = [&](float p, float q) {
-        return DRAFT ? fmaxf(__fsub_rn(p, __fmul_rn(taken, q)), 0.f) : p;
-      };
+      const bool careful = !(fine(st.x, st.y) && fine(st.z, st.w));
+      if (careful) {
+        look(cur, 1, stop, false, c, true);
+        exchange(sh, 1, join, turn);
+        st = exchanged(sh, 0, join, turn);
+      }
+      Probs<E, DRAFT> pr;
+      pr.c = c;
+      pr.mt = st.x == -INFINITY ? 0.f : st.x;
+      pr.md = st.z == -INFINITY ? 0.f : st.z;
+      pr.lt = st.y > 0.f ? -log2f(st.y) : 0.f;
+      pr.ld = st.w > 0.f ? -log2f(st.w) : 0.f;
+      pr.pt = pr.lt - pr.mt * c;
+      pr.qt = pr.ld - pr.md * c;
+      pr.taken = pr.la = 0.f;
+      pr.careful = careful;
+      float left_mass = 1.f;   // W
 
       // -------------------------------------------- children
       int refused = 0;
       for (uint64_t left = kids; left; left &= left - 1) {
         const int i = __ffsll((long long)left) - 1, x = sh.token[i];
-        const float p = p_of(sh.tl[i]), q = q_of(sh.ql[i]);
-        float r = r_of(p, q);
+        float r = pr.r_of(sh.tl[i], sh.ql[i]);
         if (!DRAFT)
           for (int j = 0; j < refused; ++j)
             if (sh.refused[j] == x) r = 0.f;
-        if (sh.u[i] * (DRAFT ? q : 1.f) * left_mass < r) {
+        if (sh.u[i] * (DRAFT ? pr.q_of(sh.ql[i], 0.f) : 1.f) * left_mass < r) {
           take = i;
           break;
         }
         if (DRAFT) {
-          taken += left_mass;
+          pr.taken += left_mass;
+          pr.la = log2f(pr.taken);
+          if (!(left & (left - 1))) break;   // (the last child: nobody asks for what is left)
           float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-          auto rest = [&](float x, float y) { w.x += r_of(p_of(x), q_of(y)); };
-          node.each(
-              [&](int, const float(&x)[N], const float(&y)[N]) {
+          row.template sweep<DRAFT, false>(
+                cur, 1, stop,
+                [&](int, const Words<E>& t, const Words<E>& d, const float(&)[N]) {
+                  float r[N], part[2] = {0.f, 0.f};
+                  pr.template rest<DRAFT>(t, d, r);
 #pragma unroll
-                for (int j = 0; j < N; ++j) rest(x[j], y[j]);
-              },
-              [&](int, float x, float y) { rest(x, y); });
+                  for (int j = 0; j < N; ++j) part[j & 1] += r[j];
+                  w.x += part[0] + part[1];
+                },
+                [&](int, float x, float y, float) { w.x += pr.r_of(x, y); }, nothing);
           left_mass = reduce(sh, w, Sum(), turn).x;
         } else {
           left_mass = fmaxf(left_mass - r, 0.f);
@@ -382,27 +612,52 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
       }
       if (take < 0) {
         // ------------------------------------------ the draw
-        if (!(left_mass > 0.f)) {   // nothing is left (p and q alike to the last bit): p itself
-          taken = 0.f;
+        float4 best = none;
+        auto race = [&](int i, float r, float e) {
+          if (r > best.x * e * 0.999999f && r > 0.f)   // (the quotient only where it may win)
+            best = best_of(best, make_float4(r / e, __int_as_float(i), 0.f, 0.f));
+        };
+        auto draw = [&](auto with_q) {
+          constexpr bool Q = decltype(with_q)::value;
+          row.template sweep<Q, true>(
+                cur, 1, stop,
+                [&](int i, const Words<E>& t, const Words<E>& d, const float(&e)[N]) {
+                  float r[N];
+                  pr.template rest<Q>(t, d, r);
+                  if (!DRAFT)
+                    for (int k = 0; k < refused; ++k)
+                      if ((unsigned)(sh.refused[k] - i) < (unsigned)N) {
+#pragma unroll
+                        for (int j = 0; j < N; ++j)
+                          if (sh.refused[k] == i + j) r[j] = 0.f;
+                      }
+#pragma unroll
+                  for (int j = 0; j < N; ++j) race(i + j, r[j], e[j]);
+                },
+                [&](int i, float x, float y, float e) {
+                  float r = pr.r_of(x, y);
+                  if (!DRAFT)
+                    for (int k = 0; k < refused; ++k)
+                      if (sh.refused[k] == i) r = 0.f;
+                  race(i, r, e);
+                },
+                nothing);
+        };
+        while (true) {
+          best = none;
+          if constexpr (DRAFT) {
+            if (pr.taken > 0.f)
+              draw(std::true_type());
+            else
+              draw(std::false_type());
+          } else {
+            draw(std::false_type());
+          }
+          best = reduce(sh, best, best_of, turn);
+          if (best.x > 0.f || (pr.taken == 0.f && refused == 0)) break;
+          pr.taken = 0.f;   // nothing is left (p and q alike to the last bit): p itself
           refused = 0;
         }
-        float4 best = make_float4(0.f, __int_as_float(0x7fffffff), 0.f, 0.f);
-        const Best op;
-        const float* noise = a.noise ? a.noise + (size_t)b * a.V : nullptr;
-        auto race = [&](int i, float x, float y) {
-          float r = r_of(p_of(x), q_of(y));
-          if (!DRAFT)
-            for (int j = 0; j < refused; ++j)
-              if (sh.refused[j] == i) r = 0.f;
-          if (r > 0.f) best = op(best, make_float4(noise ? r / noise[i] : r, __int_as_float(i), 0.f, 0.f));
-        };
-        node.each(
-            [&](int i, const float(&x)[N], const float(&y)[N]) {
-#pragma unroll
-              for (int j = 0; j < N; ++j) race(i + j, x[j], y[j]);
-            },
-            race);
-        best = reduce(sh, best, op, turn);
         next = best.x > 0.f ? __float_as_int(best.y) : -1;
       }
     }
@@ -423,8 +678,20 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
 template <typename E, bool DRAFT>
 fade_status_t launch(const Args& a, int B, cudaStream_t st) {
   cudaLaunchConfig_t lc{};
+  int device = 0;
+  const int sms = prompt_sms(&device);
+  if (sms == 0) return FADE_ERR_CUDA;
   lc.gridDim = dim3(B * kCluster);
-  lc.blockDim = dim3(kThreads);
+  lc.blockDim = dim3(B * kCluster <= sms ? 512 : 256);
+  lc.dynamicSmemBytes = lc.blockDim.x * kSlots * 16;
+  static bool opted[64];   // per device: the kernel has its shared memory
+  if (!opted[device]) {
+    if (cudaFuncSetAttribute(tree_verify_kernel<E, DRAFT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxThreads * kSlots * 16) != cudaSuccess)
+      return launch_status("fade_tree_verify shared-memory opt-in");
+    opted[device] = true;
+  }
   lc.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -507,6 +774,7 @@ extern "C" fade_status_t fade_tree_verify(const fade_config_t* c, int32_t T, int
   a.T = T;
   a.V = vocab;
   a.greedy = u == nullptr;
+  a.ahead = (long long)c->batch * T * vocab * size * (draft ? 2 : 1) <= kAheadBytes;
   const cudaStream_t s = as_stream(stream);
   if (type == FADE_LOGITS_F16) return launch<__half>(a, c->batch, s);
   if (type == FADE_LOGITS_BF16) return launch<__nv_bfloat16>(a, c->batch, s);
