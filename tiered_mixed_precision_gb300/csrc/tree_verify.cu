@@ -31,8 +31,9 @@
 namespace fade {
 namespace {
 
-constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
-constexpr int kCluster = 8;   // CTAs of a row
+// A row's CTAs, their threads and warps. At 64 rows of 128256 tokens: 77 us, as with 4 CTAs of 512; 8 of
+// 512 (which leave a row waiting for its place) 94, 2 of 512 or 1024 and 4 of 1024 from 96 to 99.
+constexpr int kCluster = 8, kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBatch = 16;    // values exchanged at once
 constexpr int kNodes = FADE_TREE_MAX_NODES + 1;   // the root first
 constexpr long long kAheadBytes = 64ll << 20;   // logits of all rows and nodes that are looked at ahead
@@ -149,7 +150,7 @@ struct Best {   // the larger value, the lower index where they are equal (y: th
 };
 
 struct Shared {
-  float4 warps[kBatch][kMaxWarps];
+  float4 warps[kBatch][kWarps];
   float4 ranks[2][kBatch][kCluster];   // what each CTA of the cluster found, two calls in turn
   float4 stats[kNodes];                // of node i - 1
   uint64_t kids[kNodes];               // children of node i - 1
@@ -180,10 +181,9 @@ template <class Op>
 __device__ __forceinline__ void exchange(Shared& sh, int count, const Op& op, int& turn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_rank(), size = cluster_size();
-  const int warps = blockDim.x / 32;   // a power of two: every group of as many lanes has them all
   __syncthreads();
-  for (int i = warp; i < count; i += warps) {
-    const float4 v = warp_reduce(sh.warps[i][lane & (warps - 1)], op, warps);
+  for (int i = warp; i < count; i += kWarps) {   // (every eight lanes have all of them)
+    const float4 v = warp_reduce(sh.warps[i][lane & (kWarps - 1)], op, kWarps);
     if (lane < size) st_remote4(remote(&sh.ranks[turn][i][rank], lane), v);
   }
   cluster_sync();
@@ -231,7 +231,8 @@ struct Row {
   static constexpr int N = Vec<E>::N;
   const Args& a;
   int b, first, step;             // the row; the thread's vectors
-  uint32_t slot0, slot_bytes;     // its slots
+  uint32_t slot0;                 // its slots: kThreads words apart
+  static constexpr uint32_t slot_bytes = kThreads * 16;
   __device__ __forceinline__ Node<E> node_at(int node) const {   // (-1: the root)
     Node<E> x;
     x.t = reinterpret_cast<const E*>(node < 0 ? a.target_root + b * a.tr_row
@@ -369,15 +370,15 @@ struct Probs {
 };
 
 template <typename E, bool DRAFT>
-__global__ void __launch_bounds__(kMaxThreads, 1) tree_verify_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_constant__ Args a) {
   constexpr int N = Vec<E>::N;
   __shared__ Shared sh;
   extern __shared__ uint4 slots[];   // [kSlots][threads]
-  const int tid = threadIdx.x, threads = blockDim.x;
+  const int tid = threadIdx.x;
   const uint32_t rank = cluster_rank(), size = cluster_size();
   const int b = blockIdx.x / size;
-  const Row<E, DRAFT> row{a, b, (int)(rank * threads + tid), (int)(size * threads),
-                          smem_u32(slots + tid), (uint32_t)threads * 16};
+  const Row<E, DRAFT> row{a, b, (int)(rank * kThreads + tid), (int)(size * kThreads),
+                          smem_u32(slots + tid)};
   int turn = 0;
   // (waited for before the first write to another CTA, which has to have started by then)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) tree_verify_kernel(const __gri
   // meanwhile, and what every CTA decides by is what CTA 0 read.
   int cur = a.target_root ? -1 : 0;
   const float own_temp = a.greedy ? 0.f : a.temperature ? a.temperature[b] : 1.f;
-  const bool mine = rank == 0 && tid < a.T, last = rank == 0 && tid == threads - 1;
+  const bool mine = rank == 0 && tid < a.T, last = rank == 0 && tid == kThreads - 1;
   int parent = -1, token = -1, nodes = a.T;
   float tl = -INFINITY, ql = -INFINITY, u = 0.f;
   if (mine) {
@@ -481,29 +482,15 @@ __global__ void __launch_bounds__(kMaxThreads, 1) tree_verify_kernel(const __gri
   } else if (last && a.n_nodes) {
     nodes = min(max(a.n_nodes[b], 0), a.T);
   }
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  for (uint32_t r = 0; r < size; ++r) {
-    if (mine) {
-      st_remote(remote(&sh.parent[tid], r), parent);
-      st_remote(remote(&sh.token[tid], r), token);
-      st_remote(remote(&sh.u[tid], r), __float_as_uint(u));
-      st_remote(remote(&sh.tl[tid], r), __float_as_uint(tl));
-      st_remote(remote(&sh.ql[tid], r), __float_as_uint(ql));
-    }
-    if (last) {
-      st_remote(remote(&sh.n, r), nodes);
-      st_remote(remote(&sh.temperature, r), __float_as_uint(own_temp));
-    }
-  }
   if (tid < kNodes) sh.kids[tid] = 0;
   uint64_t known = 0;   // nodes whose maxima and sums lie in sh.stats
   bool known_root = false;
   // nodes cur, cur + 1, .. looked at, and their values exchanged
-  auto look_on = [&](bool greedy, float c) {
+  auto look_on = [&](bool greedy, float c, auto before) {
     const int count = min(most, a.T - cur);
     const Stats join{c};
     look(cur, most, in_line, greedy, c, false);
+    before();
     if (greedy)
       exchange(sh, count, best_of, turn);
     else
@@ -518,7 +505,23 @@ __global__ void __launch_bounds__(kMaxThreads, 1) tree_verify_kernel(const __gri
         known |= 1ull << (cur + k);
     }
   };
-  look_on(!(own_temp > 0.f), scale_of(own_temp));
+  look_on(!(own_temp > 0.f), scale_of(own_temp), [&]() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    for (uint32_t r = 0; r < size; ++r) {
+      if (mine) {
+        st_remote(remote(&sh.parent[tid], r), parent);
+        st_remote(remote(&sh.token[tid], r), token);
+        st_remote(remote(&sh.u[tid], r), __float_as_uint(u));
+        st_remote(remote(&sh.tl[tid], r), __float_as_uint(tl));
+        st_remote(remote(&sh.ql[tid], r), __float_as_uint(ql));
+      }
+      if (last) {
+        st_remote(remote(&sh.n, r), nodes);
+        st_remote(remote(&sh.temperature, r), __float_as_uint(own_temp));
+      }
+    }
+  });
   const int n = sh.n;
   const bool greedy = !(sh.temperature > 0.f);
   const float c = scale_of(sh.temperature);
@@ -539,7 +542,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) tree_verify_kernel(const __gri
     const uint64_t kids = sh.kids[cur + 1];
     int take = -1;
     if (!(cur < 0 ? known_root : (known >> cur) & 1)) {
-      look_on(greedy, c);
+      look_on(greedy, c, [] {});
       __syncthreads();
     }
     float4 st = sh.stats[cur + 1];
@@ -678,20 +681,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) tree_verify_kernel(const __gri
 template <typename E, bool DRAFT>
 fade_status_t launch(const Args& a, int B, cudaStream_t st) {
   cudaLaunchConfig_t lc{};
-  int device = 0;
-  const int sms = prompt_sms(&device);
-  if (sms == 0) return FADE_ERR_CUDA;
   lc.gridDim = dim3(B * kCluster);
-  lc.blockDim = dim3(B * kCluster <= sms ? 512 : 256);
-  lc.dynamicSmemBytes = lc.blockDim.x * kSlots * 16;
-  static bool opted[64];   // per device: the kernel has its shared memory
-  if (!opted[device]) {
-    if (cudaFuncSetAttribute(tree_verify_kernel<E, DRAFT>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxThreads * kSlots * 16) != cudaSuccess)
-      return launch_status("fade_tree_verify shared-memory opt-in");
-    opted[device] = true;
-  }
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = kThreads * kSlots * 16;
   lc.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;

@@ -68,6 +68,7 @@ class DraftTree:
     ws: torch.Tensor
     v: list                        # per layer: the values its attention read
     buffers: TreeBuffers | None = None   # what mask .. ws lie in
+    parents: torch.Tensor | None = None  # i32 [B][T]
 
 
 class FadeCache:
@@ -223,32 +224,53 @@ class FadeCache:
         return x
 
     def prefill(self, layer: int, k_raw: torch.Tensor, v: torch.Tensor, prompt_len=None,
-                mass: torch.Tensor | None = None, q_raw: torch.Tensor | None = None):
+                mass: torch.Tensor | None = None, q_raw: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, window: int = 0):
         """k_raw, v: fp16 [B][Hkv][P][d] device tensors (k pre-RoPE; rotated in place).
 
         For H2O either ``mass`` (f32 [B][Hkv][P]) is given, or ``q_raw`` (fp16 [B][Hq][P][d],
         pre-RoPE, rotated in place) and the prefill attention mass is computed on the GPU.
+        ``out`` (fp16 [B][Hq][P][d], with ``q_raw``): the prompt's attention is computed, too
+        (``fade_prompt_attention``; rows past their lengths are left as they are), over all tokens or,
+        with ``window``, over the last ``window`` ones and the sinks; the mass then comes from its
+        log-sum-exp (``fade_prompt_mass``) and sees the same tokens.
         Returns the mass the prefill used (None when it used none)."""
         c = self.cfg
         B, H, P, d = k_raw.shape
         if prompt_len is None:
             prompt_len = np.full(B, P, np.int32)
+        if (out is not None or window) and q_raw is None:
+            raise ValueError("the prompt's attention needs its queries (q_raw)")
+        if window and out is None:
+            raise ValueError("a window is the attention's: give out")
         normed = self.qk_norm[layer] is not None
         if normed:
             kt = k_raw.transpose(1, 2)
             self._norm_rope(layer, None, kt, None, None, kt)
         else:
             self.rope_(k_raw, B * H, P, None, 1)
-        if mass is None and q_raw is not None and c.policy == "h2o":
+        L = self.layers[layer]
+        F.fade_cache_reset(L)
+        wants_mass = mass is None and q_raw is not None and c.policy == "h2o"
+        if wants_mass or out is not None:
             if normed:
                 qt = q_raw.transpose(1, 2)
                 self._norm_rope(layer, qt, None, None, qt, None)
             else:
                 self.rope_(q_raw, B * c.num_q_heads, P, None, 1)
+        if wants_mass:
             mass = torch.empty((B, H, P), dtype=torch.float32, device=k_raw.device)
+        if out is not None:
+            q, k = q_raw.transpose(1, 2), k_raw.transpose(1, 2)
+            lse = torch.empty((B, P, c.num_q_heads), dtype=torch.float32, device=k_raw.device)
+            ws = torch.empty(F.fade_prompt_ws_bytes(c, P, P), dtype=torch.uint8, device=k_raw.device)
+            see = dict(q_len=prompt_len, kv_len=prompt_len, n_sink=c.n_sink, window=window, ws=ws,
+                       status=L.status)
+            F.fade_prompt_attention(c, q, k, v.transpose(1, 2), out.transpose(1, 2), lse, **see)
+            if wants_mass:
+                F.fade_prompt_mass(c, q, k, lse, mass, **see)
+        elif wants_mass:
             F.fade_prefill_mass(c, q_raw, k_raw, P, prompt_len, mass)
-        L = self.layers[layer]
-        F.fade_cache_reset(L)
         F.fade_cache_prefill(L, k_raw, v, P, prompt_len, mass, self.table, self.max_pos)
         return mass
 
@@ -418,7 +440,7 @@ class FadeCache:
         self.maintain_all()
         F.fade_tree_layout(c, parents, n_nodes, self.pos, b.tensors["mask"], b.tensors["pos"])
         self.launches += 1
-        return DraftTree(n_nodes=n_nodes, v=[None] * L, buffers=b, **b.tensors)
+        return DraftTree(n_nodes=n_nodes, v=[None] * L, buffers=b, parents=parents, **b.tensors)
 
     def _hold(self, b: TreeBuffers | None):
         """What a tree's buffers need before a call on the current stream uses them, so that they can be
@@ -445,6 +467,23 @@ class FadeCache:
                               tree.mask, tree.n_nodes, out, tree.lse[layer], tree.ws)
         tree.v[layer] = v
         self.launches += 3
+
+    def tree_verify(self, tree: DraftTree, tokens: torch.Tensor, target: torch.Tensor,
+                    target_root: torch.Tensor | None = None, draft: torch.Tensor | None = None,
+                    draft_root: torch.Tensor | None = None, temperature: torch.Tensor | None = None,
+                    u: torch.Tensor | None = None, noise: torch.Tensor | None = None):
+        """Which of the tree's tokens (i32 [B][T]) are kept under the target's logits ([B][T][vocab]
+        after every node; target_root [B][vocab] after the last cached token, None: node 0 is certain)
+        and the drafter's, if the drafts were drawn from some (``fade_tree_verify``: temperature, u
+        and noise; without u the rows are greedy). Returns the paths (device i32 [B][T], for
+        ``tree_commit``), their lengths and the tokens after them (device i32 [B])."""
+        B, T = tree.parents.shape
+        new = lambda *s: torch.empty(s, dtype=torch.int32, device=self.device)
+        path, n_path, next_token = new(B, T), new(B), new(B)
+        F.fade_tree_verify(self.cfg, tree.parents, tree.n_nodes, tokens, target, target_root, draft,
+                           draft_root, temperature, u, noise, path, n_path, next_token)
+        self.launches += 1
+        return path, n_path, next_token
 
     def tree_commit(self, tree: DraftTree, path: torch.Tensor, n_path):
         """Append every row's accepted path (path: device i32 [B][T], n_path: B host lengths) to
