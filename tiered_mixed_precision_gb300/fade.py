@@ -528,6 +528,7 @@ def fade_measure_fp32_rate(blocks: int, iters: int, sink, stream=None) -> float:
 
 
 _torch = None
+_dtypes = {}   # by name, once torch is there
 
 
 def _device(stream):
@@ -539,6 +540,8 @@ def _device(stream):
         import torch
 
         _torch = torch
+        for name in ("float16", "bfloat16", "float32", "int32", "int64"):
+            _dtypes[name] = getattr(torch, name)
     if stream is not None:
         return None
     return _torch.cuda.current_device() if _torch.cuda.is_available() else -2
@@ -549,7 +552,7 @@ def _tensor(device, name, t, dtype, shape, strided=False):
     only the last dimension has to be contiguous) and lies on the device."""
     if t is None:
         return
-    if t.dtype != getattr(_torch, dtype) or t.shape != shape:
+    if t.dtype is not _dtypes[dtype] or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not "
                          f"{str(t.dtype).removeprefix('torch.')} {tuple(t.shape)}")
     if strided:
@@ -563,8 +566,20 @@ def _tensor(device, name, t, dtype, shape, strided=False):
 
 def _heads(t):
     """A [rows][tokens][heads][d] tensor as a fade_heads_t."""
-    return None if t is None else ctypes.byref(HeadsT(t.data_ptr(), t.stride(0), t.stride(1),
-                                                      t.stride(2)))
+    if t is None:
+        return None
+    rows, tokens, heads, _ = t.stride()
+    return ctypes.byref(HeadsT(t.data_ptr(), rows, tokens, heads))
+
+
+def _checked_heads(device, name, t, shape):
+    """``_heads`` of a float16 tensor that ``_tensor`` would take as strided."""
+    if t.dtype is _torch.float16 and t.shape == shape:
+        rows, tokens, heads, one = t.stride()
+        if one == 1 and (device is None or t.get_device() == device):
+            return ctypes.byref(HeadsT(t.data_ptr(), rows, tokens, heads))
+    _tensor(device, name, t, "float16", shape, True)
+    return _heads(t)
 
 
 def fade_tree_layout(cfg: Config, parents, n_nodes, base_pos, mask, pos, stream=None):
@@ -677,7 +692,16 @@ def _logits(dev, name, t, dtype, shape):
     if t is None:
         return None
     _tensor(dev, name, t, dtype, shape, True)
-    return ctypes.byref(LogitsT(t.data_ptr(), t.stride(0), t.stride(1) if t.dim() == 3 else 0))
+    s = t.stride()
+    return ctypes.byref(LogitsT(t.data_ptr(), s[0], s[1] if len(s) == 3 else 0))
+
+
+def _pointer(dev, name, t, dtype, shape):
+    """The address of a contiguous tensor (None: NULL)."""
+    if t is None:
+        return None
+    _tensor(dev, name, t, dtype, shape)
+    return t.data_ptr()
 
 
 def fade_tree_verify(cfg: Config, parents, n_nodes, tokens, target, target_root, draft, draft_root,
@@ -695,20 +719,20 @@ def fade_tree_verify(cfg: Config, parents, n_nodes, tokens, target, target_root,
     dtype = str(target.dtype).removeprefix("torch.")
     if dtype not in LOGIT_TYPES:
         raise ValueError(f"logits must be float16, bfloat16 or float32, not {dtype}")
-    for name, t, dt, shape in (("parents", parents, "int32", (B, T)), ("n_nodes", n_nodes, "int32", (B,)),
-                               ("tokens", tokens, "int32", (B, T)),
-                               ("temperature", temperature, "float32", (B,)),
-                               ("u", u, "float32", (B, T)), ("noise", noise, "float32", (B, V)),
-                               ("path", path, "int32", (B, T)), ("n_path", n_path, "int32", (B,)),
-                               ("next_token", next_token, "int32", (B,))):
-        _tensor(dev, name, t, dt, shape)
+    nodes, row, rows, vocab = (B, T), (B,), (B, T, V), (B, V)
     _check(lib().fade_tree_verify(
-        ctypes.byref(cfg.c()), T, V, LOGIT_TYPES[dtype], _ptr(parents), _ptr(n_nodes), _ptr(tokens),
-        _logits(dev, "target", target, dtype, (B, T, V)),
-        _logits(dev, "target_root", target_root, dtype, (B, V)),
-        _logits(dev, "draft", draft, dtype, (B, T, V)),
-        _logits(dev, "draft_root", draft_root, dtype, (B, V)), _ptr(temperature), _ptr(u), _ptr(noise),
-        _ptr(path), _ptr(n_path), _ptr(next_token), _stream(stream)))
+        ctypes.byref(cfg.c()), T, V, LOGIT_TYPES[dtype],
+        _pointer(dev, "parents", parents, "int32", nodes),
+        _pointer(dev, "n_nodes", n_nodes, "int32", row),
+        _pointer(dev, "tokens", tokens, "int32", nodes),
+        _logits(dev, "target", target, dtype, rows),
+        _logits(dev, "target_root", target_root, dtype, vocab),
+        _logits(dev, "draft", draft, dtype, rows),
+        _logits(dev, "draft_root", draft_root, dtype, vocab),
+        _pointer(dev, "temperature", temperature, "float32", row),
+        _pointer(dev, "u", u, "float32", nodes), _pointer(dev, "noise", noise, "float32", vocab),
+        _pointer(dev, "path", path, "int32", nodes), _pointer(dev, "n_path", n_path, "int32", row),
+        _pointer(dev, "next_token", next_token, "int32", row), _stream(stream)))
 
 
 def fade_prompt_ws_bytes(cfg: Config, n_q: int, n_kv: int) -> int:
@@ -720,29 +744,22 @@ def fade_prompt_ws_bytes(cfg: Config, n_q: int, n_kv: int) -> int:
     return n
 
 
-def _prompt_args(cfg, dev, q, k, v, q_len, kv_len, ws, status):
-    """Checks of what the prompt calls share; (n_q, n_kv, host lengths, workspace)."""
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q and k must be [rows][tokens][heads][channels]")
-    n_q, n_kv, d = q.shape[1], k.shape[1], cfg.head_dim
-    _tensor(dev, "q", q, "float16", (cfg.batch, n_q, cfg.num_q_heads, d), True)
-    kv = (cfg.batch, n_kv, cfg.num_kv_heads, d)
-    _tensor(dev, "k", k, "float16", kv, True)
-    _tensor(dev, "v", v, "float16", kv, True)
-    lens = []
-    for name, x in (("q_len", q_len), ("kv_len", kv_len)):
-        if x is not None:
-            x = np.ascontiguousarray(x, np.int32)
-            if x.shape != (cfg.batch,):
-                raise ValueError(f"{name} must hold {cfg.batch} lengths")
-        lens.append(x)
-    if status is not None:
-        _tensor(dev, "status", status, "int32", (STATUS_WORDS,))
+def _host_lens(name, x, rows):
+    """HOST i32 lengths as the bytes of a C array (None: NULL)."""
+    if x is None:
+        return None
+    x = np.ascontiguousarray(x, np.int32)
+    if x.shape != (rows,):
+        raise ValueError(f"{name} must hold {rows} lengths")
+    return x.tobytes()
+
+
+def _prompt_ws(cfg, dev, n_q, n_kv, q, ws):
     if ws is None:
-        ws = _torch.empty(fade_prompt_ws_bytes(cfg, n_q, n_kv), dtype=_torch.uint8, device=q.device)
-    elif not ws.is_contiguous() or (dev is not None and ws.get_device() != dev):
+        return _torch.empty(fade_prompt_ws_bytes(cfg, n_q, n_kv), dtype=_torch.uint8, device=q.device)
+    if not ws.is_contiguous() or (dev is not None and ws.get_device() != dev):
         raise ValueError("ws must be contiguous and on the current CUDA device")
-    return n_q, n_kv, lens, ws
+    return ws
 
 
 def fade_prompt_attention(cfg: Config, q, k, v, out, lse=None, q_len=None, kv_len=None, n_sink=0,
@@ -753,14 +770,20 @@ def fade_prompt_attention(cfg: Config, q, k, v, out, lse=None, q_len=None, kv_le
     last ``window`` tokens and the first ``n_sink``. ws: fade_prompt_ws_bytes (made here when not
     given); status: a layer's status words."""
     dev = _device(stream)
-    n_q, n_kv, (ql, kl), ws = _prompt_args(cfg, dev, q, k, v, q_len, kv_len, ws, status)
-    _tensor(dev, "out", out, "float16", q.shape, True)
-    _tensor(dev, "lse", lse, "float32", q.shape[:3])
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [rows][tokens][heads][channels]")
+    B, n_q, n_kv = cfg.batch, q.shape[1], k.shape[1]
+    shape, kv = (B, n_q, cfg.num_q_heads, cfg.head_dim), (B, n_kv, cfg.num_kv_heads, cfg.head_dim)
+    hq, ho = _checked_heads(dev, "q", q, shape), _checked_heads(dev, "out", out, shape)
+    hk, hv = _checked_heads(dev, "k", k, kv), _checked_heads(dev, "v", v, kv)
+    _tensor(dev, "lse", lse, "float32", shape[:3])
+    if status is not None:
+        _tensor(dev, "status", status, "int32", (STATUS_WORDS,))
+    ws = _prompt_ws(cfg, dev, n_q, n_kv, q, ws)
     _check(lib().fade_prompt_attention(
-        ctypes.byref(cfg.c()), _heads(q), _heads(k), _heads(v), n_q, n_kv,
-        None if ql is None else ql.ctypes.data, None if kl is None else kl.ctypes.data, n_sink, window,
-        _heads(out), _ptr(lse), _ptr(status), _ptr(ws), ws.numel() * ws.element_size(),
-        _stream(stream)))
+        ctypes.byref(cfg.c()), hq, hk, hv, n_q, n_kv, _host_lens("q_len", q_len, B),
+        _host_lens("kv_len", kv_len, B), n_sink, window, ho, _ptr(lse), _ptr(status), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def fade_prompt_mass(cfg: Config, q, k, lse, mass, q_len=None, kv_len=None, n_sink=0, window=0,
@@ -768,14 +791,22 @@ def fade_prompt_mass(cfg: Config, q, k, lse, mass, q_len=None, kv_len=None, n_si
     """Column sums of fade_prompt_attention's probabilities, from the lse it left: mass f32
     [B][H][n_kv] (accumulate: added to)."""
     dev = _device(stream)
-    n_q, n_kv, (ql, kl), ws = _prompt_args(cfg, dev, q, k, None, q_len, kv_len, ws, status)
-    _tensor(dev, "lse", lse, "float32", q.shape[:3])
-    _tensor(dev, "mass", mass, "float32", (cfg.batch, cfg.num_kv_heads, n_kv))
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [rows][tokens][heads][channels]")
+    B, H, n_q, n_kv = cfg.batch, cfg.num_kv_heads, q.shape[1], k.shape[1]
+    shape = (B, n_q, cfg.num_q_heads, cfg.head_dim)
+    hq = _checked_heads(dev, "q", q, shape)
+    hk = _checked_heads(dev, "k", k, (B, n_kv, H, cfg.head_dim))
+    _tensor(dev, "lse", lse, "float32", shape[:3])
+    _tensor(dev, "mass", mass, "float32", (B, H, n_kv))
+    if status is not None:
+        _tensor(dev, "status", status, "int32", (STATUS_WORDS,))
+    ws = _prompt_ws(cfg, dev, n_q, n_kv, q, ws)
     _check(lib().fade_prompt_mass(
-        ctypes.byref(cfg.c()), _heads(q), _heads(k), n_q, n_kv,
-        None if ql is None else ql.ctypes.data, None if kl is None else kl.ctypes.data, n_sink, window,
-        _ptr(lse), int(bool(accumulate)), _ptr(mass), _ptr(status), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream)))
+        ctypes.byref(cfg.c()), hq, hk, n_q, n_kv, _host_lens("q_len", q_len, B),
+        _host_lens("kv_len", kv_len, B), n_sink, window, lse.data_ptr(), int(bool(accumulate)),
+        mass.data_ptr(), _ptr(status), ws.data_ptr(), ws.numel() * ws.element_size(),
+        _stream(stream)))
 
 
 def fade_attention_tiled(cfg: Config) -> bool:
