@@ -528,7 +528,8 @@ def fade_measure_fp32_rate(blocks: int, iters: int, sink, stream=None) -> float:
 
 
 _torch = None
-_dtypes = {}   # by name, once torch is there
+_dtypes = {}         # by name, once torch is there
+_available = False   # CUDA is (the query is not free)
 
 
 def _device(stream):
@@ -544,7 +545,9 @@ def _device(stream):
             _dtypes[name] = getattr(torch, name)
     if stream is not None:
         return None
-    return _torch.cuda.current_device() if _torch.cuda.is_available() else -2
+    global _available
+    _available = _available or _torch.cuda.is_available()
+    return _torch.cuda.current_device() if _available else -2
 
 
 def _tensor(device, name, t, dtype, shape, strided=False):
@@ -574,6 +577,8 @@ def _heads(t):
 
 def _checked_heads(device, name, t, shape):
     """``_heads`` of a float16 tensor that ``_tensor`` would take as strided."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
     if t.dtype is _torch.float16 and t.shape == shape:
         rows, tokens, heads, one = t.stride()
         if one == 1 and (device is None or t.get_device() == device):
@@ -782,8 +787,9 @@ def fade_prompt_attention(cfg: Config, q, k, v, out, lse=None, q_len=None, kv_le
     ws = _prompt_ws(cfg, dev, n_q, n_kv, q, ws)
     _check(lib().fade_prompt_attention(
         ctypes.byref(cfg.c()), hq, hk, hv, n_q, n_kv, _host_lens("q_len", q_len, B),
-        _host_lens("kv_len", kv_len, B), n_sink, window, ho, _ptr(lse), _ptr(status), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _stream(stream)))
+        _host_lens("kv_len", kv_len, B), n_sink, window, ho,
+        None if lse is None else lse.data_ptr(), None if status is None else status.data_ptr(),
+        ws.data_ptr(), ws.nbytes, _stream(stream)))
 
 
 def fade_prompt_mass(cfg: Config, q, k, lse, mass, q_len=None, kv_len=None, n_sink=0, window=0,
@@ -805,7 +811,7 @@ def fade_prompt_mass(cfg: Config, q, k, lse, mass, q_len=None, kv_len=None, n_si
     _check(lib().fade_prompt_mass(
         ctypes.byref(cfg.c()), hq, hk, n_q, n_kv, _host_lens("q_len", q_len, B),
         _host_lens("kv_len", kv_len, B), n_sink, window, lse.data_ptr(), int(bool(accumulate)),
-        mass.data_ptr(), _ptr(status), ws.data_ptr(), ws.numel() * ws.element_size(),
+        mass.data_ptr(), None if status is None else status.data_ptr(), ws.data_ptr(), ws.nbytes,
         _stream(stream)))
 
 
