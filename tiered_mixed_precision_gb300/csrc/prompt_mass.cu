@@ -238,23 +238,25 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
     int seq = 0;
 #pragma unroll 1
     while (next()) {
-      const int k_end = it.k0 + t * kTile + kTile - 1;   // the tile's last key
+      // Of the item's query tiles: every query of [all0, all1) sees every key of this key tile, none
+      // outside [any0, any1) sees any (key 0 of it at a, query 0 of the item's first tile at `from`).
+      const int a0 = it.k0 + t * kTile, w = s.sight.window;
+      const int tile0 = it.first + it.begin, from = it.off + tile0 * per;
+      const bool sinks = a0 < s.sight.sink, all_sinks = a0 + kTile - 1 < s.sight.sink;
+      auto up = [&](int x) { return x <= 0 ? 0 : (x + per - 1) / per; };    // tiles that begin before x
+      auto whole = [&](int x) { return x <= 0 ? 0 : x / per; };             // tiles that end before x
+      const int all0 = up(a0 + kTile - 1 - from), any0 = whole(a0 - from);
+      const int all1 = min(whole(it.q_len - tile0 * per), w && !all_sinks ? whole(a0 + w - from) : it.n);
+      const int any1 = w && !sinks ? up(a0 + kTile - 1 + w - from) : it.n;
       f2x total[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) total[e] = f2_pack(0.f, 0.f);
 #pragma unroll 1
       for (int i = 0; i < it.n; ++i, ++seq) {
-        const int buf = seq & 1, tok0 = (it.first + it.begin + i) * per;
-        const int p0 = it.off + tok0, left = it.q_len - tok0;   // positions from p0, `left` queries
-        const int w = s.sight.window;
-        // whether every query sees every key of the tile, and whether any sees any
-        const bool all = k_end <= p0 && left >= per &&
-                         (!w || k_end < s.sight.sink || k_end - kTile + 1 + w >= p0 + per);
-        const bool none = k_end - kTile + 1 >= p0 + per ||
-                          (w && k_end - kTile + 1 >= s.sight.sink && p0 >= k_end + w);
+        const int buf = seq & 1;
         wait(sFull + 16 * t + 8 * buf, seq >> 1);
         fence_after();
-        if (!none) {
+        if (i >= any0 && i < any1) {
           float x[2][2][16];
 #pragma unroll
           for (int f = 0; f < 2; ++f)
@@ -269,6 +271,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
           auto sum_tile = [&](auto some) {
             uint32_t see[4];
             if constexpr (decltype(some)::value) {
+              const int p0 = from + i * per, left = it.q_len - (tile0 + i) * per;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {   // queries that see the key: columns [lo, hi)
                 const int j = it.k0 + key0 + 8 * e;
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
                 }
               }
           };
-          if (all)
+          if (i >= all0 && i < all1)
             sum_tile(std::false_type());
           else
             sum_tile(std::true_type());
