@@ -219,7 +219,7 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
 template <typename E>
 struct Node {
   const E *t, *d;
-  int head, vecs;   // elements before the first 16-byte boundary of t; whole vectors from there
+  int head;         // elements before the first 16-byte boundary of t
   bool wide_d;      // d has the same boundaries
 };
 
@@ -241,39 +241,46 @@ struct Row {
                  : reinterpret_cast<const E*>(node < 0 ? a.draft_root + b * a.dr_row
                                                        : a.draft + b * a.d_row + node * a.d_node);
     x.head = min((int)((16 - (reinterpret_cast<uintptr_t>(x.t) & 15)) & 15) / (int)sizeof(E), a.V);
-    x.vecs = (a.V - x.head) / N;
     x.wide_d = DRAFT && (reinterpret_cast<uintptr_t>(x.d + x.head) & 15) == 0;
     return x;
   }
   // One pass over the logits after node `at`, then those after then(at), .., `most` nodes (-2: no more).
-  // f(index, words of t, d, noise) for a thread's vectors, g(index, t, d, noise) for single elements at
-  // the ends, done(k) after the k-th node. D, NOISE: d and the noise are read, too. Words come by
-  // asynchronous copies into slots of the thread's own, several vectors ahead, across nodes.
-  template <bool D, bool NOISE, class Then, class F, class G, class Done>
+  // f(index, W words of t, of d, noise) for a thread's vectors, g(index, t, d, noise) for single elements
+  // at the ends, done(k) after the k-th node. D, NOISE: d and the noise are read, too (W = 1). Words come
+  // by asynchronous copies into slots of the thread's own, several vectors ahead, across nodes.
+  template <bool D, bool NOISE, int W, class Then, class F, class G, class Done>
   __device__ __forceinline__ void sweep(int at, int most, const Then& then, const F& f, const G& g,
                                         const Done& done) const {
     constexpr int EW = NOISE ? N / 4 : 0;               // words of noise a vector
-    constexpr int P = 1 + (D ? 1 : 0) + EW;             // words of a vector
+    constexpr int P = W * (1 + (D ? 1 : 0)) + EW;       // words of a vector
     constexpr int S = P == 1 ? 8 : P == 2 ? 4 : 2;      // vectors in flight
+    static_assert(P * S <= kSlots && (W == 1 || !NOISE), "slots");
+    auto vecs_of = [&](const Node<E>& x) { return (a.V - x.head) / (W * N); };
     const float* noise = NOISE && a.noise ? a.noise + (size_t)b * a.V : nullptr;
     auto wide_e = [&](const Node<E>& x) {
       return noise && (reinterpret_cast<uintptr_t>(noise + x.head) & 15) == 0;
     };
     int ai = at, ki = 0, vi = first;
     Node<E> ni = node_at(at);
+    int vecs_i = vecs_of(ni);
     uint32_t si = 0, sp = 0;
     auto issue = [&]() {
-      while (ai != -2 && vi >= ni.vecs) {
+      while (ai != -2 && vi >= vecs_i) {
         ai = ++ki < most ? then(ai) : -2;
         if (ai == -2) break;
         ni = node_at(ai);
+        vecs_i = vecs_of(ni);
         vi = first;
       }
       if (ai != -2) {
-        const int i = ni.head + vi * N;
+        const int i = ni.head + vi * (W * N);
         const uint32_t to = slot0 + si * P * slot_bytes;
-        copy16(to, ni.t + i);
-        if (D && ni.wide_d) copy16(to + slot_bytes, ni.d + i);
+#pragma unroll
+        for (int w = 0; w < W; ++w) copy16(to + w * slot_bytes, ni.t + i + w * N);
+        if (D && ni.wide_d) {
+#pragma unroll
+          for (int w = 0; w < W; ++w) copy16(to + (W + w) * slot_bytes, ni.d + i + w * N);
+        }
         if (NOISE && wide_e(ni)) {
 #pragma unroll
           for (int k = 0; k < EW; ++k) copy16(to + (P - EW + k) * slot_bytes, noise + i + 4 * k);
@@ -288,19 +295,23 @@ struct Row {
 #pragma unroll 1
     for (int k = 0; at != -2; at = ++k < most ? then(at) : -2) {
       const Node<E> node = node_at(at);
+      const int vecs = vecs_of(node);
 #pragma unroll 1
-      for (int v = first; v < node.vecs; v += step) {
-        const int i = node.head + v * N;
+      for (int v = first; v < vecs; v += step) {
+        const int i = node.head + v * (W * N);
         const uint32_t from = slot0 + sp * P * slot_bytes;
-        Words<E> t, d;
+        Words<E> t[W], d[W];
         float e[N];
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-        t.w = ld_shared16(from);
+#pragma unroll
+        for (int w = 0; w < W; ++w) t[w].w = ld_shared16(from + w * slot_bytes);
         if (D) {
-          if (node.wide_d)
-            d.w = ld_shared16(from + slot_bytes);
-          else
-            load(node.d, i, false, d);
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+            if (node.wide_d)
+              d[w].w = ld_shared16(from + (W + w) * slot_bytes);
+            else
+              load(node.d, i + w * N, false, d[w]);
         }
         if (NOISE) {
           if (wide_e(node)) {
@@ -319,9 +330,9 @@ struct Row {
         sp = sp + 1 == S ? 0 : sp + 1;
         f(i, t, d, e);
       }
-      const int ends = a.V - node.vecs * N;
+      const int ends = a.V - vecs * (W * N);
       if (first < ends) {
-        const int i = first < node.head ? first : first + node.vecs * N;
+        const int i = first < node.head ? first : first + vecs * (W * N);
         g(i, logit(to_float(node.t[i])), D ? logit(to_float(node.d[i])) : 0.f,
           NOISE && noise ? noise[i] : 1.f);
       }
@@ -394,17 +405,18 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
     if (greedy) {
       float4 best = none;
       best.x = -INFINITY;
-      row.template sweep<false, false>(
+      row.template sweep<false, false, 2>(
             at, most, then,
-            [&](int i, const Words<E>& t, const Words<E>&, const float(&)[N]) {
-              float x[N];
-              logits(t, false, x);
+            [&](int i, const Words<E>(&t)[2], const Words<E>(&)[2], const float(&)[N]) {
+              float x[2 * N];
+#pragma unroll
+              for (int j = 0; j < 2 * N; ++j) x[j] = to_float(t[j / N].e[j % N]);
               float top = x[0];
 #pragma unroll
-              for (int j = 1; j < N; ++j) top = fmaxf(top, x[j]);
+              for (int j = 1; j < 2 * N; ++j) top = fmaxf(top, x[j]);
               if (top > best.x) {   // (ascending in a thread)
 #pragma unroll
-                for (int j = 0; j < N; ++j)
+                for (int j = 0; j < 2 * N; ++j)
                   if (logit(x[j]) > best.x)
                     best = make_float4(logit(x[j]), __int_as_float(i + j), 0.f, 0.f);
               }
@@ -442,11 +454,11 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
       }
       s += part[0] + part[1];
     };
-    row.template sweep<DRAFT, false>(
+    row.template sweep<DRAFT, false, 1>(
           at, most, then,
-          [&](int, const Words<E>& t, const Words<E>& d, const float(&)[N]) {
-            add(st.x, st.y, t);
-            if (DRAFT) add(st.z, st.w, d);
+          [&](int, const Words<E>(&t)[1], const Words<E>(&d)[1], const float(&)[N]) {
+            add(st.x, st.y, t[0]);
+            if (DRAFT) add(st.z, st.w, d[0]);
           },
           [&](int, float x, float y, float) {
             st = join(st, make_float4(x, x == -INFINITY ? 0.f : 1.f, DRAFT ? y : -INFINITY,
@@ -594,11 +606,11 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
           pr.la = log2f(pr.taken);
           if (!(left & (left - 1))) break;   // (the last child: nobody asks for what is left)
           float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-          row.template sweep<DRAFT, false>(
+          row.template sweep<DRAFT, false, 1>(
                 cur, 1, stop,
-                [&](int, const Words<E>& t, const Words<E>& d, const float(&)[N]) {
+                [&](int, const Words<E>(&t)[1], const Words<E>(&d)[1], const float(&)[N]) {
                   float r[N], part[2] = {0.f, 0.f};
-                  pr.template rest<DRAFT>(t, d, r);
+                  pr.template rest<DRAFT>(t[0], d[0], r);
 #pragma unroll
                   for (int j = 0; j < N; ++j) part[j & 1] += r[j];
                   w.x += part[0] + part[1];
@@ -622,11 +634,11 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
         };
         auto draw = [&](auto with_q) {
           constexpr bool Q = decltype(with_q)::value;
-          row.template sweep<Q, true>(
+          row.template sweep<Q, true, 1>(
                 cur, 1, stop,
-                [&](int i, const Words<E>& t, const Words<E>& d, const float(&e)[N]) {
+                [&](int i, const Words<E>(&t)[1], const Words<E>(&d)[1], const float(&e)[N]) {
                   float r[N];
-                  pr.template rest<Q>(t, d, r);
+                  pr.template rest<Q>(t[0], d[0], r);
                   if (!DRAFT)
                     for (int k = 0; k < refused; ++k)
                       if ((unsigned)(sh.refused[k] - i) < (unsigned)N) {
