@@ -26,6 +26,7 @@
 //     movmatrix. Columns whose group parity differs from the row's are discarded.
 // mma.sync.m16n8k16 (fp16 in, fp32 accumulate) is used: at N = 8 query columns per KV head
 // the contraction is far below the tile sizes of the 5th-generation tensor-core instructions.
+#include <cuda.h>
 #include <math.h>
 
 #include <algorithm>
@@ -34,7 +35,6 @@
 #include <unordered_map>
 
 #include "fade_internal.cuh"
-#include "tensor_map.cuh"
 
 namespace fade {
 
@@ -1366,6 +1366,25 @@ attn_mid_mma_kernel(const __grid_constant__ CUtensorMap tk0, const __grid_consta
 }
 
 // ------------------------------------------------------------------ host side
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(p);
+  });
+  return fn;
+}
+
 // 2D map over code rows: [rows][row_bytes] u8, boxes of kTileTok rows.
 fade_status_t encode_rows(CUtensorMap* m, const void* base, unsigned long long rows,
                           int row_bytes) {
