@@ -45,20 +45,6 @@ struct Args {
   PromptSchedule sched;
 };
 
-// 16 lanes x 32 columns: v[4i .. 4i+1] row lane/4, columns 8i + 2(lane%4) + {0, 1}; v[4i+2 .. 4i+3] the
-// same columns of row lane/4 + 8.
-__device__ __forceinline__ void tm_ld_quads(uint32_t addr, float* v) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(addr)
-      : "memory");
-}
-
 // One persistent CTA per SM; an item is two tiles of 128 keys of a unit, both met by every query tile of
 // the ring. Roles meet at mbarriers: one warp loads (bulk tensor copies), two bring the rows' lse, one
 // issues the products, four warps a key tile sum; S has two buffers a key tile, so products run ahead of
@@ -262,7 +248,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
           for (int f = 0; f < 2; ++f)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-              tm_ld_quads(tS + 128 * buf + 32 * q + ((uint32_t)(16 * f) << 16), x[f][q]);
+              tm_ld32(tS + 128 * buf + 32 * q + ((uint32_t)(16 * f) << 16), x[f][q]);
           const float* l = sL + buf * kTile + 64 * half + col;
           f2x acc[4];
 #pragma unroll

@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
                   pr.template rest<Q>(t[0], d[0], r);
                   if (!DRAFT)
                     for (int k = 0; k < refused; ++k)
-                      if ((unsigned)(sh.refused[k] - i) < (unsigned)N) {
+                      if ((unsigned)sh.refused[k] - (unsigned)i < (unsigned)N) {
 #pragma unroll
                         for (int j = 0; j < N; ++j)
                           if (sh.refused[k] == i + j) r[j] = 0.f;
