@@ -524,8 +524,9 @@ typedef enum { FADE_LOGITS_F16 = 0, FADE_LOGITS_BF16 = 1, FADE_LOGITS_F32 = 2 } 
  * other nodes without parent are not reached. draft, draft_root: the logits from which the children of
  * a node were drawn, independently of each other, laid out like the target's; NULL: drafts without
  * probabilities (the drafter's likeliest tokens, a lookup).
- * temperature: DEVICE f32 [B] (NULL: 1), dividing target and drafter logits; 0 or less: a greedy row. u: DEVICE f32
- * [B][T] uniform in [0, 1), u[b][i] decides node i; NULL: every row is greedy, and draft must be NULL.
+ * temperature: DEVICE f32 [B] (NULL: 1), dividing target and drafter logits; 0 or less: a greedy row.
+ * u: DEVICE f32 [B][T] uniform in [0, 1), u[b][i] decides node i; NULL: every row is greedy, and draft
+ * must be NULL.
  * noise: DEVICE f32 [B][vocab] exponential variates (> 0) for the token after the path; NULL: the
  * likeliest one.
  * With p and q the softmax of target and drafter logits after the path's last node, its children are
@@ -538,7 +539,8 @@ typedef enum { FADE_LOGITS_F16 = 0, FADE_LOGITS_BF16 = 1, FADE_LOGITS_F32 = 2 } 
  * outside [0, vocab) are refused.
  * Writes path: i32 [B][T] (0 past its length), n_path: i32 [B], next: i32 [B] (-1 where there is nothing
  * to draw from: no logit above -inf, or no node and no target_root). fp32 arithmetic in one fixed order.
- * Reads only the logits after kept nodes. 1 <= vocab <= FADE_MAX_VOCAB. */
+ * Only the logits after kept nodes count; those after any node of the tensor may be
+ * read, past n_nodes too. 1 <= vocab <= FADE_MAX_VOCAB. */
 fade_status_t fade_tree_verify(const fade_config_t* cfg, int32_t T, int32_t vocab, int32_t type,
                                const int32_t* parents, const int32_t* n_nodes,
                                const int32_t* tokens, const fade_logits_t* target,

@@ -77,6 +77,8 @@ def test_shapes_types_and_layouts(T, mass):
     _prompt(T, 2, mass, cfg=_cfg(T, num_q_heads=6), q=_z(2, 5, 6, 64), out=_z(2, 5, 6, 64),
             lse=_z(2, 5, 6, dt=torch.float32))                     # 3 query heads a KV head
     if mass:
+        _prompt(T, None, mass, lse=None)
+        _prompt(T, None, mass, mass=None)
         _prompt(T, None, mass, mass=_z(2, 2, 9))
         _prompt(T, None, mass, mass=_z(2, 9, 2, dt=torch.float32).transpose(1, 2))
     else:
@@ -84,6 +86,8 @@ def test_shapes_types_and_layouts(T, mass):
         _prompt(T, None, out=_z(2, 5, 8, 64, dt=torch.float32))
         assert "16-byte" in _prompt(T, 1, out=big[..., :64])
         assert "every token" in _prompt(T, 2, v=_z(2, 1, 2, 64).expand(2, 9, 2, 64))
+        for one in ((1, 5, 8, 64), (2, 1, 8, 64), (2, 5, 1, 64)):   # results over each other
+            assert "share vectors" in _prompt(T, 1, out=_z(*one).expand(2, 5, 8, 64))
 
 
 @pytest.mark.parametrize("mass", [False, True])
@@ -141,6 +145,8 @@ def _verify(T, status, **kw):
 
 def test_verify_refuses(T):
     i32, f32 = torch.int32, torch.float32
+    _verify(T, None, target=None)
+    _verify(T, None, parents=None)
     _verify(T, None, target=_z(2, 5, 40, dt=torch.float64))
     _verify(T, None, target=_z(2, 4, 40))
     _verify(T, None, target=_z(5, 40))

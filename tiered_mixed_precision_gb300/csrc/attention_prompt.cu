@@ -97,19 +97,6 @@ __device__ __forceinline__ void tm_ld_row16(uint32_t addr, float* v) {
       : "r"(addr)
       : "memory");
 }
-// 16 lanes x 32 columns: v[4i .. 4i+1] row lane/4, columns 8i + 2(lane%4) + {0, 1}; v[4i+2 .. 4i+3] the
-// same columns of row lane/4 + 8.
-__device__ __forceinline__ void tm_ld_quads(uint32_t addr, float* v) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(addr)
-      : "memory");
-}
 // Words w[i] of lane k of a quad become words w[k] of lane i.
 __device__ __forceinline__ void transpose_quad(uint32_t (&w)[4]) {
   const int lane = threadIdx.x & 31;
@@ -561,7 +548,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
         for (int q = 0; q < D / 32; ++q) {
           float o[16];
           __syncwarp();
-          tm_ld_quads(tO + ((uint32_t)(16 * f) << 16) + 32 * q, o);
+          tm_ld32(tO + ((uint32_t)(16 * f) << 16) + 32 * q, o);
           tm_wait_ld();
           if (any_bad) {   // what was left out of the products, into the rows that see it
             int slot = 0;
@@ -853,6 +840,9 @@ extern "C" fade_status_t fade_prompt_attention(const fade_config_t* c, const fad
                                   &a.rows);
   if (!st) st = validate_heads(out, "out");
   if (st) return st;
+  if ((out->row_stride == 0 && a.s.B > 1) || (out->token_stride == 0 && n_q > 1) ||
+      (out->head_stride == 0 && a.s.Hq > 1))
+    return set_error(FADE_ERR_INVALID_ARGUMENT, "out: rows, queries or heads share vectors");
   if (!ws || !aligned(ws, 16))
     return set_error(FADE_ERR_INVALID_ARGUMENT, "workspace is NULL or not 16-byte aligned");
   if (!aligned(lse, 4) || !aligned(status, 4))

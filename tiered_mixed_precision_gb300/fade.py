@@ -716,7 +716,7 @@ def fade_tree_verify(cfg: Config, parents, n_nodes, tokens, target, target_root,
     node 0 is certain); draft, draft_root: the drafter's, of the same type (None: drafts without
     probabilities). temperature f32 [B] or None, u f32 [B][T] (None: greedy), noise f32 [B][vocab] or
     None -> path i32 [B][T], n_path i32 [B], next_token i32 [B]."""
-    if target.dim() != 3 or parents.dim() != 2:
+    if target is None or parents is None or target.dim() != 3 or parents.dim() != 2:
         raise ValueError("target must be [rows][nodes][vocabulary], parents [rows][nodes]")
     B, T = cfg.batch, parents.shape[1]
     V = target.shape[2]
@@ -759,9 +759,11 @@ def _host_lens(name, x, rows):
     return x.tobytes()
 
 
-def _prompt_ws(cfg, dev, n_q, n_kv, q, ws):
-    if ws is None:
-        return _torch.empty(fade_prompt_ws_bytes(cfg, n_q, n_kv), dtype=_torch.uint8, device=q.device)
+def _prompt_ws(cfg, dev, n_q, n_kv, q, ws, stream):
+    if ws is None:   # of the stream's own memory: it is given back before the kernels have run
+        with _torch.cuda.stream(stream):
+            return _torch.empty(fade_prompt_ws_bytes(cfg, n_q, n_kv), dtype=_torch.uint8,
+                                device=q.device)
     if not ws.is_contiguous() or (dev is not None and ws.get_device() != dev):
         raise ValueError("ws must be contiguous and on the current CUDA device")
     return ws
@@ -784,7 +786,7 @@ def fade_prompt_attention(cfg: Config, q, k, v, out, lse=None, q_len=None, kv_le
     _tensor(dev, "lse", lse, "float32", shape[:3])
     if status is not None:
         _tensor(dev, "status", status, "int32", (STATUS_WORDS,))
-    ws = _prompt_ws(cfg, dev, n_q, n_kv, q, ws)
+    ws = _prompt_ws(cfg, dev, n_q, n_kv, q, ws, stream)
     _check(lib().fade_prompt_attention(
         ctypes.byref(cfg.c()), hq, hk, hv, n_q, n_kv, _host_lens("q_len", q_len, B),
         _host_lens("kv_len", kv_len, B), n_sink, window, ho,
@@ -803,11 +805,13 @@ def fade_prompt_mass(cfg: Config, q, k, lse, mass, q_len=None, kv_len=None, n_si
     shape = (B, n_q, cfg.num_q_heads, cfg.head_dim)
     hq = _checked_heads(dev, "q", q, shape)
     hk = _checked_heads(dev, "k", k, (B, n_kv, H, cfg.head_dim))
+    if lse is None or mass is None:
+        raise ValueError("lse and mass are needed")
     _tensor(dev, "lse", lse, "float32", shape[:3])
     _tensor(dev, "mass", mass, "float32", (B, H, n_kv))
     if status is not None:
         _tensor(dev, "status", status, "int32", (STATUS_WORDS,))
-    ws = _prompt_ws(cfg, dev, n_q, n_kv, q, ws)
+    ws = _prompt_ws(cfg, dev, n_q, n_kv, q, ws, stream)
     _check(lib().fade_prompt_mass(
         ctypes.byref(cfg.c()), hq, hk, n_q, n_kv, _host_lens("q_len", q_len, B),
         _host_lens("kv_len", kv_len, B), n_sink, window, lse.data_ptr(), int(bool(accumulate)),
