@@ -296,6 +296,36 @@ def test_same_bits_streams_and_graphs(F):
             assert torch.equal(x, y)
 
 
+def test_workspace_made_for_another_stream(F, monkeypatch):
+    """A workspace that a call makes for itself is not given to the current stream while the call's own
+    stream has yet to use it."""
+    cfg, n = _cfg(F, 1, 8, 2, 64), 700
+    q, k, v = _draw((1, n, 8, 64), 1), _draw((1, n, 2, 64), 2), _draw((1, n, 2, 64), 3)
+    want, lse, mass = _check(F, cfg, q, k, v)[:3]
+    out, lse2, mass2 = torch.zeros_like(q), torch.zeros_like(lse), torch.zeros_like(mass)
+    made, empty = [], torch.empty
+
+    def spy(*a, **kw):
+        made.append(empty(*a, **kw))
+        return made[-1]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    monkeypatch.setattr(torch, "empty", spy)
+    ptrs = []
+    for call in (lambda: F.fade_prompt_attention(cfg, q, k, v, out, lse2, stream=side),
+                 lambda: F.fade_prompt_mass(cfg, q, k, lse2, mass2, stream=side)):
+        call()
+        ptrs.append(made[-1].data_ptr())
+        made.clear()
+    monkeypatch.undo()
+    ours = [torch.empty(F.fade_prompt_ws_bytes(cfg, n, n), dtype=torch.uint8, device="cuda")
+            for _ in range(4)]
+    assert not set(ptrs) & {x.data_ptr() for x in ours}
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse2, lse) and torch.equal(mass2, mass)
+
+
 def test_offsets_past_32_bits(F):
     """Tokens 2^25 elements apart: the last ones lie past 2^32 elements."""
     B, hq, h, d, n = 1, 2, 1, 64, 140
