@@ -31,7 +31,7 @@
 namespace fade {
 namespace {
 
-// A row's CTAs, their threads and warps. At 64 rows of 128256 tokens: 77 us, as with 4 CTAs of 512; 8 of
+// A row's CTAs, their threads and warps. At 64 rows of 128256 tokens: 77 us, and with 4 CTAs of 512 the same; 8 of
 // 512 (which leave a row waiting for its place) 94, 2 of 512 or 1024 and 4 of 1024 from 96 to 99.
 constexpr int kCluster = 8, kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBatch = 16;    // values exchanged at once
@@ -90,6 +90,24 @@ __device__ __forceinline__ void logits(const Words<E>& v, bool careful, float (&
 #pragma unroll
     for (int j = 0; j < Vec<E>::N; ++j) y[j] = logit(y[j]);
   }
+}
+
+// The largest of a vector's elements (x: the same, as `logits` gives them); NaN only if all are.
+template <typename E>
+__device__ __forceinline__ float top_of(const Words<E>& w, bool careful, const float (&x)[Vec<E>::N]) {
+  if (sizeof(E) == 4 || careful) {
+    float top = x[0];
+#pragma unroll
+    for (int j = 1; j < Vec<E>::N; ++j) top = fmaxf(top, x[j]);
+    return top;
+  }
+  if constexpr (sizeof(E) == 2) {   // two elements an instruction
+    using E2 = typename std::conditional<std::is_same<E, __half>::value, __half2, __nv_bfloat162>::type;
+    const E2* e = reinterpret_cast<const E2*>(&w.w);
+    const E2 m = __hmax2(__hmax2(e[0], e[1]), __hmax2(e[2], e[3]));
+    return fmaxf(to_float(m.x), to_float(m.y));
+  }
+  return 0.f;
 }
 
 // ---------------------------------------------------------------- cluster
@@ -383,11 +401,18 @@ struct Probs {
 #pragma unroll
       for (int j = 0; j < N; ++j) r[j] = r_of(x[j], Q ? y[j] : 0.f);
     } else {
-      const float qa = qt + la;
+      const f2x c2 = f2_pack(c, c), p2 = f2_pack(pt, pt), q2 = f2_pack(qt + la, qt + la);
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        r[j] = ex2(fmaf(x[j], c, pt));
-        if constexpr (Q) r[j] = fmaxf(r[j] - ex2(fmaf(y[j], c, qa)), 0.f);
+      for (int j = 0; j < N; j += 2) {
+        f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), c2, p2), r[j], r[j + 1]);
+        r[j] = ex2(r[j]);
+        r[j + 1] = ex2(r[j + 1]);
+        if constexpr (Q) {
+          float q[2];
+          f2_unpack(f2_fma(f2_pack(y[j], y[j + 1]), c2, q2), q[0], q[1]);
+          r[j] = fmaxf(r[j] - ex2(q[0]), 0.f);
+          r[j + 1] = fmaxf(r[j + 1] - ex2(q[1]), 0.f);
+        }
       }
     }
   }
@@ -449,9 +474,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
     auto add = [&](float& m, float& s, const Words<E>& w) {
       float x[N];
       logits(w, careful, x);
-      float top = x[0];
-#pragma unroll
-      for (int j = 1; j < N; ++j) top = fmaxf(top, x[j]);
+      const float top = top_of(w, careful, x);
       if (top > m) {
         s *= ex2((m - top) * c);   // (0 from -inf)
         m = top;
@@ -462,9 +485,15 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
 #pragma unroll
         for (int j = 0; j < N; ++j) part[j & 1] += ex2((x[j] - m) * c);
       } else {
-        const float mc = m * c;
+        const f2x c2 = f2_pack(c, c), mc2 = f2_pack(-(m * c), -(m * c));
+        f2x sum = f2_pack(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < N; ++j) part[j & 1] += ex2(fmaf(x[j], c, -mc));
+        for (int j = 0; j < N; j += 2) {
+          float y0, y1;
+          f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), c2, mc2), y0, y1);
+          sum = f2_add(sum, f2_pack(ex2(y0), ex2(y1)));
+        }
+        f2_unpack(sum, part[0], part[1]);
       }
       s += part[0] + part[1];
     };
@@ -639,10 +668,12 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
           row.template sweep<DRAFT, false, 1>(
                 cur, 1, stop,
                 [&](int, const Words<E>(&t)[1], const Words<E>(&d)[1], const float(&)[N]) {
-                  float r[N], part[2] = {0.f, 0.f};
+                  float r[N], part[2];
                   pr.template rest<DRAFT>(t[0], d[0], r);
+                  f2x sum = f2_pack(r[0], r[1]);
 #pragma unroll
-                  for (int j = 0; j < N; ++j) part[j & 1] += r[j];
+                  for (int j = 2; j < N; j += 2) sum = f2_add(sum, f2_pack(r[j], r[j + 1]));
+                  f2_unpack(sum, part[0], part[1]);
                   w.x += part[0] + part[1];
                 },
                 [&](int, float x, float y, float) { w.x += pr.r_of(x, y); }, nothing);
