@@ -12,6 +12,14 @@
 //
 // Roundings to fewer than 32 bits: P to fp16 before it meets V, the output. Products of fp16 operands
 // are exact in fp32, sums are fp32.
+//
+// What bounds it: at d = 128 the tensor cores, which a pair of tiles (256 query rows, 128 tokens) keeps
+// busy for 2048 cycles of the 2700 to 3100 that the softmax's chain takes (wait, read S, maximum,
+// exponentials, write P); at d = 64 the chain, 2300 to 2500 cycles against 1024 of products and as many
+// of exponentials. 32 query and 8 KV heads: 16383 tokens of d = 128 1380 to 1500 us, as the clocks hold
+// (1600 to 1470 TFLOP/s), of d = 64 1066 us; 2 prompts of 32768 tokens under a window of 4160 2.9 to
+// 3.1 ms; 8 prompts of 1024 to 2048 tokens of d = 64 144 us, where an item's start and end weigh as much
+// as its tiles. Single tokens read their keys and values once: 64 rows of 4164 tokens 181 us, 6.0 TB/s.
 #include <math.h>
 
 #include <algorithm>
@@ -129,7 +137,13 @@ __device__ __forceinline__ void tm_st_row16(uint32_t addr, const uint32_t* r) {
 // V tile. Roles meet at mbarriers: one warp loads (bulk tensor copies into a ring of K and V tiles), one
 // for either query tile issues its products, four softmax warps a query tile (a thread a row) turn S
 // into P. The two query tiles run free of each other but for the ring, and an item's first S is issued
-// behind the last P V of the one before, while that one's result is written out.
+// behind the last P V of the one before, while that one's result is written out. The two softmax warps
+// of a scheduler take turns at the exponentials (d = 64, 16383 tokens: 1152 us without, 1123 with). What
+// the loops run by comes from parameters and the block's index alone, which the compiler knows to be the
+// same in a whole warp: with items told through shared memory the same loops took a quarter longer.
+//
+// Twice the softmax warps, in two streams of 64 tokens a query tile (d = 64): 1066 -> 1040 us at 16383
+// tokens, 145 -> 167 at the short prompts, as instructions then fill two thirds of the slots.
 //
 // A value that is infinite or NaN would reach queries that do not see its token (0 * inf), so a warp
 // looks through the V tiles that some query of the block sees only in part, clears such values and
@@ -514,8 +528,8 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
 
       // ---------------------------------------------- the item's result
       // Read so that a quad of lanes holds consecutive channels of a row, and written 64 bytes a row:
-      // with a thread a row, every 16-byte store met 32 lines (64 single-channel tiles of d = 128 took
-      // 5 us to write, 1 us now).
+      // with a thread a row, every 16-byte store met 32 lines (16383 tokens of d = 128: 1455 us, 1403 now;
+      // 8 short prompts of d = 64: 162, 148 now).
       const bool whole = now.n == now.all;
       const uint32_t* bad = sBad + (count % kBadBufs) * (kBadTiles * 4);
       const bool any_bad =
