@@ -62,6 +62,7 @@ struct Args {
   float* part;                   // per CTA two partials: [part_rows][2] (m, L), then [part_rows][D] O
   int32_t* status;
   int part_rows;
+  PromptUnits units;
   PromptSchedule sched;
 };
 
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
   PromptItem it;
   auto next = [&](PromptItem& x) {
     return walk.next(a.sched, gridDim.x, blockIdx.x,
-                     [&](int index) { return prompt_item(s, a.rows, index); }, x);
+                     [&](int index) { return prompt_item(s, a.rows, a.units, index); }, x);
   };
 
   if (warp == 8) {
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(256) prompt_combine_kernel(const __grid_consta
   const PromptShape& s = a.s;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const auto& jn = a.sched.join[blockIdx.x];
-  const PromptItem it = prompt_item(s, a.rows, jn.item);
+  const PromptItem it = prompt_item(s, a.rows, a.units, jn.item);
   const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int tok = it.tok0 + (row >> s.log_g);   // (query tile 1 begins at row 128)
   if (tok >= a.rows.q_len[it.b]) return;
@@ -712,6 +713,7 @@ fade_status_t launch(const fade_config_t* c, Args& a, int blocks, cudaStream_t s
   const int sms = prompt_sms(&device);
   if (sms == 0) return FADE_ERR_CUDA;
   a.part_rows = partial_rows(c, a.s.n_q);
+  a.units.set(a.s);
   int P = 0;
   const int joins = prompt_schedule(a.s, a.rows, blocks, sms, a.sched, &P);
   auto kern = prompt_attention_kernel<D>;

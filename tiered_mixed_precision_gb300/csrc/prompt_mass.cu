@@ -48,6 +48,7 @@ struct Args {
   float* part;      // per CTA two partials of kPair sums
   int32_t* status;
   int add;
+  PromptUnits units;
   PromptSchedule sched;
 };
 
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
   MassItem it;
   auto next = [&]() {
     return walk.next(a.sched, gridDim.x, blockIdx.x,
-                     [&](int index) { return mass_item(s, a.rows, index); }, it);
+                     [&](int index) { return mass_item(s, a.rows, a.units, index); }, it);
   };
 
   if (warp == 16) {
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kPair) prompt_mass_join_kernel(const __grid_co
   const PromptShape& s = a.s;
   const bool shared = (int)blockIdx.x < joins;
   const MassItem it =
-      mass_item(s, a.rows, shared ? a.sched.join[blockIdx.x].item : blockIdx.x - joins);
+      mass_item(s, a.rows, a.units, shared ? a.sched.join[blockIdx.x].item : blockIdx.x - joins);
   const int j = it.k0 + threadIdx.x, kv_len = a.rows.kv_len[it.b];
   float* m = a.mass + ((size_t)it.b * s.H + it.h) * s.n_kv + j;
   if (j >= s.n_kv) return;
@@ -385,6 +386,7 @@ fade_status_t launch(Args& a, cudaStream_t st) {
     opted[device] = true;
   }
   int P = 0;
+  a.units.set(a.s);
   const int joins = mass_schedule(a.s, a.rows, sms, a.sched, &P);
   kern<<<P, Sh::THREADS, Sh::SMEM, st>>>(a);
   fade_status_t s = launch_status("fade_prompt_mass");

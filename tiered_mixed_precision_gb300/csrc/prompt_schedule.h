@@ -83,13 +83,46 @@ FADE_SCHED PromptItem prompt_block(const PromptShape& s, int b, int q_len, int k
   it.n = it.all = it.sinks + it.p1 / kPromptTile - it.lo + 1;
   return it;
 }
+// x / d for 0 <= x < 2^31 by a multiplication (Granlund and Montgomery): a division by what only the
+// host knows takes longer than the rest of an item, and a CTA's next item is waited for.
+struct PromptDivisor {
+  int d, shift;
+  uint32_t mul;
+  void set(int by) {
+    d = by;
+    for (shift = 0; (1LL << shift) < by; ++shift) {
+    }
+    mul = (uint32_t)((((1ULL << shift) - by) << 32) / by + 1);
+  }
+  FADE_SCHED int of(int x) const {
+#ifdef __CUDA_ARCH__
+    const uint32_t high = __umulhi((uint32_t)x, mul);
+#else
+    const uint32_t high = (uint32_t)(((uint64_t)(uint32_t)x * mul) >> 32);
+#endif
+    return (int)((high + (uint32_t)x) >> shift);
+  }
+};
+struct PromptUnits {
+  PromptDivisor all, heads;   // by B H, by H
+  void set(const PromptShape& s) {
+    all.set(s.B * s.H);
+    heads.set(s.H);
+  }
+};
 // Items by rank, then row (in their order by length), then head.
-FADE_SCHED PromptItem prompt_item(const PromptShape& s, const PromptRows& rows, int index) {
-  const int units = s.B * s.H, rank = index / units, u = index - rank * units;
-  const int row = u / s.H, b = rows.order[row];
+FADE_SCHED PromptItem prompt_item(const PromptShape& s, const PromptRows& rows, const PromptUnits& n,
+                                  int index) {
+  const int rank = n.all.of(index), u = index - rank * n.all.d;
+  const int row = n.heads.of(u), b = rows.order[row];
   PromptItem it = prompt_block(s, b, rows.q_len[b], rows.kv_len[b], rank);
   it.h = u - row * s.H;
   return it;
+}
+inline PromptItem prompt_item(const PromptShape& s, const PromptRows& rows, int index) {
+  PromptUnits n;
+  n.set(s);
+  return prompt_item(s, rows, n, index);
 }
 // Two tiles of 128 keys of a unit, and the query tiles [begin, begin + n) that meet them; `all` of them
 // do, from the first-th on.
@@ -99,8 +132,9 @@ struct MassItem {
   int first, begin, n, all;
 };
 // Items by pair of key tiles, then row (in their order by length), then head.
-FADE_SCHED MassItem mass_item(const PromptShape& s, const PromptRows& rows, int index) {
-  const int units = s.B * s.H, pair = index / units, u = index - pair * units, row = u / s.H;
+FADE_SCHED MassItem mass_item(const PromptShape& s, const PromptRows& rows, const PromptUnits& n,
+                              int index) {
+  const int pair = n.all.of(index), u = index - pair * n.all.d, row = n.heads.of(u);
   const int per = kPromptTile >> s.log_g;
   MassItem it;
   it.b = rows.order[row];
@@ -119,6 +153,12 @@ FADE_SCHED MassItem mass_item(const PromptShape& s, const PromptRows& rows, int 
   it.first = from / per;
   it.n = it.all = it.k0 < kv_len && from <= to ? to / per - it.first + 1 : 0;
   return it;
+}
+
+inline MassItem mass_item(const PromptShape& s, const PromptRows& rows, int index) {
+  PromptUnits n;
+  n.set(s);
+  return mass_item(s, rows, n, index);
 }
 
 // A CTA's items one after another: whole ones, forth and back over the CTAs so that the order by length
@@ -245,8 +285,10 @@ constexpr int kCostStart = 8, kCostTwo = 4, kCostOne = 3;
 
 inline int prompt_schedule(const PromptShape& s, const PromptRows& rows, int blocks, int sms,
                            PromptSchedule& a, int* ctas) {
+  PromptUnits n;
+  n.set(s);
   auto work = [&](int index) {
-    const PromptItem it = prompt_item(s, rows, index);
+    const PromptItem it = prompt_item(s, rows, n, index);
     return PromptWork{it.all, it.all == 0 || it.active == 2 ? kCostTwo : kCostOne, kCostStart};
   };
   return prompt_deal(blocks * s.B * s.H, s.H, sms, true, work, a, ctas);
@@ -256,8 +298,10 @@ inline int mass_schedule(const PromptShape& s, const PromptRows& rows, int sms, 
   const int pairs = (s.n_kv + 2 * kPromptTile - 1) / (2 * kPromptTile);
   // a pair's first 2 G tiles hide some keys from some queries, which costs half as much again; so do
   // all of a pair with sinks and other tokens (one of its two key tiles, mostly)
+  PromptUnits n;
+  n.set(s);
   auto work = [&](int index) {
-    const MassItem it = mass_item(s, rows, index);
+    const MassItem it = mass_item(s, rows, n, index);
     return PromptWork{it.all, s.sight.window && it.k0 < s.sight.sink ? 10 : 8, 16 + 8 * s.G};
   };
   return prompt_deal(pairs * s.B * s.H, s.H, sms, false, work, a, ctas);
