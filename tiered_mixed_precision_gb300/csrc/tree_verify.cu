@@ -120,11 +120,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile(
       "barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -143,31 +138,85 @@ __device__ __forceinline__ void st_remote(uint32_t at, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
-// Every CTA's share of the row's answer. Kinds of values that are reduced, four floats each.
-struct Stats {   // maximum and sum of 2^((x - maximum) c), of target and drafter
+// Kinds of values that are reduced, up to four floats each: two joined, a warp's (over groups of `width`
+// lanes, in all of which it ends), or the CTAs' of a cluster in their order.
+__device__ __forceinline__ float other(float x, int o) { return __shfl_xor_sync(~0u, x, o); }
+template <bool TWO>
+struct Stats {   // maximum and sum of 2^((x - maximum) c), of the target and (TWO) the drafter
   float c;
+  __device__ __forceinline__ float share(float m, float top) const {   // of a sum that goes with m
+    return top == -INFINITY ? 1.f : ex2((m - top) * c);                // (all empty, sums of 0)
+  }
   __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) const {
     const float n = fmaxf(m, m2);
-    if (n == -INFINITY) return;   // both empty
-    s = (m == n ? s : s * ex2((m - n) * c)) + (m2 == n ? s2 : s2 * ex2((m2 - n) * c));
+    s = s * share(m, n) + s2 * share(m2, n);
     m = n;
   }
   __device__ __forceinline__ float4 operator()(float4 a, float4 b) const {
     join(a.x, a.y, b.x, b.y);
-    join(a.z, a.w, b.z, b.w);
+    if (TWO) join(a.z, a.w, b.z, b.w);
     return a;
+  }
+  __device__ __forceinline__ float4 over(float4 v, int width) const {
+    float m = v.x, n = v.z;
+    for (int o = width / 2; o; o >>= 1) {
+      m = fmaxf(m, other(m, o));
+      if (TWO) n = fmaxf(n, other(n, o));
+    }
+    v.y *= share(v.x, m);
+    if (TWO) v.w *= share(v.z, n);
+    for (int o = width / 2; o; o >>= 1) {
+      v.y += other(v.y, o);
+      if (TWO) v.w += other(v.w, o);
+    }
+    v.x = m;
+    v.z = n;
+    return v;
+  }
+  __device__ __forceinline__ float4 all(const float4 (&v)[kCluster]) const {
+    float4 r = v[0];
+#pragma unroll
+    for (int i = 1; i < kCluster; ++i) {
+      r.x = fmaxf(r.x, v[i].x);
+      if (TWO) r.z = fmaxf(r.z, v[i].z);
+    }
+    r.y *= share(v[0].x, r.x);
+    if (TWO) r.w *= share(v[0].z, r.z);
+#pragma unroll
+    for (int i = 1; i < kCluster; ++i) {
+      r.y += v[i].y * share(v[i].x, r.x);
+      if (TWO) r.w += v[i].w * share(v[i].z, r.z);
+    }
+    return r;
   }
 };
 struct Sum {
-  __device__ __forceinline__ float4 operator()(float4 a, float4 b) const {
-    a.x += b.x;
-    return a;
+  __device__ __forceinline__ float4 over(float4 v, int width) const {
+    for (int o = width / 2; o; o >>= 1) v.x += other(v.x, o);
+    return v;
+  }
+  __device__ __forceinline__ float4 all(const float4 (&v)[kCluster]) const {
+    float4 r = v[0];
+#pragma unroll
+    for (int i = 1; i < kCluster; ++i) r.x += v[i].x;
+    return r;
   }
 };
 struct Best {   // the larger value, the lower index where they are equal (y: the index's bits)
   __device__ __forceinline__ float4 operator()(float4 a, float4 b) const {
     const bool take = b.x > a.x || (b.x == a.x && __float_as_int(b.y) < __float_as_int(a.y));
     return take ? b : a;
+  }
+  __device__ __forceinline__ float4 over(float4 v, int width) const {
+    for (int o = width / 2; o; o >>= 1)
+      v = (*this)(v, make_float4(other(v.x, o), other(v.y, o), 0.f, 0.f));
+    return v;
+  }
+  __device__ __forceinline__ float4 all(const float4 (&v)[kCluster]) const {
+    float4 r = v[0];
+#pragma unroll
+    for (int i = 1; i < kCluster; ++i) r = (*this)(r, v[i]);
+    return r;
   }
 };
 
@@ -185,37 +234,28 @@ struct Shared {
   int32_t refused[FADE_TREE_MAX_NODES];
 };
 
-template <class Op>
-__device__ __forceinline__ float4 warp_reduce(float4 v, const Op& op, int width) {
-  for (int o = width / 2; o; o >>= 1)
-    v = op(v, make_float4(__shfl_xor_sync(~0u, v.x, o), __shfl_xor_sync(~0u, v.y, o),
-                          __shfl_xor_sync(~0u, v.z, o), __shfl_xor_sync(~0u, v.w, o)));
-  return v;
-}
 // A thread's value joined over its warp, kept as the i-th.
 template <class Op>
 __device__ __forceinline__ void keep(Shared& sh, int i, float4 v, const Op& op) {
-  v = warp_reduce(v, op, 32);
+  v = op.over(v, 32);
   if ((threadIdx.x & 31) == 0) sh.warps[i][threadIdx.x >> 5] = v;
 }
 // The values 0 .. count - 1 joined over the whole cluster, from then on in sh.ranks (exchanged).
 template <class Op>
 __device__ __forceinline__ void exchange(Shared& sh, int count, const Op& op, int& turn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t rank = cluster_rank(), size = cluster_size();
+  const uint32_t rank = cluster_rank();
   __syncthreads();
   for (int i = warp; i < count; i += kWarps) {   // (every eight lanes have all of them)
-    const float4 v = warp_reduce(sh.warps[i][lane & (kWarps - 1)], op, kWarps);
-    if (lane < size) st_remote4(remote(&sh.ranks[turn][i][rank], lane), v);
+    const float4 v = op.over(sh.warps[i][lane & (kWarps - 1)], kWarps);
+    if (lane < kCluster) st_remote4(remote(&sh.ranks[turn][i][rank], lane), v);
   }
   cluster_sync();
   turn ^= 1;
 }
 template <class Op>
 __device__ __forceinline__ float4 exchanged(const Shared& sh, int i, const Op& op, int turn) {
-  float4 v = sh.ranks[turn ^ 1][i][0];
-  for (uint32_t r = 1; r < cluster_size(); ++r) v = op(v, sh.ranks[turn ^ 1][i][r]);
-  return v;
+  return op.all(sh.ranks[turn ^ 1][i]);
 }
 // The i-th value of this CTA, whole as it is, handed to every CTA as the cluster's to[i], i < count <= 2.
 template <class Op>
@@ -224,8 +264,8 @@ __device__ __forceinline__ void hand_out(Shared& sh, int count, int first, int a
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
   if (warp < count) {
-    const float4 v = warp_reduce(sh.warps[warp][lane & (kWarps - 1)], op, kWarps);
-    if (lane < cluster_size()) st_remote4(remote(&sh.ranks[turn][first + warp * apart][0], lane), v);
+    const float4 v = op.over(sh.warps[warp][lane & (kWarps - 1)], kWarps);
+    if (lane < kCluster) st_remote4(remote(&sh.ranks[turn][first + warp * apart][0], lane), v);
   }
   cluster_sync();
   turn ^= 1;
@@ -428,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
   __shared__ Shared sh;
   extern __shared__ uint4 slots[];   // [kSlots][threads]
   const int tid = threadIdx.x;
-  const uint32_t rank = cluster_rank(), size = cluster_size();
+  const uint32_t rank = cluster_rank();
+  constexpr int size = kCluster;
   const int b = blockIdx.x / size;
   const Row<E, DRAFT> row{a, b, (int)(rank * kThreads + tid), (int)(size * kThreads),
                           smem_u32(slots + tid)};
@@ -444,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
   const float4 none = make_float4(0.f, __int_as_float(0x7fffffff), 0.f, 0.f);
   auto look = [&](const Row<E, DRAFT>& row, int at, int most, auto then, bool greedy, float c,
                   bool careful) {
-    const Stats join{c};
+    const Stats<DRAFT> join{c};
     if (greedy) {
       float4 best = none;
       best.x = -INFINITY;
@@ -550,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
   // nodes cur, cur + 1, .. looked at, and their values exchanged
   auto look_on = [&](bool greedy, float c, auto before) {
     const int count = min(most, a.T - cur);
-    const Stats join{c};
+    const Stats<DRAFT> join{c};
     const bool apart = count >= kCluster / 2;
     const int mine = apart ? ((int)rank < count) + ((int)(rank + size) < count) : 0;
     if (!apart)
@@ -583,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
   look_on(!(own_temp > 0.f), scale_of(own_temp), [&]() {
     __syncwarp();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    for (uint32_t r = 0; r < size; ++r) {
+    for (int r = 0; r < size; ++r) {
       if (mine) {
         st_remote(remote(&sh.parent[tid], r), parent);
         st_remote(remote(&sh.token[tid], r), token);
@@ -600,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
   const int n = sh.n;
   const bool greedy = !(sh.temperature > 0.f);
   const float c = scale_of(sh.temperature);
-  const Stats join{c};
+  const Stats<DRAFT> join{c};
   if (tid < n)
     atomicOr(reinterpret_cast<unsigned long long*>(&sh.kids[sh.parent[tid] + 1]), 1ull << tid);
   __syncthreads();
