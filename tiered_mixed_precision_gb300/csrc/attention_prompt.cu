@@ -18,8 +18,8 @@
 // exponentials, write P); at d = 64 the chain, 2300 to 2500 cycles against 1024 of products and as many
 // of exponentials. 32 query and 8 KV heads: 16383 tokens of d = 128 1380 to 1500 us, as the clocks hold
 // (1600 to 1470 TFLOP/s), of d = 64 1066 us; 2 prompts of 32768 tokens under a window of 4160 2.9 to
-// 3.1 ms; 8 prompts of 1024 to 2048 tokens of d = 64 144 us, where an item's start and end weigh as much
-// as its tiles. Single tokens read their keys and values once: 64 rows of 4164 tokens 181 us, 6.0 TB/s.
+// 3.1 ms; 8 prompts of 1024 to 2048 tokens of d = 64 135 us, where an item's start and end cost
+// as much as three of its six to eight tiles. Single tokens read their keys and values once: 64 rows of 4164 tokens 181 us, 6.0 TB/s.
 #include <math.h>
 
 #include <algorithm>

@@ -13,8 +13,8 @@
 //
 // What bounds it: instruction issue, 0.66 to 0.70 a cycle and scheduler. Of some 260 instructions of a
 // warp and tile, 140 are the 64 exponentials, their scaling and their sums. 32 query and 8 KV heads: 8
-// prompts of 1024 to 2048 tokens of d = 64 95 us (the exponentials alone, 32 a clock and SM: 37); 32768
-// tokens of d = 128 under a window of 4160 864 to 1050 us, as the clocks hold (1210 to 1000 TFLOP/s).
+// prompts of 1024 to 2048 tokens of d = 64 94 us (the exponentials alone, 32 a clock and SM: 37); 32768
+// tokens of d = 128 under a window of 4160 865 to 1050 us, as the clocks hold (1210 to 1000 TFLOP/s).
 #include <math.h>
 
 #include <algorithm>

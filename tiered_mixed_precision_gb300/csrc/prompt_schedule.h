@@ -84,7 +84,8 @@ FADE_SCHED PromptItem prompt_block(const PromptShape& s, int b, int q_len, int k
   return it;
 }
 // x / d for 0 <= x < 2^31 by a multiplication (Granlund and Montgomery): a division by what only the
-// host knows takes longer than the rest of an item, and a CTA's next item is waited for.
+// host knows takes longer than the rest of an item, and a CTA's next item is waited for (8 short prompts
+// of d = 64: attention 145 -> 136 us, mass 95.5 -> 94).
 struct PromptDivisor {
   int d, shift;
   uint32_t mul;

@@ -21,7 +21,7 @@
 // same numbers. Where all nodes' logits are little to read, their maxima and sums are taken in one pass
 // at the start, which leaves the chain one exchange. A pass costs its vectors (words come by asynchronous
 // copies, several vectors ahead: 100 us from registers, 77 so, at 64 trees of 128256 tokens) and 2 to 4 us
-// of reduction, exchange and waiting for the cluster's slowest: 64 trees of 16 nodes 74 us, 16 chains of 8
+// of reduction, exchange and waiting for the cluster's slowest: 64 trees of 16 nodes 66 us, 16 chains of 8
 // nodes over 50257 tokens 21 us, one greedy chain of 5 over 32000 10 us, of which a launch is half.
 #include <cuda_bf16.h>
 #include <math.h>
@@ -34,11 +34,12 @@
 namespace fade {
 namespace {
 
-// A row's CTAs, their threads and warps. At 64 rows of 128256 tokens 77 us (74 with two logits an
-// instruction), and with 4 CTAs of 512 the same; 8 of 512 (which leave a row waiting for its place) 94,
-// 2 of 512 or 1024 and 4 of 1024 from 96 to 99.
+// A row's CTAs, their threads and warps. At 64 rows of 128256 tokens 77 us (66 since, by other steps),
+// and with 4 CTAs of 512 the same; 8 of 512 (which leave a row waiting for its place) 94, 2 of 512 or
+// 1024 and 4 of 1024 from 96 to 99.
 constexpr int kCluster = 8, kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBatch = 16;    // values exchanged at once
+static_assert(kBatch <= 2 * kCluster && (kWarps & (kWarps - 1)) == 0 && kWarps <= 32, "hand_out, over");
 constexpr int kNodes = FADE_TREE_MAX_NODES + 1;   // the root first
 constexpr long long kAheadBytes = 64ll << 20;   // logits of all rows and nodes that are looked at ahead
 constexpr float kLog2e = 1.4426950408889634f;
@@ -139,7 +140,8 @@ __device__ __forceinline__ void st_remote(uint32_t at, uint32_t v) {
 }
 
 // Kinds of values that are reduced, up to four floats each: two joined, a warp's (over groups of `width`
-// lanes, in all of which it ends), or the CTAs' of a cluster in their order.
+// lanes, in all of which it ends), or the CTAs' of a cluster in their order. Maxima come first and every
+// sum is scaled once (scaled at each of a warp's five steps: 74 us at 64 trees, 66 now).
 __device__ __forceinline__ float other(float x, int o) { return __shfl_xor_sync(~0u, x, o); }
 template <bool TWO>
 struct Stats {   // maximum and sum of 2^((x - maximum) c), of the target and (TWO) the drafter
