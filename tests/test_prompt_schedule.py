@@ -235,3 +235,34 @@ def test_balance(run, name, args, slack):
     """The largest share of tiles is near the mean of tiles and items' starts."""
     P, joins, whole, mean, most, largest = run(*args)
     assert most <= slack * mean + 16, (name, P, joins, whole, mean, most, largest)
+
+
+def test_divisor(tmp_path):
+    """Divisions by multiplication, at multiples, their neighbours and the ends of the range."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    (tmp_path / "main.cpp").write_text(r"""
+#include <stdio.h>
+#include "prompt_schedule.h"
+int main() {
+  const int last = 0x7fffffff;
+  for (int d = 1; d <= 65536; d += d < 2100 ? 1 : 61) {
+    fade::PromptDivisor by;
+    by.set(d);
+    unsigned seed = d;
+    for (int i = 0; i < 600; ++i) {
+      seed = seed * 1664525u + 1013904223u;
+      const int q = (int)(seed >> 1) / d, x = q * d;
+      for (int y : {x, x - 1, (int)(seed >> 1), i, last - i})
+        if (y >= 0 && by.of(y) != y / d) return printf("%d / %d\n", y, d), 1;
+    }
+  }
+  return 0;
+}
+""")
+    subprocess.run([gxx, "-O1", "-std=c++17", "-Wall", "-Werror",
+                    f"-I{ROOT}/tiered_mixed_precision_gb300/csrc", f"-I{ROOT}/include",
+                    str(tmp_path / "main.cpp"), "-o", str(tmp_path / "main")], check=True)
+    r = subprocess.run([str(tmp_path / "main")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout

@@ -282,7 +282,7 @@ int prompt_deal(int items, int group, int sms, bool rounds, const F& work, Promp
 
 // What an item of the attention costs, in quarters of a tile of two query tiles: its tiles, and its
 // start and end.
-constexpr int kCostStart = 8, kCostTwo = 4, kCostOne = 3;
+constexpr int kCostStart = 12, kCostTwo = 4, kCostOne = 3;
 
 inline int prompt_schedule(const PromptShape& s, const PromptRows& rows, int blocks, int sms,
                            PromptSchedule& a, int* ctas) {
