@@ -16,10 +16,11 @@
 // What bounds it: at d = 128 the tensor cores, which a pair of tiles (256 query rows, 128 tokens) keeps
 // busy for 2048 cycles of the 2700 to 3100 that the softmax's chain takes (wait, read S, maximum,
 // exponentials, write P); at d = 64 the chain, 2300 to 2500 cycles against 1024 of products and as many
-// of exponentials. 32 query and 8 KV heads: 16383 tokens of d = 128 1380 to 1500 us, as the clocks hold
-// (1600 to 1470 TFLOP/s), of d = 64 1066 us; 2 prompts of 32768 tokens under a window of 4160 2.9 to
-// 3.1 ms; 8 prompts of 1024 to 2048 tokens of d = 64 135 us, where an item's start and end cost
-// as much as three of its six to eight tiles. Single tokens read their keys and values once: 64 rows of 4164 tokens 181 us, 6.0 TB/s.
+// of exponentials. 32 query and 8 KV heads: 16383 tokens of d = 128 1330 to 1500 us, as the clocks hold
+// (1650 to 1470 TFLOP/s), of d = 64 1068 us; 2 prompts of 32768 tokens under a window of 4160 2.9 to
+// 3.1 ms; 8 prompts of 1024 to 2048 tokens of d = 64 132 us, where an item's start and end cost as much
+// as three of its six to eight tiles. Single tokens read their keys and values once: 64 rows of 4164
+// tokens 181 us, 6.0 TB/s.
 #include <math.h>
 
 #include <algorithm>
@@ -220,185 +221,191 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
                      [&](int index) { return prompt_item(s, a.rows, a.units, index); }, x);
   };
 
-  if (warp == 8) {
-    // ================================================================ loads
-    const bool issuer = elect_one();
-    const int per = kTile >> s.log_g;
-    int seq = 0, q_uses[2] = {0, 0};
+  // The softmax's warps take registers from the others: 4 x 80 + 8 x 208 of 12 x 168 a lane. What they
+  // spilled otherwise lay in an item's end (d = 128, 8 short prompts: 172 us without, 157 with).
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 8) {
+      // ================================================================ loads
+      const bool issuer = elect_one();
+      const int per = kTile >> s.log_g;
+      int seq = 0, q_uses[2] = {0, 0};
 #pragma unroll 1
-    while (next(it)) {
+      while (next(it)) {
 #pragma unroll 1
-      for (int j = 0; j < it.n; ++j) {
-        const int kt = it.tile(j);
-        const bool masked = is_masked(s.sight, it, kt);
+        for (int j = 0; j < it.n; ++j) {
+          const int kt = it.tile(j);
+          const bool masked = is_masked(s.sight, it, kt);
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++seq) {
-          const int st = seq % NS, use = seq / NS;
-          if (use > 0) wait(empty + 8 * st, use - 1);
+          for (int kv = 0; kv < 2; ++kv, ++seq) {
+            const int st = seq % NS, use = seq / NS;
+            if (use > 0) wait(empty + 8 * st, use - 1);
+            if (issuer) {
+              const uint32_t bar = (kv && masked ? loaded : full) + 8 * st;
+              mbar_expect_tx(bar, Sh::TILE);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                load_box(ring + st * Sh::TILE + c * kBlk, kv ? &a.v : &a.k, 64 * c, kt * kTile,
+                         it.h * s.kv_head[kv], it.b * s.kv_row[kv], bar);
+            }
+            __syncwarp();
+          }
+          if (j > 0) continue;
+          // Q after the item's first tiles, whose copies need not wait for the last item
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t >= it.active) break;
+            const int buf = 2 * (q_uses[t] % QB) + t, use = q_uses[t] / QB;
+            ++q_uses[t];
+            if (use > 0) wait(qFree + 8 * buf, use - 1);
+            if (issuer) {
+              mbar_expect_tx(qFull + 8 * buf, Sh::TILE);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                load_box(sQ + buf * Sh::TILE + c * kBlk, &a.q, 64 * c, it.h * s.G, it.tok0 + t * per,
+                         it.b * s.q_row, qFull + 8 * buf);
+            }
+            __syncwarp();
+          }
+        }
+      }
+    } else if (warp == 9 || warp == 10) {
+      // ================================================================ products of query tile t
+      const bool issuer = elect_one();
+      const int t = warp - 9;
+      const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(ring, 16, 1024);
+      const uint64_t dV = smem_desc(ring, kBlk, 1024);
+      const uint32_t tS = tm + 128 * t, tO = tm + 256 + D * t, tP = Sh::OVER ? tS : tm + 384 + 64 * t;
+      constexpr uint32_t kStage = Sh::TILE >> 4;
+      int seq = 0, q_uses = 0, n_s = 0, n_p = 0;   // S issued, P taken
+#pragma unroll 1
+      while (next(it)) {
+        if (t >= it.active) {   // (full first: a stage's next use has then begun)
+#pragma unroll 1
+          for (int j = 0; j < 2 * it.n; ++j, ++seq) {
+            wait(full + 8 * (seq % NS), seq / NS);
+            if (issuer) mbar_arrive(empty + 8 * (seq % NS));
+            __syncwarp();
+          }
+          continue;
+        }
+        const int buf = 2 * (q_uses % QB) + t;
+        wait(qFull + 8 * buf, q_uses / QB);
+        ++q_uses;
+        auto issue_s = [&](int at, bool last) {   // S = Q K^T of the tile whose K is at ring place `at`
+          wait(full + 8 * (at % NS), at / NS);
+          if (!Sh::OVER && n_s > 0) wait(sRead + 8 * t, n_s - 1);
+          ++n_s;
+          fence_after();
           if (issuer) {
-            const uint32_t bar = (kv && masked ? loaded : full) + 8 * st;
-            mbar_expect_tx(bar, Sh::TILE);
+            const uint64_t q = dQ + buf * kStage, kk = dK + (at % NS) * kStage;
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              load_box(ring + st * Sh::TILE + c * kBlk, kv ? &a.v : &a.k, 64 * c, kt * kTile,
-                       it.h * s.kv_head[kv], it.b * s.kv_row[kv], bar);
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t off = ((i >> 2) * kBlk + (i & 3) * 32) >> 4;
+              mma_ss(tS, q + off, kk + off, instr_desc(kTile, false), i > 0);
+            }
+            mma_commit(sFull + 8 * t);
+            mma_commit(empty + 8 * (at % NS));
+            if (last) mma_commit(qFree + 8 * buf);
           }
           __syncwarp();
-        }
-        if (j > 0) continue;
-        // Q after the item's first tiles, whose copies need not wait for the last item
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t >= it.active) break;
-          const int buf = 2 * (q_uses[t] % QB) + t, use = q_uses[t] / QB;
-          ++q_uses[t];
-          if (use > 0) wait(qFree + 8 * buf, use - 1);
+        };
+        issue_s(seq, it.n == 1);
+#pragma unroll 1
+        for (int j = 0; j < it.n; ++j, seq += 2) {
+          const int sv = (seq + 1) % NS;
+          const bool more = j + 1 < it.n;
+          if (!Sh::OVER && more) issue_s(seq + 2, j + 2 == it.n);
+          wait(full + 8 * sv, (seq + 1) / NS);
+          wait(pFull + 8 * t, n_p++);
+          fence_after();
           if (issuer) {
-            mbar_expect_tx(qFull + 8 * buf, Sh::TILE);
+            const uint64_t v = dV + sv * kStage;
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              load_box(sQ + buf * Sh::TILE + c * kBlk, &a.q, 64 * c, it.h * s.G, it.tok0 + t * per,
-                       it.b * s.q_row, qFull + 8 * buf);
+            for (int i = 0; i < kTile / 16; ++i)
+              mma_ts(tO, tP + 8 * i, v + ((i * 2048) >> 4), instr_desc(D, true), j > 0 || i > 0);
+            mma_commit(oDone + 8 * t);
+            mma_commit(empty + 8 * sv);
           }
           __syncwarp();
+          if (Sh::OVER && more) issue_s(seq + 2, j + 2 == it.n);
         }
       }
-    }
-  } else if (warp == 9 || warp == 10) {
-    // ================================================================ products of query tile t
-    const bool issuer = elect_one();
-    const int t = warp - 9;
-    const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(ring, 16, 1024);
-    const uint64_t dV = smem_desc(ring, kBlk, 1024);
-    const uint32_t tS = tm + 128 * t, tO = tm + 256 + D * t, tP = Sh::OVER ? tS : tm + 384 + 64 * t;
-    constexpr uint32_t kStage = Sh::TILE >> 4;
-    int seq = 0, q_uses = 0, n_s = 0, n_p = 0;   // S issued, P taken
+    } else {
+      // ================================================================ values that are not finite
+      uint32_t phases = 0, dirty = 0;   // of `loaded`, a bit a stage; buffers that hold marks
+      int seq = 0, count = 0;
 #pragma unroll 1
-    while (next(it)) {
-      if (t >= it.active) {   // (full first: a stage's next use has then begun)
-#pragma unroll 1
-        for (int j = 0; j < 2 * it.n; ++j, ++seq) {
-          wait(full + 8 * (seq % NS), seq / NS);
-          if (issuer) mbar_arrive(empty + 8 * (seq % NS));
-          __syncwarp();
-        }
-        continue;
-      }
-      const int buf = 2 * (q_uses % QB) + t;
-      wait(qFull + 8 * buf, q_uses / QB);
-      ++q_uses;
-      auto issue_s = [&](int at, bool last) {   // S = Q K^T of the tile whose K is at ring place `at`
-        wait(full + 8 * (at % NS), at / NS);
-        if (!Sh::OVER && n_s > 0) wait(sRead + 8 * t, n_s - 1);
-        ++n_s;
-        fence_after();
-        if (issuer) {
-          const uint64_t q = dQ + buf * kStage, kk = dK + (at % NS) * kStage;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t off = ((i >> 2) * kBlk + (i & 3) * 32) >> 4;
-            mma_ss(tS, q + off, kk + off, instr_desc(kTile, false), i > 0);
+      for (; next(it); ++count) {
+        const int buf = count % kBadBufs;
+        uint32_t* bad = sBad + buf * (kBadTiles * 4);
+        bool ready = false;
+        auto own = [&]() {   // the buffer's last user is done with it (a bounded wait)
+          if (!ready && count >= kBadBufs) {
+            const long long t0 = clock64();
+            while (!*sDead && __any_sync(0xffffffffu, sDone[lane & 7] <= count - kBadBufs))
+              if (clock64() - t0 > kWaitCycles) *sDead = 1;
           }
-          mma_commit(sFull + 8 * t);
-          mma_commit(empty + 8 * (at % NS));
-          if (last) mma_commit(qFree + 8 * buf);
-        }
-        __syncwarp();
-      };
-      issue_s(seq, it.n == 1);
-#pragma unroll 1
-      for (int j = 0; j < it.n; ++j, seq += 2) {
-        const int sv = (seq + 1) % NS;
-        const bool more = j + 1 < it.n;
-        if (!Sh::OVER && more) issue_s(seq + 2, j + 2 == it.n);
-        wait(full + 8 * sv, (seq + 1) / NS);
-        wait(pFull + 8 * t, n_p++);
-        fence_after();
-        if (issuer) {
-          const uint64_t v = dV + sv * kStage;
-#pragma unroll
-          for (int i = 0; i < kTile / 16; ++i)
-            mma_ts(tO, tP + 8 * i, v + ((i * 2048) >> 4), instr_desc(D, true), j > 0 || i > 0);
-          mma_commit(oDone + 8 * t);
-          mma_commit(empty + 8 * sv);
-        }
-        __syncwarp();
-        if (Sh::OVER && more) issue_s(seq + 2, j + 2 == it.n);
-      }
-    }
-  } else if (warp == 11) {
-    // ================================================================ values that are not finite
-    uint32_t phases = 0, dirty = 0;   // of `loaded`, a bit a stage; buffers that hold marks
-    int seq = 0, count = 0;
-#pragma unroll 1
-    for (; next(it); ++count) {
-      const int buf = count % kBadBufs;
-      uint32_t* bad = sBad + buf * (kBadTiles * 4);
-      bool ready = false;
-      auto own = [&]() {   // the buffer's last user is done with it (a bounded wait)
-        if (!ready && count >= kBadBufs) {
-          const long long t0 = clock64();
-          while (!*sDead && __any_sync(0xffffffffu, sDone[lane & 7] <= count - kBadBufs))
-            if (clock64() - t0 > kWaitCycles) *sDead = 1;
-        }
-        ready = true;
-      };
-      if ((dirty >> buf) & 1) {
-        own();
-        bad[lane] = 0;
-        dirty &= ~(1u << buf);
-        __syncwarp();
-      }
-      int slot = 0;
-#pragma unroll 1
-      for (int j = 0; j < it.n; ++j, seq += 2) {
-        if (!is_masked(s.sight, it, it.tile(j))) continue;
-        const int st = (seq + 1) % NS;
-        wait(loaded + 8 * st, (phases >> st) & 1);
-        phases ^= 1u << st;
-        uint4* tile = reinterpret_cast<uint4*>(tiles + st * Sh::TILE);
-#pragma unroll 1
-        for (int i0 = lane; i0 < Sh::TILE / 16; i0 += 8 * 32) {
-          uint32_t inf[8];
-          uint4 x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = tile[i0 + 32 * e];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            auto f = [](uint32_t w) { return (w & 0x7c007c00u) + 0x04000400u; };
-            inf[e] = (f(x[e].x) | f(x[e].y) | f(x[e].z) | f(x[e].w)) & 0x80008000u;
-          }
-          if (!__any_sync(0xffffffffu, inf[0] | inf[1] | inf[2] | inf[3] | inf[4] | inf[5] | inf[6] |
-                                           inf[7]))
-            continue;
+          ready = true;
+        };
+        if ((dirty >> buf) & 1) {
           own();
-          dirty |= 1u << buf;
+          bad[lane] = 0;
+          dirty &= ~(1u << buf);
+          __syncwarp();
+        }
+        int slot = 0;
 #pragma unroll 1
-          for (int e = 0; e < 8; ++e) {
-            const int i = i0 + 32 * e, row = (i >> 3) & 127;
-            uint32_t w[4] = {tile[i].x, tile[i].y, tile[i].z, tile[i].w};
-            bool any = false;
+        for (int j = 0; j < it.n; ++j, seq += 2) {
+          if (!is_masked(s.sight, it, it.tile(j))) continue;
+          const int st = (seq + 1) % NS;
+          wait(loaded + 8 * st, (phases >> st) & 1);
+          phases ^= 1u << st;
+          uint4* tile = reinterpret_cast<uint4*>(tiles + st * Sh::TILE);
+#pragma unroll 1
+          for (int i0 = lane; i0 < Sh::TILE / 16; i0 += 8 * 32) {
+            uint32_t inf[8];
+            uint4 x[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t lo = (w[q] & 0x7c00u) == 0x7c00u ? 0xffffu : 0u;
-              const uint32_t hi = (w[q] & 0x7c000000u) == 0x7c000000u ? 0xffff0000u : 0u;
-              any |= (lo | hi) != 0;
-              w[q] &= ~(lo | hi);
+            for (int e = 0; e < 8; ++e) x[e] = tile[i0 + 32 * e];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              auto f = [](uint32_t w) { return (w & 0x7c007c00u) + 0x04000400u; };
+              inf[e] = (f(x[e].x) | f(x[e].y) | f(x[e].z) | f(x[e].w)) & 0x80008000u;
             }
-            if (any) {
-              tile[i] = make_uint4(w[0], w[1], w[2], w[3]);
-              atomicOr(bad + 4 * slot + (row >> 5), 1u << (row & 31));
+            if (!__any_sync(0xffffffffu, inf[0] | inf[1] | inf[2] | inf[3] | inf[4] | inf[5] | inf[6] |
+                                             inf[7]))
+              continue;
+            own();
+            dirty |= 1u << buf;
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+              const int i = i0 + 32 * e, row = (i >> 3) & 127;
+              uint32_t w[4] = {tile[i].x, tile[i].y, tile[i].z, tile[i].w};
+              bool any = false;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t lo = (w[q] & 0x7c00u) == 0x7c00u ? 0xffffu : 0u;
+                const uint32_t hi = (w[q] & 0x7c000000u) == 0x7c000000u ? 0xffff0000u : 0u;
+                any |= (lo | hi) != 0;
+                w[q] &= ~(lo | hi);
+              }
+              if (any) {
+                tile[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                atomicOr(bad + 4 * slot + (row >> 5), 1u << (row & 31));
+              }
             }
           }
+          ++slot;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full + 8 * st);
         }
-        ++slot;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full + 8 * st);
       }
     }
   } else {
     // ================================================================ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tm + 128 * t + lanes, tO = tm + 256 + D * t + lanes;
@@ -545,25 +552,25 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
       }
       const float inv = 1.f / sum;
       part += 2 * a.part_rows;
+      // A thread's rows are 8 apart, so by whole tokens (G <= 8) and with one head.
+      const int row0 = (warp & 3) * 32 + (lane >> 2), step = 8 >> s.log_g;
+      const int tk0 = now.tok0 + t * per + (row0 >> s.log_g);
+      const int64_t at0 = now.b * a.o_row + tk0 * a.o_tok + (now.h * s.G + (row0 & (s.G - 1))) * a.o_head;
 #pragma unroll 1
       for (int f = 0; f < 2; ++f) {   // 16 rows at a time, two of them in a thread
-        int64_t at[2];
-        int row[2], tk[2];
         float scale[2];
         bool mine[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          row[e] = (warp & 3) * 32 + 16 * f + 8 * e + (lane >> 2);
-          tk[e] = now.tok0 + t * per + (row[e] >> s.log_g);
-          mine[e] = tk[e] < q_len;
+          mine[e] = tk0 + (2 * f + e) * step < q_len;
           scale[e] = __shfl_sync(0xffffffffu, inv, 16 * f + 8 * e + (lane >> 2));
-          at[e] = now.b * a.o_row + tk[e] * a.o_tok + (now.h * s.G + (row[e] & (s.G - 1))) * a.o_head;
         }
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          float o[16];
+        for (int q = 0; q < D / 32; q += 2) {
+          float o[2][16];
           __syncwarp();
-          tm_ld32(tO + ((uint32_t)(16 * f) << 16) + 32 * q, o);
+#pragma unroll
+          for (int z = 0; z < 2; ++z) tm_ld32(tO + ((uint32_t)(16 * f) << 16) + 32 * (q + z), o[z]);
           tm_wait_ld();
           if (any_bad) {   // what was left out of the products, into the rows that see it
             int slot = 0;
@@ -580,11 +587,11 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
                                       32 * q + 2 * (lane & 3);
 #pragma unroll
                   for (int e = 0; e < 2; ++e) {
-                    if (!mine[e] || !sees(s.sight, now.off + tk[e], key)) continue;
+                    if (!mine[e] || !sees(s.sight, now.off + tk0 + (2 * f + e) * step, key)) continue;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 16; ++i) {
                       const float y = h2f(v[8 * (i >> 1) + (i & 1)]);
-                      if (!isfinite(y)) o[4 * (i >> 1) + 2 * e + (i & 1)] += y;
+                      if (!isfinite(y)) o[i >> 3][4 * ((i & 7) >> 1) + 2 * e + (i & 1)] += y;
                     }
                   }
                 }
@@ -594,24 +601,27 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             if (whole) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const __half2 h2 = __floats2half2_rn(o[4 * i + 2 * e] * scale[e],
-                                                     o[4 * i + 2 * e + 1] * scale[e]);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
+              uint16_t* out = a.out + at0 + (2 * f + e) * (step * a.o_tok) + 32 * q + 8 * (lane & 3);
               __syncwarp();
-              transpose_quad(w);
-              if (mine[e])
-                *reinterpret_cast<uint4*>(a.out + at[e] + 32 * q + 8 * (lane & 3)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const __half2 h2 = __floats2half2_rn(o[z][4 * i + 2 * e] * scale[e],
+                                                       o[z][4 * i + 2 * e + 1] * scale[e]);
+                  w[i] = *reinterpret_cast<const uint32_t*>(&h2);
+                }
+                transpose_quad(w);
+                if (mine[e])
+                  *reinterpret_cast<uint4*>(out + 32 * z) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
             } else if (mine[e]) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float2*>(part + (size_t)(128 * t + row[e]) * D + 32 * q + 8 * i +
-                                           2 * (lane & 3)) =
-                    make_float2(o[4 * i + 2 * e], o[4 * i + 2 * e + 1]);
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float2*>(part + (size_t)(128 * t + row0 + 8 * (2 * f + e)) * D + 32 * q +
+                                           8 * i + 2 * (lane & 3)) =
+                    make_float2(o[i >> 2][4 * (i & 3) + 2 * e], o[i >> 2][4 * (i & 3) + 2 * e + 1]);
             }
           }
         }
