@@ -464,7 +464,7 @@ struct Probs {
   }
 };
 
-template <typename E, bool DRAFT>
+template <typename E, bool DRAFT, bool AHEAD>
 __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_constant__ Args a) {
   constexpr int N = Vec<E>::N;
   __shared__ Shared sh;
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
   };
   auto scale_of = [](float temp) { return kLog2e / fminf(fmaxf(temp, 1e-30f), 1e30f); };
   auto in_line = [&](int at) { return at + 1 < a.T ? at + 1 : -2; };
-  const int most = a.ahead ? kBatch : 1;
+  constexpr int most = AHEAD ? kBatch : 1;
   // Several nodes at once: a CTA takes whole ones, whose values are joined once and not in every CTA
   // (16 chains of 8 nodes, 50257 tokens: 28.8 us without, 22 with).
   const Row<E, DRAFT> alone{a, b, tid, kThreads, smem_u32(slots + tid)};
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
   auto look_on = [&](bool greedy, float c, auto before) {
     const int count = min(most, a.T - cur);
     const Stats<DRAFT> join{c};
-    const bool apart = count >= kCluster / 2;
+    const bool apart = AHEAD && count >= kCluster / 2;
     const int mine = apart ? ((int)rank < count) + ((int)(rank + size) < count) : 0;
     if (!apart)
       look(row, cur, most, in_line, greedy, c, false);
@@ -810,7 +810,8 @@ fade_status_t launch(const Args& a, int B, cudaStream_t st) {
   at[0].val.clusterDim = {kCluster, 1, 1};
   lc.attrs = at;
   lc.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&lc, tree_verify_kernel<E, DRAFT>, a);
+  const cudaError_t e = a.ahead ? cudaLaunchKernelEx(&lc, tree_verify_kernel<E, DRAFT, true>, a)
+                                : cudaLaunchKernelEx(&lc, tree_verify_kernel<E, DRAFT, false>, a);
   if (e != cudaSuccess)
     return set_error(FADE_ERR_CUDA, "fade_tree_verify: %s", cudaGetErrorString(e));
   return launch_status("fade_tree_verify");
