@@ -16,11 +16,11 @@
 // What bounds it: at d = 128 the tensor cores, which a pair of tiles (256 query rows, 128 tokens) keeps
 // busy for 2048 cycles of the 2700 to 3100 that the softmax's chain takes (wait, read S, maximum,
 // exponentials, write P); at d = 64 the chain, 2300 to 2500 cycles against 1024 of products and as many
-// of exponentials. 32 query and 8 KV heads: 16383 tokens of d = 128 1330 to 1500 us, as the clocks hold
-// (1650 to 1470 TFLOP/s), of d = 64 1068 us; 2 prompts of 32768 tokens under a window of 4160 2.9 to
-// 3.1 ms; 8 prompts of 1024 to 2048 tokens of d = 64 132 us, where an item's start and end cost as much
+// of exponentials. 32 query and 8 KV heads: 16383 tokens of d = 128 1320 to 1470 us, as the clocks hold
+// (1660 to 1500 TFLOP/s), of d = 64 1068 us; 2 prompts of 32768 tokens under a window of 4160 2.8 to
+// 3.0 ms; 8 prompts of 1024 to 2048 tokens of d = 64 132 us, where an item's start and end cost as much
 // as three of its six to eight tiles. Single tokens read their keys and values once: 64 rows of 4164
-// tokens 181 us, 6.0 TB/s.
+// tokens 175 us, 6.2 TB/s.
 #include <math.h>
 
 #include <algorithm>

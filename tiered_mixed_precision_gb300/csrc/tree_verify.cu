@@ -21,7 +21,7 @@
 // same numbers. Where all nodes' logits are little to read, their maxima and sums are taken in one pass
 // at the start, which leaves the chain one exchange. A pass costs its vectors (words come by asynchronous
 // copies, several vectors ahead: 100 us from registers, 77 so, at 64 trees of 128256 tokens) and 2 to 4 us
-// of reduction, exchange and waiting for the cluster's slowest: 64 trees of 16 nodes 66 us, 16 chains of 8
+// of reduction, exchange and waiting for the cluster's slowest: 64 trees of 16 nodes 64 us, 16 chains of 8
 // nodes over 50257 tokens 21 us, one greedy chain of 5 over 32000 10 us, of which a launch is half.
 #include <cuda_bf16.h>
 #include <math.h>
@@ -34,7 +34,7 @@
 namespace fade {
 namespace {
 
-// A row's CTAs, their threads and warps. At 64 rows of 128256 tokens 77 us (66 since, by other steps),
+// A row's CTAs, their threads and warps. At 64 rows of 128256 tokens 77 us (64 since, by other steps),
 // and with 4 CTAs of 512 the same; 8 of 512 (which leave a row waiting for its place) 94, 2 of 512 or
 // 1024 and 4 of 1024 from 96 to 99.
 constexpr int kCluster = 8, kThreads = 256, kWarps = kThreads / 32;
