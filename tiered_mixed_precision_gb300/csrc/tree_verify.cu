@@ -41,7 +41,11 @@ constexpr int kCluster = 8, kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBatch = 16;    // values exchanged at once
 static_assert(kBatch <= 2 * kCluster && (kWarps & (kWarps - 1)) == 0 && kWarps <= 32, "hand_out, over");
 constexpr int kNodes = FADE_TREE_MAX_NODES + 1;   // the root first
-constexpr long long kAheadBytes = 64ll << 20;   // logits of all rows and nodes that are looked at ahead
+// All nodes are looked at ahead where a row has at most kAheadLogits of them (nodes x vocabulary, the
+// drafter's too), all rows kAheadBytes. us ahead and not, for chains and for trees, of which fewer nodes
+// are kept: 16 rows of 0.51 M logits 19 and 29, 21 and 21; of 1.03 M 31 and 39, 28 and 23; one row of
+// 2.05 M 35 and 23, 37 and 21; 64 rows of 0.51 M (66 MB) 33 and 41, 128 rows of 0.26 M (66 MB) 43 and 43.
+constexpr long long kAheadLogits = 3 << 18, kAheadBytes = 128ll << 20;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
     if (greedy) {
       float4 best = none;
       best.x = -INFINITY;
-      row.template sweep<false, false, 2>(
+      row.template sweep<false, false, 2>(   // (two words a vector: 12.4 -> 10.4 us at a chain of 5)
             at, most, then,
             [&](int i, const Words<E>(&t)[2], const Words<E>(&)[2], const float(&)[N]) {
               float x[2 * N];
@@ -887,7 +891,8 @@ extern "C" fade_status_t fade_tree_verify(const fade_config_t* c, int32_t T, int
   a.T = T;
   a.V = vocab;
   a.greedy = u == nullptr;
-  a.ahead = (long long)c->batch * T * vocab * size * (draft ? 2 : 1) <= kAheadBytes;
+  const long long row = (long long)T * vocab * (draft ? 2 : 1);
+  a.ahead = row <= kAheadLogits && c->batch * row * size <= kAheadBytes;
   const cudaStream_t s = as_stream(stream);
   if (type == FADE_LOGITS_F16) return launch<__half>(a, c->batch, s);
   if (type == FADE_LOGITS_BF16) return launch<__nv_bfloat16>(a, c->batch, s);
