@@ -34,7 +34,7 @@ template <int D>
 struct Shape {
   static constexpr int TILE = D / 64 * kBlk;          // bytes of a K or Q tile
   static constexpr int STAGES = D == 128 ? 4 : 8;     // ring of Q tiles
-  static constexpr int SMALL = 3072;
+  static constexpr int SMALL = 3 * 1024;   // barriers, lse, halves
   static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + SMALL;
   static constexpr int THREADS = 640;   // 16 warps that sum, load, products, 2 that scale lse
 };
