@@ -304,3 +304,25 @@ def test_same_bits_and_graphs(F):
     for o in outs:
         for x, y in zip(o, plain):
             assert np.array_equal(x.cpu().numpy(), y)
+
+
+@pytest.mark.parametrize("mode", ["sampled", "certain", "greedy"])
+def test_largest_vocabulary(F, mode):
+    """2^24 tokens: the last one is likeliest by far (probability 1 - 2^24 e^-40), is kept where it is the
+    draft, and comes next where it is not."""
+    B, T, V = 2, 1, 1 << 24
+    target = torch.zeros((B, T + 1, V), dtype=torch.float16, device="cuda")
+    target[:, :, -1] = 40
+    d = dict(parents=torch.full((B, T), -1, dtype=torch.int32, device="cuda"), n_nodes=None,
+             tokens=torch.tensor([[V - 1], [V // 2]], dtype=torch.int32, device="cuda"),
+             target=target[:, 1:], target_root=target[:, 0],
+             draft=target[:, 1:] if mode == "sampled" else None,
+             draft_root=target[:, 0] if mode == "sampled" else None,
+             temperature=None, u=None if mode == "greedy" else torch.full((B, T), 0.5, device="cuda"),
+             noise=None if mode == "greedy" else torch.ones((B, V), device="cuda"))
+    if mode == "sampled":   # the drafter's likeliest token is another one
+        d["draft"], d["draft_root"] = d["draft"].clone(), d["draft_root"].clone()
+        for x in (d["draft"], d["draft_root"]):
+            x[1:, ..., V // 2], x[1:, ..., -1] = 40, 0
+    path, n_path, nxt = _call(F, None, B, T, d)
+    assert n_path.tolist() == [1, 0] and path[0, 0] == 0 and nxt.tolist() == [V - 1, V - 1]
