@@ -530,7 +530,13 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
         s *= ex2((m - top) * c);   // (0 from -inf)
         m = top;
       }
-      if (m == -INFINITY) return;
+      if (m == -INFINITY) {   // nothing above -inf so far; NaN has to show in the sum all the same
+        float any = x[0];
+#pragma unroll
+        for (int j = 1; j < N; ++j) any += x[j];
+        if (any != any) s = any;
+        return;
+      }
       float part[2] = {0.f, 0.f};
       if (careful) {
 #pragma unroll
