@@ -11,9 +11,10 @@
 // W_k+1 = W_k - p(x). The final draw is the largest r(i) / E_i with E_i given exponential variates (the
 // first of independent arrivals at rates r), greedy rows take the largest logit.
 //
-// p(i) = 2^(x_i c - M c - log2 S) in fp32 with c = log2(e) / temperature and M the row's maximum; what M c
-// and log2 S lose in rounding is the same for every token. Sums are fp32, in one fixed order. A row with
-// NaN or +inf (its sum says so) is gone over again with those replaced.
+// p(i) = 2^((x_i - M) c - log2 S) in fp32 with c = log2(e) / temperature and M the row's maximum. The
+// difference comes first: x_i c - M c would lose the last bits of M c, and u q W < r compares p itself, so that
+// low temperatures, or logits far from 0, would decide by what was lost. Sums are fp32, in one fixed order.
+// A row with NaN or +inf (its sum says so) is gone over again with those replaced.
 //
 // What bounds it: only nodes on the kept path are looked at, one after another, so a row is a chain of
 // passes over its vocabulary. A cluster of CTAs takes a row, each a share of the vocabulary; sums and
@@ -21,7 +22,7 @@
 // same numbers. Where all nodes' logits are little to read, their maxima and sums are taken in one pass
 // at the start, which leaves the chain one exchange. A pass costs its vectors (words come by asynchronous
 // copies, several vectors ahead: 100 us from registers, 77 so, at 64 trees of 128256 tokens) and 2 to 4 us
-// of reduction, exchange and waiting for the cluster's slowest: 64 trees of 16 nodes 64 us, 16 chains of 8
+// of reduction, exchange and waiting for the cluster's slowest: 64 trees of 16 nodes 66 us, 16 chains of 8
 // nodes over 50257 tokens 21 us, one greedy chain of 5 over 32000 10 us, of which a launch is half.
 #include <cuda_bf16.h>
 #include <math.h>
@@ -34,7 +35,7 @@
 namespace fade {
 namespace {
 
-// A row's CTAs, their threads and warps. At 64 rows of 128256 tokens 77 us (64 since, by other steps),
+// A row's CTAs, their threads and warps. At 64 rows of 128256 tokens 77 us (66 since, by other steps),
 // and with 4 CTAs of 512 the same; 8 of 512 (which leave a row waiting for its place) 94, 2 of 512 or
 // 1024 and 4 of 1024 from 96 to 99.
 constexpr int kCluster = 8, kThreads = 256, kWarps = kThreads / 32;
@@ -422,47 +423,39 @@ struct Row {
   }
 };
 
-// The distributions after a node. p(i) = 2^(x_i c + pt), a q(i) = 2^(y_i c + qt + la); an empty row's are
-// 2^-inf. Where p and q are the same numbers, p - 1 q is nothing to the last bit. careful: the logits
-// have NaN or infinities, or are too large to multiply first.
+// The distributions after a node. p(i) = 2^((x_i - mt) c + lt), a q(i) = 2^((y_i - md) c + ld + la); an empty
+// row's are 2^-inf. Where p and q are the same numbers, p - 1 q is nothing to the last bit. careful: the
+// logits have NaN or infinities.
 template <typename E, bool DRAFT>
 struct Probs {
   static constexpr int N = Vec<E>::N;
-  float c, mt, md, lt, ld, pt, qt;
+  float c, mt, md, lt, ld;
   float taken, la;   // a, log2 a
   bool careful;
-  __device__ __forceinline__ float p_of(float x) const {
-    return ex2(careful ? (x - mt) * c + lt : fmaf(x, c, pt));
-  }
-  __device__ __forceinline__ float q_of(float y, float l) const {
-    return ex2(careful ? (y - md) * c + (ld + l) : fmaf(y, c, qt + l));
-  }
+  __device__ __forceinline__ float p_of(float x) const { return ex2(fmaf(x - mt, c, lt)); }
+  __device__ __forceinline__ float q_of(float y, float l) const { return ex2(fmaf(y - md, c, ld + l)); }
   __device__ __forceinline__ float r_of(float x, float y) const {
     const float p = p_of(x);
     return DRAFT && taken > 0.f ? fmaxf(p - q_of(y, la), 0.f) : p;
   }
-  // r of a vector: the cases are told apart once for all of it
+  // r of a vector, two elements an instruction (the same bits as r_of's)
   template <bool Q>
   __device__ __forceinline__ void rest(const Words<E>& t, const Words<E>& d, float (&r)[N]) const {
     float x[N], y[N];
     logits(t, careful, x);
     if constexpr (Q) logits(d, careful, y);
-    if (careful) {
+    const f2x c2 = f2_pack(c, c), mt2 = f2_pack(mt, mt), lt2 = f2_pack(lt, lt);
+    const f2x md2 = f2_pack(md, md), ld2 = f2_pack(ld + la, ld + la);
 #pragma unroll
-      for (int j = 0; j < N; ++j) r[j] = r_of(x[j], Q ? y[j] : 0.f);
-    } else {
-      const f2x c2 = f2_pack(c, c), p2 = f2_pack(pt, pt), q2 = f2_pack(qt + la, qt + la);
-#pragma unroll
-      for (int j = 0; j < N; j += 2) {
-        f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), c2, p2), r[j], r[j + 1]);
-        r[j] = ex2(r[j]);
-        r[j + 1] = ex2(r[j + 1]);
-        if constexpr (Q) {
-          float q[2];
-          f2_unpack(f2_fma(f2_pack(y[j], y[j + 1]), c2, q2), q[0], q[1]);
-          r[j] = fmaxf(r[j] - ex2(q[0]), 0.f);
-          r[j + 1] = fmaxf(r[j + 1] - ex2(q[1]), 0.f);
-        }
+    for (int j = 0; j < N; j += 2) {
+      f2_unpack(f2_fma(f2_sub(f2_pack(x[j], x[j + 1]), mt2), c2, lt2), r[j], r[j + 1]);
+      r[j] = ex2(r[j]);
+      r[j + 1] = ex2(r[j + 1]);
+      if constexpr (Q) {
+        float q[2];
+        f2_unpack(f2_fma(f2_sub(f2_pack(y[j], y[j + 1]), md2), c2, ld2), q[0], q[1]);
+        r[j] = fmaxf(r[j] - ex2(q[0]), 0.f);
+        r[j + 1] = fmaxf(r[j + 1] - ex2(q[1]), 0.f);
       }
     }
   }
@@ -537,22 +530,17 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
         if (any != any) s = any;
         return;
       }
-      float part[2] = {0.f, 0.f};
-      if (careful) {
+      const f2x c2 = f2_pack(c, c), m2 = f2_pack(m, m);
+      f2x sum = f2_pack(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < N; ++j) part[j & 1] += ex2((x[j] - m) * c);
-      } else {
-        const f2x c2 = f2_pack(c, c), mc2 = f2_pack(-(m * c), -(m * c));
-        f2x sum = f2_pack(0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < N; j += 2) {
-          float y0, y1;
-          f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), c2, mc2), y0, y1);
-          sum = f2_add(sum, f2_pack(ex2(y0), ex2(y1)));
-        }
-        f2_unpack(sum, part[0], part[1]);
+      for (int j = 0; j < N; j += 2) {
+        float y0, y1;
+        f2_unpack(f2_mul(f2_sub(f2_pack(x[j], x[j + 1]), m2), c2), y0, y1);
+        sum = f2_add(sum, f2_pack(ex2(y0), ex2(y1)));
       }
-      s += part[0] + part[1];
+      float s0, s1;
+      f2_unpack(sum, s0, s1);
+      s += s0 + s1;
     };
     row.template sweep<DRAFT, false, 1>(
           at, most, then,
@@ -683,11 +671,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
       }
       next = top;
     } else {
-      // maxima and sums are numbers (NaN and +inf show in them), and maximum times c is, too
-      auto fine = [&](float m, float s) {
-        return s < INFINITY && (m == -INFINITY || fabsf(m) * c < 1e38f);
-      };
-      const bool careful = !(fine(st.x, st.y) && fine(st.z, st.w));
+      const bool careful = !(st.y < INFINITY && st.w < INFINITY);   // (NaN and +inf show in the sums)
       if (careful) {
         look(row, cur, 1, stop, false, c, true);
         exchange(sh, 1, join, turn);
@@ -699,8 +683,6 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
       pr.md = st.z == -INFINITY ? 0.f : st.z;
       pr.lt = st.y > 0.f ? -log2f(st.y) : 0.f;
       pr.ld = st.w > 0.f ? -log2f(st.w) : 0.f;
-      pr.pt = pr.lt - pr.mt * c;
-      pr.qt = pr.ld - pr.md * c;
       pr.taken = pr.la = 0.f;
       pr.careful = careful;
       float left_mass = 1.f;   // W
