@@ -684,12 +684,13 @@ __global__ void __launch_bounds__(256) prompt_combine_kernel(const __grid_consta
     for (int z = 0; z < 8; ++z) {
       // without a maximum nothing was seen, sum 0, or NaN alone, sum NaN
       const float w = ml[z].x == -INFINITY ? ml[z].y : ex2(ml[z].x - Mn);
-      if (w == 0.f) continue;
-      L = fmaf(ml[z].y, w, L);
+      // (a weight of 0 leaves nothing of numbers, but what is none reaches the result, as in a whole item)
+      auto add = [&](float v, float sum) { return isfinite(v) ? fmaf(v, w, sum) : sum + v; };
+      L = add(ml[z].y, L);
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
-        o[2 * i] = fmaf(x[z][i].x, w, o[2 * i]);
-        o[2 * i + 1] = fmaf(x[z][i].y, w, o[2 * i + 1]);
+        o[2 * i] = add(x[z][i].x, o[2 * i]);
+        o[2 * i + 1] = add(x[z][i].y, o[2 * i + 1]);
       }
     }
     M = Mn;
