@@ -223,6 +223,22 @@ class FadeCache:
                           pos_start, pos_step)
         return x
 
+    def _check_prompt(self, k_raw, v, q_raw, prompt_len):
+        """Raises what a prefill would come upon with its prompt half rotated."""
+        c = self.cfg
+        B, H, P, d = k_raw.shape
+        for name, x, heads in (("k_raw", k_raw, c.num_kv_heads), ("v", v, c.num_kv_heads),
+                               ("q_raw", q_raw, c.num_q_heads)):
+            if x is None:
+                continue
+            want = (c.batch, heads, P, c.head_dim)
+            if x.dtype != torch.float16 or tuple(x.shape) != want or not x.is_contiguous():
+                raise ValueError(f"{name} must be contiguous float16 {want}, not "
+                                 f"{str(x.dtype).removeprefix('torch.')} {tuple(x.shape)}")
+        lens = np.asarray(prompt_len)
+        if lens.shape != (B,) or lens.min() < 0 or lens.max() > P:
+            raise ValueError(f"prompt_len must hold {B} lengths in [0, {P}]")
+
     def prefill(self, layer: int, k_raw: torch.Tensor, v: torch.Tensor, prompt_len=None,
                 mass: torch.Tensor | None = None, q_raw: torch.Tensor | None = None,
                 out: torch.Tensor | None = None, window: int = 0):
@@ -234,6 +250,8 @@ class FadeCache:
         (``fade_prompt_attention``; rows past their lengths are left as they are), over all tokens or,
         with ``window``, over the last ``window`` ones and the sinks; the mass then comes from its
         log-sum-exp (``fade_prompt_mass``) and sees the same tokens.
+        Arguments are looked at before anything is rotated or reset. (What the cache itself has no room
+        for, ``fade_cache_prefill`` refuses afterwards.)
         Returns the mass the prefill used (None when it used none)."""
         c = self.cfg
         B, H, P, d = k_raw.shape
@@ -243,15 +261,23 @@ class FadeCache:
             raise ValueError("the prompt's attention needs its queries (q_raw)")
         if window and out is None:
             raise ValueError("a window is the attention's: give out")
+        L = self.layers[layer]
+        wants_mass = mass is None and q_raw is not None and c.policy == "h2o"
+        self._check_prompt(k_raw, v, q_raw if wants_mass or out is not None else None, prompt_len)
+        if out is not None:
+            q, k, vt = (x.transpose(1, 2) for x in (q_raw, k_raw, v))
+            lse = torch.empty((B, P, c.num_q_heads), dtype=torch.float32, device=k_raw.device)
+            ws = torch.empty(F.fade_prompt_ws_bytes(c, P, P), dtype=torch.uint8, device=k_raw.device)
+            see = dict(kv_len=prompt_len, n_sink=c.n_sink, window=window, ws=ws, status=L.status)
+            # (without queries: looks at its arguments and does nothing)
+            F.fade_prompt_attention(c, q, k, vt, out.transpose(1, 2), lse, q_len=np.zeros(B, np.int32),
+                                    **see)
         normed = self.qk_norm[layer] is not None
         if normed:
             kt = k_raw.transpose(1, 2)
             self._norm_rope(layer, None, kt, None, None, kt)
         else:
             self.rope_(k_raw, B * H, P, None, 1)
-        L = self.layers[layer]
-        F.fade_cache_reset(L)
-        wants_mass = mass is None and q_raw is not None and c.policy == "h2o"
         if wants_mass or out is not None:
             if normed:
                 qt = q_raw.transpose(1, 2)
@@ -260,17 +286,13 @@ class FadeCache:
                 self.rope_(q_raw, B * c.num_q_heads, P, None, 1)
         if wants_mass:
             mass = torch.empty((B, H, P), dtype=torch.float32, device=k_raw.device)
-        if out is not None:
-            q, k = q_raw.transpose(1, 2), k_raw.transpose(1, 2)
-            lse = torch.empty((B, P, c.num_q_heads), dtype=torch.float32, device=k_raw.device)
-            ws = torch.empty(F.fade_prompt_ws_bytes(c, P, P), dtype=torch.uint8, device=k_raw.device)
-            see = dict(q_len=prompt_len, kv_len=prompt_len, n_sink=c.n_sink, window=window, ws=ws,
-                       status=L.status)
-            F.fade_prompt_attention(c, q, k, v.transpose(1, 2), out.transpose(1, 2), lse, **see)
-            if wants_mass:
-                F.fade_prompt_mass(c, q, k, lse, mass, **see)
-        elif wants_mass:
+        if out is None and wants_mass:
             F.fade_prefill_mass(c, q_raw, k_raw, P, prompt_len, mass)
+        F.fade_cache_reset(L)   # (its status words are the attention's, too)
+        if out is not None:
+            F.fade_prompt_attention(c, q, k, vt, out.transpose(1, 2), lse, q_len=prompt_len, **see)
+            if wants_mass:
+                F.fade_prompt_mass(c, q, k, lse, mass, q_len=prompt_len, **see)
         F.fade_cache_prefill(L, k_raw, v, P, prompt_len, mass, self.table, self.max_pos)
         return mass
 
