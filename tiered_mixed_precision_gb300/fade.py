@@ -749,14 +749,27 @@ def fade_prompt_ws_bytes(cfg: Config, n_q: int, n_kv: int) -> int:
     return n
 
 
+_INT32 = np.dtype(np.int32)
+
+
 def _host_lens(name, x, rows):
     """HOST i32 lengths as the bytes of a C array (None: NULL)."""
     if x is None:
         return None
-    x = np.ascontiguousarray(x, np.int32)
-    if x.shape != (rows,):
+    lens = np.ascontiguousarray(x)
+    if lens.shape != (rows,):
         raise ValueError(f"{name} must hold {rows} lengths")
-    return x.tobytes()
+    if lens.dtype != _INT32:
+        x, lens = lens, lens.astype(_INT32)
+        if not (lens == x).all():   # wider integers, fractions
+            raise ValueError(f"{name} must be 32-bit integers")
+    return lens.tobytes()
+
+
+def _i32(x):
+    """An integer of any size as the 32-bit one that the prompt calls treat alike (no prompt has so many
+    tokens; ctypes would take it modulo 2^32)."""
+    return x if 0 <= x < 2 ** 31 else max(-1, min(x, 2 ** 31 - 1))
 
 
 def _prompt_ws(cfg, dev, n_q, n_kv, q, ws, stream):
@@ -789,7 +802,7 @@ def fade_prompt_attention(cfg: Config, q, k, v, out, lse=None, q_len=None, kv_le
     ws = _prompt_ws(cfg, dev, n_q, n_kv, q, ws, stream)
     _check(lib().fade_prompt_attention(
         ctypes.byref(cfg.c()), hq, hk, hv, n_q, n_kv, _host_lens("q_len", q_len, B),
-        _host_lens("kv_len", kv_len, B), n_sink, window, ho,
+        _host_lens("kv_len", kv_len, B), _i32(n_sink), _i32(window), ho,
         None if lse is None else lse.data_ptr(), None if status is None else status.data_ptr(),
         ws.data_ptr(), ws.nbytes, _stream(stream)))
 
@@ -814,9 +827,9 @@ def fade_prompt_mass(cfg: Config, q, k, lse, mass, q_len=None, kv_len=None, n_si
     ws = _prompt_ws(cfg, dev, n_q, n_kv, q, ws, stream)
     _check(lib().fade_prompt_mass(
         ctypes.byref(cfg.c()), hq, hk, n_q, n_kv, _host_lens("q_len", q_len, B),
-        _host_lens("kv_len", kv_len, B), n_sink, window, lse.data_ptr(), int(bool(accumulate)),
-        mass.data_ptr(), None if status is None else status.data_ptr(), ws.data_ptr(), ws.nbytes,
-        _stream(stream)))
+        _host_lens("kv_len", kv_len, B), _i32(n_sink), _i32(window), lse.data_ptr(),
+        int(bool(accumulate)), mass.data_ptr(), None if status is None else status.data_ptr(),
+        ws.data_ptr(), ws.nbytes, _stream(stream)))
 
 
 def fade_attention_tiled(cfg: Config) -> bool:
