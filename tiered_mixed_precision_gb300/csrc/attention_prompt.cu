@@ -24,6 +24,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "prompt.cuh"
 #include "tensor_core.cuh"
@@ -728,7 +729,7 @@ fade_status_t launch(const fade_config_t* c, Args& a, int blocks, cudaStream_t s
   int P = 0;
   const int joins = prompt_schedule(a.s, a.rows, blocks, sms, a.sched, &P);
   auto kern = prompt_attention_kernel<D>;
-  static bool opted[64];   // per device: the kernel has its shared memory
+  static std::atomic<bool> opted[64];   // per device: the kernel has its shared memory
   if (!opted[device]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM) !=
         cudaSuccess)
@@ -760,21 +761,21 @@ size_t prompt_attention_ws(const fade_config_t* c, int32_t n_q) {
 }
 
 int prompt_sms(int* device) {
-  static int known[64];
+  static std::atomic<int> known[64];
   if (cudaGetDevice(device) != cudaSuccess || *device >= 64) {
     set_error(FADE_ERR_CUDA, "no device, or one past the 64th");
     return 0;
   }
   const int d = *device;
-  if (known[d] == 0) {
-    int n = 0;
+  int n = known[d];
+  if (n == 0) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d) != cudaSuccess) {
       launch_status("SM count");
       return 0;
     }
-    known[d] = n < kPromptSMs ? n : kPromptSMs;
+    known[d] = n = n < kPromptSMs ? n : kPromptSMs;
   }
-  return known[d];
+  return n;
 }
 
 fade_status_t prompt_shape(const fade_config_t* c, const fade_heads_t* q, const fade_heads_t* k,

@@ -18,6 +18,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "prompt.cuh"
 #include "tensor_core.cuh"
@@ -378,7 +379,7 @@ fade_status_t launch(Args& a, cudaStream_t st) {
   const int sms = prompt_sms(&device);
   if (sms == 0) return FADE_ERR_CUDA;
   auto kern = prompt_mass_kernel<D>;
-  static bool opted[64];   // per device: the kernel has its shared memory
+  static std::atomic<bool> opted[64];   // per device: the kernel has its shared memory
   if (!opted[device]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM) !=
         cudaSuccess)

@@ -540,9 +540,9 @@ def _device(stream):
     if _torch is None:
         import torch
 
-        _torch = torch
         for name in ("float16", "bfloat16", "float32", "int32", "int64"):
             _dtypes[name] = getattr(torch, name)
+        _torch = torch   # (last: another thread that sees it uses the types, too)
     if stream is not None:
         return None
     global _available
