@@ -65,11 +65,6 @@ __device__ __forceinline__ void tm_wait_ld() {
 __device__ __forceinline__ void tm_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // Waits for the phase-th completion of an mbarrier, for kWaitCycles at most: a wait that gives up sets
 // the CTA's word `dead`, which ends every other wait at once; the flow stays the same.

@@ -1,4 +1,5 @@
-// Shared by the drafted-token translation units: what their kernels read and the host checks.
+// Shared by the drafted-token translation units (and, through prompt.cuh, the prompts): what their kernels
+// read, 2^x, and the host checks.
 #pragma once
 
 #include "fade_internal.cuh"
@@ -16,6 +17,12 @@ struct TreeArgs {
   fade_heads_t tk, tv;     // the nodes' keys and values, H heads
   int B, H, Hq, G, log_g, S, W, C, T;   // G = 1 << log_g
 };
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // The i-th node of row b's path; a node outside the tree reads as node 0 (the commit records it).
 __device__ __forceinline__ int tree_node(const TreeArgs& a, const int32_t* path, int b, int i) {

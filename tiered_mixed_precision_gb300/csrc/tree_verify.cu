@@ -30,7 +30,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "prompt.cuh"
+#include "tree.cuh"
 
 namespace fade {
 namespace {
@@ -59,11 +59,6 @@ struct Args {
   int ahead;          // all nodes are looked at in one pass, kBatch of them a time
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // A logit as it counts: NaN reads as -inf, +inf as the largest number.
 __device__ __forceinline__ float logit(float x) {
   return x != x ? -INFINITY : fminf(x, 3.402823466e38f);
