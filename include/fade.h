@@ -538,7 +538,9 @@ typedef enum { FADE_LOGITS_F16 = 0, FADE_LOGITS_BF16 = 1, FADE_LOGITS_F32 = 2 } 
  * lowest token. Logits of -inf or NaN have no probability, +inf reads as the largest number; tokens
  * outside [0, vocab) are refused.
  * Writes path: i32 [B][T] (0 past its length), n_path: i32 [B], next: i32 [B] (-1 where there is nothing
- * to draw from: no logit above -inf, or no node and no target_root). fp32 arithmetic in one fixed order.
+ * to draw from: no logit above -inf, or no node and no target_root). fp32 arithmetic in one fixed order,
+ * on differences from the largest logit: an offset that all logits share, or a temperature near 0 (1e-30
+ * counts as the lowest), loses nothing.
  * Only the logits after kept nodes count; those after any node of the tensor may be
  * read, past n_nodes too. 1 <= vocab <= FADE_MAX_VOCAB. */
 fade_status_t fade_tree_verify(const fade_config_t* cfg, int32_t T, int32_t vocab, int32_t type,

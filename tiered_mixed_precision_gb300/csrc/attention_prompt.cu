@@ -10,15 +10,19 @@
 // a maximum and moves only when a tile's maximum passes it by more than 14 (P stays below 2^15; fp16
 // loses only what is 2^-31 of the largest P), which spares most rescalings of O.
 //
-// Roundings to fewer than 32 bits: P to fp16 before it meets V, the output. Products of fp16 operands
-// are exact in fp32, sums are fp32.
+// Roundings to fewer than 32 bits: P to fp16 before it meets V, the output. The tensor cores take P in 16
+// bits, as V is; fp16 has three bits more than bf16, and the reference keeps P in its range. That is half a
+// step, 2^-11, of every probability: errors of 2.5e-4 to 3.0e-4 of the output's norm against 64 bits, where
+// the output's own rounding alone makes 2.0e-4. A second product, with what is lost of P, would take it away
+// for half as many products again. L sums P before its rounding. Products of fp16 operands are exact in
+// fp32, sums are fp32.
 //
 // What bounds it: at d = 128 the tensor cores, which a pair of tiles (256 query rows, 128 tokens) keeps
 // busy for 2048 cycles of the 2700 to 3100 that the softmax's chain takes (wait, read S, maximum,
 // exponentials, write P); at d = 64 the chain, 2300 to 2500 cycles against 1024 of products and as many
-// of exponentials. 32 query and 8 KV heads: 16383 tokens of d = 128 1320 to 1470 us, as the clocks hold
-// (1660 to 1500 TFLOP/s), of d = 64 1068 us; 2 prompts of 32768 tokens under a window of 4160 2.8 to
-// 3.0 ms; 8 prompts of 1024 to 2048 tokens of d = 64 132 us, where an item's start and end cost as much
+// of exponentials. 32 query and 8 KV heads: 16383 tokens of d = 128 1320 to 1510 us, as the clocks hold
+// (1660 to 1460 TFLOP/s), of d = 64 1070 us; 2 prompts of 32768 tokens under a window of 4160 2.8 to
+// 3.1 ms; 8 prompts of 1024 to 2048 tokens of d = 64 132 us, where an item's start and end cost as much
 // as three of its six to eight tiles. Single tokens read their keys and values once: 64 rows of 4164
 // tokens 175 us, 6.2 TB/s.
 #include <math.h>

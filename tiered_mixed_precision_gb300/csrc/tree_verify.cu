@@ -12,9 +12,9 @@
 // first of independent arrivals at rates r), greedy rows take the largest logit.
 //
 // p(i) = 2^((x_i - M) c - log2 S) in fp32 with c = log2(e) / temperature and M the row's maximum. The
-// difference comes first: x_i c - M c would lose the last bits of M c, and u q W < r compares p itself, so that
-// low temperatures, or logits far from 0, would decide by what was lost. Sums are fp32, in one fixed order.
-// A row with NaN or +inf (its sum says so) is gone over again with those replaced.
+// difference comes first: x_i c - M c would lose the last bits of M c, and u q W < r compares p itself,
+// so that low temperatures, or logits far from 0, would decide by what was lost. Sums are fp32, in one fixed
+// order. A row with NaN or +inf (its sum says so) is gone over again with those replaced.
 //
 // What bounds it: only nodes on the kept path are looked at, one after another, so a row is a chain of
 // passes over its vocabulary. A cluster of CTAs takes a row, each a share of the vocabulary; sums and
@@ -43,9 +43,16 @@ constexpr int kBatch = 16;    // values exchanged at once
 static_assert(kBatch <= 2 * kCluster && (kWarps & (kWarps - 1)) == 0 && kWarps <= 32, "hand_out, over");
 constexpr int kNodes = FADE_TREE_MAX_NODES + 1;   // the root first
 // All nodes are looked at ahead where a row has at most kAheadLogits of them (nodes x vocabulary, the
-// drafter's too), all rows kAheadBytes. us ahead and not, for chains and for trees, of which fewer nodes
-// are kept: 16 rows of 0.51 M logits 19 and 29, 21 and 21; of 1.03 M 31 and 39, 28 and 23; one row of
-// 2.05 M 35 and 23, 37 and 21; 64 rows of 0.51 M (66 MB) 33 and 41, 128 rows of 0.26 M (66 MB) 43 and 43.
+// drafter's too), all rows kAheadBytes. us ahead / not, replayed, by a row's logits in M (of trees, fewer
+// nodes are kept):
+//   1 row    chains: greedy 0.16 10.4 / 16.4, 0.64 16.5 / 22.7; sampled 0.51 16.5 / 14.5, 0.77 24.6 / 24.7,
+//            2.05 36.9 / 22.6; certain 0.40 16.5 / 16.5, 1.03 24.7 / 20.6
+//            trees: greedy 2.05 24.7 / 12.3; sampled 1.02 22.6 / 14.5; certain 0.51 16.5 / 12.5, 2.05 35 / 21
+//   16 rows  chains: sampled 0.51 18.5 / 28.8; certain 0.40 19.5 / 31, 1.03 30.8 / 39.0
+//            trees: greedy 0.51 16.6 / 16.5; sampled 1.02 28.8 / 22.6; certain 0.51 20.6 / 20.6
+//   64 rows  sampled chains 0.51 33 / 41, trees 0.26 31 / 33, 1.02 51 / 34; 128 rows, chains 0.26 44 / 43.5
+// So the rule has a price where logits alone do not tell: 2 to 4 us for one row's sampled chain or certain
+// tree of 0.51, 8 us for 16 rows' certain chains of 1.03. Rows and mode would have to be in it.
 constexpr long long kAheadLogits = 3 << 18, kAheadBytes = 128ll << 20;
 constexpr float kLog2e = 1.4426950408889634f;
 

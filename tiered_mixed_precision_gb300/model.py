@@ -445,7 +445,8 @@ class FadeCache:
         [B][T], n_nodes: device i32 [B] or None): every layer's maintenance is done, and the
         tree's masks and positions are built. Then ``tree_attend`` every layer and
         ``tree_commit`` the accepted paths (or begin again, which leaves the cache as it is). A
-        cache that evicts needs mid_capacity >= int4_budget + T. Trees of as many nodes share their
+        cache that evicts needs mid_capacity >= int4_budget + T. ``parents`` and ``n_nodes`` are read
+        again by the tree's other calls: leave them as they are until its commit. Trees of as many nodes share their
         buffers: the next one reuses them. They live as long as such a tree does, or, once used in a
         captured step, as the cache; the last tree's until the next."""
         c, L = self.cfg, len(self.layers)
