@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -29,3 +30,10 @@ def pytest_collection_modifyitems(config, items):
     for item in items:
         if "gpu" in item.keywords:
             item.add_marker(skip)
+
+
+def pytest_runtest_setup(item):
+    # what earlier tests left in cycles may hold CUDA graphs, and one that is destroyed while a test
+    # captures ends its capture
+    if "gpu" in item.keywords:
+        gc.collect()

@@ -8,7 +8,9 @@ CUDA library on the caller's stream; this module only allocates buffers and pass
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import gc
 import weakref
 from dataclasses import dataclass
 
@@ -38,6 +40,21 @@ def _record_event(ev):
                                           1)  # cudaEventRecordExternal
     if rc != 0:
         raise RuntimeError(f"cudaEventRecordWithFlags failed ({rc})")
+
+
+@contextlib.contextmanager
+def _capturing(graph):
+    """A capture into ``graph`` during which Python collects no cycles: one that some part of the
+    program left behind may hold a graph, which, destroyed meanwhile, ends the capture with an
+    error."""
+    collects = gc.isenabled()
+    gc.disable()
+    try:
+        with torch.cuda.graph(graph):
+            yield
+    finally:
+        if collects:
+            gc.enable()
 
 
 class TreeBuffers:
@@ -425,7 +442,7 @@ class FadeCache:
         metadata (ring head, live buffer). Raises if a step would change the counts."""
         before = self.mirror()
         g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g):
+        with _capturing(g):
             if side is None and not pipelined:
                 self.step_all(q, k, v, out)
             else:
@@ -631,7 +648,7 @@ class FadeCache:
                                "and with full sinks and recent windows")
         before = self.mirror()
         g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g):
+        with _capturing(g):
             for layer in range(len(self.layers)):
                 self.step_layer(layer, q[layer], k[layer], v[layer], out[layer])
         for L, (s, m, r) in zip(self.layers, before):
